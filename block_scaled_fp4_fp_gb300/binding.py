@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -55,6 +56,11 @@ SIGNATURES = {
     "qmm": (_INT, [_VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _INT, _INT, _INT, _VP, _VP]),
     "fp4_debug_inject_wait_timeout": (_INT, [_INT]),
     "fp4_debug_stream_weights": (_INT, [_VP, _VP, _I64, _I64, _VP]),
+    "kv_plan": (_INT, [_VP, _VP, _I64, _INT, _VP, _I64, _VP, _I64, _I64, _VP, _VP, _VP, _VP, _I64, _VP, _VP]),
+    "kv_append": (_INT, [_VP, _VP, _I64, _I64, _VP, _I64, _I64, _VP, _I64, _VP]),
+    "kv_attention_workspace_bytes": (c.c_size_t, [_I64, _I64, _I64, _I64, _I64]),
+    "kv_attention": (_INT, [_VP, _VP, _I64, _I64, _I64, _I64, _VP, _VP, _I64, _VP, _I64, _I64, _I64, _F, _I64, _VP,
+                            c.c_size_t, _VP, _VP, _VP]),
     "fp4_amax_global_scale_noalloc": (_INT, [_VP, _I64, _VP, _VP, _VP]),
 }
 
@@ -321,6 +327,105 @@ def qmm(x: torch.Tensor, w: torch.Tensor, scales: torch.Tensor, biases=None, glo
         out = torch.empty((M, N), dtype=torch.bfloat16, device=w.device)
     _check(lib().qmm(_p(x), _p(w), _p(scales), _p(biases), _p(global_scale_w), M, N, K, mode, 4, group_size, _p(out),
                      _s(stream)), "qmm")
+    return out
+
+
+class KvCache(c.Structure):
+    """fp4_kv_cache: one layer's paged 4-bit cache (make it with kv_cache, which keeps the tensors alive)."""
+    _fields_ = [("k_codes", c.c_void_p), ("k_scales", c.c_void_p), ("v_codes", c.c_void_p), ("v_scales", c.c_void_p),
+                ("global_scale_k", c.c_void_p), ("global_scale_v", c.c_void_p), ("num_pages", c.c_int64),
+                ("page_size", c.c_int32), ("kv_heads", c.c_int32), ("head_dim", c.c_int32), ("mode", c.c_int)]
+
+
+def kv_cache(k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor, v_scales: torch.Tensor,
+             mode: int = MODE_NVFP4, global_scale_k=None, global_scale_v=None) -> KvCache:
+    """A cache over the caller's tensors: codes int32 [pages, kv_heads, page_size, head_dim/8], scales uint8
+    [pages, kv_heads, page_size, head_dim/group], all contiguous."""
+    pages, heads, page, words = k_codes.shape
+    if v_codes.shape != k_codes.shape:
+        raise ValueError(f"k and v codes differ in shape: {tuple(k_codes.shape)}, {tuple(v_codes.shape)}")
+    want = (pages, heads, page, words * 8 // GROUP[mode])
+    for name, t, shape, dt in (("k_codes", k_codes, tuple(k_codes.shape), torch.int32),
+                               ("v_codes", v_codes, tuple(k_codes.shape), torch.int32),
+                               ("k_scales", k_scales, want, torch.uint8), ("v_scales", v_scales, want, torch.uint8)):
+        if tuple(t.shape) != shape or t.dtype != dt or not t.is_contiguous():
+            raise ValueError(f"{name}: a contiguous {dt} tensor of shape {shape} is needed, got {t.dtype} "
+                             f"{tuple(t.shape)}")
+    cache = KvCache(_p(k_codes), _p(k_scales), _p(v_codes), _p(v_scales), _p(global_scale_k), _p(global_scale_v),
+                    pages, page, heads, words * 8, mode)
+    cache.tensors = (k_codes, k_scales, v_codes, v_scales, global_scale_k, global_scale_v)
+    return cache
+
+
+def kv_cache_empty(num_pages: int, kv_heads: int, page_size: int, head_dim: int, mode: int = MODE_NVFP4,
+                   global_scale_k=None, global_scale_v=None, device="cuda") -> KvCache:
+    """A zero-filled cache of one layer."""
+    codes = [torch.zeros((num_pages, kv_heads, page_size, head_dim // 8), dtype=torch.int32, device=device)
+             for _ in range(2)]
+    scales = [torch.zeros((num_pages, kv_heads, page_size, head_dim // GROUP[mode]), dtype=torch.uint8, device=device)
+              for _ in range(2)]
+    return kv_cache(codes[0], scales[0], codes[1], scales[1], mode, global_scale_k, global_scale_v)
+
+
+class KvPlan(NamedTuple):
+    """kv_plan's outputs (device tensors)."""
+    total_lens: torch.Tensor   # int32 [batch]
+    query_start: torch.Tensor  # int32 [batch + 1]
+    slot_map: torch.Tensor     # int64 [tokens]
+    positions: torch.Tensor    # int32 [tokens]
+    pages_taken: torch.Tensor  # int32 scalar
+
+
+def kv_plan(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor, block_table: torch.Tensor,
+            page_size: int, tokens: int, plan: KvPlan = None, stream=None) -> KvPlan:
+    """Places a step's tokens: completes block_table [batch, max_pages] in place from free_pages and returns the
+    lengths, slots and positions of up to `tokens` tokens (entries past the step's own are -1)."""
+    batch = cached_lens.numel()
+    if plan is None:
+        ints = torch.empty(2 * batch + 2 + tokens, dtype=torch.int32, device=cached_lens.device)
+        slots = torch.empty(tokens, dtype=torch.int64, device=cached_lens.device)
+        total, start, pos, taken = ints.split_with_sizes((batch, batch + 1, tokens, 1))
+        plan = KvPlan(total, start, slots, pos, taken[0])
+    _check(lib().kv_plan(_p(cached_lens), _p(new_lens), batch, page_size, _p(free_pages), free_pages.numel(),
+                         _p(block_table), block_table.stride(0), block_table.shape[1], _p(plan.total_lens),
+                         _p(plan.query_start), _p(plan.slot_map), _p(plan.positions), plan.slot_map.numel(),
+                         _p(plan.pages_taken), _s(stream)), "kv_plan")
+    return plan
+
+
+def kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, stream=None):
+    """Quantizes k and v [tokens, kv_heads, head_dim] (views with strides are read in place) into their slots."""
+    for name, t in (("k", k), ("v", v)):
+        if t.shape[1:] != (cache.kv_heads, cache.head_dim) or t.shape[0] != slot_map.numel() or t.stride(2) != 1:
+            raise ValueError(f"{name}: [{slot_map.numel()}, {cache.kv_heads}, {cache.head_dim}] with unit stride in a "
+                             f"row is needed, got {tuple(t.shape)}, strides {t.stride()}")
+    _check(lib().kv_append(c.byref(cache), _p(k), k.stride(0), k.stride(1), _p(v), v.stride(0), v.stride(1),
+                           _p(slot_map), k.shape[0], _s(stream)), "kv_append")
+
+
+def kv_attention_workspace(cache: KvCache, batch: int, q_heads: int, max_query_len: int = 1, device="cuda"):
+    """A zero-filled workspace for kv_attention (allocate once, reuse)."""
+    n = lib().kv_attention_workspace_bytes(batch, q_heads, cache.kv_heads, cache.head_dim, max_query_len)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def kv_attention(cache: KvCache, q: torch.Tensor, query_start: torch.Tensor, total_lens: torch.Tensor,
+                 block_table: torch.Tensor, ws: torch.Tensor, max_query_len: int = 1, scale: float = None,
+                 window: int = 0, out=None, lse=None, stream=None):
+    """Causal attention of q [tokens, q_heads, head_dim] over the paged 4-bit cache; scale defaults to
+    head_dim ** -0.5."""
+    tokens, heads, dim = q.shape
+    batch = total_lens.numel()
+    if dim != cache.head_dim or q.stride(2) != 1 or query_start.numel() != batch + 1 or block_table.shape[0] != batch:
+        raise ValueError(f"q {tuple(q.shape)} (strides {q.stride()}), query_start {tuple(query_start.shape)}, total_lens "
+                         f"{tuple(total_lens.shape)} and block_table {tuple(block_table.shape)} do not belong together "
+                         f"for head_dim {cache.head_dim}")
+    if out is None:
+        out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=q.device)
+    _check(lib().kv_attention(c.byref(cache), _p(q), q.stride(0), q.stride(1), tokens, heads, _p(query_start),
+                              _p(total_lens), batch, _p(block_table), block_table.stride(0),
+                              block_table.shape[1], max_query_len, dim ** -0.5 if scale is None else scale, window,
+                              _p(ws), ws.numel() * ws.element_size(), _p(out), _p(lse), _s(stream)), "kv_attention")
     return out
 
 

@@ -486,6 +486,143 @@ fp4_status qmm(const fp4_bf16* x, const uint32_t* w, const void* scales, const f
                               g_inject_timeout.load(), stream));
 }
 
+namespace {
+// The cache every kv_ entry point takes.
+fp4_status check_kv_cache(const fp4_kv_cache* c) {
+  if (!c) return FP4_ERR_INVALID_ARG;
+  if (c->mode != FP4_MODE_NVFP4 && c->mode != FP4_MODE_MXFP4) return FP4_ERR_UNSUPPORTED;
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128) return FP4_ERR_UNSUPPORTED;
+  if (c->head_dim > 256 || c->head_dim % 32 != 0) return FP4_ERR_UNSUPPORTED;
+  if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales) return FP4_ERR_INVALID_ARG;
+  if (c->num_pages < 1 || c->kv_heads < 1 || c->head_dim < 32) return FP4_ERR_INVALID_ARG;
+  if (c->num_pages > INT32_MAX || c->num_pages * c->page_size > INT32_MAX / c->kv_heads) return FP4_ERR_INVALID_ARG;
+  if ((c->global_scale_k || c->global_scale_v) && c->mode != FP4_MODE_NVFP4) return FP4_ERR_INVALID_ARG;
+  if (!aligned(c->k_codes, 16) || !aligned(c->k_scales, 16) || !aligned(c->v_codes, 16) || !aligned(c->v_scales, 16) ||
+      !aligned(c->global_scale_k, 4) || !aligned(c->global_scale_v, 4))
+    return FP4_ERR_ALIGNMENT;
+  return FP4_OK;
+}
+
+KvCacheDesc kv_desc(const fp4_kv_cache* c) {
+  KvCacheDesc d;
+  d.k_codes = c->k_codes;
+  d.k_scales = c->k_scales;
+  d.v_codes = c->v_codes;
+  d.v_scales = c->v_scales;
+  d.gs_k = c->global_scale_k;
+  d.gs_v = c->global_scale_v;
+  d.num_pages = c->num_pages;
+  d.page_size = c->page_size;
+  d.kv_heads = c->kv_heads;
+  d.head_dim = c->head_dim;
+  d.mode = c->mode;
+  return d;
+}
+
+// a [tokens, heads, dim] view: strides of whole 16-byte pieces that keep the rows apart
+bool view_ok(int64_t token, int64_t head, int64_t heads, int64_t dim) {
+  return (heads == 1 || head >= dim) && token >= dim && token <= INT32_MAX && head <= INT32_MAX;
+}
+}  // namespace
+
+fp4_status kv_plan(const int32_t* cached_lens, const int32_t* new_lens, int64_t batch, int page_size,
+                   const int32_t* free_pages, int64_t num_free, int32_t* block_table, int64_t table_stride,
+                   int64_t max_pages, int32_t* total_lens, int32_t* query_start, int64_t* slot_map,
+                   int32_t* positions, int64_t tokens, int32_t* pages_taken, cudaStream_t stream) {
+  if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return FP4_ERR_UNSUPPORTED;
+  if (!cached_lens || !new_lens || !block_table || !total_lens || !query_start || !slot_map || !positions ||
+      !pages_taken || batch < 1 || tokens < 1 || max_pages < 1 || num_free < 0 || (num_free > 0 && !free_pages))
+    return FP4_ERR_INVALID_ARG;
+  if (batch > 16384) return FP4_ERR_UNSUPPORTED;  // both prefix sums stay in shared memory
+  if (tokens > INT32_MAX || num_free > INT32_MAX || max_pages > INT32_MAX / 128 || table_stride < max_pages ||
+      table_stride > INT32_MAX)
+    return FP4_ERR_INVALID_ARG;
+  if (total_lens == cached_lens || total_lens == new_lens) return FP4_ERR_INVALID_ARG;
+  if (!aligned(cached_lens, 4) || !aligned(new_lens, 4) || !aligned(free_pages, 4) || !aligned(block_table, 4) ||
+      !aligned(total_lens, 4) || !aligned(query_start, 4) || !aligned(slot_map, 8) || !aligned(positions, 4) ||
+      !aligned(pages_taken, 4))
+    return FP4_ERR_ALIGNMENT;
+  const DevInfo* d = nullptr;
+  fp4_status st = current(&d);
+  if (st != FP4_OK) return st;
+  return from_cuda(launch_kv_plan(*d, cached_lens, new_lens, batch, page_size, free_pages, num_free, block_table,
+                                  table_stride, max_pages, total_lens, query_start, slot_map, positions, tokens,
+                                  pages_taken, stream));
+}
+
+fp4_status kv_append(const fp4_kv_cache* cache, const fp4_bf16* k, int64_t k_token_stride, int64_t k_head_stride,
+                     const fp4_bf16* v, int64_t v_token_stride, int64_t v_head_stride, const int64_t* slot_map,
+                     int64_t tokens, cudaStream_t stream) {
+  fp4_status st = check_kv_cache(cache);
+  if (st != FP4_OK) return st;
+  if (!k || !v || !slot_map || tokens < 1 || tokens > INT32_MAX) return FP4_ERR_INVALID_ARG;
+  if (!view_ok(k_token_stride, k_head_stride, cache->kv_heads, cache->head_dim) ||
+      !view_ok(v_token_stride, v_head_stride, cache->kv_heads, cache->head_dim))
+    return FP4_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slot_map, 8) || k_token_stride % 8 || k_head_stride % 8 ||
+      v_token_stride % 8 || v_head_stride % 8)
+    return FP4_ERR_ALIGNMENT;
+  const DevInfo* d = nullptr;
+  st = current(&d);
+  if (st != FP4_OK) return st;
+  return from_cuda(launch_kv_append(*d, kv_desc(cache), k, k_token_stride, k_head_stride, v, v_token_stride,
+                                    v_head_stride, slot_map, tokens, stream));
+}
+
+size_t kv_attention_workspace_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                    int64_t max_query_len) {
+  if (batch < 1 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || head_dim < 32 || head_dim > 256 ||
+      max_query_len < 1)
+    return 0;
+  return kv_attention_ws_bytes(batch, q_heads, kv_heads, head_dim, max_query_len);
+}
+
+fp4_status kv_attention(const fp4_kv_cache* cache, const fp4_bf16* q, int64_t q_token_stride, int64_t q_head_stride,
+                        int64_t tokens, int64_t q_heads, const int32_t* query_start, const int32_t* total_lens,
+                        int64_t batch, const int32_t* block_table, int64_t table_stride, int64_t max_pages,
+                        int64_t max_query_len, float softmax_scale, int64_t window, void* ws, size_t ws_bytes,
+                        fp4_bf16* out, float* lse, cudaStream_t stream) {
+  fp4_status st = check_kv_cache(cache);
+  if (st != FP4_OK) return st;
+  if (!q || !query_start || !total_lens || !block_table || !ws || !out) return FP4_ERR_INVALID_ARG;
+  if (tokens < 1 || tokens > INT32_MAX || batch < 1 || batch > INT32_MAX / 2 || q_heads < 1 || q_heads > 65535 ||
+      max_pages < 1 || max_pages > INT32_MAX / 128 || table_stride < max_pages || table_stride > INT32_MAX ||
+      max_query_len < 1 || max_query_len > INT32_MAX || window < 0 || window > INT32_MAX)
+    return FP4_ERR_INVALID_ARG;
+  if (q_heads % cache->kv_heads != 0 || !view_ok(q_token_stride, q_head_stride, q_heads, cache->head_dim))
+    return FP4_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.0f) || softmax_scale > 3.0e38f) return FP4_ERR_INVALID_ARG;
+  if (ws_bytes < kv_attention_workspace_bytes(batch, q_heads, cache->kv_heads, cache->head_dim, max_query_len))
+    return FP4_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(ws, 16) || !aligned(query_start, 4) || !aligned(total_lens, 4) ||
+      !aligned(block_table, 4) || !aligned(lse, 4) || q_token_stride % 8 || q_head_stride % 8)
+    return FP4_ERR_ALIGNMENT;
+  const DevInfo* d = nullptr;
+  st = current(&d);
+  if (st != FP4_OK) return st;
+  KvAttentionArgs a;
+  a.cache = kv_desc(cache);
+  a.q = q;
+  a.q_token = q_token_stride;
+  a.q_head = q_head_stride;
+  a.tokens = tokens;
+  a.q_heads = (int)q_heads;
+  a.batch = (int)batch;
+  a.max_query_len = (int)max_query_len;
+  a.max_pages = (int)max_pages;
+  a.window = (int)window;
+  a.query_start = query_start;
+  a.total_lens = total_lens;
+  a.block_table = block_table;
+  a.table_stride = table_stride;
+  a.scale = softmax_scale;
+  a.out = out;
+  a.lse = lse;
+  a.ws = ws;
+  a.err = d->err;
+  return from_cuda(launch_kv_attention(*d, a, stream));
+}
+
 fp4_status fp4_debug_stream_weights(const uint32_t* w, const uint8_t* scales, int64_t N, int64_t K,
                                     cudaStream_t stream) {
   if (!w || !scales || N <= 0 || K <= 0 || K % 256 != 0 || N > INT32_MAX / 2 || K > (1 << 24))

@@ -113,4 +113,42 @@ cudaError_t launch_qmm(const DevInfo& d, const uint16_t* x, int64_t M, const uin
                        const uint16_t* biases, const float* gs_w, int64_t N, int64_t K, int mode, int group,
                        uint16_t* out, int inject_timeout, cudaStream_t s);
 
+// kv_cache.cu, kv_attention.cu: the paged 4-bit KV cache (fp4_kv_cache of the C ABI) and
+// what works on it
+struct KvCacheDesc {
+  uint32_t* k_codes = nullptr;
+  uint8_t* k_scales = nullptr;
+  uint32_t* v_codes = nullptr;
+  uint8_t* v_scales = nullptr;
+  const float* gs_k = nullptr;
+  const float* gs_v = nullptr;
+  int64_t num_pages = 0;
+  int page_size = 0, kv_heads = 0, head_dim = 0, mode = 0;
+};
+cudaError_t launch_kv_plan(const DevInfo& d, const int32_t* cached, const int32_t* fresh, int64_t B, int page_size,
+                           const int32_t* free_pages, int64_t num_free, int32_t* table, int64_t table_stride,
+                           int64_t max_pages, int32_t* total_lens, int32_t* query_start, int64_t* slot_map,
+                           int32_t* positions, int64_t T, int32_t* pages_taken, cudaStream_t s);
+cudaError_t launch_kv_append(const DevInfo& d, const KvCacheDesc& c, const uint16_t* k, int64_t k_token, int64_t k_head,
+                             const uint16_t* v, int64_t v_token, int64_t v_head, const int64_t* slot_map, int64_t T,
+                             cudaStream_t s);
+struct KvAttentionArgs {
+  KvCacheDesc cache;
+  const uint16_t* q = nullptr;  // [tokens, q_heads, head_dim]; strides in elements
+  int64_t q_token = 0, q_head = 0, tokens = 0;
+  int q_heads = 0, batch = 0, max_query_len = 0, max_pages = 0, window = 0;  // window 0: none
+  const int32_t* query_start = nullptr;
+  const int32_t* total_lens = nullptr;
+  const int32_t* block_table = nullptr;
+  int64_t table_stride = 0;
+  float scale = 0.f;
+  uint16_t* out = nullptr;  // [tokens, q_heads, head_dim]
+  float* lse = nullptr;     // [tokens, q_heads] or nullptr
+  void* ws = nullptr;
+  unsigned* err = nullptr;
+};
+// the attention's dispatch (kv_attention.cu) and its workspace
+size_t kv_attention_ws_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_query_len);
+cudaError_t launch_kv_attention(const DevInfo& d, const KvAttentionArgs& args, cudaStream_t s);
+
 }  // namespace fp4

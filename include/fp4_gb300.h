@@ -361,6 +361,107 @@ fp4_status qmm(const fp4_bf16* x, const uint32_t* w, const void* scales, const f
 fp4_status fp4_amax_global_scale_noalloc(const fp4_bf16* x, int64_t n, float* gs_out, float* amax_out,
                                          cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Serving: a paged KV cache held in 4 bits, the plan that places a step's tokens
+ * in it, the append that fills it and the attention that reads it.
+ *
+ * One layer's cache is four matrices of this header's formats (linear scales,
+ * mode NVFP4 or MXFP4), each with one row of head_dim elements per (page, kv
+ * head, slot):
+ *   k_codes, v_codes    uint32[num_pages, kv_heads, page_size, head_dim/8]
+ *   k_scales, v_scales  uint8[num_pages, kv_heads, page_size, head_dim/group]
+ * so fp4_dequantize reads it as num_pages*kv_heads*page_size rows.  All four are
+ * 16-byte aligned.  global_scale_k / global_scale_v: NVFP4 only, device fp32
+ * multiplier-form global scales of K and V (or NULL: 1); fixed for the cache's
+ * life, since every stored row was quantized with them.
+ * page_size is 16, 32, 64 or 128; head_dim a multiple of 32, at most 256;
+ * num_pages * kv_heads * page_size < 2^31.  Slot s of the cache is slot
+ * s % page_size of page s / page_size. */
+typedef struct fp4_kv_cache {
+  uint32_t* k_codes;
+  uint8_t* k_scales;
+  uint32_t* v_codes;
+  uint8_t* v_scales;
+  const float* global_scale_k;
+  const float* global_scale_v;
+  int64_t num_pages;
+  int32_t page_size;
+  int32_t kv_heads;
+  int32_t head_dim;
+  fp4_mode mode;
+} fp4_kv_cache;
+
+/* kv_plan: block tables, slots and positions of a step, from the requests'
+ * lengths, in one launch (capturable: lengths stay on the device).
+ *   cached_lens  int32[batch] tokens already in the cache;  new_lens int32[batch]
+ *                tokens this step adds (0 allowed in both)
+ *   free_pages   int32[num_free] page ids, taken from the front
+ *   block_table  int32[batch, table_stride], the first max_pages entries of a row used,
+ *                in/out: entries below ceil(cached/page_size) are read; request b's
+ *                further entries up to ceil((cached+new)/page_size) are written with
+ *                free pages, in request order
+ *   total_lens   int32[batch] out: cached + new
+ *   query_start  int32[batch+1] out: first token of each request, then their number
+ *   slot_map     int64[tokens] out: cache slot of each token;  positions int32[tokens]
+ *                out: its position.  Entries past the step's tokens are -1.
+ *   pages_taken  int32 scalar out: free pages used
+ * total_lens must not overlap cached_lens.  Negative lengths count as 0.  If the free list
+ * runs out, a row of the table is full, or the step has more than `tokens`
+ * tokens, the tokens concerned get slot -1 (or no entry), nothing outside the
+ * arrays is touched, and the next fp4_check_device_error returns
+ * FP4_ERR_INVALID_ARG.  batch <= 16384. */
+fp4_status kv_plan(const int32_t* cached_lens, const int32_t* new_lens, int64_t batch, int page_size,
+                   const int32_t* free_pages, int64_t num_free, int32_t* block_table, int64_t table_stride,
+                   int64_t max_pages, int32_t* total_lens, int32_t* query_start, int64_t* slot_map,
+                   int32_t* positions, int64_t tokens, int32_t* pages_taken, cudaStream_t stream);
+
+/* kv_append: the step's new K and V rows, quantized by fp4_quantize's rule (bit
+ * for bit its codes and scales), into their slots of the cache.
+ *   k, v       bf16[tokens, kv_heads, head_dim], 16-byte aligned; strides in elements
+ *              between tokens and between heads, multiples of 8 (views of a fused
+ *              q|k|v row are read in place)
+ *   slot_map   int64[tokens]; a negative slot skips the token, a slot past the cache
+ *              skips it and makes the next fp4_check_device_error return
+ *              FP4_ERR_INVALID_ARG; two tokens of one call must not share a slot. */
+fp4_status kv_append(const fp4_kv_cache* cache, const fp4_bf16* k, int64_t k_token_stride, int64_t k_head_stride,
+                     const fp4_bf16* v, int64_t v_token_stride, int64_t v_head_stride, const int64_t* slot_map,
+                     int64_t tokens, cudaStream_t stream);
+
+/* Workspace bytes kv_attention needs (any argument out of range: 0). */
+size_t kv_attention_workspace_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                    int64_t max_query_len);
+
+/* kv_attention: causal attention of the step's queries over the cache.
+ *   out[t, h] = sum_j p_j V_j / sum_j p_j,  p_j = exp(softmax_scale * q[t, h] . K_j)
+ * for token t of request b (query_start[b] <= t < query_start[b+1]) at position
+ * pos = total_lens[b] - (query_start[b+1] - t), over the keys j with 0 <= j <= pos
+ * and, when window > 0, j > pos - window, of kv head h / (q_heads / kv_heads).
+ * A row that sees no key gives zeros (lse = -inf).
+ *   q            bf16[tokens, q_heads, head_dim], 16-byte aligned; strides in elements,
+ *                multiples of 8;  q_heads a multiple of kv_heads
+ *   query_start  int32[batch+1], total_lens int32[batch] (kv_plan's outputs, after
+ *                kv_append); tokens outside every request's range are not written
+ *   block_table  int32[batch, table_stride], max_pages entries of a row valid; pages that
+ *                no query of the request can see are not read (a sliding window's
+ *                freed pages may be stale)
+ *   max_query_len  the longest request's query count, at least 1: it picks the kernel
+ *   ws           device workspace, 16-byte aligned, ws_bytes >=
+ *                kv_attention_workspace_bytes(batch, q_heads, kv_heads, head_dim,
+ *                max_query_len); zero-filled once when allocated, each call leaves it
+ *                ready for the next.  Calls that overlap on the GPU must not share one.
+ *   out          bf16[tokens, q_heads, head_dim], 16-byte aligned
+ *   lse          fp32[tokens, q_heads] or NULL: log of the sum of exp(score), with which
+ *                results over disjoint keys can be merged
+ * Scores, softmax statistics and sums are fp32.  A page id outside [0, num_pages),
+ * a request with more than max_query_len queries or more tokens than its table
+ * row holds makes the next fp4_check_device_error return FP4_ERR_INVALID_ARG
+ * and leaves that request's rows unspecified; nothing outside the arrays is read. */
+fp4_status kv_attention(const fp4_kv_cache* cache, const fp4_bf16* q, int64_t q_token_stride, int64_t q_head_stride,
+                        int64_t tokens, int64_t q_heads, const int32_t* query_start, const int32_t* total_lens,
+                        int64_t batch, const int32_t* block_table, int64_t table_stride, int64_t max_pages,
+                        int64_t max_query_len, float softmax_scale, int64_t window, void* ws, size_t ws_bytes,
+                        fp4_bf16* out, float* lse, cudaStream_t stream);
+
 /* Test hook, off by default: when `enable` is nonzero the next launches of the
  * tensor-core kernels -- qqmm, qmv's NVFP4/MXFP4 path and gather_qmm -- make
  * their MMA-issuing thread wait on a barrier nothing arrives at, with a 1 ms

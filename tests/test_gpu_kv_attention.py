@@ -1,0 +1,203 @@
+"""kv_attention against a 64-bit implementation over the decoded cache.
+
+Tolerance, element by element, with A = sum_j p_j |v_j| / sum_j p_j:
+    |out - exact| <= 2^-8 |exact| + ((1 + 2^-8) exp(2 ds) - 1) A
+The first term is the bf16 rounding of the result (2^-9) with room for the
+division; a kernel may hold p in as few as 8 significant bits (2^-9 of every
+p, and of their sum), which moves the result by at most 2^-8 A; and scores may be
+off by ds = 2^-16 max|q| max_j |k_j|_1 scale: the tensor-core form writes q as
+terms that leave 2^-17 of the row's largest element, and fp32 sums add less than as
+much again.  A shift of ds moves every p by a factor within exp(+-ds), the
+quotient by at most exp(2 ds)."""
+import numpy as np
+import pytest
+import torch
+
+import kv_reference as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def B():
+    from block_scaled_fp4_fp_gb300 import build, binding
+    build.build()
+    binding.fp4_init(0)
+    return binding
+
+
+def check(B, p, scale=None, lse=True, ws=None, q=None):
+    cache, t = p.cuda(B)
+    if q is not None:
+        t["q"] = q
+    mq = max(1, max(p.new))
+    if ws is None:
+        ws = B.kv_attention_workspace(cache, len(p.new), p.q_heads, mq)
+    out = torch.full((p.q.shape[0], p.q_heads, p.dim), 7.0, dtype=torch.bfloat16, device="cuda")
+    sums = torch.full((p.q.shape[0], p.q_heads), 7.0, device="cuda") if lse else None
+    B.kv_attention(cache, t["q"], t["query_start"], t["total_lens"], t["block_table"], ws, max_query_len=mq,
+                   scale=scale, window=p.window, out=out, lse=sums)
+    assert B.fp4_check_device_error() == B.FP4_OK
+    want, wlse, bound = p.attention(scale)
+    got = out.double().cpu().numpy()
+    assert np.isfinite(got).all()
+    over = np.abs(got - want) - bound
+    assert (over <= 0).all(), f"off by up to {np.abs(got - want).max():.3g}, {float((over > 0).mean()):.3g} over the bound"
+    if lse:
+        g = sums.double().cpu().numpy()
+        empty = np.isneginf(wlse)
+        assert np.isneginf(g[empty]).all()
+        assert (np.abs(g - wlse)[~empty] <= p.lse_bound(scale)[~empty]).all()
+    return out, ws
+
+
+SHAPES = [  # dim, kv heads, group
+    (128, 2, 8), (128, 3, 1), (128, 2, 5), (128, 1, 16), (128, 1, 33), (64, 2, 8), (64, 3, 1), (64, 1, 24),
+    (256, 1, 8), (256, 2, 2), (256, 1, 16), (96, 2, 4), (32, 1, 2),
+]
+
+
+@pytest.mark.parametrize("mode", [2, 1])
+@pytest.mark.parametrize("dim,kv,group", SHAPES)
+def test_decode(B, mode, dim, kv, group):
+    """One token a request: contexts from one token, on both sides of pages, tiles and several tiles."""
+    total = [1, 2, 15, 16, 17, 127, 128, 129, 255, 257, 700, 1300]
+    p = R.Problem(mode, dim, kv, group, 64, [n - 1 for n in total], [1] * len(total), gs=mode == 2, seed=dim + group)
+    check(B, p)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("mode", [2, 1])
+@pytest.mark.parametrize("window", [0, 1, 100, 128, 300])
+def test_decode_pages_and_windows(B, mode, page, window):
+    total = [1, 90, 128, 200, 413, 1025]
+    p = R.Problem(mode, 128, 2, 4, page, [n - 1 for n in total], [1] * len(total), window=window, seed=page + window)
+    check(B, p)
+
+
+@pytest.mark.parametrize("mode", [2, 1])
+@pytest.mark.parametrize("dim,kv,group", [(128, 2, 8), (128, 4, 1), (64, 1, 8), (64, 2, 3), (256, 1, 4), (32, 2, 2)])
+@pytest.mark.parametrize("window", [0, 77])
+def test_a_few_tokens(B, mode, dim, kv, group, window):
+    """Ragged query counts, requests without queries among them, causal inside the step."""
+    p = R.Problem(mode, dim, kv, group, 32, [0, 5, 126, 300, 0, 511, 40], [3, 4, 2, 0, 1, 4, 1], window=window, seed=dim)
+    check(B, p)
+
+
+@pytest.mark.parametrize("mode", [2, 1])
+@pytest.mark.parametrize("dim,kv,group", [(128, 2, 4), (128, 2, 1), (64, 2, 8), (64, 1, 5), (256, 1, 2), (96, 1, 2)])
+@pytest.mark.parametrize("window", [0, 150])
+def test_prompts(B, mode, dim, kv, group, window):
+    """Whole prompts and chunks over what is cached; lengths around the tiles' edges."""
+    p = R.Problem(mode, dim, kv, group, 16, [0, 130, 0, 300, 77, 0], [200, 129, 0, 64, 1, 257], window=window, gs=mode == 2,
+                  seed=dim + window)
+    check(B, p)
+
+
+@pytest.mark.parametrize("mode", [2, 1])
+@pytest.mark.parametrize("group", [1, 8])
+def test_one_long_context(B, mode, group):
+    """The work of one request is split along the context and joined."""
+    p = R.Problem(mode, 128, 2, group, 128, [9000], [1], seed=group)
+    check(B, p)
+
+
+def test_sharp_and_rising_scores(B):
+    """Scores that grow along the context (the running maximum moves in every tile) and that leave one key."""
+    p = R.Problem(2, 128, 1, 8, 64, [1500, 640], [1, 1], seed=3, q_std=12.0)
+    for b in range(2):  # later keys larger: scale bytes grow along the sequence
+        j = np.arange(p.total[b])
+        p.scales["k"][p.table[b, j // 64], 0, j % 64] = (0x20 + (24 * j // p.total[b]))[:, None].astype(np.uint8)
+    check(B, p)
+    check(B, p, scale=3.0)
+
+
+def test_mxfp4_scales_far_apart(B):
+    """V blocks whose scales differ by many powers of two between channels, and between tokens."""
+    p = R.Problem(1, 128, 1, 8, 64, [700], [1], seed=4)
+    p.scales["v"][:, :, :, 0] += 40
+    p.scales["v"][:, :, :, 2] -= 60
+    j = np.arange(701)
+    p.scales["v"][p.table[0, j // 64], 0, j % 64] += (j % 7).astype(np.uint8)[:, None]
+    p.scales["v"][p.unseen()] = 0xFF
+    check(B, p)
+
+
+def test_strided_queries_other_stream_and_reused_workspace(B):
+    p = R.Problem(2, 128, 2, 8, 64, [3000, 10, 700], [1, 1, 1], gs=True, seed=8)
+    wide = torch.zeros((3, p.q_heads + 5, p.dim), dtype=torch.bfloat16, device="cuda")
+    wide[:, 2:2 + p.q_heads] = p.q.cuda()
+    first, ws = check(B, p, q=wide[:, 2:2 + p.q_heads])
+    again, _ = check(B, p, ws=ws)
+    assert torch.equal(first, again)  # the same bits, the workspace left ready
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        third, _ = check(B, p, ws=ws, lse=False)
+    side.synchronize()
+    assert torch.equal(first, third)
+
+
+def test_captured_in_a_graph_with_new_lengths(B):
+    """plan, append and attention captured once, replayed as the requests grow: lengths are read on the device."""
+    batch, kv, heads, dim, page = 3, 2, 16, 128, 32
+    cache = B.kv_cache_empty(40, kv, page, dim, B.MODE_NVFP4)
+    lens = torch.tensor([0, 30, 63], dtype=torch.int32, device="cuda")
+    one = torch.ones(batch, dtype=torch.int32, device="cuda")
+    table = torch.zeros((batch, 8), dtype=torch.int32, device="cuda")
+    table[1, 0], table[2, 0], table[2, 1] = 1, 2, 3
+    free = torch.arange(10, 40, dtype=torch.int32, device="cuda")
+    qkv = torch.zeros((batch, heads + 2 * kv, dim), dtype=torch.bfloat16, device="cuda")
+    ws = B.kv_attention_workspace(cache, batch, heads)
+
+    def step():
+        pl = B.kv_plan(lens, one, free, table, page, batch)
+        B.kv_append(cache, qkv[:, heads:heads + kv], qkv[:, heads + kv:], pl.slot_map)
+        out = B.kv_attention(cache, qkv[:, :heads], pl.query_start, pl.total_lens, table, ws)
+        lens.copy_(pl.total_lens)
+        free.copy_(torch.roll(free, -1))
+        return out
+
+    g = torch.Generator(device="cuda").manual_seed(0)
+    rows = [torch.randn(qkv.shape, generator=g, device="cuda").bfloat16() for _ in range(6)]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    state = [t.clone() for t in (lens, table, free, *cache.tensors[:4])]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for live in (False, True):
+        for t, s in zip((lens, table, free, *cache.tensors[:4]), state):
+            t.copy_(s)
+        got = []
+        for r in rows:
+            qkv.copy_(r)
+            if live:
+                got.append(step().clone())
+            else:
+                graph.replay()
+                got.append(out.clone())
+        torch.cuda.synchronize()
+        if live:
+            assert all(torch.equal(a, b) for a, b in zip(first, got))
+        first = got
+    assert B.fp4_check_device_error() == B.FP4_OK
+
+
+def test_contract_violations_on_the_device_are_reported(B):
+    for what in ("page id", "query length", "table row"):
+        p = R.Problem(2, 128, 1, 8, 64, [200], [2], seed=1)
+        cache, t = p.cuda(B)
+        mq = 2
+        if what == "page id":
+            t["block_table"][0, 1] = p.num_pages
+        elif what == "query length":
+            mq = 1
+        else:
+            t["block_table"] = t["block_table"][:, :2]
+        ws = B.kv_attention_workspace(cache, 1, p.q_heads, 2)
+        B.kv_attention(cache, t["q"], t["query_start"], t["total_lens"], t["block_table"], ws, max_query_len=mq)
+        assert B.fp4_check_device_error() == B.FP4_ERR_INVALID_ARG, what
+        assert B.fp4_check_device_error() == B.FP4_OK
