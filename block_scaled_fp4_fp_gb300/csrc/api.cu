@@ -591,6 +591,7 @@ fp4_status kv_attention(const fp4_kv_cache* cache, const fp4_bf16* q, int64_t q_
     return FP4_ERR_INVALID_ARG;
   if (q_heads % cache->kv_heads != 0 || !view_ok(q_token_stride, q_head_stride, q_heads, cache->head_dim))
     return FP4_ERR_INVALID_ARG;
+  if (max_query_len * (q_heads / cache->kv_heads) > INT32_MAX) return FP4_ERR_INVALID_ARG;
   if (!(softmax_scale > 0.0f) || softmax_scale > 3.0e38f) return FP4_ERR_INVALID_ARG;
   if (ws_bytes < kv_attention_workspace_bytes(batch, q_heads, cache->kv_heads, cache->head_dim, max_query_len))
     return FP4_ERR_INVALID_ARG;
@@ -620,6 +621,7 @@ fp4_status kv_attention(const fp4_kv_cache* cache, const fp4_bf16* q, int64_t q_
   a.lse = lse;
   a.ws = ws;
   a.err = d->err;
+  a.inject_timeout = g_inject_timeout.load();
   return from_cuda(launch_kv_attention(*d, a, stream));
 }
 

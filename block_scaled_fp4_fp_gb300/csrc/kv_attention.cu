@@ -8,6 +8,8 @@
 // (lane e owns head_dim / 32 neighbouring channels), and the block joins the
 // warps' (m, l, o) at the end.  All sums in fp32.  One key costs a warp a
 // five-step shuffle reduction: bound by instruction latency, not by memory.
+#include <cuda.h>
+
 #include "../../include/fp4_gb300.h"
 #include "common.cuh"
 #include "launch.h"
@@ -144,14 +146,31 @@ cudaError_t launch_any(const KvAttentionArgs& args, cudaStream_t s) {
 
 }  // namespace
 
+bool kv_code_maps(const KvCacheDesc& c, CUtensorMap* tmK, CUtensorMap* tmV) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t row = (cuuint64_t)c.head_dim / 2;
+  const cuuint64_t dims[2] = {row, (cuuint64_t)c.num_pages * c.kv_heads * c.page_size};
+  const cuuint64_t strides[1] = {row};
+  const cuuint32_t box[2] = {(cuuint32_t)row, (cuuint32_t)c.page_size}, estr[2] = {1, 1};
+  const CUtensorMapSwizzle swz = row == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+                                 : row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                             : CU_TENSOR_MAP_SWIZZLE_128B;
+  for (int i = 0; i < 2; ++i)
+    if (fn(i ? tmV : tmK, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, i ? c.v_codes : c.k_codes, dims, strides, box, estr,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  return true;
+}
+
 size_t kv_attention_ws_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                              int64_t max_query_len) {
-  (void)batch, (void)q_heads, (void)kv_heads, (void)head_dim, (void)max_query_len;
-  return 16;
+  return kv_decode_supported((int)head_dim) ? kv_decode_ws_bytes(batch, q_heads, kv_heads, head_dim, max_query_len) : 16;
 }
 
 cudaError_t launch_kv_attention(const DevInfo& d, const KvAttentionArgs& args, cudaStream_t s) {
-  (void)d;
+  if (kv_decode_supported(args.cache.head_dim)) return launch_kv_decode(d, args, s);
   return launch_any(args, s);
 }
 

@@ -1,0 +1,1242 @@
+// kv_decode.cu -- attention of a few query rows over the paged 4-bit cache: the
+// serving form for single tokens (and for a handful of tokens a request), where the
+// cache is read once and its bytes are the work.
+//
+//   o_r = sum_j p_rj v_j / sum_j p_rj,   p_rj = 2^(s_rj - m_r),   s_rj = c_r q_r . k_j
+// with c_r = softmax_scale log2(e) gs_k, over the keys j that row r may see.  A row r is
+// one (query token, head of the kv head's group); R = 8 NB rows share a pass over
+// the keys of their kv head.
+//
+// Scores on the 5th-generation tensor cores, K never dequantized: a tile of 128
+// keys is the block-scaled FP4 A operand of tcgen05.mma.kind::mxf4nvf4 (one key per
+// accumulator lane, its E4M3/E8M0 scales applied by the hardware), and the R query
+// rows are the B operand, each written as kTerms = 6 FP4 terms in radix 8,
+//     q = 2^e0 (sum_t d_t 2^(6-3t) + rest),  d_t in {-4..4},  max|q| / 2^e0 in [128, 256),
+// exact but for |rest| <= 2^-10, 2^-17 of the row's largest element.  Term t of row r is
+// column t R + r, so the thread that owns a key sums a row's six columns in
+// registers: no score crosses a lane.  Dequantizing K instead would cost an
+// instruction stream as long as V's, the larger half of what the SM issues.
+//
+// Values in registers: a warp owns 32 keys of the tile (its tensor-memory lane
+// quadrant) from scores to output.  V's codes come from shared memory in the
+// m16n8k16 A-fragment order (channels as rows, keys as columns: neighbouring keys'
+// codes are merged into bytes by one LOP3 and become f16 pairs by the hardware's
+// e2m1x2 converter, times their scales: exact in f16), the probabilities go through
+// 512 bytes of shared memory and ldmatrix.trans, and the mma.sync sums stay in
+// registers.  (tcgen05 would want V as 16-bit shared-memory tiles: 512 bytes of
+// shared memory traffic a key more, which alone is as long as the key's DRAM time.)
+// With more than eight rows, NB warps share a quadrant: each owns eight rows'
+// softmax and 1 / NB of the channels, and reads the others' probabilities.
+// Every quadrant of every group keeps its own running reference m, sum and output:
+// they meet only at the end of a (request, kv head).
+//
+// Range.  p = 2^(s - m) is rounded to f16 (2^-11).  m is set kHead below the largest
+// score and moves only when a score passes it by kMax: p stays between f16's
+// largest value and, for scores within 2^23 of m, its rounding error stays below
+// 2^-9 of p.  A warp whose tile holds a smaller p (not zero: down to 2^-126) multiplies that
+// tile in bf16 instead: codes to bf16 by shifts and masks (twice the instructions
+// of the converter), p with bf16's range.  Sharp score distributions pay this; no
+// probability is lost in either.
+// MXFP4's E8M0 scales have the range of fp32, f16 has not: a thread's V values are
+// held relative to 2^E, E the largest scale exponent so far of the channel group it owns;
+// a tile with scales 2^20 below it takes the bf16 form too.
+//
+// Work split.  The tiles of all (request, kv head, row block) are dealt out evenly
+// to the CTAs (one an SM) as one sequence (the lengths are on the device: every CTA
+// sums them itself).  A piece that does not cover its (request, kv head) leaves
+// (m, l, o) in the workspace; the last CTA to arrive there joins the pieces in
+// order, so the result does not depend on who is last.
+//
+//   consumers   kGroups groups of 4 NB warps; group g takes the CTA's tiles i with i % kGroups == g
+//   then one warp each:
+//   TMA         per tile and page K and V codes (boxes of page_size rows, swizzled by the
+//               row's length) and their scales (bulk copies)
+//   scales      moves a tile's K scales into the 32x16-byte order tcgen05.cp reads
+//   MMA         issues that copy and the MMAs
+//   queries     query rows as FP4 terms, one segment ahead
+//
+// Bound by HBM: 2 D (1/2 + 1/g) bytes a key and kv head.
+#include <algorithm>
+#include <type_traits>
+
+#include "../../include/fp4_gb300.h"
+#include "common.cuh"
+#include "kv_common.cuh"
+#include "launch.h"
+
+namespace fp4 {
+namespace {
+
+constexpr int kTerms = 6;
+constexpr int kTile = 128;  // keys per tile: the MMA's M
+constexpr int kMaxStages = 8;
+constexpr float kLog2e = 1.4426950408889634f;
+// What a (request, kv head, row block) costs a CTA besides its tiles, in tiles: starting on new queries, joining
+// the sets and writing the rows take about 1.5 us, a tile 0.45 us (measured, D = 128).  Counted when the
+// work is dealt out, so that a CTA with many short requests does not finish last.
+constexpr int kItemCost = 3;
+constexpr float kHead = 7.0f;   // a new reference m is the largest score less this (log2)
+constexpr float kMax = 15.0f;   // and moves when a score passes it by this: p <= 2^15
+constexpr float kTiny = 23.0f;  // scores further below m than this need bf16's range
+constexpr float kNone = -1e30f; // m before any score: exp2 of a hidden key's -inf less this is 0, of this less a score too
+
+template <int MODE, int D, int NB>
+struct Dec {
+  static constexpr int kR = 8 * NB;                          // query rows
+  static constexpr int kN = kTerms * kR;                     // MMA N
+  static constexpr int kGroup = MODE == 2 ? 16 : 32;
+  static constexpr int kSB = D / kGroup;                     // scale bytes of a row
+  static constexpr int kWords = kSB < 4 ? 1 : kSB / 4;       // and its 32-bit words
+  static constexpr int kRowB = D / 2;                        // code bytes of a row
+  static constexpr uint32_t kSwz = D == 64 ? 0x10 : D == 128 ? 0x30 : 0x70;
+  static constexpr uint32_t kCodes = kTile * kRowB;
+  static constexpr uint32_t kScales = kTile * kSB;
+  // consumer warps: as many as their output fragments (D / 4 registers a thread) leave registers for
+  static constexpr int kWarps = D <= 128 ? 16 : NB == 1 ? 12 : 8;
+  static constexpr int kGroups = kWarps / (4 * NB);
+  static constexpr int kBufs = kGroups < 2 ? 2 : kGroups;    // score buffers
+  static constexpr int kConsumers = kWarps * 32;
+  static constexpr int kThreads = kConsumers + 128;
+  static constexpr int kCh = D / NB / 8;                     // channels of a consumer thread
+  static constexpr int kPieces = D / 8;                      // float2 of its output
+  static constexpr int kPBufs = NB == 1 ? 1 : 2;             // probability buffers of a quadrant
+  static constexpr uint32_t kQBytes = (kN * kRowB + 1023) / 1024 * 1024;
+  static constexpr int kSStride = NB == 1 ? 64 : kN;         // tensor-memory columns between score buffers
+  static constexpr uint32_t kSfa = kBufs * kSStride;         // K scales, kBufs buffers of 16 columns
+  static constexpr uint32_t kSfb = kSfa + 16 * kBufs;        // term scales, 8 columns
+  static constexpr uint32_t kTmemCols = 512;
+  static_assert(kSfb + 8 <= kTmemCols, "tensor memory");
+  // shared memory: [stages: K codes, V codes][queries x 2][K scales as tcgen05.cp reads them][outputs]
+  // [probabilities][stages: K scales, V scales][row data][barriers]
+  static constexpr int kSets = kGroups * 4;                  // quadrants with their own m, l, output
+  static constexpr uint32_t kSfaBytes = kWords * 512;
+  static constexpr uint32_t kOutBytes = kWarps * kPieces * 32 * 8;
+  static constexpr uint32_t kPBytes = kSets * kPBufs * NB * 512;
+  // score factors, key ranges and output rows x 2, m and l of the sets, joined m and l, flags and factors of the
+  // probability buffers, segments x 2
+  static constexpr uint32_t kRowBytes =
+      2 * 3 * kR * 4 + 2 * kR * 8 + kSets * kR * 8 + 2 * kR * 4 + kSets * kPBufs * NB * (32 + 8) + 128;
+  static constexpr uint32_t kFixed =
+      2 * kQBytes + kBufs * kSfaBytes + kOutBytes + kPBytes + kRowBytes + 512 + 1024;
+  static constexpr uint32_t kBudget = 226u * 1024u;
+  static constexpr int kStages0 = (int)((kBudget - kFixed) / (2 * kCodes + 2 * kScales));
+  static constexpr int kStages = kStages0 > kMaxStages ? kMaxStages : kStages0;
+  static constexpr uint32_t kSmem = kFixed + kStages * (2 * kCodes + 2 * kScales);
+  static_assert(kStages >= 2 && kSmem <= kBudget, "shared memory");
+  static constexpr int kSlot = kR * D + 2 * kR;              // floats of a workspace piece (output, m, l)
+};
+
+// byte of the term scale 2^(7-3t) (see the FP4 GEMV's terms: exact in both formats)
+template <int MODE>
+__device__ __forceinline__ uint32_t term_scale(int t) {
+  const int e = 7 - 3 * t;
+  if (MODE == 1) return (uint32_t)(127 + e);
+  return e >= -6 ? (uint32_t)((e + 7) << 3) : (1u << (e + 9));
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t a, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(a));
+}
+
+// four bytes of two e2m1 codes -> four f16 pairs
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&o)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]) : "r"(w));
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+               "{%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// e2m1 code I (0..3) of each 16-bit half -> bf16 pair of the code's value times 2^-126: sign to bit 15, the
+// exponent and mantissa bits to the lowest exponent bits and the highest mantissa bit (code 1 is subnormal there too)
+template <int I>
+__device__ __forceinline__ uint32_t e2m1_to_bf16(uint32_t n) {
+  const uint32_t sign = I == 3 ? n : n << (12 - 4 * I);
+  const uint32_t mag = I <= 1 ? n << (6 - 4 * I) : n >> (4 * I - 6);
+  return (sign & 0x80008000u) | (mag & 0x01C001C0u);
+}
+// two f16 -> two bf16, times 2^8
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2_256(uint32_t h) {
+  return pack_bf16x2_rn(f16_lo_to_f32(h) * 256.0f, f16_hi_to_f32(h) * 256.0f);
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+               "{%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
+// shared-memory reads by 32-bit address
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .b16 h;\n\tld.shared.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+template <int N>
+__device__ __forceinline__ void named_sync(int id) { asm volatile("bar.sync %0, %1;" :: "r"(id), "n"(N) : "memory"); }
+
+// Where CTA k of n starts in a sequence of `all`.
+__device__ __forceinline__ int64_t share(int64_t all, int k, int n) {
+  return all <= INT32_MAX / 160 ? (int64_t)((unsigned)all * (unsigned)k / (unsigned)n) : all * k / n;
+}
+// The CTA whose share holds position `at`.
+__device__ __forceinline__ int owner(int64_t all, int64_t at, int n) {
+  return all <= INT32_MAX / 160 ? (int)(((unsigned)(at + 1) * (unsigned)n - 1) / (unsigned)all)
+                                : (int)(((at + 1) * n - 1) / all);
+}
+
+// The keys of a thread's fragment column pair c, of the slab's 16: base(c) + offset(i), i = 0..3
+// (columns 2c, 2c + 1, 2c + 8, 2c + 9).  Any order serves as long as the probabilities
+// follow it; these make a warp's V loads touch every bank once per phase under the
+// row's swizzle.
+template <int D>
+__device__ __forceinline__ int key_of(int c, int i) {
+  if (D == 64) return c + 4 * i;
+  if (D == 128) return (c & 1) + 4 * (c >> 1) + ((i & 1) << 1) + ((i >> 1) << 3);
+  return 2 * c + (i & 1) + ((i >> 1) << 3);
+}
+
+// One request as this kernel deals it out.
+struct Req {
+  int q0, qlen, total, first;  // first token row, query count, keys, first visible key
+  int tiles, lo_tile, blocks;  // tiles per pass, first tile, row blocks
+  __device__ __forceinline__ int cost() const { return tiles + kItemCost; }  // of an item (if it has tiles at all)
+  __device__ __forceinline__ int64_t units(int kv_heads) const {
+    return tiles > 0 ? (int64_t)cost() * blocks * kv_heads : 0;
+  }
+};
+
+__device__ __forceinline__ Req load_req(const KvAttentionArgs& a, int b, int group, int R) {
+  Req r;
+  r.q0 = __ldg(a.query_start + b);
+  r.qlen = __ldg(a.query_start + b + 1) - r.q0;
+  r.total = __ldg(a.total_lens + b);
+  r.total = min(r.total, a.max_pages * a.cache.page_size);
+  if (r.qlen > a.max_query_len || r.q0 < 0 || (int64_t)r.q0 + r.qlen > a.tokens) r.qlen = 0;
+  r.first = a.window > 0 ? max(0, r.total - r.qlen + 1 - a.window) : 0;
+  r.lo_tile = r.first / kTile;
+  r.blocks = r.qlen > 0 ? (int)((unsigned)(r.qlen * group + R - 1) / (unsigned)R) : 0;
+  r.tiles = (r.total > 0 && r.qlen > 0) ? (r.total + kTile - 1) / kTile - r.lo_tile : 0;
+  return r;
+}
+
+// A CTA's walk over its share of the sequence: request by request, in it kv head by kv head, in it row block
+// by row block; each of these items is its tiles and then kItemCost units that hold no work.
+struct Walk {
+  const KvAttentionArgs* a;
+  int group, R, b, item, off;
+  int64_t at, end;  // position in the sequence
+  Req r;
+  // the current segment
+  int h, rb, ta, tb;
+  int64_t start;  // where the item's tile 0 sits in the sequence
+  __device__ __forceinline__ void begin(const KvAttentionArgs& args, int g, int rows, int b0, int item0, int off0,
+                                        int64_t f0, int64_t f1) {
+    a = &args;
+    group = g;
+    R = rows;
+    b = b0;
+    at = f0;
+    end = f1;
+    item = item0;
+    off = off0;
+    r = load_req(args, b, group, R);
+  }
+  __device__ __forceinline__ bool next() {
+    for (;;) {
+      if (at >= end) return false;
+      while (r.tiles == 0 || item == a->cache.kv_heads * r.blocks) {
+        if (++b >= a->batch) return false;
+        r = load_req(*a, b, group, R);
+        item = 0;
+      }
+      h = item / r.blocks;
+      rb = item - h * r.blocks;
+      start = at - off;
+      const int to = (int)min((int64_t)r.cost(), off + (end - at));
+      ta = min(off, r.tiles);
+      tb = min(to, r.tiles);
+      at += to - off;
+      off = 0;
+      ++item;
+      if (ta < tb) return true;
+    }
+  }
+};
+
+// A segment as the query warp hands it to the MMA warp and the consumers (in shared memory).
+struct Seg {
+  int b, h, rb, ta, tb;        // ta = tb: the CTA's share is done
+  int q0, qlen, total, first;  // the request's
+  int lo_tile, tiles, lo_max, hi_min;
+  int pad;
+  int64_t start;  // where the item's tile 0 sits in the sequence
+};
+
+// Query rows r0 .. r0 + N - 1 of a segment as FP4 terms in the B operand's order (a warp): term t of row r is
+// operand row t R + r.  Writes each row's score factor.
+template <int MODE, int D, int NB, int N>
+__device__ __forceinline__ void query_rows(const KvAttentionArgs& a, uint8_t* dst, const int64_t* row_out, float* row_c,
+                                           int r0, int group, int lane) {
+  using C = Dec<MODE, D, NB>;
+  constexpr int EL = D / 32;  // elements of a lane
+  uint32_t x[N][EL / 2];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int64_t at = row_out[r0 + k];  // token * q_heads + head
+    const int64_t tok = at / a.q_heads;
+    const uint16_t* src = a.q + tok * a.q_token + (at - tok * a.q_heads) * a.q_head + lane * EL;
+#pragma unroll
+    for (int e = 0; e < EL / 2; ++e) x[k][e] = at >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(src) + e) : 0u;
+  }
+  const float mult = a.scale * kLog2e * ((MODE == 2 && a.cache.gs_k) ? __ldg(a.cache.gs_k) : 1.0f);
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    uint32_t mb = 0;
+#pragma unroll
+    for (int e = 0; e < EL / 2; ++e) mb = __vmaxu2(mb, x[k][e] & 0x7FFF7FFFu);
+    mb = __reduce_max_sync(0xffffffffu, max(mb & 0xFFFFu, mb >> 16));
+    // 2^e0 = the largest element's power of two / 128 (2^-127 at least); a NaN or infinity makes every score NaN
+    const uint32_t E = max(mb >> 7, 7u);
+    const float pre = __uint_as_float((261u - min(E, 254u)) << 23);  // 2^-e0, e0 = E - 134
+    if (lane == 0)
+      row_c[r0 + k] = mb < 0x7F80u ? mult * (E >= 8u ? __uint_as_float((E - 7u) << 23) : 0x1p-127f) : __int_as_float(0x7FC00000);
+    float v[EL];
+#pragma unroll
+    for (int e = 0; e < EL / 2; ++e) {
+      v[2 * e] = bf16_lo(x[k][e]) * pre;
+      v[2 * e + 1] = bf16_hi(x[k][e]) * pre;
+    }
+#pragma unroll
+    for (int t = 0; t < kTerms; ++t) {
+      // d / 2 = rint(v 2^(3t-6)) / 2 by adding and subtracting 1.5 * 2^22; v keeps the rest
+      const float inv = __int_as_float((127 + 3 * t - 7) << 23), sc = __int_as_float((127 + 7 - 3 * t) << 23);
+      uint32_t codes = 0;
+#pragma unroll
+      for (int e = 0; e < EL / 2; ++e) {
+        const float d0 = __fsub_rn(__fmaf_rn(v[2 * e], inv, 6291456.0f), 6291456.0f);
+        const float d1 = __fsub_rn(__fmaf_rn(v[2 * e + 1], inv, 6291456.0f), 6291456.0f);
+        v[2 * e] = __fmaf_rn(-sc, d0, v[2 * e]);
+        v[2 * e + 1] = __fmaf_rn(-sc, d1, v[2 * e + 1]);
+        codes |= e2m1x2_rn(d0, d1) << (8 * e);
+      }
+      uint32_t off = (uint32_t)((t * C::kR + r0 + k) * C::kRowB + lane * (EL / 2));
+      off ^= (off >> 3) & C::kSwz;
+      if (EL == 2) dst[off] = (uint8_t)codes;
+      else if (EL == 4) *reinterpret_cast<uint16_t*>(dst + off) = (uint16_t)codes;
+      else *reinterpret_cast<uint32_t*>(dst + off) = codes;
+    }
+  }
+}
+
+template <int MODE, int D, int NB>
+__global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_kernel(
+    const KvAttentionArgs a, int group, int max_blocks, int* __restrict__ counters, float* __restrict__ pieces, int inject_timeout) {
+  using C = Dec<MODE, D, NB>;
+  constexpr int R = C::kR, ST = C::kStages, BUFS = C::kBufs, SETS = C::kSets;
+  constexpr int kThreads = C::kThreads, kConsumers = C::kConsumers;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw);
+  constexpr uint32_t offQ = ST * 2 * C::kCodes, offSfa = offQ + 2 * C::kQBytes, offOut = offSfa + BUFS * C::kSfaBytes,
+                     offP = offOut + C::kOutBytes, offS = offP + C::kPBytes, offRow = offS + ST * 2 * C::kScales,
+                     offBar = (offRow + C::kRowBytes + 7) / 8 * 8;
+  float* row_c = reinterpret_cast<float*>(smem + offRow);         // [2][R] score factor of a row
+  int* row_lo = reinterpret_cast<int*>(row_c + 2 * R);            // [2][R] first key it sees
+  int* row_hi = row_lo + 2 * R;                                   // [2][R] first key past those it sees
+  int64_t* row_out = reinterpret_cast<int64_t*>(row_hi + 2 * R);  // [2][R] its place in out and lse, or -1
+  float* set_m = reinterpret_cast<float*>(row_out + 2 * R);       // [SETS][R] running references
+  float* set_l = set_m + SETS * R;                                // [SETS][R] sums
+  float* join_m = set_l + SETS * R;                               // [R]
+  float* join_l = join_m + R;                                     // [R]
+  float* p_alpha = join_l + R;                                    // [SETS][kPBufs][NB][8] a moved reference's factors
+  int* p_flags = reinterpret_cast<int*>(p_alpha + SETS * C::kPBufs * NB * 8);  // [SETS][kPBufs][NB][2]
+  Seg* segs = reinterpret_cast<Seg*>(p_flags + SETS * C::kPBufs * NB * 2);     // [2]
+  static_assert(sizeof(Seg) == 64 && (C::kRowBytes - 128) % 8 == 0 && offRow % 16 == 0, "segment records");
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + offBar);    // a tile has landed
+  uint64_t* empty = full + ST;                                    // and is done with
+  uint64_t* sfull = empty + ST;                                   // scores computed
+  uint64_t* sempty = sfull + BUFS;                                // and read
+  uint64_t* qfull = sempty + BUFS;                                   // query terms written
+  uint64_t* qempty = qfull + 2;                                   // and done with
+  uint64_t* sfirst = qempty + 2;                                  // the first segment is known
+  uint64_t* tbar = sfirst + 1;                                    // tensor memory allocated, term scales stored
+  uint64_t* never = tbar + 1;                                     // fault injection: nothing arrives here
+  int64_t* plan = reinterpret_cast<int64_t*>(never + 1);          // this CTA's share [f0, f1); all units; CTAs
+  int* plan_at = reinterpret_cast<int*>(plan + 5);                // its first item: request, item, tile
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(plan_at + 3);
+  int* last_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  static_assert((2 * ST + 2 * BUFS + 4 + 3) * 8 + 5 * 8 + 12 + 8 <= 512, "barrier area");
+  __shared__ int64_t scan[kThreads / 32 + 1];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&full[s], 64);  // every lane of the two loading warps
+      mbar_init(&empty[s], 4 * NB);
+    }
+    for (int s = 0; s < BUFS; ++s) {
+      mbar_init(&sfull[s], 1);
+      mbar_init(&sempty[s], 4 * NB);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&qfull[s], 32 + C::kWarps);
+      mbar_init(&qempty[s], 1 + C::kWarps);
+    }
+    mbar_init(tbar, 1);
+    mbar_init(sfirst, 32);
+    mbar_init(never, 1);
+    fence_barrier_init();
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // ---- this CTA's share of the tiles of all requests (a block scan over the lengths)
+  {
+    const int per = (a.batch + kThreads - 1) / kThreads;
+    const int b0 = min(a.batch, (int)threadIdx.x * per), b1 = min(a.batch, b0 + per);
+    int64_t sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      const Req r = load_req(a, b, group, R);
+      sum += r.units(a.cache.kv_heads);
+    }
+    int64_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += scan[w];
+      all += scan[w];
+    }
+    before += incl - sum;
+    // a CTA takes two tiles (of an item of its own) at least: its groups work side by side
+    const int64_t ctas = min((int64_t)gridDim.x, (all + kItemCost + 1) / (kItemCost + 2));
+    int64_t f0 = 0, f1 = 0;
+    if ((int64_t)blockIdx.x < ctas) {
+      f0 = share(all, blockIdx.x, (int)ctas);
+      f1 = share(all, blockIdx.x + 1, (int)ctas);
+    }
+    if (threadIdx.x == 0) {
+      plan[0] = f0;
+      plan[1] = f1;
+      plan[3] = all;
+      plan[4] = ctas;
+    }
+    if (f0 < f1 && f0 >= before && f0 < before + sum) {  // the thread whose requests hold the first unit
+      int64_t off = f0 - before;
+      int b = b0;
+      for (;; ++b) {
+        const Req r = load_req(a, b, group, R);
+        const int64_t n = r.units(a.cache.kv_heads);
+        if (off < n) {
+          const int item = (int)(off / r.cost());
+          plan_at[0] = b;
+          plan_at[1] = item;
+          plan_at[2] = (int)(off - (int64_t)item * r.cost());
+          break;
+        }
+        off -= n;
+      }
+    }
+  }
+  __syncthreads();
+  const int64_t f0 = plan[0], f1 = plan[1], all_units = plan[3];
+  const int ctas = (int)plan[4];
+  bool failed = false;
+
+  // requests that see no key give zeros; requests outside the contract are reported
+  for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+    const int q0 = __ldg(a.query_start + b), ql = __ldg(a.query_start + b + 1) - q0, n = __ldg(a.total_lens + b);
+    const Req r = load_req(a, b, group, R);
+    if (threadIdx.x == 0 && (ql < 0 || (ql > 0 && r.qlen == 0) || n > r.total)) record_error(a.err, kErrIndex);
+    if (r.qlen > 0 && r.tiles == 0) {
+      for (int64_t i = threadIdx.x; i < (int64_t)r.qlen * a.q_heads * (D / 8); i += kThreads)
+        reinterpret_cast<uint4*>(a.out + (int64_t)r.q0 * a.q_heads * D)[i] = make_uint4(0, 0, 0, 0);
+      if (a.lse)
+        for (int64_t i = threadIdx.x; i < (int64_t)r.qlen * a.q_heads; i += kThreads)
+          a.lse[(int64_t)r.q0 * a.q_heads + i] = -INFINITY;
+    }
+  }
+  if (f0 >= f1) return;  // (uniform) no tile for this CTA
+
+  const int page_size = a.cache.page_size, page_shift = 31 - __clz(page_size);
+
+  if (warp < C::kWarps + 2 && warp >= C::kWarps) {
+    // -------------------------------------------------- loads: K, and V
+    // Sixteen-byte asynchronous copies: a copy's row, chunk and page are the lane's own arithmetic, so a tile
+    // costs the same few dozen instructions whatever the page size.  (Bulk and tensor copies, whose
+    // operands are uniform registers, took ~140 cycles each to issue, and a tile of 16-row pages is 32 of them.)
+    const bool is_v = warp == C::kWarps + 1;
+    const uint8_t* codes = reinterpret_cast<const uint8_t*>(is_v ? a.cache.v_codes : a.cache.k_codes);
+    const uint8_t* scales = is_v ? a.cache.v_scales : a.cache.k_scales;
+    constexpr int CPR = C::kRowB / 16, RPI = 32 / CPR;  // chunks of a row, rows (512 bytes) of an instruction
+    constexpr int SPI = 512 / C::kSB;                   // keys whose scales an instruction moves
+    const int tile_shift = 7 - page_shift;              // log2 of a tile's pages
+    const int srow = lane * 16 / C::kSB;
+    // a lane's place in 512 bytes of codes, under the row swizzle; where its period is 1024 bytes (D = 256) the
+    // second 512 have their own
+    const uint32_t at = lane * 16, at0 = at ^ ((at >> 3) & C::kSwz), at1 = (at + 512) ^ (((at + 512) >> 3) & C::kSwz);
+    codes += lane * 16;
+    int s = 0, round = 0;
+    Walk w;
+    w.begin(a, group, R, plan_at[0], plan_at[1], plan_at[2], f0, f1);
+    while (w.next()) {
+      // Cache rows of the table's next 32 pages, a page a lane, and the 32 after them on their way: one
+      // table load's latency a tile would bound the ring.
+      const int32_t* table = a.block_table + (int64_t)w.b * a.table_stride;
+      const int last = (w.r.total - 1) >> page_shift;
+      int batch = (w.r.lo_tile + w.ta) << tile_shift;
+      int nxt = __ldg(table + min(batch + lane, last));
+      int cur = 0, left = 0;
+      for (int t = w.ta; t < w.tb; ++t) {
+        const int j0 = (w.r.lo_tile + t) * kTile;
+        // pages of the tile that hold visible keys (a window's first page, the request's last)
+        const int pa = max(w.r.first - j0, 0) >> page_shift;
+        const int pb = (min(w.r.total - j0, kTile) + page_size - 1) >> page_shift;
+        const int first_pg = (w.r.lo_tile + t) << tile_shift;
+        if (left == 0) {  // (a tile's pages never straddle two batches: both are powers of two)
+          if (first_pg != (w.r.lo_tile + w.ta) << tile_shift) batch += 32;
+          const int pg = batch + lane;
+          if ((nxt < 0 || nxt >= a.cache.num_pages) && pg <= last && pg >= w.r.first >> page_shift) {
+            record_error(a.err, kErrIndex);
+            nxt = 0;
+          }
+          cur = (max(nxt, 0) * a.cache.kv_heads + w.h) << page_shift;
+          nxt = __ldg(table + min(batch + 32 + lane, last));
+          left = 32 >> tile_shift;
+        }
+        --left;
+        if (round > 0) mbar_wait(&empty[s], (round - 1) & 1, a.err, failed);
+        const uint32_t dc = base + (2 * s + is_v) * C::kCodes, ds = base + offS + (2 * s + is_v) * C::kScales;
+        const int idx = first_pg - batch;  // the tile's first page in the batch
+        auto pages = [&](auto ipp) {       // instructions of a page
+          constexpr int IPP = decltype(ipp)::value, NP = kTile / RPI / IPP;
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            const int row = __shfl_sync(0xffffffffu, cur, idx + p);
+            if (p >= pa && p < pb) {
+              const uint8_t* src = codes + (int64_t)row * C::kRowB;
+              const uint32_t dst = dc + p * (IPP * 512);
+#pragma unroll
+              for (int i = 0; i < IPP; ++i) cp_async16(dst + i * 512 + (i & 1 ? at1 - 512 : at0), src + i * 512);
+            }
+          }
+        };
+        switch (page_shift) {
+          case 4: pages(std::integral_constant<int, 16 / RPI>()); break;
+          case 5: pages(std::integral_constant<int, 32 / RPI>()); break;
+          case 6: pages(std::integral_constant<int, 64 / RPI>()); break;
+          default: pages(std::integral_constant<int, 128 / RPI>()); break;
+        }
+#pragma unroll
+        for (int i = 0; i < (kTile + SPI - 1) / SPI; ++i) {
+          const int r = i * SPI + srow, p = min(r, kTile - 1) >> page_shift;
+          const int row = __shfl_sync(0xffffffffu, cur, idx + p) + (r & (page_size - 1));
+          if (r < kTile && p >= pa && p < pb) cp_async16(ds + r * C::kSB, scales + (int64_t)row * C::kSB);
+        }
+        // arrives when this lane's copies have landed
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(&full[s])) : "memory");
+        if (++s == ST) { s = 0; ++round; }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // no copy may still be writing shared memory when the CTA exits
+  } else if (warp == C::kWarps + 2) {
+    // ------------------------------------------------- K scales, MMA issue
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 :: "r"(smem_u32(tmem_slot)), "n"(C::kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    // the query terms' scales, column n / 32 (four further from row 128 on) of lane n % 32, copied to every
+    // lane quadrant from the first kilobyte of the output area, idle until the first segment ends
+    {
+      uint32_t v[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int n = 32 * c + lane;
+        v[c] = n < C::kN ? term_scale<MODE>(n / R) * 0x01010101u : 0u;
+      }
+      uint4* st = reinterpret_cast<uint4*>(smem + offOut);
+      st[lane] = make_uint4(v[0], v[1], v[2], v[3]);
+      st[32 + lane] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    tc_fence_before();
+    __syncwarp();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t leader = elect_one_sync();
+    if (leader) {
+      if (inject_timeout) {
+        bool injected = false;  // separate flag: the injected expiry must not stop later waits
+        mbar_wait(never, 0, a.err, injected, 2000000LL);
+      }
+      tc_cp_sf(tmem + C::kSfb, desc_sf(base + offOut));
+      if (C::kN > 128) tc_cp_sf(tmem + C::kSfb + 4, desc_sf(base + offOut + 512));
+      mbar_arrive(tbar);  // publishes tmem_slot to the consumers
+    }
+    constexpr uint32_t idesc0 = (1u << 7) | (1u << 10) | ((uint32_t)(C::kN >> 3) << 17) | (MODE == 1 ? 1u << 23 : 0u) |
+                                ((128u >> 4) << 24);
+    constexpr uint32_t layout = D == 64 ? 6u : D == 128 ? 4u : 2u;  // 32-, 64-, 128-byte swizzle
+    int s = 0, round = 0, it = 0;
+    for (int seg = 0;; ++seg) {
+      const int qb = seg & 1;
+      mbar_wait(&qfull[qb], (seg >> 1) & 1, a.err, failed);
+      const int n = failed ? 0 : segs[qb].tb - segs[qb].ta;
+      if (n <= 0) break;
+      for (int i = 0; i < n; ++i, ++it) {
+        const int buf = it % BUFS;
+        // the scores of tile it - BUFS have been read, so its MMAs and scale copy are done
+        if (it >= BUFS) mbar_wait(&sempty[buf], (it / BUFS - 1) & 1, a.err, failed);
+        mbar_wait(&full[s], round & 1, a.err, failed);
+        // lane n % 32, word n / 32: key n's scale word j, for every k-step group j
+        const uint8_t* lin = smem + offS + 2 * s * C::kScales;
+        uint32_t v[4][C::kWords];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint8_t* src = lin + (32 * c + lane) * C::kSB;
+          if (C::kSB == 2) v[c][0] = *reinterpret_cast<const uint16_t*>(src);
+          else if (C::kSB == 4) v[c][0] = *reinterpret_cast<const uint32_t*>(src);
+          else
+#pragma unroll
+            for (int j = 0; j < C::kWords; j += 2) {
+              const uint2 x = *reinterpret_cast<const uint2*>(src + 4 * j);
+              v[c][j] = x.x;
+              v[c][(j + 1) % C::kWords] = x.y;
+            }
+        }
+        uint4* dst = reinterpret_cast<uint4*>(smem + offSfa + buf * C::kSfaBytes) + lane;
+#pragma unroll
+        for (int j = 0; j < C::kWords; ++j) dst[32 * j] = make_uint4(v[0][j], v[1][j], v[2][j], v[3][j]);
+        // both these and the copied codes, seen through the barrier, become visible to the tensor core
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (leader) {
+          tc_fence_after();
+#pragma unroll
+          for (int j = 0; j < C::kWords; ++j)
+            tc_cp_sf(tmem + C::kSfa + 16 * buf + 4 * j, desc_sf(base + offSfa + buf * C::kSfaBytes + 512 * j));
+          const uint64_t ad = desc_k(base + 2 * s * C::kCodes, 8 * C::kRowB, layout);
+          const uint64_t bd = desc_k(base + offQ + qb * C::kQBytes, 8 * C::kRowB, layout);
+#pragma unroll
+          for (int ks = 0; ks < D / 64; ++ks) {
+            const int word = MODE == 2 ? ks : ks / 2;
+            const uint32_t id = MODE == 2 ? 0u : 2u * (ks & 1);
+            mma_fp4<MODE>(tmem + C::kSStride * buf, ad + 2 * ks, bd + 2 * ks, idesc0 | (id << 29) | (id << 4),
+                          tmem + C::kSfa + 16 * buf + 4 * word, tmem + C::kSfb, ks > 0);
+          }
+          tc_commit(&sfull[buf]);
+          if (i + 1 == n) tc_commit(&qempty[qb]);
+        }
+        __syncwarp();
+        if (++s == ST) { s = 0; ++round; }
+      }
+    }
+  } else if (warp == C::kWarps + 3) {
+
+    // ------------------------------------------------------------ queries
+    Walk w;
+    w.begin(a, group, R, plan_at[0], plan_at[1], plan_at[2], f0, f1);
+    for (int seg = 0;; ++seg) {
+      const int qb = seg & 1;
+      if (seg >= 2) mbar_wait(&qempty[qb], ((seg >> 1) - 1) & 1, a.err, failed);
+      if (!w.next()) {
+        if (lane == 0) segs[qb].ta = segs[qb].tb = 0;
+        if (lane < C::kWarps) mbar_arrive(&qfull[qb]);
+        mbar_arrive(&qfull[qb]);
+        break;
+      }
+      {  // lane r: the keys row r sees and where it goes (R <= 32); rows past the block are not used
+        const int rr = w.rb * R + lane, i = rr / group;
+        const bool real = lane < R && rr < w.r.qlen * group;
+        const int pos = w.r.total - w.r.qlen + i;
+        const int hi = real ? max(pos + 1, 0) : INT32_MAX;
+        const int lo = real && a.window > 0 ? max(pos + 1 - a.window, 0) : 0;
+        if (lane < R) {
+          row_hi[qb * R + lane] = hi;
+          row_lo[qb * R + lane] = lo;
+          row_out[qb * R + lane] = real ? (int64_t)(w.r.q0 + i) * a.q_heads + w.h * group + (rr - i * group) : -1;
+        }
+        const int hi_min = __reduce_min_sync(0xffffffffu, hi), lo_max = __reduce_max_sync(0xffffffffu, lo);
+        if (lane == 0) segs[qb] = Seg{w.b, w.h, w.rb, w.ta, w.tb, w.r.q0, w.r.qlen, w.r.total, w.r.first, w.r.lo_tile,
+                                      w.r.tiles, lo_max, hi_min, 0, w.start};
+      }
+      __syncwarp();
+      if (seg == 0) {
+        mbar_arrive(sfirst);  // the consumers write the first segment's terms: it takes this warp several times as long
+      } else {
+#pragma unroll 1
+        for (int r0 = 0; r0 < R; r0 += 4) query_rows<MODE, D, NB, 4>(a, smem + offQ + qb * C::kQBytes, row_out + qb * R, row_c + qb * R, r0, group, lane);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      if (seg > 0 && lane < C::kWarps) mbar_arrive(&qfull[qb]);  // in the consumers' place
+      mbar_arrive(&qfull[qb]);
+    }
+  } else {
+    // ----------------------------------------------------------- consumers
+    const int grp = warp / (4 * NB), sub = (warp >> 2) % NB, quad = warp & 3, set = grp * 4 + quad;
+    const int g = lane >> 2, c = lane & 3;
+    mbar_wait(tbar, 0, a.err, failed);
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot + ((uint32_t)(32 * quad) << 16) + 8 * sub;
+    const uint32_t pbuf = base + offP + set * (C::kPBufs * NB * 512);
+    const uint32_t pread =
+        pbuf + (uint32_t)(((lane >> 4) * 16 + key_of<D>((lane & 7) >> 1, (lane & 1) + ((lane >> 3) & 1) * 2)) * 16);
+    float* mm = set_m + set * R + 8 * sub;
+    float* alphas = p_alpha + set * (C::kPBufs * NB * 8);
+    int* flags = p_flags + set * (C::kPBufs * NB * 2);
+    const float gsv = (MODE == 2 && a.cache.gs_v) ? __ldg(a.cache.gs_v) : 1.0f;
+    constexpr int CH = C::kCh, VB = CH / 2;                          // channels, code bytes of a thread's key
+    constexpr int SPT = MODE == 2 && CH > 16 ? CH / 16 : 1;           // its scales
+    // Where its keys' codes and scales lie in a stage.  Keys i of a slab differ by 128 bytes of codes (i & 1: the
+    // bit the row swizzle folds onto bit 4) and by eight rows (i >> 1).
+    const uint32_t vc = (uint32_t)((32 * quad + key_of<D>(c, 0)) * C::kRowB + sub * (C::kRowB / NB) + g * VB);
+    const uint32_t vc0 = vc ^ ((vc >> 3) & C::kSwz), vc1 = (vc0 + 128) ^ 16;
+    const uint32_t vsc = (uint32_t)((32 * quad + key_of<D>(c, 0)) * C::kSB + (sub * (D / NB) + g * CH) / C::kGroup);
+    constexpr int KSTEP = 128 / C::kRowB;  // keys between i = 0 and i = 1
+    const uint32_t mm_a = smem_u32(mm);
+    // the first segment's query terms
+    mbar_wait(sfirst, 0, a.err, failed);
+#pragma unroll 1
+    for (int r = warp; r < R; r += C::kWarps) query_rows<MODE, D, NB, 1>(a, smem + offQ, row_out, row_c, r, group, lane);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&qfull[0]);
+    int s = 0, round = 0, it = 0, use = 0;
+    for (int seg = 0;; ++seg) {
+      const int qb = seg & 1;
+      mbar_wait(&qfull[qb], (seg >> 1) & 1, a.err, failed);
+      const int n_tiles = failed ? 0 : segs[qb].tb - segs[qb].ta;
+      if (n_tiles <= 0) break;
+      float acc[CH / 2][NB][4] = {};
+      float l[8] = {};
+      int vexp = -127;  // MXFP4: V is held relative to 2^vexp
+      if (lane < 8) mm[lane] = kNone;
+      __syncwarp();
+      const uint32_t rc_a = smem_u32(row_c + qb * R + 8 * sub);
+      const int key0 = (segs[qb].lo_tile + segs[qb].ta) * kTile;
+      const int lo_max = segs[qb].lo_max, hi_min = segs[qb].hi_min;
+      int o = (grp + C::kGroups - it % C::kGroups) % C::kGroups;  // this group's first tile of the segment
+      s += o;
+      for (; o < n_tiles; o += C::kGroups, s += C::kGroups) {
+        while (s >= ST) { s -= ST; ++round; }
+        const int j0 = key0 + o * kTile;
+        // masks only in tiles that hold an end of some row's keys
+        const bool edge = j0 < lo_max || j0 + kTile > hi_min;
+        const int j = j0 + 32 * quad + lane;  // this lane's key
+        const int buf = (it + o) % BUFS, pb_i = C::kPBufs == 1 ? 0 : use & 1;
+        mbar_wait(&full[s], round & 1, a.err, failed);
+        const uint32_t codes = base + (2 * s + 1) * C::kCodes;
+        uint32_t vs[2][4];  // V scale bytes of the thread's eight keys (two each where SPT == 2)
+        {
+          const uint32_t sa = base + offS + (2 * s + 1) * C::kScales + vsc;
+#pragma unroll
+          for (int slab = 0; slab < 2; ++slab)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t at = sa + (16 * slab + KSTEP * (i & 1) + 8 * (i >> 1)) * C::kSB;
+              vs[slab][i] = SPT == 2 ? lds16(at) : lds8(at);
+            }
+        }
+        mbar_wait(&sfull[buf], ((it + o) / BUFS) & 1, a.err, failed);
+        tc_fence_after();
+        // ---- scores of this lane's key: the six terms of each row
+        float sc[8];
+        {
+          uint32_t d[3][8];
+#pragma unroll
+          for (int k = 0; k < 3; ++k) tmem_ld8(tmem + (uint32_t)(C::kSStride * buf + k * R), d[k]);
+          const uint4 f0 = lds128(rc_a), f1 = lds128(rc_a + 16);
+          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+          for (int r = 0; r < 8; ++r) sc[r] = __uint_as_float(d[0][r]) + __uint_as_float(d[1][r]) + __uint_as_float(d[2][r]);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) tmem_ld8(tmem + (uint32_t)(C::kSStride * buf + (k + 3) * R), d[k]);
+          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+          tc_fence_before();
+          if (lane == 0) mbar_arrive(&sempty[buf]);  // a later tile may overwrite them
+          const uint32_t fr[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            sc[r] += __uint_as_float(d[0][r]) + __uint_as_float(d[1][r]) + __uint_as_float(d[2][r]);
+            sc[r] *= __uint_as_float(fr[r]);
+          }
+        }
+        if (edge) {
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            if (j >= row_hi[qb * R + 8 * sub + r] || j < row_lo[qb * R + 8 * sub + r]) sc[r] = -INFINITY;
+#pragma unroll
+          for (int slab = 0; slab < 2; ++slab)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              // keys no row sees may hold anything: their scale becomes a finite one (p is zero)
+              const int key = j0 + 32 * quad + 16 * slab + key_of<D>(c, i);
+              if (key >= segs[qb].total || key < segs[qb].first) vs[slab][i] = MODE == 2 ? 0 : (uint32_t)(vexp + 127);
+            }
+        }
+        // ---- softmax of eight rows
+        const uint4 m0 = lds128(mm_a), m1 = lds128(mm_a + 16);
+        const uint32_t mr[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+        float x[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) x[r] = sc[r] - __uint_as_float(mr[r]);
+        float high = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+        const bool grew = __any_sync(0xffffffffu, high > kMax);
+        if (grew) {  // move the references that a score has passed (or that are not set yet)
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            const float top = warp_max(sc[r]), m = __uint_as_float(mr[r]);
+            const float n = top > m + kMax ? top - kHead : m;
+            const float f = exp2f(m - n);
+            l[r] *= f;
+            x[r] = sc[r] - n;
+            if (lane == 0) {
+              mm[r] = n;
+              alphas[(pb_i * NB + sub) * 8 + r] = f;
+            }
+          }
+        }
+        const float low = fminf(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), fminf(fminf(x[4], x[5]), fminf(x[6], x[7])));
+        bool tiny = false;  // probabilities outside f16's range in this tile
+        if (__any_sync(0xffffffffu, low < -kTiny)) {
+#pragma unroll
+          for (int r = 0; r < 8; ++r) tiny |= x[r] < -kTiny && x[r] > -126.0f;
+          tiny = __any_sync(0xffffffffu, tiny);
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          x[r] = exp2_approx(x[r]);
+          l[r] += x[r];
+        }
+        uint32_t pk[4];
+        if (!tiny) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) pk[r] = pack_f16x2(x[2 * r], x[2 * r + 1]);
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) pk[r] = pack_bf16x2_rn(x[2 * r] * 256.0f, x[2 * r + 1] * 256.0f);
+        }
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                     :: "r"(pbuf + (pb_i * NB + sub) * 512 + lane * 16), "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3])
+                     : "memory");
+        if (NB > 1 && lane == 0)
+          *reinterpret_cast<int2*>(flags + (pb_i * NB + sub) * 2) = make_int2(grew, tiny);
+        if (NB == 1) __syncwarp();
+        else named_sync<NB * 32>(2 + set);
+        // ---- the quadrant's probabilities, as B fragments: keys 0-15 of the warp, keys 16-31
+        uint32_t pb[NB][4];
+        unsigned wide = 0;  // blocks in bf16
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(pb[nb][0]), "=r"(pb[nb][1]), "=r"(pb[nb][2]), "=r"(pb[nb][3])
+                       : "r"(pread + (pb_i * NB + nb) * 512) : "memory");
+          int2 fl = make_int2(grew, tiny);
+          if (NB > 1) fl = *reinterpret_cast<const int2*>(flags + (pb_i * NB + nb) * 2);
+          wide |= fl.y ? 1u << nb : 0u;
+          if (fl.x) {  // (warp-uniform)
+            const float2 f = *reinterpret_cast<const float2*>(alphas + (pb_i * NB + nb) * 8 + 2 * c);
+#pragma unroll
+            for (int i = 0; i < CH / 2; ++i) {
+              acc[i][nb][0] *= f.x;
+              acc[i][nb][1] *= f.y;
+              acc[i][nb][2] *= f.x;
+              acc[i][nb][3] *= f.y;
+            }
+          }
+        }
+        if (MODE == 1) {
+          int hi = 0, lo = 255;
+#pragma unroll
+          for (int slab = 0; slab < 2; ++slab)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              hi = max(hi, (int)vs[slab][i]);
+              lo = min(lo, (int)vs[slab][i]);
+            }
+          hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
+          hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, 2)) - 127;
+          if (__any_sync(0xffffffffu, hi > vexp)) {
+            const int n = max(hi, vexp);
+            const float f = exp2f((float)max(vexp - n, -200));
+            vexp = n;
+#pragma unroll
+            for (int i = 0; i < CH / 2; ++i)
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[i][nb][k] *= f;
+          }
+          if (__any_sync(0xffffffffu, lo - 127 - vexp < -20)) {  // V outside f16's range: everything in bf16
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              if (!(wide >> nb & 1))
+#pragma unroll
+                for (int k = 0; k < 4; ++k) pb[nb][k] = f16x2_to_bf16x2_256(pb[nb][k]);
+            wide = (1u << NB) - 1;
+          }
+        }
+        // ---- o += p V, sixteen keys at a time
+#pragma unroll
+        for (int slab = 0; slab < 2; ++slab) {
+          uint32_t wd[4][(CH + 7) / 8];  // the four keys' codes of the thread's channels
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t at = codes + (i & 1 ? vc1 : vc0) + (16 * slab + 8 * (i >> 1)) * C::kRowB;
+            if (VB == 1) {
+              wd[i][0] = lds8(at);
+            } else if (VB == 2) {
+              wd[i][0] = lds16(at);
+            } else if (VB == 4) {
+              wd[i][0] = lds32(at);
+            } else if (VB == 8) {
+              const uint2 v = lds64(at);
+              wd[i][0] = v.x;
+              wd[i][1 % ((CH + 7) / 8)] = v.y;
+            } else {
+              const uint4 v = lds128(at);
+              wd[i][0] = v.x;
+              wd[i][1 % ((CH + 7) / 8)] = v.y;
+              wd[i][2 % ((CH + 7) / 8)] = v.z;
+              wd[i][3 % ((CH + 7) / 8)] = v.w;
+            }
+          }
+          constexpr int PW = CH < 8 ? CH / 2 : 4;  // channel pairs of a word
+          if (wide != (1u << NB) - 1) {
+            uint32_t s2[SPT][2];  // scales of key pairs (0, 1) and (2, 3) as f16
+#pragma unroll
+            for (int k = 0; k < SPT; ++k)
+#pragma unroll
+              for (int p = 0; p < 2; ++p) {
+                const uint32_t x0 = (vs[slab][2 * p] >> (8 * k)) & 0xFFu, x1 = (vs[slab][2 * p + 1] >> (8 * k)) & 0xFFu;
+                if (MODE == 2) {
+                  const uint16_t both = (uint16_t)(x0 | (x1 << 8));
+                  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2[k][p]) : "h"(both));
+                } else {
+                  // 2^(E - vexp) by its fp32 bits: E is within [-20, 0] of vexp here
+                  s2[k][p] = pack_f16x2(__uint_as_float(x0 * 0x800000u - (uint32_t)vexp * 0x800000u),
+                                        __uint_as_float(x1 * 0x800000u - (uint32_t)vexp * 0x800000u));
+                }
+              }
+#pragma unroll
+            for (int q = 0; q < (CH + 7) / 8; ++q) {
+              const int k = SPT == 2 ? q / 2 : 0;
+              uint32_t ev[2][4], od[2][4];  // two keys' codes in a byte: even channels, odd channels
+#pragma unroll
+              for (int p = 0; p < 2; ++p) {
+                const uint32_t x = wd[2 * p][q], y = wd[2 * p + 1][q];
+                e2m1x8_to_f16((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), ev[p]);
+                e2m1x8_to_f16(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), od[p]);
+              }
+#pragma unroll
+              for (int i = 0; i < PW; ++i) {
+                const uint32_t af[4] = {mul_f16x2(ev[0][i], s2[k][0]), mul_f16x2(od[0][i], s2[k][0]),
+                                        mul_f16x2(ev[1][i], s2[k][1]), mul_f16x2(od[1][i], s2[k][1])};
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+                  if (NB == 1 || !(wide >> nb & 1)) mma_f16(acc[4 * q + i][nb], af, pb[nb][2 * slab], pb[nb][2 * slab + 1]);
+              }
+            }
+          }
+          if (wide) {
+            uint32_t s2[SPT][2];  // scales times 2^118 as bf16: V times 2^-8, p carries 2^8
+#pragma unroll
+            for (int k = 0; k < SPT; ++k)
+#pragma unroll
+              for (int p = 0; p < 2; ++p) {
+                const uint32_t x0 = (vs[slab][2 * p] >> (8 * k)) & 0xFFu, x1 = (vs[slab][2 * p + 1] >> (8 * k)) & 0xFFu;
+                if (MODE == 2)
+                  s2[k][p] = pack_bf16x2_rn(e4m3_to_f32(x0) * 0x1p118f, e4m3_to_f32(x1) * 0x1p118f);
+                else
+                  s2[k][p] = pack_bf16x2_rn(exp2i_f32(max((int)x0 - 9 - vexp, -126)),
+                                            exp2i_f32(max((int)x1 - 9 - vexp, -126)));
+              }
+#pragma unroll
+            for (int q = 0; q < (CH + 7) / 8; ++q) {
+              const int k = SPT == 2 ? q / 2 : 0;
+              const uint32_t n0[2] = {__byte_perm(wd[0][q], wd[1][q], 0x5410), __byte_perm(wd[0][q], wd[1][q], 0x7632)};
+              const uint32_t n1[2] = {__byte_perm(wd[2][q], wd[3][q], 0x5410), __byte_perm(wd[2][q], wd[3][q], 0x7632)};
+#pragma unroll
+              for (int i = 0; i < PW; ++i) {
+                const uint32_t x = n0[i >> 1], y = n1[i >> 1];
+                const uint32_t af[4] = {
+                    mul_bf16x2(i & 1 ? e2m1_to_bf16<2>(x) : e2m1_to_bf16<0>(x), s2[k][0]),
+                    mul_bf16x2(i & 1 ? e2m1_to_bf16<3>(x) : e2m1_to_bf16<1>(x), s2[k][0]),
+                    mul_bf16x2(i & 1 ? e2m1_to_bf16<2>(y) : e2m1_to_bf16<0>(y), s2[k][1]),
+                    mul_bf16x2(i & 1 ? e2m1_to_bf16<3>(y) : e2m1_to_bf16<1>(y), s2[k][1])};
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+                  if (NB == 1 || (wide >> nb & 1)) mma_bf16(acc[4 * q + i][nb], af, pb[nb][2 * slab], pb[nb][2 * slab + 1]);
+              }
+            }
+          }
+        }
+        __syncwarp();  // every lane's loads of the stage (and of the probabilities) are done
+        if (lane == 0) mbar_arrive(&empty[s]);
+        ++use;
+      }
+      s -= o - n_tiles;  // where the segment's last tile leaves the ring
+      while (s < 0) { s += ST; --round; }
+      it += n_tiles;
+
+      // ---- the segment's end: join the sets
+      const Seg e = segs[qb];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        float v = l[r];
+#pragma unroll
+        for (int x = 16; x; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+        if (lane == 0) set_l[set * R + 8 * sub + r] = v;
+      }
+      named_sync<kConsumers>(1);
+      if (threadIdx.x < R) {
+        float m = -INFINITY, v = 0.f;
+#pragma unroll
+        for (int k = 0; k < SETS; ++k) m = fmaxf(m, set_m[k * R + threadIdx.x]);
+#pragma unroll
+        for (int k = 0; k < SETS; ++k) {
+          v += set_l[k * R + threadIdx.x] * exp2f(set_m[k * R + threadIdx.x] - m);
+        }
+        join_m[threadIdx.x] = m;
+        join_l[threadIdx.x] = v;
+      }
+      float2* dump = reinterpret_cast<float2*>(smem + offOut) + warp * (C::kPieces * 32) + lane;
+      const float ve = MODE == 1 ? exp2i_f32(vexp) : 1.0f;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = 8 * nb + 2 * c + h;
+          float m = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < SETS; ++k) m = fmaxf(m, set_m[k * R + r]);
+          const float f = exp2f(set_m[set * R + r] - m) * ve;
+#pragma unroll
+          for (int i = 0; i < CH / 2; ++i)
+            dump[((i * NB + nb) * 2 + h) * 32] = make_float2(acc[i][nb][h] * f, acc[i][nb][2 + h] * f);
+        }
+      named_sync<kConsumers>(1);
+      constexpr int X = NB * C::kPieces * 32;                          // float2 of the output
+      constexpr int XN = (X + kConsumers - 1) / kConsumers;            // of a thread
+      // element x: slice x / (32 kPieces), row 8 nb + 2 c + h, two channels
+      auto row_of = [](int x) { return 8 * (((x >> 5) % C::kPieces >> 1) % NB) + 2 * (x & 3) + ((x >> 5) & 1); };
+      auto total = [&](int x) {
+        const float2* src = reinterpret_cast<const float2*>(smem + offOut) +
+                            (x / (C::kPieces * 32)) * (4 * C::kPieces * 32) + x % (C::kPieces * 32);
+        float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < SETS; ++k) {
+          const float2 u = src[((k >> 2) * NB * 4 + (k & 3)) * (C::kPieces * 32)];
+          v.x += u.x;
+          v.y += u.y;
+        }
+        return v;
+      };
+      auto store = [&](int x, float2 v) {
+        const int r = row_of(x), ln = x & 31, i = ((x >> 5) % C::kPieces >> 1) / NB;
+        const int ch = (x / (C::kPieces * 32)) * (D / NB) + CH * (ln >> 2) + 2 * i;
+        const int64_t at = row_out[qb * R + r];
+        if (at < 0) return;
+        const float ls = join_l[r];
+        const float inv = ls == 0.f ? 0.f : gsv / ls;
+        *reinterpret_cast<uint32_t*>(a.out + at * D + ch) = pack_bf16x2_rn(v.x * inv, v.y * inv);
+        if (a.lse && ch == 0) a.lse[at] = ls == 0.f ? -INFINITY : (join_m[r] + log2f(ls)) * 0.6931471805599453f;
+      };
+      auto release = [&]() {  // the segment's query rows, key ranges and output rows are done with
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&qempty[qb]);
+      };
+      if (e.ta == 0 && e.tb == e.tiles) {
+        for (int x = threadIdx.x; x < X; x += kConsumers) store(x, total(x));
+        release();
+        continue;
+      }
+      // A piece: into the workspace; the CTA that completes the item's count joins its pieces.  A CTA
+      // starts inside at most one item (its piece 0) and ends inside at most one other (piece 1).
+      const int c0 = owner(all_units, e.start, ctas), c1 = owner(all_units, e.start + e.tiles - 1, ctas);
+      const int tail0 = share(all_units, c0, ctas) < e.start ? 1 : 0;  // only the first CTA can end in the item
+      auto piece = [&](int k) { return pieces + (int64_t)(2 * k + (k == c0 ? tail0 : 0)) * C::kSlot; };
+      float* mine = piece(blockIdx.x);
+      for (int x = threadIdx.x; x < X; x += kConsumers) __stcg(reinterpret_cast<float2*>(mine) + x, total(x));
+      if (threadIdx.x < R) {
+        __stcg(mine + 2 * X + threadIdx.x, join_m[threadIdx.x]);
+        __stcg(mine + 2 * X + R + threadIdx.x, join_l[threadIdx.x]);
+      }
+      __threadfence();
+      named_sync<kConsumers>(1);
+      if (threadIdx.x == 0) {
+        int* ctr = counters + ((int64_t)e.b * a.cache.kv_heads + e.h) * max_blocks + e.rb;
+        const int n = atomicAdd(ctr, 1);
+        *last_flag = n == c1 - c0;
+        if (n == c1 - c0) *ctr = 0;  // ready for the next call
+      }
+      named_sync<kConsumers>(1);
+      if (!*last_flag) {
+        release();
+        continue;
+      }
+      __threadfence();
+      for (int r = warp; r < R; r += C::kWarps) {  // a warp a row, a lane a piece
+        float m = -INFINITY, v = 0.f;
+        for (int k = c0 + lane; k <= c1; k += 32) m = fmaxf(m, __ldcg(piece(k) + 2 * X + r));
+        m = warp_max(m);
+        for (int k = c0 + lane; k <= c1; k += 32) {
+          const float pm = __ldcg(piece(k) + 2 * X + r), pl = __ldcg(piece(k) + 2 * X + R + r);
+          v += pl * exp2f(pm - m);
+        }
+#pragma unroll
+        for (int x = 16; x; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+        if (lane == 0) {
+          join_m[r] = m;
+          join_l[r] = v;
+        }
+      }
+      named_sync<kConsumers>(1);
+      float* fac = reinterpret_cast<float*>(smem + offP);  // pieces' factors, a chunk at a time
+      constexpr int KC = C::kPBytes / 4 / R;
+      float2 v[XN] = {};
+      for (int k0 = c0; k0 <= c1; k0 += KC) {
+        const int nk = min(KC, c1 + 1 - k0);
+        for (int x = threadIdx.x; x < nk * R; x += kConsumers) {
+          fac[x] = exp2f(__ldcg(piece(k0 + x / R) + 2 * X + x % R) - join_m[x % R]);
+        }
+        named_sync<kConsumers>(1);
+#pragma unroll
+        for (int i = 0; i < XN; ++i) {
+          const int x = threadIdx.x + i * kConsumers;
+          if (x < X) {
+            const int r = row_of(x);
+#pragma unroll 8
+            for (int k = 0; k < nk; ++k) {
+              const float2 u = __ldcg(reinterpret_cast<const float2*>(piece(k0 + k)) + x);
+              v[i].x += u.x * fac[k * R + r];
+              v[i].y += u.y * fac[k * R + r];
+            }
+          }
+        }
+        named_sync<kConsumers>(1);
+      }
+#pragma unroll
+      for (int i = 0; i < XN; ++i)
+        if ((int)threadIdx.x + i * kConsumers < X) store(threadIdx.x + i * kConsumers, v[i]);
+      release();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::kWarps + 2) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(*tmem_slot), "n"(C::kTmemCols)
+                 : "memory");
+  }
+}
+
+template <int MODE, int D, int NB>
+cudaError_t launch(const DevInfo& d, const KvAttentionArgs& a, cudaStream_t s) {
+  using C = Dec<MODE, D, NB>;
+  const int group = a.q_heads / a.cache.kv_heads;
+  const int64_t rows = (int64_t)std::min<int64_t>(a.max_query_len, a.tokens) * group;
+  const int max_blocks = (int)((rows + C::kR - 1) / C::kR);
+  cudaError_t e =
+      cudaFuncSetAttribute(kv_decode_kernel<MODE, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  static_assert(kKvDecodeCtas <= 160, "share() and owner() multiply by the CTA count in 32 bits");
+  cfg.gridDim = dim3((unsigned)std::min(kKvDecodeCtas, d.sm_count));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  const size_t head = kv_decode_counter_bytes(a.batch, a.q_heads, a.cache.kv_heads, a.max_query_len);
+  return cudaLaunchKernelEx(&cfg, kv_decode_kernel<MODE, D, NB>, a, group, max_blocks,
+                            reinterpret_cast<int*>(ws), reinterpret_cast<float*>(ws + head), a.inject_timeout);
+}
+
+template <int MODE, int D>
+cudaError_t launch_rows(const DevInfo& d, const KvAttentionArgs& a, cudaStream_t s) {
+  const int64_t rows = (int64_t)a.max_query_len * (a.q_heads / a.cache.kv_heads);
+  if (rows <= 8) return launch<MODE, D, 1>(d, a, s);
+  if (rows <= 16 || D == 256) return launch<MODE, D, 2>(d, a, s);
+  return launch<MODE, D, D == 256 ? 2 : 4>(d, a, s);
+}
+
+}  // namespace
+
+// One counter per (request, kv head, row block of at least 8 rows), zero between calls.
+size_t kv_decode_counter_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t max_query_len) {
+  const int64_t blocks = (max_query_len * (q_heads / kv_heads) + 7) / 8;
+  return (size_t)((batch * kv_heads * blocks * 4 + 255) / 256 * 256);
+}
+
+// Two pieces a CTA, sized for the most rows of a launch with this many.
+size_t kv_decode_ws_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_query_len) {
+  const int64_t rows = max_query_len * (q_heads / kv_heads), R = rows <= 8 ? 8 : rows <= 16 || head_dim == 256 ? 16 : 32;
+  return kv_decode_counter_bytes(batch, q_heads, kv_heads, max_query_len) +
+         (size_t)(2 * kKvDecodeCtas * (R * head_dim + 2 * R) * 4);
+}
+
+bool kv_decode_supported(int head_dim) { return head_dim == 64 || head_dim == 128 || head_dim == 256; }
+
+cudaError_t launch_kv_decode(const DevInfo& d, const KvAttentionArgs& a, cudaStream_t s) {
+  const int D = a.cache.head_dim;
+  if (a.cache.mode == FP4_MODE_NVFP4)
+    return D == 64 ? launch_rows<2, 64>(d, a, s) : D == 128 ? launch_rows<2, 128>(d, a, s) : launch_rows<2, 256>(d, a, s);
+  return D == 64 ? launch_rows<1, 64>(d, a, s) : D == 128 ? launch_rows<1, 128>(d, a, s) : launch_rows<1, 256>(d, a, s);
+}
+
+}  // namespace fp4
