@@ -92,7 +92,7 @@ struct Dec {
   static constexpr uint32_t kCodes = kTile * kRowB;
   static constexpr uint32_t kScales = kTile * kSB;
   // consumer warps: as many as their output fragments (D / 4 registers a thread) leave registers for
-  static constexpr int kWarps = D <= 128 ? 16 : NB == 1 ? 12 : 8;
+  static constexpr int kWarps = D <= 128 ? 16 : 8;
   static constexpr int kGroups = kWarps / (4 * NB);
   static constexpr int kBufs = kGroups < 2 ? 2 : kGroups;    // score buffers
   static constexpr int kConsumers = kWarps * 32;
@@ -123,6 +123,8 @@ struct Dec {
   static constexpr int kStages = kStages0 > kMaxStages ? kMaxStages : kStages0;
   static constexpr uint32_t kSmem = kFixed + kStages * (2 * kCodes + 2 * kScales);
   static_assert(kStages >= 2 && kSmem <= kBudget, "shared memory");
+  // a group's parity wait on a stage must not be two phases ahead of it
+  static_assert(kStages >= kGroups, "the ring holds a tile of every group");
   static constexpr int kSlot = kR * D + 2 * kR;              // floats of a workspace piece (output, m, l)
 };
 
