@@ -146,31 +146,26 @@ cudaError_t launch_any(const KvAttentionArgs& args, cudaStream_t s) {
 
 }  // namespace
 
-bool kv_code_maps(const KvCacheDesc& c, CUtensorMap* tmK, CUtensorMap* tmV) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t row = (cuuint64_t)c.head_dim / 2;
-  const cuuint64_t dims[2] = {row, (cuuint64_t)c.num_pages * c.kv_heads * c.page_size};
-  const cuuint64_t strides[1] = {row};
-  const cuuint32_t box[2] = {(cuuint32_t)row, (cuuint32_t)c.page_size}, estr[2] = {1, 1};
-  const CUtensorMapSwizzle swz = row == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
-                                 : row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                             : CU_TENSOR_MAP_SWIZZLE_128B;
-  for (int i = 0; i < 2; ++i)
-    if (fn(i ? tmV : tmK, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, i ? c.v_codes : c.k_codes, dims, strides, box, estr,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return false;
-  return true;
+// Up to 32 query rows a kv head share the few-row kernel's one pass over the cache; more fill the tiles of the
+// many-row kernel.
+constexpr int64_t kFewRows = 32;
+
+bool few_rows(int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_query_len) {
+  return kv_decode_supported((int)head_dim) &&
+         (max_query_len * (q_heads / kv_heads) <= kFewRows || !kv_prefill_supported((int)head_dim));
 }
 
 size_t kv_attention_ws_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                              int64_t max_query_len) {
-  return kv_decode_supported((int)head_dim) ? kv_decode_ws_bytes(batch, q_heads, kv_heads, head_dim, max_query_len) : 16;
+  return few_rows(q_heads, kv_heads, head_dim, max_query_len)
+             ? kv_decode_ws_bytes(batch, q_heads, kv_heads, head_dim, max_query_len)
+             : 16;
 }
 
 cudaError_t launch_kv_attention(const DevInfo& d, const KvAttentionArgs& args, cudaStream_t s) {
-  if (kv_decode_supported(args.cache.head_dim)) return launch_kv_decode(d, args, s);
+  const KvCacheDesc& c = args.cache;
+  if (few_rows(args.q_heads, c.kv_heads, c.head_dim, args.max_query_len)) return launch_kv_decode(d, args, s);
+  if (kv_prefill_supported(c.head_dim)) return launch_kv_prefill(d, args, s);
   return launch_any(args, s);
 }
 

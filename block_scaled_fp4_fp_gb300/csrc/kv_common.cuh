@@ -1,8 +1,5 @@
-// kv_common.cuh -- what the tensor-core attention kernels share: tcgen05 issue and
-// descriptor helpers, and the tensor maps of a cache's codes.
+// kv_common.cuh -- what the tensor-core attention kernels share: tcgen05 issue and descriptor helpers.
 #pragma once
-#include <cuda.h>
-
 #include "common.cuh"
 #include "launch.h"
 

@@ -1,0 +1,608 @@
+// kv_prefill.cu -- causal attention of many query rows over the paged 4-bit cache: the
+// serving form for prompts and prompt chunks, where the tensor cores' rate is the bound.
+//
+//   o_r = sum_j p_rj v_j / sum_j p_rj,   p_rj = 2^(s_rj - m_r),   s_rj = c q_r . k_j
+// with c = softmax_scale log2(e) gs_k, over the keys row r may see.  A row r is one (query
+// token, head of the kv head's group), heads fastest, so that the rows of a tile
+// see nearly the same keys.
+//
+// A CTA (one an SM) owns an item: 256 rows of one request and kv head as two tiles of 128
+// (the MMA's M, one row per accumulator lane), and walks the keys 128 at a time:
+//   S_i = Q_i K^T    tcgen05.mma.kind::f16 (bf16), both operands in shared memory
+//   O_i += P_i V     P_i in tensor memory, in the columns S_i leaves; V as it is stored, keys as
+//                    rows (an MN-major B operand)
+// Scores, P and outputs stay in tensor memory (S: 2 x 128 columns, O: 2 x head_dim): while
+// one tile's softmax runs, the tensor cores work on the other tile.
+//
+// K and V are dequantized once per item and key by four warps into bf16 tiles
+// (exact: e2m1 times an E4M3 or E8M0 scale has at most six significant bits): the codes
+// become f16 pairs by the hardware's converter, their exponents move to bf16's place with a
+// shift and two masks, and one multiply by the block scale (two for E8M0, whose range
+// needs it) restores the value.  256 rows an item halve that work a row.
+//
+// Softmax: a thread owns a row.  P is bf16 and so has fp32's range: the reference m_r is the
+// first tile's maximum and moves only when a score passes it by 2^64, so the scores are read
+// once (twice in the first tile) and the output is almost never rescaled; p is rounded
+// to bf16 (2^-9), everything else is fp32.
+//
+// Items are handed out by an atomic counter, the longest rows of a request first (their
+// keys are the most); a warp fetches the next item and its queries while the last one ends.
+//
+//   warps 0-7    softmax and output of tile warp / 4 (lane quadrant warp % 4)
+//   warps 8-11   K and V: codes loaded a tile ahead into registers, dequantized into a
+//                double-buffered tile each; thread t owns key t
+//   warp 12      MMA issue
+//   warps 13-15  items, query tiles
+#include <algorithm>
+#include <cuda.h>
+
+#include "../../include/fp4_gb300.h"
+#include "common.cuh"
+#include "kv_common.cuh"
+#include "launch.h"
+
+namespace fp4 {
+namespace {
+
+constexpr int kRows = 256;      // query rows of an item
+constexpr int kKeys = 128;      // keys of a tile
+constexpr int kThreads = 512;
+constexpr float kLazy = 64.0f;  // a score may pass the row's reference by this (log2) before it moves
+constexpr float kNone = -1e30f;
+
+template <int D>
+struct Pre {
+  static constexpr uint32_t kQ = 128 * D * 2;      // one query tile
+  static constexpr uint32_t kKV = kKeys * D * 2;   // one K or V tile
+  static constexpr uint32_t kHalf = 128 * 128;     // 64 elements of 128 rows
+  static constexpr uint32_t offK = 2 * kQ, offV = offK + 2 * kKV, offBar = offV + 2 * kKV;
+  static constexpr uint32_t kSmem = offBar + 1024 + 5 * 1024;
+  static constexpr uint32_t kO = 256;              // output columns of tile 0; tile 1 follows
+};
+
+struct Item {
+  int b, h, q0, qlen, total;  // total: keys
+  int row0, rows;             // first row of the item in the request's (token, head) rows; rows of the request
+  int j0;                     // first key tile
+  int n[2];                   // key tiles of the two row tiles
+  int stop, pad;
+};
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+// MN-major operand tile (keys as rows of 64 swizzled elements): 8-key atoms 1024 bytes apart, the next 64
+// elements `lbo` bytes further
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lbo) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+#define R8(v, o) "=r"(v[o]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]), "=r"(v[o + 5]), "=r"(v[o + 6]), "=r"(v[o + 7])
+__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : R8(v, 0), R8(v, 8), R8(v, 16), R8(v, 24) : "r"(a));
+}
+#undef R8
+#define R8(v, o) "r"(v[o]), "r"(v[o + 1]), "r"(v[o + 2]), "r"(v[o + 3]), "r"(v[o + 4]), "r"(v[o + 5]), "r"(v[o + 6]), "r"(v[o + 7])
+__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+      :: "r"(a), R8(v, 0), R8(v, 8) : "memory");
+}
+#undef R8
+__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(a));
+}
+__device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Eight codes of a scale group -> eight bf16 (16 bytes).  `sc`: the scale times 2^112 (NVFP4), or
+// the scale times 2^12 (MXFP4), as a bf16 pair.
+template <int MODE>
+__device__ __forceinline__ uint4 dequant8(uint32_t w, uint32_t sc) {
+  uint32_t h[4];
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // f16 bits moved to bf16's exponent place: the value times 2^-112
+    uint32_t v = (h[i] & 0x80008000u) | ((h[i] >> 3) & 0x0FFF0FFFu);
+    if (MODE == 1) v = mul_bf16x2(v, 0x71807180u);  // 2^100
+    h[i] = mul_bf16x2(v, sc);
+  }
+  return make_uint4(h[0], h[1], h[2], h[3]);
+}
+template <int MODE>
+__device__ __forceinline__ uint32_t scale_pair(uint32_t byte) {
+  const float s = MODE == 2 ? e4m3_to_f32(byte) * 0x1p112f : exp2i_f32(min((int)byte - 127 + 12, 127));
+  return pack_bf16x2_rn(s, s);
+}
+
+template <int MODE, int D>
+__global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttentionArgs a, int group,
+                                                                  int* __restrict__ counters, int inject_timeout) {
+  using C = Pre<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw);
+  uint64_t* sfull = reinterpret_cast<uint64_t*>(smem + C::offBar);  // [2] scores of a row tile
+  uint64_t* pfull = sfull + 2;                                      // [2] its probabilities
+  uint64_t* ofull = pfull + 2;                                      // [2] its output complete
+  uint64_t* kfull = ofull + 2;                                      // [2] K tile dequantized
+  uint64_t* kempty = kfull + 2;                                     // [2] and read
+  uint64_t* vfull = kempty + 2;                                     // [2]
+  uint64_t* vempty = vfull + 2;                                     // [2]
+  uint64_t* qfull = vempty + 2;                                     // query tiles landed
+  uint64_t* qempty = qfull + 1;                                     // and read
+  uint64_t* ifull = qempty + 1;                                     // [2] item known
+  uint64_t* iempty = ifull + 2;                                     // [2] and done with
+  uint64_t* never = iempty + 2;                                     // fault injection: nothing arrives here
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
+  Item* items = reinterpret_cast<Item*>(smem + C::offBar + 512);   // [2]
+  int64_t* prefix = reinterpret_cast<int64_t*>(smem + C::offBar + 1024);  // [kThreads + 1] items before a thread's requests
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sfull[s], 1);
+      mbar_init(&pfull[s], 4);
+      mbar_init(&ofull[s], 1);
+      mbar_init(&kfull[s], 128);
+      mbar_init(&kempty[s], 1);
+      mbar_init(&vfull[s], 128);
+      mbar_init(&vempty[s], 1);
+      mbar_init(&ifull[s], 1);
+      mbar_init(&iempty[s], 16);
+    }
+    mbar_init(qfull, 96);
+    mbar_init(qempty, 1);
+    mbar_init(never, 1);
+    fence_barrier_init();
+  }
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 :: "r"(smem_u32(tmem_slot)), "n"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // items before each thread's requests; requests outside the contract are reported by the first CTA
+  const int per = (a.batch + kThreads - 1) / kThreads;
+  auto blocks_of = [&](int b) {
+    const int q0 = __ldg(a.query_start + b), ql = __ldg(a.query_start + b + 1) - q0;
+    if (ql <= 0 || ql > a.max_query_len || q0 < 0 || (int64_t)q0 + ql > a.tokens) return 0;
+    return (ql * group + kRows - 1) / kRows;
+  };
+  {
+    int64_t sum = 0;
+    for (int b = min(a.batch, (int)threadIdx.x * per); b < min(a.batch, ((int)threadIdx.x + 1) * per); ++b) {
+      sum += blocks_of(b);
+      if (blockIdx.x == 0) {
+        const int ql = __ldg(a.query_start + b + 1) - __ldg(a.query_start + b);
+        if (ql < 0 || (ql > 0 && blocks_of(b) == 0) || __ldg(a.total_lens + b) > (int64_t)a.max_pages * a.cache.page_size)
+          record_error(a.err, kErrIndex);
+      }
+    }
+    sum *= a.cache.kv_heads;
+    int64_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    __shared__ int64_t wsum[kThreads / 32];
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    int64_t before = 0;
+    for (int w = 0; w < warp; ++w) before += wsum[w];
+    prefix[threadIdx.x + 1] = before + incl;
+    if (threadIdx.x == 0) prefix[0] = 0;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  bool failed = false;
+  const int page_size = a.cache.page_size, page_shift = 31 - __clz(page_size);
+
+  if (warp >= 13) {
+    // ------------------------------------------------------ items, queries
+    const int64_t total_items = prefix[kThreads];
+    for (int k = 0;; ++k) {
+      Item* it = &items[k & 1];
+      if (warp == 13) {
+        if (k >= 2) mbar_wait(&iempty[k & 1], ((k >> 1) - 1) & 1, a.err, failed);
+        if (lane == 0) {
+          Item x = {};
+          const int64_t idx = failed ? total_items : (int64_t)atomicAdd(counters, 1);
+          x.stop = idx >= total_items;
+          if (x.stop) {
+            // the last CTA to find the work gone leaves the counters ready for the next call
+            if (atomicAdd(counters + 1, 1) == (int)gridDim.x - 1) {
+              counters[0] = 0;
+              counters[1] = 0;
+            }
+          } else {
+            int lo = 0, hi = kThreads;  // the thread whose requests hold the item
+            while (hi - lo > 1) {
+              const int mid = (lo + hi) >> 1;
+              if (prefix[mid] <= idx) lo = mid; else hi = mid;
+            }
+            int64_t off = idx - prefix[lo];
+            int b = lo * per, nb = blocks_of(b);
+            while (off >= (int64_t)nb * a.cache.kv_heads) {
+              off -= (int64_t)nb * a.cache.kv_heads;
+              nb = blocks_of(++b);
+            }
+            const int rb = nb - 1 - (int)(off / a.cache.kv_heads);  // longest rows first
+            x.b = b;
+            x.h = (int)(off % a.cache.kv_heads);
+            x.q0 = __ldg(a.query_start + b);
+            x.qlen = __ldg(a.query_start + b + 1) - x.q0;
+            x.total = min(__ldg(a.total_lens + b), a.max_pages * page_size);
+            x.row0 = rb * kRows;
+            x.rows = x.qlen * group;
+            const int pos0 = x.total - x.qlen + x.row0 / group;  // of the first row
+            x.j0 = a.window > 0 ? max(pos0 + 1 - a.window, 0) / kKeys : 0;
+            for (int i = 0; i < 2; ++i) {
+              const int last = min(x.row0 + 128 * (i + 1), x.rows) - 1;  // the tile's last row
+              const int end = last >= x.row0 + 128 * i ? x.total - x.qlen + last / group + 1 : 0;  // keys it sees
+              x.n[i] = max((end + kKeys - 1) / kKeys - x.j0, 0);
+            }
+          }
+          *it = x;
+          mbar_arrive(&ifull[k & 1]);
+        }
+        __syncwarp();
+      }
+      mbar_wait(&ifull[k & 1], (k >> 1) & 1, a.err, failed);
+      const Item x = *it;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&iempty[k & 1]);
+      if (x.stop || failed) break;
+      if (k > 0) mbar_wait(qempty, (k - 1) & 1, a.err, failed);
+      // 256 rows of D / 8 chunks; rows past the request's are zeros
+      for (int e = threadIdx.x - 13 * 32; e < kRows * (D / 8); e += 96) {
+        const int r = e / (D / 8), ch = e % (D / 8), rr = x.row0 + r;
+        const int tok = rr / group;
+        const bool ok = rr < x.rows;
+        const uint16_t* src = a.q + (int64_t)(x.q0 + (ok ? tok : 0)) * a.q_token +
+                              (int64_t)(x.h * group + (ok ? rr - tok * group : 0)) * a.q_head + ch * 8;
+        const uint32_t dst = base + (r >> 7) * C::kQ + (ch >> 3) * C::kHalf + (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(qfull)) : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == 12) {
+    // ------------------------------------------------------------ MMA issue
+    const uint32_t leader = elect_one_sync();
+    if (leader && inject_timeout) {
+      bool injected = false;  // separate flag: the injected expiry must not stop later waits
+      mbar_wait(never, 0, a.err, injected, 2000000LL);
+    }
+    constexpr uint32_t idesc_s = (1u << 4) | (1u << 7) | (1u << 10) | ((kKeys >> 3) << 17) | ((128u >> 4) << 24);
+    constexpr uint32_t idesc_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((128u >> 4) << 24);
+    int g = 0, u[2] = {0, 0};  // key tiles so far; probabilities consumed of each row tile
+    for (int k = 0;; ++k) {
+      mbar_wait(&ifull[k & 1], (k >> 1) & 1, a.err, failed);
+      const Item x = items[k & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&iempty[k & 1]);
+      if (x.stop || failed) break;
+      const int n = max(x.n[0], x.n[1]);
+      mbar_wait(qfull, k & 1, a.err, failed);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the copied queries, for the tensor core
+      auto scores = [&](int i, int kb) {
+        const uint64_t qd = desc_k(base + i * C::kQ, 1024, 2), kd = desc_k(base + C::offK + kb * C::kKV, 1024, 2);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          mma_ss(tmem + 128 * i, qd + (ks >> 2) * (C::kHalf >> 4) + 2 * (ks & 3), kd + (ks >> 2) * (C::kHalf >> 4) + 2 * (ks & 3),
+                 idesc_s, ks > 0);
+        tc_commit(&sfull[i]);
+      };
+      auto values = [&](int i, int vb, bool first) {
+        const uint64_t vd = desc_mn(base + C::offV + vb * C::kKV, C::kHalf);
+#pragma unroll
+        for (int ks = 0; ks < kKeys / 16; ++ks)
+          mma_ts(tmem + C::kO + D * i, tmem + 128 * i + 8 * ks, vd + ks * (2048 >> 4), idesc_o, !first || ks > 0);
+      };
+      if (n == 0 && leader) tc_commit(qempty);
+      if (n > 0) {
+        mbar_wait(&kfull[g & 1], (g >> 1) & 1, a.err, failed);
+        tc_fence_after();
+        if (leader) {
+          for (int i = 0; i < 2; ++i)
+            if (x.n[i] > 0) scores(i, g & 1);
+          tc_commit(&kempty[g & 1]);
+          if (n == 1) tc_commit(qempty);
+        }
+      }
+      for (int j = 0; j < n; ++j, ++g) {
+        mbar_wait(&vfull[g & 1], (g >> 1) & 1, a.err, failed);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (j < x.n[i]) {
+            mbar_wait(&pfull[i], u[i] & 1, a.err, failed);
+            ++u[i];
+            tc_fence_after();
+            if (leader) {
+              values(i, g & 1, j == 0);
+              if (j == x.n[i] - 1) tc_commit(&ofull[i]);
+            }
+          }
+          if (i == 1 && leader) tc_commit(&vempty[g & 1]);
+          if (i == 0 && j + 1 < n) mbar_wait(&kfull[(g + 1) & 1], ((g + 1) >> 1) & 1, a.err, failed);
+          tc_fence_after();
+          if (j + 1 < x.n[i] && leader) scores(i, (g + 1) & 1);
+        }
+        if (j + 1 < n && leader) {
+          tc_commit(&kempty[(g + 1) & 1]);
+          if (j + 2 == n) tc_commit(qempty);
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------- K and V
+    const int t = threadIdx.x - 256;
+    constexpr int GR = MODE == 2 ? 16 : 32, SB = D / GR, W = D / 8;  // scale bytes, code words of a row
+    int g = 0;
+    for (int k = 0;; ++k) {
+      mbar_wait(&ifull[k & 1], (k >> 1) & 1, a.err, failed);
+      const Item x = items[k & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&iempty[k & 1]);
+      if (x.stop || failed) break;
+      const int n = max(x.n[0], x.n[1]);
+      const int32_t* table = a.block_table + (int64_t)x.b * a.table_stride;
+      const int lo = a.window > 0 ? max(x.total - x.qlen + x.row0 / group + 1 - a.window, 0) : 0;
+      const int hi = min(x.total, (x.j0 + n) * kKeys);
+      auto row_of = [&](int j) -> int {  // cache row of this thread's key of tile j, or -1
+        const int key = (x.j0 + j) * kKeys + t;
+        if (j >= n || key < lo || key >= hi) return -1;
+        int page = __ldg(table + (key >> page_shift));
+        if (page < 0 || page >= a.cache.num_pages) {
+          record_error(a.err, kErrIndex);
+          page = 0;
+        }
+        return ((page * a.cache.kv_heads + x.h) << page_shift) + (key & (page_size - 1));
+      };
+      uint4 kc[W / 4], vc[W / 4];
+      uint32_t ks[(SB + 3) / 4], vs[(SB + 3) / 4];
+      auto load = [&](const uint32_t* codes, const uint8_t* scales, int row, uint4 (&q)[W / 4], uint32_t (&s)[(SB + 3) / 4]) {
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i)
+          q[i] = row >= 0 ? __ldg(reinterpret_cast<const uint4*>(codes + (int64_t)row * W) + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < (SB + 3) / 4; ++i)  // (a key no row sees: a scale of zero, or 2^-127, whatever is stored)
+          s[i] = row < 0 ? 0u
+                 : SB >= 4 ? __ldg(reinterpret_cast<const uint32_t*>(scales + (int64_t)row * SB) + i)
+                           : (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(scales + (int64_t)row * SB));
+      };
+      auto store = [&](uint32_t dst, const uint4 (&q)[W / 4], const uint32_t (&s)[(SB + 3) / 4]) {
+        const uint32_t r = dst + t * 128;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {  // word i: channels 8 i .. 8 i + 7
+          const int sb = i * 8 / GR;
+          const uint4 v = q[i / 4];
+          const uint32_t w = (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
+          const uint4 o = dequant8<MODE>(w, scale_pair<MODE>((s[sb / 4] >> (8 * (sb & 3))) & 0xFFu));
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                       :: "r"(r + (i >> 3) * C::kHalf + (((i & 7) ^ (t & 7)) << 4)), "r"(o.x), "r"(o.y), "r"(o.z), "r"(o.w)
+                       : "memory");
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      };
+      int row = row_of(0), next = row_of(1);
+      load(a.cache.k_codes, a.cache.k_scales, row, kc, ks);
+      for (int j = 0; j < n; ++j, ++g) {
+        load(a.cache.v_codes, a.cache.v_scales, row, vc, vs);
+        if (g >= 2) mbar_wait(&kempty[g & 1], ((g >> 1) - 1) & 1, a.err, failed);
+        store(base + C::offK + (g & 1) * C::kKV, kc, ks);
+        mbar_arrive(&kfull[g & 1]);
+        row = next;
+        next = row_of(j + 2);
+        load(a.cache.k_codes, a.cache.k_scales, row, kc, ks);
+        if (g >= 2) mbar_wait(&vempty[g & 1], ((g >> 1) - 1) & 1, a.err, failed);
+        store(base + C::offV + (g & 1) * C::kKV, vc, vs);
+        mbar_arrive(&vfull[g & 1]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------ softmax, output
+    const int i = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t ts = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 128 * i;
+    const uint32_t to = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + C::kO + D * i;
+    const float gsk = (MODE == 2 && a.cache.gs_k) ? __ldg(a.cache.gs_k) : 1.0f;
+    const float gsv = (MODE == 2 && a.cache.gs_v) ? __ldg(a.cache.gs_v) : 1.0f;
+    const float cs = a.scale * 1.4426950408889634f * gsk;
+    int use = 0, outs = 0;
+    for (int k = 0;; ++k) {
+      mbar_wait(&ifull[k & 1], (k >> 1) & 1, a.err, failed);
+      const Item x = items[k & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&iempty[k & 1]);
+      if (x.stop || failed) break;
+      const int rr = x.row0 + 128 * i + row, tok = rr / group;
+      const bool real = rr < x.rows;
+      const int pos = x.total - x.qlen + tok;
+      const int hi = real ? max(pos + 1, 0) : INT32_MAX;  // keys lo .. hi - 1 (rows past the request's are not used)
+      const int lo = real && a.window > 0 ? max(pos + 1 - a.window, 0) : 0;
+      float m = kNone, l = 0.f;
+      const int n = x.n[i];
+      for (int j = 0; j < n; ++j, ++use) {
+        const int key0 = (x.j0 + j) * kKeys;
+        const bool mask = __any_sync(0xffffffffu, key0 < lo || key0 + kKeys > hi);
+        mbar_wait(&sfull[i], use & 1, a.err, failed);
+        tc_fence_after();
+        uint32_t s[32];
+        auto hide = [&](int c) {  // scores of keys the row does not see
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int key = key0 + 32 * c + e;
+            if (key >= hi || key < lo) s[e] = 0xFF800000u;
+          }
+        };
+        auto top = [&]() {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            v[e] = fmaxf(fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 8])), fmaxf(__uint_as_float(s[e + 16]), __uint_as_float(s[e + 24])));
+          return fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
+        };
+        if (j == 0) {
+          float t = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld32(ts + 32 * c, s);
+            ld_wait();
+            if (mask) hide(c);
+            t = fmaxf(t, top());
+          }
+          m = fmaxf(t * cs, kNone);
+        }
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld32(ts + 32 * c, s);
+          ld_wait();
+          if (mask) hide(c);
+          const float t = top() * cs;
+          if (__any_sync(0xffffffffu, t > m + kLazy)) {
+            // move this row's reference: what it has summed so far is scaled down
+            const float nm = t > m + kLazy ? t : m, f = exp2f(m - nm);
+            m = nm;
+            l *= f;
+            for (int cc = 0; cc < c; ++cc) {  // probabilities of this tile
+              uint32_t p[16];
+              tmem_ld16(ts + 16 * cc, p);
+              ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) p[e] = pack_bf16x2_rn(bf16_lo(p[e]) * f, bf16_hi(p[e]) * f);
+              tmem_st16(ts + 16 * cc, p);
+            }
+            if (j > 0)  // the output: no MMA is adding to it (this tile's scores were issued after the last that did)
+              for (int cc = 0; cc < D / 16; ++cc) {
+                uint32_t p[16];
+                tmem_ld16(to + 16 * cc, p);
+                ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) p[e] = __float_as_uint(__uint_as_float(p[e]) * f);
+                tmem_st16(to + 16 * cc, p);
+              }
+            st_wait();
+          }
+          uint32_t p[16];
+          float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float p0 = exp2_approx(fmaf(__uint_as_float(s[2 * e]), cs, -m));
+            const float p1 = exp2_approx(fmaf(__uint_as_float(s[2 * e + 1]), cs, -m));
+            l0 += p0;
+            l1 += p1;
+            p[e] = pack_bf16x2_rn(p0, p1);
+          }
+          l += l0 + l1;
+          tmem_st16(ts + 16 * c, p);
+        }
+        st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[i]);
+      }
+      // ---- output
+      const int64_t at = (int64_t)(x.q0 + tok) * a.q_heads + x.h * group + (rr - tok * group);
+      const float inv = l == 0.f ? 0.f : gsv / l;
+      if (n > 0) {
+        mbar_wait(&ofull[i], outs & 1, a.err, failed);
+        ++outs;
+        tc_fence_after();
+      }
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (n > 0) {
+          tmem_ld32(to + 32 * c, o);
+          ld_wait();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0;
+        }
+        if (real) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + at * D + 32 * c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t v[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+              v[h] = pack_bf16x2_rn(__uint_as_float(o[8 * e + 2 * h]) * inv, __uint_as_float(o[8 * e + 2 * h + 1]) * inv);
+            dst[e] = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        }
+      }
+      if (real && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      tc_fence_before();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "n"(512) : "memory");
+  }
+}
+
+template <int MODE, int D>
+cudaError_t launch(const DevInfo& d, const KvAttentionArgs& a, cudaStream_t s) {
+  const int smem = (int)Pre<D>::kSmem + 1024;
+  cudaError_t e = cudaFuncSetAttribute(kv_prefill_kernel<MODE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)d.sm_count);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_prefill_kernel<MODE, D>, a, a.q_heads / a.cache.kv_heads, static_cast<int*>(a.ws),
+                            a.inject_timeout);
+}
+
+}  // namespace
+
+bool kv_prefill_supported(int head_dim) { return head_dim == 64 || head_dim == 128; }
+
+cudaError_t launch_kv_prefill(const DevInfo& d, const KvAttentionArgs& a, cudaStream_t s) {
+  if (a.cache.mode == FP4_MODE_NVFP4)
+    return a.cache.head_dim == 64 ? launch<2, 64>(d, a, s) : launch<2, 128>(d, a, s);
+  return a.cache.head_dim == 64 ? launch<1, 64>(d, a, s) : launch<1, 128>(d, a, s);
+}
+
+}  // namespace fp4

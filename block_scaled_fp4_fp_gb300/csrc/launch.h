@@ -151,14 +151,14 @@ struct KvAttentionArgs {
 // the attention's dispatch (kv_attention.cu) and its workspace
 size_t kv_attention_ws_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_query_len);
 cudaError_t launch_kv_attention(const DevInfo& d, const KvAttentionArgs& args, cudaStream_t s);
-// tensor maps of K's and V's codes, boxes of page_size rows x head_dim / 2 bytes, swizzled by the row's length
-// (head_dim 64, 128, 256)
-bool kv_code_maps(const KvCacheDesc& c, CUtensorMap* tmK, CUtensorMap* tmV);
 // kv_decode.cu: a few query rows a request, head_dim 64, 128 or 256
 constexpr int kKvDecodeCtas = 160;  // CTAs of a launch at most (one an SM)
 bool kv_decode_supported(int head_dim);
 size_t kv_decode_counter_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t max_query_len);
 size_t kv_decode_ws_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_query_len);
 cudaError_t launch_kv_decode(const DevInfo& d, const KvAttentionArgs& args, cudaStream_t s);
+// kv_prefill.cu: many query rows a request, head_dim 64 or 128 (workspace: two zeroed ints)
+bool kv_prefill_supported(int head_dim);
+cudaError_t launch_kv_prefill(const DevInfo& d, const KvAttentionArgs& args, cudaStream_t s);
 
 }  // namespace fp4
