@@ -74,6 +74,8 @@ class Fp4Error(RuntimeError):
 def lib():
     """Load libfp4gb300.so (built in-tree by __graft_entry__.build())."""
     global _lib
+    if _lib is not None:  # set once, below, when it is complete
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -101,9 +103,13 @@ def _p(t):
 
 
 def _s(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return stream.cuda_stream
+    """The raw handle of `stream`, or of the current stream of the current device.  (Without the stream object of
+    torch.cuda.current_stream(), which costs ~3 us a call: as much as a launch.)"""
+    if stream is not None:
+        return stream.cuda_stream
+    if torch.cuda.is_initialized():
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def padded_scale_dims(rows: int, scale_cols: int):
@@ -382,10 +388,10 @@ def kv_plan(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch
     lengths, slots and positions of up to `tokens` tokens (entries past the step's own are -1)."""
     batch = cached_lens.numel()
     if plan is None:
-        ints = torch.empty(2 * batch + 2 + tokens, dtype=torch.int32, device=cached_lens.device)
-        slots = torch.empty(tokens, dtype=torch.int64, device=cached_lens.device)
-        total, start, pos, taken = ints.split_with_sizes((batch, batch + 1, tokens, 1))
-        plan = KvPlan(total, start, slots, pos, taken[0])
+        dev, i32 = cached_lens.device, torch.int32
+        plan = KvPlan(torch.empty(batch, dtype=i32, device=dev), torch.empty(batch + 1, dtype=i32, device=dev),
+                      torch.empty(tokens, dtype=torch.int64, device=dev), torch.empty(tokens, dtype=i32, device=dev),
+                      torch.empty((), dtype=i32, device=dev))
     _check(lib().kv_plan(_p(cached_lens), _p(new_lens), batch, page_size, _p(free_pages), free_pages.numel(),
                          _p(block_table), block_table.stride(0), block_table.shape[1], _p(plan.total_lens),
                          _p(plan.query_start), _p(plan.slot_map), _p(plan.positions), plan.slot_map.numel(),

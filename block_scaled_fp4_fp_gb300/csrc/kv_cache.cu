@@ -218,7 +218,8 @@ cudaError_t launch_kv_plan(const DevInfo& d, const int32_t* cached, const int32_
                            int64_t max_pages, int32_t* total_lens, int32_t* query_start, int64_t* slot_map,
                            int32_t* positions, int64_t T, int32_t* pages_taken, cudaStream_t s) {
   const size_t smem = (size_t)B * 2 * sizeof(int);
-  cudaError_t e = cudaFuncSetAttribute(kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * 4 * 16384);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(d, kv_plan_kernel, 2 * 4 * 16384, done);
   if (e != cudaSuccess) return e;
   int64_t grid = (T + kPlanThreads - 1) / kPlanThreads;
   if (grid > d.sm_count) grid = d.sm_count;

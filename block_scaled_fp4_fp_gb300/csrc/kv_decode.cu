@@ -1189,8 +1189,8 @@ cudaError_t launch(const DevInfo& d, const KvAttentionArgs& a, cudaStream_t s) {
   const int group = a.q_heads / a.cache.kv_heads;
   const int64_t rows = (int64_t)std::min<int64_t>(a.max_query_len, a.tokens) * group;
   const int max_blocks = (int)((rows + C::kR - 1) / C::kR);
-  cudaError_t e =
-      cudaFuncSetAttribute(kv_decode_kernel<MODE, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(d, kv_decode_kernel<MODE, D, NB>, (int)C::kSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   static_assert(kKvDecodeCtas <= 160, "share() and owner() multiply by the CTA count in 32 bits");

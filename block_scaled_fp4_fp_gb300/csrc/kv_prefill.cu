@@ -579,7 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
 template <int MODE, int D>
 cudaError_t launch(const DevInfo& d, const KvAttentionArgs& a, cudaStream_t s) {
   const int smem = (int)Pre<D>::kSmem + 1024;
-  cudaError_t e = cudaFuncSetAttribute(kv_prefill_kernel<MODE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(d, kv_prefill_kernel<MODE, D>, smem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)d.sm_count);

@@ -3,6 +3,7 @@
 // been validated by api.cu; each returns the cudaError_t of its launch(es).
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -21,6 +22,17 @@ struct DevInfo {
 // api.cu: the current device's cached properties (initialized on first use);
 // returns an fp4_status value
 int current_device_info(const DevInfo** out);
+
+// Lets a kernel use `bytes` of dynamic shared memory, once per device and kernel: the attribute stays set,
+// and setting it costs a driver call.  `done`: a bit per device, the caller's static.
+template <typename Kernel>
+cudaError_t allow_smem(const DevInfo& d, Kernel kernel, int bytes, std::atomic<uint64_t>& done) {
+  const uint64_t bit = 1ull << (d.device & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // quant.cu
 size_t amax_workspace_bytes(int64_t n);
