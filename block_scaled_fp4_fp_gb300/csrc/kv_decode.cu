@@ -12,10 +12,13 @@
 // accumulator lane, its E4M3/E8M0 scales applied by the hardware), and the R query
 // rows are the B operand, each written as kTerms = 6 FP4 terms in radix 8,
 //     q = 2^e0 (sum_t d_t 2^(6-3t) + rest),  d_t in {-4..4},  max|q| / 2^e0 in [128, 256),
-// exact but for |rest| <= 2^-10, 2^-17 of the row's largest element.  Term t of row r is
-// column t R + r, so the thread that owns a key sums a row's six columns in
-// registers: no score crosses a lane.  Dequantizing K instead would cost an
-// instruction stream as long as V's, the larger half of what the SM issues.
+// exact but for |rest| <= 2^-10, 2^-17 of the row's largest element.  Terms t and t + 3 of row r
+// add up in column (t mod 3) R + r (two MMAs a step of 64 channels, ~143 cycles each whatever
+// N is), so the thread that owns a key sums a row's three columns in registers: no
+// score crosses a lane.  (Six columns and one MMA cost the consumers 27 more instructions per 32
+// keys and eight rows; one column and six MMAs would take the tensor cores longer than
+// the tile's DRAM time.)  Dequantizing K instead would cost an instruction stream as long as
+// V's, the larger half of what the SM issues.
 //
 // Values in registers: a warp owns 32 keys of the tile (its tensor-memory lane
 // quadrant) from scores to output.  V's codes come from shared memory in the
@@ -68,13 +71,15 @@ namespace fp4 {
 namespace {
 
 constexpr int kTerms = 6;
+constexpr int kCols = 3;                 // score columns of a row
+constexpr int kChains = kTerms / kCols;  // terms added into each
 constexpr int kTile = 128;  // keys per tile: the MMA's M
 constexpr int kMaxStages = 8;
 constexpr float kLog2e = 1.4426950408889634f;
-// What a (request, kv head, row block) costs a CTA besides its tiles, in tiles: starting on new queries, joining
-// the sets and writing the rows take about 1.5 us, a tile 0.45 us (measured, D = 128).  Counted when the
-// work is dealt out, so that a CTA with many short requests does not finish last.
-constexpr int kItemCost = 3;
+// Boundaries between the CTAs' shares within this many units of an item's end are moved there: a piece costs
+// two CTAs and its join more than the tiles it moves.
+constexpr int kSnap = 6;
+constexpr int kMinShare = 8;  // units of a CTA at least (of all requests together, before boundaries move)
 constexpr float kHead = 7.0f;   // a new reference m is the largest score less this (log2)
 constexpr float kMax = 15.0f;   // and moves when a score passes it by this: p <= 2^15
 constexpr float kTiny = 23.0f;  // scores further below m than this need bf16's range
@@ -83,7 +88,7 @@ constexpr float kNone = -1e30f; // m before any score: exp2 of a hidden key's -i
 template <int MODE, int D, int NB>
 struct Dec {
   static constexpr int kR = 8 * NB;                          // query rows
-  static constexpr int kN = kTerms * kR;                     // MMA N
+  static constexpr int kN = (kCols * kR + 15) / 16 * 16;     // MMA N (rows past kCols kR feed columns nothing reads)
   static constexpr int kGroup = MODE == 2 ? 16 : 32;
   static constexpr int kSB = D / kGroup;                     // scale bytes of a row
   static constexpr int kWords = kSB < 4 ? 1 : kSB / 4;       // and its 32-bit words
@@ -100,12 +105,13 @@ struct Dec {
   static constexpr int kCh = D / NB / 8;                     // channels of a consumer thread
   static constexpr int kPieces = D / 8;                      // float2 of its output
   static constexpr int kPBufs = NB == 1 ? 1 : 2;             // probability buffers of a quadrant
-  static constexpr uint32_t kQBytes = (kN * kRowB + 1023) / 1024 * 1024;
-  static constexpr int kSStride = NB == 1 ? 64 : kN;         // tensor-memory columns between score buffers
+  static constexpr uint32_t kQChain = (kN * kRowB + 1023) / 1024 * 1024;
+  static constexpr uint32_t kQBytes = kChains * kQChain;
+  static constexpr int kSStride = (kN + 31) / 32 * 32;       // tensor-memory columns between score buffers
   static constexpr uint32_t kSfa = kBufs * kSStride;         // K scales, kBufs buffers of 16 columns
-  static constexpr uint32_t kSfb = kSfa + 16 * kBufs;        // term scales, 8 columns
+  static constexpr uint32_t kSfb = kSfa + 16 * kBufs;        // term scales, 4 columns a chain
   static constexpr uint32_t kTmemCols = 512;
-  static_assert(kSfb + 8 <= kTmemCols, "tensor memory");
+  static_assert(kSfb + 4 * kChains <= kTmemCols && kN <= 128, "tensor memory");
   // shared memory: [stages: K codes, V codes][queries x 2][K scales as tcgen05.cp reads them][outputs]
   // [probabilities][stages: K scales, V scales][row data][barriers]
   static constexpr int kSets = kGroups * 4;                  // quadrants with their own m, l, output
@@ -115,7 +121,7 @@ struct Dec {
   // score factors, key ranges and output rows x 2, m and l of the sets, joined m and l, flags and factors of the
   // probability buffers, segments x 2
   static constexpr uint32_t kRowBytes =
-      2 * 3 * kR * 4 + 2 * kR * 8 + kSets * kR * 8 + 2 * kR * 4 + kSets * kPBufs * NB * (32 + 8) + 128;
+      2 * 3 * kR * 4 + 2 * kR * 8 + kSets * kR * 12 + 2 * kR * 4 + kSets * kPBufs * NB * (32 + 8) + 128;
   static constexpr uint32_t kFixed =
       2 * kQBytes + kBufs * kSfaBytes + kOutBytes + kPBytes + kRowBytes + 512 + 1024;
   static constexpr uint32_t kBudget = 226u * 1024u;
@@ -125,6 +131,10 @@ struct Dec {
   static_assert(kStages >= 2 && kSmem <= kBudget, "shared memory");
   // a group's parity wait on a stage must not be two phases ahead of it
   static_assert(kStages >= kGroups, "the ring holds a tile of every group");
+  // What an item costs a CTA besides its tiles, in tiles: starting on new queries, draining the groups, joining the
+  // sets and writing the rows take about 4 us, a tile 0.4 to 1.8 us (measured).  Counted when the work is
+  // dealt out, so that a CTA with many short requests does not finish last.
+  static constexpr int kItemCost = NB == 1 ? 8 : NB == 2 ? 5 : 3;
   static constexpr int kSlot = kR * D + 2 * kR;              // floats of a workspace piece (output, m, l)
 };
 
@@ -191,6 +201,25 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
 }
+// two fp32 values in a register pair, and the packed add and multiply-add (each lane rounded to nearest)
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 // shared-memory reads by 32-bit address
 __device__ __forceinline__ uint32_t lds8(uint32_t a) {
   uint32_t v;
@@ -246,13 +275,13 @@ __device__ __forceinline__ int key_of(int c, int i) {
 struct Req {
   int q0, qlen, total, first;  // first token row, query count, keys, first visible key
   int tiles, lo_tile, blocks;  // tiles per pass, first tile, row blocks
-  __device__ __forceinline__ int cost() const { return tiles + kItemCost; }  // of an item (if it has tiles at all)
+  int cost;                    // units of an item: its tiles, and the fixed cost
   __device__ __forceinline__ int64_t units(int kv_heads) const {
-    return tiles > 0 ? (int64_t)cost() * blocks * kv_heads : 0;
+    return tiles > 0 ? (int64_t)cost * blocks * kv_heads : 0;
   }
 };
 
-__device__ __forceinline__ Req load_req(const KvAttentionArgs& a, int b, int group, int R) {
+__device__ __forceinline__ Req load_req(const KvAttentionArgs& a, int b, int group, int R, int item_cost) {
   Req r;
   r.q0 = __ldg(a.query_start + b);
   r.qlen = __ldg(a.query_start + b + 1) - r.q0;
@@ -263,43 +292,45 @@ __device__ __forceinline__ Req load_req(const KvAttentionArgs& a, int b, int gro
   r.lo_tile = r.first / kTile;
   r.blocks = r.qlen > 0 ? (int)((unsigned)(r.qlen * group + R - 1) / (unsigned)R) : 0;
   r.tiles = (r.total > 0 && r.qlen > 0) ? (r.total + kTile - 1) / kTile - r.lo_tile : 0;
+  r.cost = r.tiles + item_cost;
   return r;
 }
 
 // A CTA's walk over its share of the sequence: request by request, in it kv head by kv head, in it row block
-// by row block; each of these items is its tiles and then kItemCost units that hold no work.
+// by row block; each of these items is its tiles and then some units that hold no work.
 struct Walk {
   const KvAttentionArgs* a;
-  int group, R, b, item, off;
+  int group, R, item_cost, b, item, off;
   int64_t at, end;  // position in the sequence
   Req r;
   // the current segment
   int h, rb, ta, tb;
   int64_t start;  // where the item's tile 0 sits in the sequence
-  __device__ __forceinline__ void begin(const KvAttentionArgs& args, int g, int rows, int b0, int item0, int off0,
-                                        int64_t f0, int64_t f1) {
+  __device__ __forceinline__ void begin(const KvAttentionArgs& args, int g, int rows, int fixed, int b0, int item0,
+                                        int off0, int64_t f0, int64_t f1) {
     a = &args;
     group = g;
     R = rows;
+    item_cost = fixed;
     b = b0;
     at = f0;
     end = f1;
     item = item0;
     off = off0;
-    r = load_req(args, b, group, R);
+    r = load_req(args, b, group, R, item_cost);
   }
   __device__ __forceinline__ bool next() {
     for (;;) {
       if (at >= end) return false;
       while (r.tiles == 0 || item == a->cache.kv_heads * r.blocks) {
         if (++b >= a->batch) return false;
-        r = load_req(*a, b, group, R);
+        r = load_req(*a, b, group, R, item_cost);
         item = 0;
       }
       h = item / r.blocks;
       rb = item - h * r.blocks;
       start = at - off;
-      const int to = (int)min((int64_t)r.cost(), off + (end - at));
+      const int to = (int)min((int64_t)r.cost, off + (end - at));
       ta = min(off, r.tiles);
       tb = min(to, r.tiles);
       at += to - off;
@@ -319,8 +350,8 @@ struct Seg {
   int64_t start;  // where the item's tile 0 sits in the sequence
 };
 
-// Query rows r0 .. r0 + N - 1 of a segment as FP4 terms in the B operand's order (a warp): term t of row r is
-// operand row t R + r.  Writes each row's score factor.
+// Query rows r0 .. r0 + N - 1 of a segment as FP4 terms in the B operands' order (a warp): term t of row r is
+// row (t mod kCols) R + r of chain t / kCols.  Writes each row's score factor.
 template <int MODE, int D, int NB, int N>
 __device__ __forceinline__ void query_rows(const KvAttentionArgs& a, uint8_t* dst, const int64_t* row_out, float* row_c,
                                            int r0, int group, int lane) {
@@ -366,8 +397,8 @@ __device__ __forceinline__ void query_rows(const KvAttentionArgs& a, uint8_t* ds
         v[2 * e + 1] = __fmaf_rn(-sc, d1, v[2 * e + 1]);
         codes |= e2m1x2_rn(d0, d1) << (8 * e);
       }
-      uint32_t off = (uint32_t)((t * C::kR + r0 + k) * C::kRowB + lane * (EL / 2));
-      off ^= (off >> 3) & C::kSwz;
+      uint32_t off = (uint32_t)(((t % kCols) * C::kR + r0 + k) * C::kRowB + lane * (EL / 2));
+      off = (off ^ ((off >> 3) & C::kSwz)) + (t / kCols) * C::kQChain;
       if (EL == 2) dst[off] = (uint8_t)codes;
       else if (EL == 4) *reinterpret_cast<uint16_t*>(dst + off) = (uint16_t)codes;
       else *reinterpret_cast<uint32_t*>(dst + off) = codes;
@@ -393,7 +424,8 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
   int* row_hi = row_lo + 2 * R;                                   // [2][R] first key past those it sees
   int64_t* row_out = reinterpret_cast<int64_t*>(row_hi + 2 * R);  // [2][R] its place in out and lse, or -1
   float* set_m = reinterpret_cast<float*>(row_out + 2 * R);       // [SETS][R] running references
-  float* set_l = set_m + SETS * R;                                // [SETS][R] sums
+  float* set_n = set_m + SETS * R;                                // [SETS][R] their negatives
+  float* set_l = set_n + SETS * R;                                // [SETS][R] sums
   float* join_m = set_l + SETS * R;                               // [R]
   float* join_l = join_m + R;                                     // [R]
   float* p_alpha = join_l + R;                                    // [SETS][kPBufs][NB][8] a moved reference's factors
@@ -444,7 +476,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
     const int b0 = min(a.batch, (int)threadIdx.x * per), b1 = min(a.batch, b0 + per);
     int64_t sum = 0;
     for (int b = b0; b < b1; ++b) {
-      const Req r = load_req(a, b, group, R);
+      const Req r = load_req(a, b, group, R, C::kItemCost);
       sum += r.units(a.cache.kv_heads);
     }
     int64_t incl = sum;
@@ -462,33 +494,41 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
       all += scan[w];
     }
     before += incl - sum;
-    // a CTA takes two tiles (of an item of its own) at least: its groups work side by side
-    const int64_t ctas = min((int64_t)gridDim.x, (all + kItemCost + 1) / (kItemCost + 2));
-    int64_t f0 = 0, f1 = 0;
-    if ((int64_t)blockIdx.x < ctas) {
-      f0 = share(all, blockIdx.x, (int)ctas);
-      f1 = share(all, blockIdx.x + 1, (int)ctas);
-    }
+    const int64_t ctas = max((int64_t)1, min((int64_t)gridDim.x, all / kMinShare));
+    const bool has = (int64_t)blockIdx.x < ctas && all > 0;
     if (threadIdx.x == 0) {
-      plan[0] = f0;
-      plan[1] = f1;
+      plan[0] = plan[1] = 0;
       plan[3] = all;
       plan[4] = ctas;
     }
-    if (f0 < f1 && f0 >= before && f0 < before + sum) {  // the thread whose requests hold the first unit
-      int64_t off = f0 - before;
-      int b = b0;
-      for (;; ++b) {
-        const Req r = load_req(a, b, group, R);
-        const int64_t n = r.units(a.cache.kv_heads);
-        if (off < n) {
-          const int item = (int)(off / r.cost());
-          plan_at[0] = b;
-          plan_at[1] = item;
-          plan_at[2] = (int)(off - (int64_t)item * r.cost());
-          break;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {  // the share's two boundaries; the thread whose requests hold one places it
+      const int64_t f = has ? share(all, blockIdx.x + e, (int)ctas) : -1;
+      if (e == 1 && f == all && threadIdx.x == 0) plan[1] = all;
+      if (f >= before && f < before + sum) {
+        int64_t off = f - before;
+        int b = b0;
+        for (;; ++b) {
+          const Req r = load_req(a, b, group, R, C::kItemCost);
+          const int64_t n = r.units(a.cache.kv_heads);
+          if (off < n) {
+            int item = (int)((unsigned)off / (unsigned)r.cost), at = 0;  // (off < 2^31: at most 16 million keys a request)
+            if (n > INT32_MAX) item = (int)(off / r.cost);
+            at = (int)(off - (int64_t)item * r.cost);
+            int move = 0;  // to an end of the item, if one is near
+            if (at <= kSnap && at <= r.cost - at) move = -at;
+            else if (r.cost - at <= kSnap) move = r.cost - at;
+            plan[e] = f + move;
+            if (e == 0) {
+              plan_at[0] = b;
+              plan_at[1] = move > 0 ? item + 1 : item;
+              plan_at[2] = move != 0 ? 0 : at;
+            }
+            break;
+          }
+          off -= n;
         }
-        off -= n;
       }
     }
   }
@@ -500,7 +540,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
   // requests that see no key give zeros; requests outside the contract are reported
   for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
     const int q0 = __ldg(a.query_start + b), ql = __ldg(a.query_start + b + 1) - q0, n = __ldg(a.total_lens + b);
-    const Req r = load_req(a, b, group, R);
+    const Req r = load_req(a, b, group, R, C::kItemCost);
     if (threadIdx.x == 0 && (ql < 0 || (ql > 0 && r.qlen == 0) || n > r.total)) record_error(a.err, kErrIndex);
     if (r.qlen > 0 && r.tiles == 0) {
       for (int64_t i = threadIdx.x; i < (int64_t)r.qlen * a.q_heads * (D / 8); i += kThreads)
@@ -532,7 +572,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
     codes += lane * 16;
     int s = 0, round = 0;
     Walk w;
-    w.begin(a, group, R, plan_at[0], plan_at[1], plan_at[2], f0, f1);
+    w.begin(a, group, R, C::kItemCost, plan_at[0], plan_at[1], plan_at[2], f0, f1);
     while (w.next()) {
       // Cache rows of the table's next 32 pages, a page a lane, and the 32 after them on their way: one
       // table load's latency a tile would bound the ring.
@@ -598,18 +638,17 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                  :: "r"(smem_u32(tmem_slot)), "n"(C::kTmemCols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    // the query terms' scales, column n / 32 (four further from row 128 on) of lane n % 32, copied to every
-    // lane quadrant from the first kilobyte of the output area, idle until the first segment ends
-    {
-      uint32_t v[8];
+    // the query terms' scales, column n / 32 of lane n % 32 of a chain, copied to every lane quadrant from the
+    // first kilobyte of the output area, idle until the first segment ends
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
+    for (int ch = 0; ch < kChains; ++ch) {
+      uint32_t v[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
         const int n = 32 * c + lane;
-        v[c] = n < C::kN ? term_scale<MODE>(n / R) * 0x01010101u : 0u;
+        v[c] = n < kCols * R ? term_scale<MODE>(ch * kCols + n / R) * 0x01010101u : 0u;
       }
-      uint4* st = reinterpret_cast<uint4*>(smem + offOut);
-      st[lane] = make_uint4(v[0], v[1], v[2], v[3]);
-      st[32 + lane] = make_uint4(v[4], v[5], v[6], v[7]);
+      reinterpret_cast<uint4*>(smem + offOut)[32 * ch + lane] = make_uint4(v[0], v[1], v[2], v[3]);
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     tc_fence_before();
@@ -622,8 +661,8 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
         bool injected = false;  // separate flag: the injected expiry must not stop later waits
         mbar_wait(never, 0, a.err, injected, 2000000LL);
       }
-      tc_cp_sf(tmem + C::kSfb, desc_sf(base + offOut));
-      if (C::kN > 128) tc_cp_sf(tmem + C::kSfb + 4, desc_sf(base + offOut + 512));
+#pragma unroll
+      for (int ch = 0; ch < kChains; ++ch) tc_cp_sf(tmem + C::kSfb + 4 * ch, desc_sf(base + offOut + 512 * ch));
       mbar_arrive(tbar);  // publishes tmem_slot to the consumers
     }
     constexpr uint32_t idesc0 = (1u << 7) | (1u << 10) | ((uint32_t)(C::kN >> 3) << 17) | (MODE == 1 ? 1u << 23 : 0u) |
@@ -670,12 +709,15 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
           const uint64_t ad = desc_k(base + 2 * s * C::kCodes, 8 * C::kRowB, layout);
           const uint64_t bd = desc_k(base + offQ + qb * C::kQBytes, 8 * C::kRowB, layout);
 #pragma unroll
-          for (int ks = 0; ks < D / 64; ++ks) {
-            const int word = MODE == 2 ? ks : ks / 2;
-            const uint32_t id = MODE == 2 ? 0u : 2u * (ks & 1);
-            mma_fp4<MODE>(tmem + C::kSStride * buf, ad + 2 * ks, bd + 2 * ks, idesc0 | (id << 29) | (id << 4),
-                          tmem + C::kSfa + 16 * buf + 4 * word, tmem + C::kSfb, ks > 0);
-          }
+          for (int ch = 0; ch < kChains; ++ch)
+#pragma unroll
+            for (int ks = 0; ks < D / 64; ++ks) {
+              const int word = MODE == 2 ? ks : ks / 2;
+              const uint32_t id = MODE == 2 ? 0u : 2u * (ks & 1);
+              mma_fp4<MODE>(tmem + C::kSStride * buf, ad + 2 * ks, bd + ch * (C::kQChain >> 4) + 2 * ks,
+                            idesc0 | (id << 29) | (id << 4), tmem + C::kSfa + 16 * buf + 4 * word,
+                            tmem + C::kSfb + 4 * ch, ch > 0 || ks > 0);
+            }
           tc_commit(&sfull[buf]);
           if (i + 1 == n) tc_commit(&qempty[qb]);
         }
@@ -687,13 +729,15 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
 
     // ------------------------------------------------------------ queries
     Walk w;
-    w.begin(a, group, R, plan_at[0], plan_at[1], plan_at[2], f0, f1);
+    w.begin(a, group, R, C::kItemCost, plan_at[0], plan_at[1], plan_at[2], f0, f1);
     for (int seg = 0;; ++seg) {
       const int qb = seg & 1;
       if (seg >= 2) mbar_wait(&qempty[qb], ((seg >> 1) - 1) & 1, a.err, failed);
       if (!w.next()) {
         if (lane == 0) segs[qb].ta = segs[qb].tb = 0;
-        if (lane < C::kWarps) mbar_arrive(&qfull[qb]);
+        __syncwarp();
+        if (seg == 0) mbar_arrive(sfirst);  // (a share that holds nothing but fixed costs)
+        else if (lane < C::kWarps) mbar_arrive(&qfull[qb]);
         mbar_arrive(&qfull[qb]);
         break;
       }
@@ -745,11 +789,13 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
     const uint32_t vc0 = vc ^ ((vc >> 3) & C::kSwz), vc1 = (vc0 + 128) ^ 16;
     const uint32_t vsc = (uint32_t)((32 * quad + key_of<D>(c, 0)) * C::kSB + (sub * (D / NB) + g * CH) / C::kGroup);
     constexpr int KSTEP = 128 / C::kRowB;  // keys between i = 0 and i = 1
-    const uint32_t mm_a = smem_u32(mm);
+    float* mn = set_n + set * R + 8 * sub;
+    const uint32_t mn_a = smem_u32(mn);
     // the first segment's query terms
     mbar_wait(sfirst, 0, a.err, failed);
 #pragma unroll 1
-    for (int r = warp; r < R; r += C::kWarps) query_rows<MODE, D, NB, 1>(a, smem + offQ, row_out, row_c, r, group, lane);
+    for (int r = warp; r < R && !failed && segs[0].ta < segs[0].tb; r += C::kWarps)
+      query_rows<MODE, D, NB, 1>(a, smem + offQ, row_out, row_c, r, group, lane);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if (lane == 0) mbar_arrive(&qfull[0]);
@@ -760,9 +806,12 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
       const int n_tiles = failed ? 0 : segs[qb].tb - segs[qb].ta;
       if (n_tiles <= 0) break;
       float acc[CH / 2][NB][4] = {};
-      float l[8] = {};
+      uint64_t l2[4] = {};  // sums of rows (2 i, 2 i + 1)
       int vexp = -127;  // MXFP4: V is held relative to 2^vexp
-      if (lane < 8) mm[lane] = kNone;
+      if (lane < 8) {
+        mm[lane] = kNone;
+        mn[lane] = -kNone;
+      }
       __syncwarp();
       const uint32_t rc_a = smem_u32(row_c + qb * R + 8 * sub);
       const int key0 = (segs[qb].lo_tile + segs[qb].ta) * kTile;
@@ -791,32 +840,36 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
         }
         mbar_wait(&sfull[buf], ((it + o) / BUFS) & 1, a.err, failed);
         tc_fence_after();
-        // ---- scores of this lane's key: the six terms of each row
-        float sc[8];
+        // ---- scores of this lane's key, two rows a register pair
+        uint64_t t2[4], x2[4], f2[4];
         {
-          uint32_t d[3][8];
+          uint32_t d[kCols][8];
 #pragma unroll
-          for (int k = 0; k < 3; ++k) tmem_ld8(tmem + (uint32_t)(C::kSStride * buf + k * R), d[k]);
-          const uint4 f0 = lds128(rc_a), f1 = lds128(rc_a + 16);
-          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-          for (int r = 0; r < 8; ++r) sc[r] = __uint_as_float(d[0][r]) + __uint_as_float(d[1][r]) + __uint_as_float(d[2][r]);
-#pragma unroll
-          for (int k = 0; k < 3; ++k) tmem_ld8(tmem + (uint32_t)(C::kSStride * buf + (k + 3) * R), d[k]);
+          for (int k = 0; k < kCols; ++k) tmem_ld8(tmem + (uint32_t)(C::kSStride * buf + k * R), d[k]);
+          const uint4 f0 = lds128(rc_a), f1 = lds128(rc_a + 16), n0 = lds128(mn_a), n1 = lds128(mn_a + 16);
           asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
           tc_fence_before();
           if (lane == 0) mbar_arrive(&sempty[buf]);  // a later tile may overwrite them
-          const uint32_t fr[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+          f2[0] = pack2(f0.x, f0.y), f2[1] = pack2(f0.z, f0.w), f2[2] = pack2(f1.x, f1.y), f2[3] = pack2(f1.z, f1.w);
+          const uint64_t n2[4] = {pack2(n0.x, n0.y), pack2(n0.z, n0.w), pack2(n1.x, n1.y), pack2(n1.z, n1.w)};
 #pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            sc[r] += __uint_as_float(d[0][r]) + __uint_as_float(d[1][r]) + __uint_as_float(d[2][r]);
-            sc[r] *= __uint_as_float(fr[r]);
+          for (int r = 0; r < 4; ++r) {
+            t2[r] = add2(add2(pack2(d[0][2 * r], d[0][2 * r + 1]), pack2(d[1][2 * r], d[1][2 * r + 1])),
+                         pack2(d[2][2 * r], d[2][2 * r + 1]));
+            x2[r] = fma2(t2[r], f2[r], n2[r]);
           }
         }
+        float x[8];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) unpack2(x2[r], x[2 * r], x[2 * r + 1]);
+        unsigned hidden = 0;
         if (edge) {
 #pragma unroll
           for (int r = 0; r < 8; ++r)
-            if (j >= row_hi[qb * R + 8 * sub + r] || j < row_lo[qb * R + 8 * sub + r]) sc[r] = -INFINITY;
+            if (j >= row_hi[qb * R + 8 * sub + r] || j < row_lo[qb * R + 8 * sub + r]) {
+              hidden |= 1u << r;
+              x[r] = -INFINITY;
+            }
 #pragma unroll
           for (int slab = 0; slab < 2; ++slab)
 #pragma unroll
@@ -827,24 +880,26 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
             }
         }
         // ---- softmax of eight rows
-        const uint4 m0 = lds128(mm_a), m1 = lds128(mm_a + 16);
-        const uint32_t mr[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
-        float x[8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r) x[r] = sc[r] - __uint_as_float(mr[r]);
         float high = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
         const bool grew = __any_sync(0xffffffffu, high > kMax);
         if (grew) {  // move the references that a score has passed (or that are not set yet)
 #pragma unroll
           for (int r = 0; r < 8; ++r) {
-            const float top = warp_max(sc[r]), m = __uint_as_float(mr[r]);
-            const float n = top > m + kMax ? top - kHead : m;
-            const float f = exp2f(m - n);
-            l[r] *= f;
-            x[r] = sc[r] - n;
+            float t[2], f[2], l[2];
+            unpack2(t2[r >> 1], t[0], t[1]);
+            unpack2(f2[r >> 1], f[0], f[1]);
+            unpack2(l2[r >> 1], l[0], l[1]);
+            const float sc = hidden >> r & 1 ? -INFINITY : t[r & 1] * f[r & 1];
+            const float top = warp_max(sc), m = mm[r];
+            const float n = top > m + kMax ? top - kHead : m, scale = exp2f(m - n);
+            l[r & 1] *= scale;
+            l2[r >> 1] = pack2(__float_as_uint(l[0]), __float_as_uint(l[1]));
+            x[r] = sc - n;
+            __syncwarp();
             if (lane == 0) {
               mm[r] = n;
-              alphas[(pb_i * NB + sub) * 8 + r] = f;
+              mn[r] = -n;
+              alphas[(pb_i * NB + sub) * 8 + r] = scale;
             }
           }
         }
@@ -856,10 +911,10 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
           tiny = __any_sync(0xffffffffu, tiny);
         }
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          x[r] = exp2_approx(x[r]);
-          l[r] += x[r];
-        }
+        for (int r = 0; r < 8; ++r) x[r] = exp2_approx(x[r]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          l2[r] = add2(l2[r], pack2(__float_as_uint(x[2 * r]), __float_as_uint(x[2 * r + 1])));
         uint32_t pk[4];
         if (!tiny) {
 #pragma unroll
@@ -1035,7 +1090,9 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
       const Seg e = segs[qb];
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
-        float v = l[r];
+        float l0, l1;
+        unpack2(l2[r >> 1], l0, l1);
+        float v = r & 1 ? l1 : l0;
 #pragma unroll
         for (int x = 16; x; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
         if (lane == 0) set_l[set * R + 8 * sub + r] = v;
@@ -1104,30 +1161,31 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
         continue;
       }
       // A piece: into the workspace; the CTA that completes the item's count joins its pieces.  A CTA
-      // starts inside at most one item (its piece 0) and ends inside at most one other (piece 1).
-      const int c0 = owner(all_units, e.start, ctas), c1 = owner(all_units, e.start + e.tiles - 1, ctas);
-      const int tail0 = share(all_units, c0, ctas) < e.start ? 1 : 0;  // only the first CTA can end in the item
-      auto piece = [&](int k) { return pieces + (int64_t)(2 * k + (k == c0 ? tail0 : 0)) * C::kSlot; };
+      // starts inside at most one item (its piece 0) and ends inside at most one that it began (piece 1).
+      // (boundaries within kSnap of the item's ends have moved there)
+      const int c0 = owner(all_units, e.start + kSnap, ctas);
+      const int c1 = owner(all_units, e.start + min(e.tiles - 1, e.tiles + C::kItemCost - kSnap - 1), ctas);
+      auto piece = [&](int k) { return pieces + (int64_t)(2 * k + (k == c0)) * C::kSlot; };
       float* mine = piece(blockIdx.x);
       for (int x = threadIdx.x; x < X; x += kConsumers) __stcg(reinterpret_cast<float2*>(mine) + x, total(x));
       if (threadIdx.x < R) {
         __stcg(mine + 2 * X + threadIdx.x, join_m[threadIdx.x]);
         __stcg(mine + 2 * X + R + threadIdx.x, join_l[threadIdx.x]);
       }
-      __threadfence();
       named_sync<kConsumers>(1);
       if (threadIdx.x == 0) {
+        __threadfence();  // the barrier has ordered every thread's stores before it
         int* ctr = counters + ((int64_t)e.b * a.cache.kv_heads + e.h) * max_blocks + e.rb;
         const int n = atomicAdd(ctr, 1);
         *last_flag = n == c1 - c0;
         if (n == c1 - c0) *ctr = 0;  // ready for the next call
+        __threadfence();
       }
       named_sync<kConsumers>(1);
       if (!*last_flag) {
         release();
         continue;
       }
-      __threadfence();
       for (int r = warp; r < R; r += C::kWarps) {  // a warp a row, a lane a piece
         float m = -INFINITY, v = 0.f;
         for (int k = c0 + lane; k <= c1; k += 32) m = fmaxf(m, __ldcg(piece(k) + 2 * X + r));
