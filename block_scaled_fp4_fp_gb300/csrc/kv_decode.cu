@@ -74,7 +74,7 @@ constexpr int kTerms = 6;
 constexpr int kCols = 3;                 // score columns of a row
 constexpr int kChains = kTerms / kCols;  // terms added into each
 constexpr int kTile = 128;  // keys per tile: the MMA's M
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 12;
 constexpr float kLog2e = 1.4426950408889634f;
 // Boundaries between the CTAs' shares within this many units of an item's end are moved there: a piece costs
 // two CTAs and its join more than the tiles it moves.
@@ -112,25 +112,28 @@ struct Dec {
   static constexpr uint32_t kSfb = kSfa + 16 * kBufs;        // term scales, 4 columns a chain
   static constexpr uint32_t kTmemCols = 512;
   static_assert(kSfb + 4 * kChains <= kTmemCols && kN <= 128, "tensor memory");
-  // shared memory: [stages: K codes, V codes][queries x 2][K scales as tcgen05.cp reads them][outputs]
-  // [probabilities][stages: K scales, V scales][row data][barriers]
+  // shared memory: [K codes][V codes][queries x 2][K scales as tcgen05.cp reads them][outputs of half the sets]
+  // [probabilities][K scales][V scales][row data][barriers]
   static constexpr int kSets = kGroups * 4;                  // quadrants with their own m, l, output
   static constexpr uint32_t kSfaBytes = kWords * 512;
-  static constexpr uint32_t kOutBytes = kWarps * kPieces * 32 * 8;
+  static constexpr uint32_t kOutBytes = kWarps / 2 * kPieces * 32 * 8;
   static constexpr uint32_t kPBytes = kSets * kPBufs * NB * 512;
   // score factors, key ranges and output rows x 2, m and l of the sets, joined m and l, flags and factors of the
   // probability buffers, segments x 2
   static constexpr uint32_t kRowBytes =
-      2 * 3 * kR * 4 + 2 * kR * 8 + kSets * kR * 12 + 2 * kR * 4 + kSets * kPBufs * NB * (32 + 8) + 128;
+      2 * 3 * kR * 4 + 2 * kR * 8 + kSets * kR * 12 + 2 * kR * 4 + kSets * kPBufs * NB * (32 + 8) + 128;  // (a multiple of 8)
   static constexpr uint32_t kFixed =
-      2 * kQBytes + kBufs * kSfaBytes + kOutBytes + kPBytes + kRowBytes + 512 + 1024;
+      2 * kQBytes + kBufs * kSfaBytes + kOutBytes + kPBytes + kRowBytes + 1024 + 1024;
   static constexpr uint32_t kBudget = 226u * 1024u;
-  static constexpr int kStages0 = (int)((kBudget - kFixed) / (2 * kCodes + 2 * kScales));
-  static constexpr int kStages = kStages0 > kMaxStages ? kMaxStages : kStages0;
-  static constexpr uint32_t kSmem = kFixed + kStages * (2 * kCodes + 2 * kScales);
-  static_assert(kStages >= 2 && kSmem <= kBudget, "shared memory");
+  // Two rings: a K tile is read once its scores are issued, a V tile is held until its group is through
+  // with it, so of the tiles that fit V gets more.
+  static constexpr int kFit = (int)((kBudget - kFixed) / (kCodes + kScales));
+  static constexpr int kStK0 = (kFit - kGroups + 1) / 2, kStK = kStK0 > kMaxStages ? kMaxStages : kStK0;
+  static constexpr int kStV0 = kFit - kStK, kStV = kStV0 > kMaxStages ? kMaxStages : kStV0;
+  static constexpr uint32_t kSmem = kFixed + (kStK + kStV) * (kCodes + kScales);
+  static_assert(kStK >= 2 && kStV >= 2 && kSmem <= kBudget, "shared memory");
   // a group's parity wait on a stage must not be two phases ahead of it
-  static_assert(kStages >= kGroups, "the ring holds a tile of every group");
+  static_assert(kStV >= kGroups, "the V ring holds a tile of every group");
   // What an item costs a CTA besides its tiles, in tiles: starting on new queries, draining the groups, joining the
   // sets and writing the rows take about 4 us, a tile 0.4 to 1.8 us (measured).  Counted when the work is
   // dealt out, so that a CTA with many short requests does not finish last.
@@ -410,14 +413,14 @@ template <int MODE, int D, int NB>
 __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_kernel(
     const KvAttentionArgs a, int group, int max_blocks, int* __restrict__ counters, float* __restrict__ pieces, int inject_timeout) {
   using C = Dec<MODE, D, NB>;
-  constexpr int R = C::kR, ST = C::kStages, BUFS = C::kBufs, SETS = C::kSets;
+  constexpr int R = C::kR, SK = C::kStK, SV = C::kStV, BUFS = C::kBufs, SETS = C::kSets;
   constexpr int kThreads = C::kThreads, kConsumers = C::kConsumers;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw);
-  constexpr uint32_t offQ = ST * 2 * C::kCodes, offSfa = offQ + 2 * C::kQBytes, offOut = offSfa + BUFS * C::kSfaBytes,
-                     offP = offOut + C::kOutBytes, offS = offP + C::kPBytes, offRow = offS + ST * 2 * C::kScales,
+  constexpr uint32_t offV = SK * C::kCodes, offQ = offV + SV * C::kCodes, offSfa = offQ + 2 * C::kQBytes, offOut = offSfa + BUFS * C::kSfaBytes,
+                     offP = offOut + C::kOutBytes, offS = offP + C::kPBytes, offSv = offS + SK * C::kScales, offRow = offSv + SV * C::kScales,
                      offBar = (offRow + C::kRowBytes + 7) / 8 * 8;
   float* row_c = reinterpret_cast<float*>(smem + offRow);         // [2][R] score factor of a row
   int* row_lo = reinterpret_cast<int*>(row_c + 2 * R);            // [2][R] first key it sees
@@ -432,9 +435,11 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
   int* p_flags = reinterpret_cast<int*>(p_alpha + SETS * C::kPBufs * NB * 8);  // [SETS][kPBufs][NB][2]
   Seg* segs = reinterpret_cast<Seg*>(p_flags + SETS * C::kPBufs * NB * 2);     // [2]
   static_assert(sizeof(Seg) == 64 && (C::kRowBytes - 128) % 8 == 0 && offRow % 16 == 0, "segment records");
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + offBar);    // a tile has landed
-  uint64_t* empty = full + ST;                                    // and is done with
-  uint64_t* sfull = empty + ST;                                   // scores computed
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + offBar);   // a K tile has landed
+  uint64_t* kempty = kfull + SK;                                  // and is done with
+  uint64_t* vfull = kempty + SK;                                  // a V tile
+  uint64_t* vempty = vfull + SV;
+  uint64_t* sfull = vempty + SV;                                  // scores computed
   uint64_t* sempty = sfull + BUFS;                                // and read
   uint64_t* qfull = sempty + BUFS;                                   // query terms written
   uint64_t* qempty = qfull + 2;                                   // and done with
@@ -445,15 +450,19 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
   int* plan_at = reinterpret_cast<int*>(plan + 5);                // its first item: request, item, tile
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(plan_at + 3);
   int* last_flag = reinterpret_cast<int*>(tmem_slot + 1);
-  static_assert((2 * ST + 2 * BUFS + 4 + 3) * 8 + 5 * 8 + 12 + 8 <= 512, "barrier area");
+  static_assert((2 * SK + 2 * SV + 2 * BUFS + 4 + 3) * 8 + 5 * 8 + 12 + 8 <= 1024, "barrier area");
   __shared__ int64_t scan[kThreads / 32 + 1];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
-    for (int s = 0; s < ST; ++s) {
-      mbar_init(&full[s], 64);  // every lane of the two loading warps
-      mbar_init(&empty[s], 4 * NB);
+    for (int s = 0; s < SK; ++s) {
+      mbar_init(&kfull[s], 32);  // every lane of the loading warp
+      mbar_init(&kempty[s], 1);
+    }
+    for (int s = 0; s < SV; ++s) {
+      mbar_init(&vfull[s], 32);
+      mbar_init(&vempty[s], 4 * NB);
     }
     for (int s = 0; s < BUFS; ++s) {
       mbar_init(&sfull[s], 1);
@@ -560,6 +569,10 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
     // costs the same few dozen instructions whatever the page size.  (Bulk and tensor copies, whose
     // operands are uniform registers, took ~140 cycles each to issue, and a tile of 16-row pages is 32 of them.)
     const bool is_v = warp == C::kWarps + 1;
+    uint64_t* full = is_v ? vfull : kfull;
+    uint64_t* empty = is_v ? vempty : kempty;
+    const int stages = is_v ? SV : SK;
+    const uint32_t ring = base + (is_v ? offV : 0), scale_ring = base + (is_v ? offSv : offS);
     const uint8_t* codes = reinterpret_cast<const uint8_t*>(is_v ? a.cache.v_codes : a.cache.k_codes);
     const uint8_t* scales = is_v ? a.cache.v_scales : a.cache.k_scales;
     constexpr int CPR = C::kRowB / 16, RPI = 32 / CPR;  // chunks of a row, rows (512 bytes) of an instruction
@@ -600,7 +613,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
         }
         --left;
         if (round > 0) mbar_wait(&empty[s], (round - 1) & 1, a.err, failed);
-        const uint32_t dc = base + (2 * s + is_v) * C::kCodes, ds = base + offS + (2 * s + is_v) * C::kScales;
+        const uint32_t dc = ring + s * C::kCodes, ds = scale_ring + s * C::kScales;
         const int idx = first_pg - batch;  // the tile's first page in the batch
         auto pages = [&](auto ipp) {       // instructions of a page
           constexpr int IPP = decltype(ipp)::value, NP = kTile / RPI / IPP;
@@ -629,7 +642,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
         }
         // arrives when this lane's copies have landed
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(&full[s])) : "memory");
-        if (++s == ST) { s = 0; ++round; }
+        if (++s == stages) { s = 0; ++round; }
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // no copy may still be writing shared memory when the CTA exits
@@ -678,9 +691,9 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
         const int buf = it % BUFS;
         // the scores of tile it - BUFS have been read, so its MMAs and scale copy are done
         if (it >= BUFS) mbar_wait(&sempty[buf], (it / BUFS - 1) & 1, a.err, failed);
-        mbar_wait(&full[s], round & 1, a.err, failed);
+        mbar_wait(&kfull[s], round & 1, a.err, failed);
         // lane n % 32, word n / 32: key n's scale word j, for every k-step group j
-        const uint8_t* lin = smem + offS + 2 * s * C::kScales;
+        const uint8_t* lin = smem + offS + s * C::kScales;
         uint32_t v[4][C::kWords];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -706,7 +719,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
 #pragma unroll
           for (int j = 0; j < C::kWords; ++j)
             tc_cp_sf(tmem + C::kSfa + 16 * buf + 4 * j, desc_sf(base + offSfa + buf * C::kSfaBytes + 512 * j));
-          const uint64_t ad = desc_k(base + 2 * s * C::kCodes, 8 * C::kRowB, layout);
+          const uint64_t ad = desc_k(base + s * C::kCodes, 8 * C::kRowB, layout);
           const uint64_t bd = desc_k(base + offQ + qb * C::kQBytes, 8 * C::kRowB, layout);
 #pragma unroll
           for (int ch = 0; ch < kChains; ++ch)
@@ -719,10 +732,11 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
                             tmem + C::kSfb + 4 * ch, ch > 0 || ks > 0);
             }
           tc_commit(&sfull[buf]);
+          tc_commit(&kempty[s]);
           if (i + 1 == n) tc_commit(&qempty[qb]);
         }
         __syncwarp();
-        if (++s == ST) { s = 0; ++round; }
+        if (++s == SK) { s = 0; ++round; }
       }
     }
   } else if (warp == C::kWarps + 3) {
@@ -819,17 +833,17 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
       int o = (grp + C::kGroups - it % C::kGroups) % C::kGroups;  // this group's first tile of the segment
       s += o;
       for (; o < n_tiles; o += C::kGroups, s += C::kGroups) {
-        while (s >= ST) { s -= ST; ++round; }
+        while (s >= SV) { s -= SV; ++round; }
         const int j0 = key0 + o * kTile;
         // masks only in tiles that hold an end of some row's keys
         const bool edge = j0 < lo_max || j0 + kTile > hi_min;
         const int j = j0 + 32 * quad + lane;  // this lane's key
         const int buf = (it + o) % BUFS, pb_i = C::kPBufs == 1 ? 0 : use & 1;
-        mbar_wait(&full[s], round & 1, a.err, failed);
-        const uint32_t codes = base + (2 * s + 1) * C::kCodes;
+        mbar_wait(&vfull[s], round & 1, a.err, failed);
+        const uint32_t codes = base + offV + s * C::kCodes;
         uint32_t vs[2][4];  // V scale bytes of the thread's eight keys (two each where SPT == 2)
         {
-          const uint32_t sa = base + offS + (2 * s + 1) * C::kScales + vsc;
+          const uint32_t sa = base + offSv + s * C::kScales + vsc;
 #pragma unroll
           for (int slab = 0; slab < 2; ++slab)
 #pragma unroll
@@ -1079,11 +1093,11 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
           }
         }
         __syncwarp();  // every lane's loads of the stage (and of the probabilities) are done
-        if (lane == 0) mbar_arrive(&empty[s]);
+        if (lane == 0) mbar_arrive(&vempty[s]);
         ++use;
       }
       s -= o - n_tiles;  // where the segment's last tile leaves the ring
-      while (s < 0) { s += ST; --round; }
+      while (s < 0) { s += SV; --round; }
       it += n_tiles;
 
       // ---- the segment's end: join the sets
@@ -1109,7 +1123,8 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
         join_m[threadIdx.x] = m;
         join_l[threadIdx.x] = v;
       }
-      float2* dump = reinterpret_cast<float2*>(smem + offOut) + warp * (C::kPieces * 32) + lane;
+      // outputs on the joint reference; the second half of the sets hands its own to the first (half the space)
+      float2* dump = reinterpret_cast<float2*>(smem + offOut) + ((set % (SETS / 2)) * NB + sub) * (C::kPieces * 32) + lane;
       const float ve = MODE == 1 ? exp2i_f32(vexp) : 1.0f;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
@@ -1121,21 +1136,34 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
           for (int k = 0; k < SETS; ++k) m = fmaxf(m, set_m[k * R + r]);
           const float f = exp2f(set_m[set * R + r] - m) * ve;
 #pragma unroll
-          for (int i = 0; i < CH / 2; ++i)
-            dump[((i * NB + nb) * 2 + h) * 32] = make_float2(acc[i][nb][h] * f, acc[i][nb][2 + h] * f);
+          for (int i = 0; i < CH / 2; ++i) {
+            acc[i][nb][h] *= f;
+            acc[i][nb][2 + h] *= f;
+            if (set >= SETS / 2) dump[((i * NB + nb) * 2 + h) * 32] = make_float2(acc[i][nb][h], acc[i][nb][2 + h]);
+          }
         }
+      named_sync<kConsumers>(1);
+      if (set < SETS / 2)
+#pragma unroll
+        for (int i = 0; i < CH / 2; ++i)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float2& u = dump[((i * NB + nb) * 2 + h) * 32];
+              u = make_float2(u.x + acc[i][nb][h], u.y + acc[i][nb][2 + h]);
+            }
       named_sync<kConsumers>(1);
       constexpr int X = NB * C::kPieces * 32;                          // float2 of the output
       constexpr int XN = (X + kConsumers - 1) / kConsumers;            // of a thread
       // element x: slice x / (32 kPieces), row 8 nb + 2 c + h, two channels
       auto row_of = [](int x) { return 8 * (((x >> 5) % C::kPieces >> 1) % NB) + 2 * (x & 3) + ((x >> 5) & 1); };
       auto total = [&](int x) {
-        const float2* src = reinterpret_cast<const float2*>(smem + offOut) +
-                            (x / (C::kPieces * 32)) * (4 * C::kPieces * 32) + x % (C::kPieces * 32);
+        const float2* src = reinterpret_cast<const float2*>(smem + offOut) + x;
         float2 v = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < SETS; ++k) {
-          const float2 u = src[((k >> 2) * NB * 4 + (k & 3)) * (C::kPieces * 32)];
+        for (int k = 0; k < SETS / 2; ++k) {
+          const float2 u = src[k * X];
           v.x += u.x;
           v.y += u.y;
         }
