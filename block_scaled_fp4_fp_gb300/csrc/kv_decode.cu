@@ -28,8 +28,10 @@
 // 512 bytes of shared memory and ldmatrix.trans, and the mma.sync sums stay in
 // registers.  (tcgen05 would want V as 16-bit shared-memory tiles: 512 bytes of
 // shared memory traffic a key more, which alone is as long as the key's DRAM time.)
-// With more than eight rows, NB warps share a quadrant: each owns eight rows'
-// softmax and 1 / NB of the channels, and reads the others' probabilities.
+// With up to sixteen rows (NB = 2) a warp takes both blocks of eight in turn and dequantizes V once for
+// them; more rows are more passes over the cache, the later ones out of L2.  (Four blocks a
+// pass, with a quadrant's softmax and channels split over four warps that meet in a barrier each
+// tile, was slower than two passes: 100 us against 72 for 16 requests x 4 tokens x 8 heads a group.)
 // Every quadrant of every group keeps its own running reference m, sum and output:
 // they meet only at the end of a (request, kv head).
 //
@@ -50,7 +52,7 @@
 // (m, l, o) in the workspace; the last CTA to arrive there joins the pieces in
 // order, so the result does not depend on who is last.
 //
-//   consumers   kGroups groups of 4 NB warps; group g takes the CTA's tiles i with i % kGroups == g
+//   consumers   kGroups groups of four warps; group g takes the CTA's tiles i with i % kGroups == g
 //   then one warp each:
 //   TMA         per tile and page K and V codes (boxes of page_size rows, swizzled by the
 //               row's length) and their scales (bulk copies)
@@ -96,15 +98,14 @@ struct Dec {
   static constexpr uint32_t kSwz = D == 64 ? 0x10 : D == 128 ? 0x30 : 0x70;
   static constexpr uint32_t kCodes = kTile * kRowB;
   static constexpr uint32_t kScales = kTile * kSB;
-  // consumer warps: as many as their output fragments (D / 4 registers a thread) leave registers for
-  static constexpr int kWarps = D <= 128 ? 16 : 8;
-  static constexpr int kGroups = kWarps / (4 * NB);
+  // consumer warps: as many as their output fragments (D NB / 4 registers a thread) leave registers for
+  static constexpr int kWarps = D * NB <= 128 ? 12 : 8;
+  static constexpr int kGroups = kWarps / 4;
   static constexpr int kBufs = kGroups < 2 ? 2 : kGroups;    // score buffers
   static constexpr int kConsumers = kWarps * 32;
   static constexpr int kThreads = kConsumers + 128;
-  static constexpr int kCh = D / NB / 8;                     // channels of a consumer thread
-  static constexpr int kPieces = D / 8;                      // float2 of its output
-  static constexpr int kPBufs = NB == 1 ? 1 : 2;             // probability buffers of a quadrant
+  static constexpr int kCh = D / 8;                     // channels of a consumer thread
+  static constexpr int kPieces = D * NB / 8;                 // float2 of its output
   static constexpr uint32_t kQChain = (kN * kRowB + 1023) / 1024 * 1024;
   static constexpr uint32_t kQBytes = kChains * kQChain;
   static constexpr int kSStride = (kN + 31) / 32 * 32;       // tensor-memory columns between score buffers
@@ -117,11 +118,11 @@ struct Dec {
   static constexpr int kSets = kGroups * 4;                  // quadrants with their own m, l, output
   static constexpr uint32_t kSfaBytes = kWords * 512;
   static constexpr uint32_t kOutBytes = kWarps / 2 * kPieces * 32 * 8;
-  static constexpr uint32_t kPBytes = kSets * kPBufs * NB * 512;
-  // score factors, key ranges and output rows x 2, m and l of the sets, joined m and l, flags and factors of the
-  // probability buffers, segments x 2
+  static constexpr uint32_t kPBytes = kSets * NB * 512;
+  // score factors, key ranges and output rows x 2, m, -m and l of the sets, joined m and l, factors of moved
+  // references, segments x 2
   static constexpr uint32_t kRowBytes =
-      2 * 3 * kR * 4 + 2 * kR * 8 + kSets * kR * 12 + 2 * kR * 4 + kSets * kPBufs * NB * (32 + 8) + 128;  // (a multiple of 8)
+      2 * 3 * kR * 4 + 2 * kR * 16 + kSets * kR * 12 + 2 * kR * 4 + kSets * kR * 4 + 128;  // (a multiple of 8)
   static constexpr uint32_t kFixed =
       2 * kQBytes + kBufs * kSfaBytes + kOutBytes + kPBytes + kRowBytes + 1024 + 1024;
   static constexpr uint32_t kBudget = 226u * 1024u;
@@ -137,7 +138,7 @@ struct Dec {
   // What an item costs a CTA besides its tiles, in tiles: starting on new queries, draining the groups, joining the
   // sets and writing the rows take about 4 us, a tile 0.4 to 1.8 us (measured).  Counted when the work is
   // dealt out, so that a CTA with many short requests does not finish last.
-  static constexpr int kItemCost = NB == 1 ? 8 : NB == 2 ? 5 : 3;
+  static constexpr int kItemCost = NB == 1 ? 8 : 5;
   static constexpr int kSlot = kR * D + 2 * kR;              // floats of a workspace piece (output, m, l)
 };
 
@@ -356,16 +357,15 @@ struct Seg {
 // Query rows r0 .. r0 + N - 1 of a segment as FP4 terms in the B operands' order (a warp): term t of row r is
 // row (t mod kCols) R + r of chain t / kCols.  Writes each row's score factor.
 template <int MODE, int D, int NB, int N>
-__device__ __forceinline__ void query_rows(const KvAttentionArgs& a, uint8_t* dst, const int64_t* row_out, float* row_c,
-                                           int r0, int group, int lane) {
+__device__ __forceinline__ void query_rows(const KvAttentionArgs& a, uint8_t* dst, const int64_t* row_q, float* row_c,
+                                           int r0, int lane) {
   using C = Dec<MODE, D, NB>;
   constexpr int EL = D / 32;  // elements of a lane
   uint32_t x[N][EL / 2];
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    const int64_t at = row_out[r0 + k];  // token * q_heads + head
-    const int64_t tok = at / a.q_heads;
-    const uint16_t* src = a.q + tok * a.q_token + (at - tok * a.q_heads) * a.q_head + lane * EL;
+    const int64_t at = row_q[r0 + k];
+    const uint16_t* src = a.q + at + lane * EL;
 #pragma unroll
     for (int e = 0; e < EL / 2; ++e) x[k][e] = at >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(src) + e) : 0u;
   }
@@ -426,14 +426,14 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
   int* row_lo = reinterpret_cast<int*>(row_c + 2 * R);            // [2][R] first key it sees
   int* row_hi = row_lo + 2 * R;                                   // [2][R] first key past those it sees
   int64_t* row_out = reinterpret_cast<int64_t*>(row_hi + 2 * R);  // [2][R] its place in out and lse, or -1
-  float* set_m = reinterpret_cast<float*>(row_out + 2 * R);       // [SETS][R] running references
+  int64_t* row_q = row_out + 2 * R;                               // [2][R] its place in q (elements), or -1
+  float* set_m = reinterpret_cast<float*>(row_q + 2 * R);         // [SETS][R] running references
   float* set_n = set_m + SETS * R;                                // [SETS][R] their negatives
   float* set_l = set_n + SETS * R;                                // [SETS][R] sums
   float* join_m = set_l + SETS * R;                               // [R]
   float* join_l = join_m + R;                                     // [R]
-  float* p_alpha = join_l + R;                                    // [SETS][kPBufs][NB][8] a moved reference's factors
-  int* p_flags = reinterpret_cast<int*>(p_alpha + SETS * C::kPBufs * NB * 8);  // [SETS][kPBufs][NB][2]
-  Seg* segs = reinterpret_cast<Seg*>(p_flags + SETS * C::kPBufs * NB * 2);     // [2]
+  float* set_f = join_l + R;                                      // [SETS][R] a moved reference's factors
+  Seg* segs = reinterpret_cast<Seg*>(set_f + SETS * R);           // [2]
   static_assert(sizeof(Seg) == 64 && (C::kRowBytes - 128) % 8 == 0 && offRow % 16 == 0, "segment records");
   uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + offBar);   // a K tile has landed
   uint64_t* kempty = kfull + SK;                                  // and is done with
@@ -462,11 +462,11 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
     }
     for (int s = 0; s < SV; ++s) {
       mbar_init(&vfull[s], 32);
-      mbar_init(&vempty[s], 4 * NB);
+      mbar_init(&vempty[s], 4);
     }
     for (int s = 0; s < BUFS; ++s) {
       mbar_init(&sfull[s], 1);
-      mbar_init(&sempty[s], 4 * NB);
+      mbar_init(&sempty[s], 4);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&qfull[s], 32 + C::kWarps);
@@ -764,7 +764,9 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
         if (lane < R) {
           row_hi[qb * R + lane] = hi;
           row_lo[qb * R + lane] = lo;
-          row_out[qb * R + lane] = real ? (int64_t)(w.r.q0 + i) * a.q_heads + w.h * group + (rr - i * group) : -1;
+          const int head = w.h * group + rr - i * group;
+          row_out[qb * R + lane] = real ? (int64_t)(w.r.q0 + i) * a.q_heads + head : -1;
+          row_q[qb * R + lane] = real ? (int64_t)(w.r.q0 + i) * a.q_token + (int64_t)head * a.q_head : -1;
         }
         const int hi_min = __reduce_min_sync(0xffffffffu, hi), lo_max = __reduce_max_sync(0xffffffffu, lo);
         if (lane == 0) segs[qb] = Seg{w.b, w.h, w.rb, w.ta, w.tb, w.r.q0, w.r.qlen, w.r.total, w.r.first, w.r.lo_tile,
@@ -775,7 +777,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
         mbar_arrive(sfirst);  // the consumers write the first segment's terms: it takes this warp several times as long
       } else {
 #pragma unroll 1
-        for (int r0 = 0; r0 < R; r0 += 4) query_rows<MODE, D, NB, 4>(a, smem + offQ + qb * C::kQBytes, row_out + qb * R, row_c + qb * R, r0, group, lane);
+        for (int r0 = 0; r0 < R; r0 += 4) query_rows<MODE, D, NB, 4>(a, smem + offQ + qb * C::kQBytes, row_q + qb * R, row_c + qb * R, r0, lane);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       if (seg > 0 && lane < C::kWarps) mbar_arrive(&qfull[qb]);  // in the consumers' place
@@ -783,51 +785,50 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
     }
   } else {
     // ----------------------------------------------------------- consumers
-    const int grp = warp / (4 * NB), sub = (warp >> 2) % NB, quad = warp & 3, set = grp * 4 + quad;
+    const int grp = warp >> 2, quad = warp & 3, set = warp;
     const int g = lane >> 2, c = lane & 3;
     mbar_wait(tbar, 0, a.err, failed);
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot + ((uint32_t)(32 * quad) << 16) + 8 * sub;
-    const uint32_t pbuf = base + offP + set * (C::kPBufs * NB * 512);
+    const uint32_t tmem = *tmem_slot + ((uint32_t)(32 * quad) << 16);
+    const uint32_t pbuf = base + offP + set * (NB * 512);
     const uint32_t pread =
         pbuf + (uint32_t)(((lane >> 4) * 16 + key_of<D>((lane & 7) >> 1, (lane & 1) + ((lane >> 3) & 1) * 2)) * 16);
-    float* mm = set_m + set * R + 8 * sub;
-    float* alphas = p_alpha + set * (C::kPBufs * NB * 8);
-    int* flags = p_flags + set * (C::kPBufs * NB * 2);
+    float* mm = set_m + set * R;
+    float* factors = set_f + set * R;
     const float gsv = (MODE == 2 && a.cache.gs_v) ? __ldg(a.cache.gs_v) : 1.0f;
     constexpr int CH = C::kCh, VB = CH / 2;                          // channels, code bytes of a thread's key
     constexpr int SPT = MODE == 2 && CH > 16 ? CH / 16 : 1;           // its scales
     // Where its keys' codes and scales lie in a stage.  Keys i of a slab differ by 128 bytes of codes (i & 1: the
     // bit the row swizzle folds onto bit 4) and by eight rows (i >> 1).
-    const uint32_t vc = (uint32_t)((32 * quad + key_of<D>(c, 0)) * C::kRowB + sub * (C::kRowB / NB) + g * VB);
+    const uint32_t vc = (uint32_t)((32 * quad + key_of<D>(c, 0)) * C::kRowB + g * VB);
     const uint32_t vc0 = vc ^ ((vc >> 3) & C::kSwz), vc1 = (vc0 + 128) ^ 16;
-    const uint32_t vsc = (uint32_t)((32 * quad + key_of<D>(c, 0)) * C::kSB + (sub * (D / NB) + g * CH) / C::kGroup);
+    const uint32_t vsc = (uint32_t)((32 * quad + key_of<D>(c, 0)) * C::kSB + g * CH / C::kGroup);
     constexpr int KSTEP = 128 / C::kRowB;  // keys between i = 0 and i = 1
-    float* mn = set_n + set * R + 8 * sub;
+    float* mn = set_n + set * R;
     const uint32_t mn_a = smem_u32(mn);
     // the first segment's query terms
     mbar_wait(sfirst, 0, a.err, failed);
 #pragma unroll 1
     for (int r = warp; r < R && !failed && segs[0].ta < segs[0].tb; r += C::kWarps)
-      query_rows<MODE, D, NB, 1>(a, smem + offQ, row_out, row_c, r, group, lane);
+      query_rows<MODE, D, NB, 1>(a, smem + offQ, row_q, row_c, r, lane);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if (lane == 0) mbar_arrive(&qfull[0]);
-    int s = 0, round = 0, it = 0, use = 0;
+    int s = 0, round = 0, it = 0;
     for (int seg = 0;; ++seg) {
       const int qb = seg & 1;
       mbar_wait(&qfull[qb], (seg >> 1) & 1, a.err, failed);
       const int n_tiles = failed ? 0 : segs[qb].tb - segs[qb].ta;
       if (n_tiles <= 0) break;
       float acc[CH / 2][NB][4] = {};
-      uint64_t l2[4] = {};  // sums of rows (2 i, 2 i + 1)
+      uint64_t l2[NB][4] = {};  // sums of rows (8 nb + 2 i, + 1)
       int vexp = -127;  // MXFP4: V is held relative to 2^vexp
-      if (lane < 8) {
+      if (lane < R) {
         mm[lane] = kNone;
         mn[lane] = -kNone;
       }
       __syncwarp();
-      const uint32_t rc_a = smem_u32(row_c + qb * R + 8 * sub);
+      const uint32_t rc_a = smem_u32(row_c + qb * R);
       const int key0 = (segs[qb].lo_tile + segs[qb].ta) * kTile;
       const int lo_max = segs[qb].lo_max, hi_min = segs[qb].hi_min;
       int o = (grp + C::kGroups - it % C::kGroups) % C::kGroups;  // this group's first tile of the segment
@@ -838,7 +839,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
         // masks only in tiles that hold an end of some row's keys
         const bool edge = j0 < lo_max || j0 + kTile > hi_min;
         const int j = j0 + 32 * quad + lane;  // this lane's key
-        const int buf = (it + o) % BUFS, pb_i = C::kPBufs == 1 ? 0 : use & 1;
+        const int buf = (it + o) % BUFS;
         mbar_wait(&vfull[s], round & 1, a.err, failed);
         const uint32_t codes = base + offV + s * C::kCodes;
         uint32_t vs[2][4];  // V scale bytes of the thread's eight keys (two each where SPT == 2)
@@ -854,36 +855,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
         }
         mbar_wait(&sfull[buf], ((it + o) / BUFS) & 1, a.err, failed);
         tc_fence_after();
-        // ---- scores of this lane's key, two rows a register pair
-        uint64_t t2[4], x2[4], f2[4];
-        {
-          uint32_t d[kCols][8];
-#pragma unroll
-          for (int k = 0; k < kCols; ++k) tmem_ld8(tmem + (uint32_t)(C::kSStride * buf + k * R), d[k]);
-          const uint4 f0 = lds128(rc_a), f1 = lds128(rc_a + 16), n0 = lds128(mn_a), n1 = lds128(mn_a + 16);
-          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-          tc_fence_before();
-          if (lane == 0) mbar_arrive(&sempty[buf]);  // a later tile may overwrite them
-          f2[0] = pack2(f0.x, f0.y), f2[1] = pack2(f0.z, f0.w), f2[2] = pack2(f1.x, f1.y), f2[3] = pack2(f1.z, f1.w);
-          const uint64_t n2[4] = {pack2(n0.x, n0.y), pack2(n0.z, n0.w), pack2(n1.x, n1.y), pack2(n1.z, n1.w)};
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            t2[r] = add2(add2(pack2(d[0][2 * r], d[0][2 * r + 1]), pack2(d[1][2 * r], d[1][2 * r + 1])),
-                         pack2(d[2][2 * r], d[2][2 * r + 1]));
-            x2[r] = fma2(t2[r], f2[r], n2[r]);
-          }
-        }
-        float x[8];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) unpack2(x2[r], x[2 * r], x[2 * r + 1]);
-        unsigned hidden = 0;
         if (edge) {
-#pragma unroll
-          for (int r = 0; r < 8; ++r)
-            if (j >= row_hi[qb * R + 8 * sub + r] || j < row_lo[qb * R + 8 * sub + r]) {
-              hidden |= 1u << r;
-              x[r] = -INFINITY;
-            }
 #pragma unroll
           for (int slab = 0; slab < 2; ++slab)
 #pragma unroll
@@ -893,70 +865,67 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
               if (key >= segs[qb].total || key < segs[qb].first) vs[slab][i] = MODE == 2 ? 0 : (uint32_t)(vexp + 127);
             }
         }
-        // ---- softmax of eight rows
-        float high = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-        const bool grew = __any_sync(0xffffffffu, high > kMax);
-        if (grew) {  // move the references that a score has passed (or that are not set yet)
-#pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            float t[2], f[2], l[2];
-            unpack2(t2[r >> 1], t[0], t[1]);
-            unpack2(f2[r >> 1], f[0], f[1]);
-            unpack2(l2[r >> 1], l[0], l[1]);
-            const float sc = hidden >> r & 1 ? -INFINITY : t[r & 1] * f[r & 1];
-            const float top = warp_max(sc), m = mm[r];
-            const float n = top > m + kMax ? top - kHead : m, scale = exp2f(m - n);
-            l[r & 1] *= scale;
-            l2[r >> 1] = pack2(__float_as_uint(l[0]), __float_as_uint(l[1]));
-            x[r] = sc - n;
-            __syncwarp();
-            if (lane == 0) {
-              mm[r] = n;
-              mn[r] = -n;
-              alphas[(pb_i * NB + sub) * 8 + r] = scale;
-            }
-          }
-        }
-        const float low = fminf(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), fminf(fminf(x[4], x[5]), fminf(x[6], x[7])));
-        bool tiny = false;  // probabilities outside f16's range in this tile
-        if (__any_sync(0xffffffffu, low < -kTiny)) {
-#pragma unroll
-          for (int r = 0; r < 8; ++r) tiny |= x[r] < -kTiny && x[r] > -126.0f;
-          tiny = __any_sync(0xffffffffu, tiny);
-        }
-#pragma unroll
-        for (int r = 0; r < 8; ++r) x[r] = exp2_approx(x[r]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          l2[r] = add2(l2[r], pack2(__float_as_uint(x[2 * r]), __float_as_uint(x[2 * r + 1])));
-        uint32_t pk[4];
-        if (!tiny) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) pk[r] = pack_f16x2(x[2 * r], x[2 * r + 1]);
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) pk[r] = pack_bf16x2_rn(x[2 * r] * 256.0f, x[2 * r + 1] * 256.0f);
-        }
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
-                     :: "r"(pbuf + (pb_i * NB + sub) * 512 + lane * 16), "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3])
-                     : "memory");
-        if (NB > 1 && lane == 0)
-          *reinterpret_cast<int2*>(flags + (pb_i * NB + sub) * 2) = make_int2(grew, tiny);
-        if (NB == 1) __syncwarp();
-        else named_sync<NB * 32>(2 + set);
-        // ---- the quadrant's probabilities, as B fragments: keys 0-15 of the warp, keys 16-31
-        uint32_t pb[NB][4];
-        unsigned wide = 0;  // blocks in bf16
+        unsigned wide = 0;  // blocks of rows whose probabilities are bf16
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(pb[nb][0]), "=r"(pb[nb][1]), "=r"(pb[nb][2]), "=r"(pb[nb][3])
-                       : "r"(pread + (pb_i * NB + nb) * 512) : "memory");
-          int2 fl = make_int2(grew, tiny);
-          if (NB > 1) fl = *reinterpret_cast<const int2*>(flags + (pb_i * NB + nb) * 2);
-          wide |= fl.y ? 1u << nb : 0u;
-          if (fl.x) {  // (warp-uniform)
-            const float2 f = *reinterpret_cast<const float2*>(alphas + (pb_i * NB + nb) * 8 + 2 * c);
+          // ---- scores of this lane's key, two rows a register pair
+          uint64_t t2[4], x2[4], f2[4];
+          {
+            uint32_t d[kCols][8];
+#pragma unroll
+            for (int k = 0; k < kCols; ++k) tmem_ld8(tmem + (uint32_t)(C::kSStride * buf + k * R + 8 * nb), d[k]);
+            const uint4 f0 = lds128(rc_a + 32 * nb), f1 = lds128(rc_a + 32 * nb + 16);
+            const uint4 n0 = lds128(mn_a + 32 * nb), n1 = lds128(mn_a + 32 * nb + 16);
+            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+            if (nb == NB - 1) {
+              tc_fence_before();
+              if (lane == 0) mbar_arrive(&sempty[buf]);  // a later tile may overwrite them
+            }
+            f2[0] = pack2(f0.x, f0.y), f2[1] = pack2(f0.z, f0.w), f2[2] = pack2(f1.x, f1.y), f2[3] = pack2(f1.z, f1.w);
+            const uint64_t n2[4] = {pack2(n0.x, n0.y), pack2(n0.z, n0.w), pack2(n1.x, n1.y), pack2(n1.z, n1.w)};
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              t2[r] = add2(add2(pack2(d[0][2 * r], d[0][2 * r + 1]), pack2(d[1][2 * r], d[1][2 * r + 1])),
+                           pack2(d[2][2 * r], d[2][2 * r + 1]));
+              x2[r] = fma2(t2[r], f2[r], n2[r]);
+            }
+          }
+          float x[8];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) unpack2(x2[r], x[2 * r], x[2 * r + 1]);
+          unsigned hidden = 0;
+          if (edge) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+              if (j >= row_hi[qb * R + 8 * nb + r] || j < row_lo[qb * R + 8 * nb + r]) {
+                hidden |= 1u << r;
+                x[r] = -INFINITY;
+              }
+          }
+          // ---- softmax of eight rows
+          const float high = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+          if (__any_sync(0xffffffffu, high > kMax)) {  // move the references that a score has passed (or that are not set)
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+              float t[2], f[2], l[2];
+              unpack2(t2[r >> 1], t[0], t[1]);
+              unpack2(f2[r >> 1], f[0], f[1]);
+              unpack2(l2[nb][r >> 1], l[0], l[1]);
+              const float sc = hidden >> r & 1 ? -INFINITY : t[r & 1] * f[r & 1];
+              const float top = warp_max(sc), m = mm[8 * nb + r];
+              const float n = top > m + kMax ? top - kHead : m, scale = exp2f(m - n);
+              l[r & 1] *= scale;
+              l2[nb][r >> 1] = pack2(__float_as_uint(l[0]), __float_as_uint(l[1]));
+              x[r] = sc - n;
+              __syncwarp();
+              if (lane == 0) {
+                mm[8 * nb + r] = n;
+                mn[8 * nb + r] = -n;
+                factors[8 * nb + r] = scale;
+              }
+            }
+            __syncwarp();
+            const float2 f = *reinterpret_cast<const float2*>(factors + 8 * nb + 2 * c);
 #pragma unroll
             for (int i = 0; i < CH / 2; ++i) {
               acc[i][nb][0] *= f.x;
@@ -965,19 +934,60 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
               acc[i][nb][3] *= f.y;
             }
           }
+          const float low = fminf(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), fminf(fminf(x[4], x[5]), fminf(x[6], x[7])));
+          bool tiny = false;  // probabilities outside f16's range in this tile
+          if (__any_sync(0xffffffffu, low < -kTiny)) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) tiny |= x[r] < -kTiny && x[r] > -126.0f;
+            tiny = __any_sync(0xffffffffu, tiny);
+          }
+#pragma unroll
+          for (int r = 0; r < 8; ++r) x[r] = exp2_approx(x[r]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            l2[nb][r] = add2(l2[nb][r], pack2(__float_as_uint(x[2 * r]), __float_as_uint(x[2 * r + 1])));
+          uint32_t pk[4];
+          if (!tiny) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) pk[r] = pack_f16x2(x[2 * r], x[2 * r + 1]);
+          } else {
+            wide |= 1u << nb;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) pk[r] = pack_bf16x2_rn(x[2 * r] * 256.0f, x[2 * r + 1] * 256.0f);
+          }
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                       :: "r"(pbuf + nb * 512 + lane * 16), "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3]) : "memory");
         }
+        __syncwarp();
+        // ---- the probabilities as B fragments: keys 0-15 of the warp, keys 16-31
+        uint32_t pb[NB][4];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(pb[nb][0]), "=r"(pb[nb][1]), "=r"(pb[nb][2]), "=r"(pb[nb][3])
+                       : "r"(pread + nb * 512) : "memory");
+        uint32_t below[2][4];  // MXFP4: how far each key's scale lies below 2^vexp
         if (MODE == 1) {
-          int hi = 0, lo = 255;
+          uint32_t far = 0;  // (a scale above it wraps to a large distance)
+          auto distances = [&]() {
+            far = 0;
 #pragma unroll
-          for (int slab = 0; slab < 2; ++slab)
+            for (int slab = 0; slab < 2; ++slab)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              hi = max(hi, (int)vs[slab][i]);
-              lo = min(lo, (int)vs[slab][i]);
-            }
-          hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
-          hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, 2)) - 127;
-          if (__any_sync(0xffffffffu, hi > vexp)) {
+              for (int i = 0; i < 4; ++i) {
+                below[slab][i] = (uint32_t)(vexp + 127) - vs[slab][i];
+                far = max(far, below[slab][i]);
+              }
+          };
+          distances();
+          if (__any_sync(0xffffffffu, far > 20u)) {
+            int hi = 0;
+#pragma unroll
+            for (int slab = 0; slab < 2; ++slab)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) hi = max(hi, (int)vs[slab][i]);
+            hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
+            hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, 2)) - 127;
             const int n = max(hi, vexp);
             const float f = exp2f((float)max(vexp - n, -200));
             vexp = n;
@@ -987,42 +997,38 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
               for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) acc[i][nb][k] *= f;
-          }
-          if (__any_sync(0xffffffffu, lo - 127 - vexp < -20)) {  // V outside f16's range: everything in bf16
+            distances();
+            if (__any_sync(0xffffffffu, far > 20u)) {  // V outside f16's range: everything in bf16
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-              if (!(wide >> nb & 1))
+              for (int nb = 0; nb < NB; ++nb)
+                if (!(wide >> nb & 1))
 #pragma unroll
-                for (int k = 0; k < 4; ++k) pb[nb][k] = f16x2_to_bf16x2_256(pb[nb][k]);
-            wide = (1u << NB) - 1;
+                  for (int k = 0; k < 4; ++k) pb[nb][k] = f16x2_to_bf16x2_256(pb[nb][k]);
+              wide = (1u << NB) - 1;
+            }
           }
         }
         // ---- o += p V, sixteen keys at a time
 #pragma unroll
         for (int slab = 0; slab < 2; ++slab) {
-          uint32_t wd[4][(CH + 7) / 8];  // the four keys' codes of the thread's channels
+          uint32_t wd[4][CH / 8];  // the four keys' codes of the thread's channels
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t at = codes + (i & 1 ? vc1 : vc0) + (16 * slab + 8 * (i >> 1)) * C::kRowB;
-            if (VB == 1) {
-              wd[i][0] = lds8(at);
-            } else if (VB == 2) {
-              wd[i][0] = lds16(at);
-            } else if (VB == 4) {
+            if (VB == 4) {
               wd[i][0] = lds32(at);
             } else if (VB == 8) {
               const uint2 v = lds64(at);
               wd[i][0] = v.x;
-              wd[i][1 % ((CH + 7) / 8)] = v.y;
+              wd[i][1 % (CH / 8)] = v.y;
             } else {
               const uint4 v = lds128(at);
               wd[i][0] = v.x;
-              wd[i][1 % ((CH + 7) / 8)] = v.y;
-              wd[i][2 % ((CH + 7) / 8)] = v.z;
-              wd[i][3 % ((CH + 7) / 8)] = v.w;
+              wd[i][1 % (CH / 8)] = v.y;
+              wd[i][2 % (CH / 8)] = v.z;
+              wd[i][3 % (CH / 8)] = v.w;
             }
           }
-          constexpr int PW = CH < 8 ? CH / 2 : 4;  // channel pairs of a word
           if (wide != (1u << NB) - 1) {
             uint32_t s2[SPT][2];  // scales of key pairs (0, 1) and (2, 3) as f16
 #pragma unroll
@@ -1035,12 +1041,12 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
                   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2[k][p]) : "h"(both));
                 } else {
                   // 2^(E - vexp) by its fp32 bits: E is within [-20, 0] of vexp here
-                  s2[k][p] = pack_f16x2(__uint_as_float(x0 * 0x800000u - (uint32_t)vexp * 0x800000u),
-                                        __uint_as_float(x1 * 0x800000u - (uint32_t)vexp * 0x800000u));
+                  s2[k][p] = pack_f16x2(__uint_as_float((127u - below[slab][2 * p]) << 23),
+                                        __uint_as_float((127u - below[slab][2 * p + 1]) << 23));
                 }
               }
 #pragma unroll
-            for (int q = 0; q < (CH + 7) / 8; ++q) {
+            for (int q = 0; q < CH / 8; ++q) {
               const int k = SPT == 2 ? q / 2 : 0;
               uint32_t ev[2][4], od[2][4];  // two keys' codes in a byte: even channels, odd channels
 #pragma unroll
@@ -1050,7 +1056,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
                 e2m1x8_to_f16(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), od[p]);
               }
 #pragma unroll
-              for (int i = 0; i < PW; ++i) {
+              for (int i = 0; i < 4; ++i) {
                 const uint32_t af[4] = {mul_f16x2(ev[0][i], s2[k][0]), mul_f16x2(od[0][i], s2[k][0]),
                                         mul_f16x2(ev[1][i], s2[k][1]), mul_f16x2(od[1][i], s2[k][1])};
 #pragma unroll
@@ -1073,12 +1079,12 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
                                             exp2i_f32(max((int)x1 - 9 - vexp, -126)));
               }
 #pragma unroll
-            for (int q = 0; q < (CH + 7) / 8; ++q) {
+            for (int q = 0; q < CH / 8; ++q) {
               const int k = SPT == 2 ? q / 2 : 0;
               const uint32_t n0[2] = {__byte_perm(wd[0][q], wd[1][q], 0x5410), __byte_perm(wd[0][q], wd[1][q], 0x7632)};
               const uint32_t n1[2] = {__byte_perm(wd[2][q], wd[3][q], 0x5410), __byte_perm(wd[2][q], wd[3][q], 0x7632)};
 #pragma unroll
-              for (int i = 0; i < PW; ++i) {
+              for (int i = 0; i < 4; ++i) {
                 const uint32_t x = n0[i >> 1], y = n1[i >> 1];
                 const uint32_t af[4] = {
                     mul_bf16x2(i & 1 ? e2m1_to_bf16<2>(x) : e2m1_to_bf16<0>(x), s2[k][0]),
@@ -1094,7 +1100,6 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
         }
         __syncwarp();  // every lane's loads of the stage (and of the probabilities) are done
         if (lane == 0) mbar_arrive(&vempty[s]);
-        ++use;
       }
       s -= o - n_tiles;  // where the segment's last tile leaves the ring
       while (s < 0) { s += SV; --round; }
@@ -1103,13 +1108,13 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
       // ---- the segment's end: join the sets
       const Seg e = segs[qb];
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
+      for (int r = 0; r < R; ++r) {
         float l0, l1;
-        unpack2(l2[r >> 1], l0, l1);
+        unpack2(l2[r >> 3][(r >> 1) & 3], l0, l1);
         float v = r & 1 ? l1 : l0;
 #pragma unroll
         for (int x = 16; x; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
-        if (lane == 0) set_l[set * R + 8 * sub + r] = v;
+        if (lane == 0) set_l[set * R + r] = v;
       }
       named_sync<kConsumers>(1);
       if (threadIdx.x < R) {
@@ -1124,7 +1129,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
         join_l[threadIdx.x] = v;
       }
       // outputs on the joint reference; the second half of the sets hands its own to the first (half the space)
-      float2* dump = reinterpret_cast<float2*>(smem + offOut) + ((set % (SETS / 2)) * NB + sub) * (C::kPieces * 32) + lane;
+      float2* dump = reinterpret_cast<float2*>(smem + offOut) + (set % (SETS / 2)) * (C::kPieces * 32) + lane;
       const float ve = MODE == 1 ? exp2i_f32(vexp) : 1.0f;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
@@ -1154,10 +1159,10 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
               u = make_float2(u.x + acc[i][nb][h], u.y + acc[i][nb][2 + h]);
             }
       named_sync<kConsumers>(1);
-      constexpr int X = NB * C::kPieces * 32;                          // float2 of the output
+      constexpr int X = C::kPieces * 32;                          // float2 of the output
       constexpr int XN = (X + kConsumers - 1) / kConsumers;            // of a thread
-      // element x: slice x / (32 kPieces), row 8 nb + 2 c + h, two channels
-      auto row_of = [](int x) { return 8 * (((x >> 5) % C::kPieces >> 1) % NB) + 2 * (x & 3) + ((x >> 5) & 1); };
+      // element x: row 8 nb + 2 c + h, channels kCh g + 2 i, + 1
+      auto row_of = [](int x) { return 8 * ((x >> 6) % NB) + 2 * (x & 3) + ((x >> 5) & 1); };
       auto total = [&](int x) {
         const float2* src = reinterpret_cast<const float2*>(smem + offOut) + x;
         float2 v = make_float2(0.f, 0.f);
@@ -1169,22 +1174,20 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
         }
         return v;
       };
-      auto store = [&](int x, float2 v) {
-        const int r = row_of(x), ln = x & 31, i = ((x >> 5) % C::kPieces >> 1) / NB;
-        const int ch = (x / (C::kPieces * 32)) * (D / NB) + CH * (ln >> 2) + 2 * i;
+      auto store = [&](int x, float2 v, float jm, float ls) {
+        const int r = row_of(x), ch = CH * ((x & 31) >> 2) + 2 * ((x >> 6) / NB);
         const int64_t at = row_out[qb * R + r];
         if (at < 0) return;
-        const float ls = join_l[r];
         const float inv = ls == 0.f ? 0.f : gsv / ls;
         *reinterpret_cast<uint32_t*>(a.out + at * D + ch) = pack_bf16x2_rn(v.x * inv, v.y * inv);
-        if (a.lse && ch == 0) a.lse[at] = ls == 0.f ? -INFINITY : (join_m[r] + log2f(ls)) * 0.6931471805599453f;
+        if (a.lse && ch == 0) a.lse[at] = ls == 0.f ? -INFINITY : (jm + log2f(ls)) * 0.6931471805599453f;
       };
       auto release = [&]() {  // the segment's query rows, key ranges and output rows are done with
         __syncwarp();
         if (lane == 0) mbar_arrive(&qempty[qb]);
       };
       if (e.ta == 0 && e.tb == e.tiles) {
-        for (int x = threadIdx.x; x < X; x += kConsumers) store(x, total(x));
+        for (int x = threadIdx.x; x < X; x += kConsumers) store(x, total(x), join_m[row_of(x)], join_l[row_of(x)]);
         release();
         continue;
       }
@@ -1214,49 +1217,64 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
         release();
         continue;
       }
-      for (int r = warp; r < R; r += C::kWarps) {  // a warp a row, a lane a piece
-        float m = -INFINITY, v = 0.f;
-        for (int k = c0 + lane; k <= c1; k += 32) m = fmaxf(m, __ldcg(piece(k) + 2 * X + r));
-        m = warp_max(m);
-        for (int k = c0 + lane; k <= c1; k += 32) {
-          const float pm = __ldcg(piece(k) + 2 * X + r), pl = __ldcg(piece(k) + 2 * X + R + r);
-          v += pl * exp2f(pm - m);
-        }
-#pragma unroll
-        for (int x = 16; x; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
-        if (lane == 0) {
-          join_m[r] = m;
-          join_l[r] = v;
-        }
-      }
-      named_sync<kConsumers>(1);
-      float* fac = reinterpret_cast<float*>(smem + offP);  // pieces' factors, a chunk at a time
-      constexpr int KC = C::kPBytes / 4 / R;
+      // Every piece's m and l into shared memory (a chunk of pieces at a time) while this thread's outputs of them
+      // are on their way; references only grow from chunk to chunk.
+      constexpr int KC = NB == 1 ? 32 : 16;
+      static_assert(3 * KC * R * 4 + R * 4 <= (int)C::kPBytes, "a chunk's m, l and factors fit the probabilities' space");
+      float* cm = reinterpret_cast<float*>(smem + offP);
+      float* cl = cm + KC * R;
+      float* cf = cl + KC * R;  // factors to the chunk's reference
+      float* cr = cf + KC * R;  // that reference
       float2 v[XN] = {};
+      float jm[XN], jl[XN];
+#pragma unroll
+      for (int i = 0; i < XN; ++i) jm[i] = kNone, jl[i] = 0.f;
       for (int k0 = c0; k0 <= c1; k0 += KC) {
         const int nk = min(KC, c1 + 1 - k0);
         for (int x = threadIdx.x; x < nk * R; x += kConsumers) {
-          fac[x] = exp2f(__ldcg(piece(k0 + x / R) + 2 * X + x % R) - join_m[x % R]);
+          const float* src = piece(k0 + x / R) + 2 * X + x % R;
+          cm[x] = __ldcg(src);
+          cl[x] = __ldcg(src + R);
         }
-        named_sync<kConsumers>(1);
 #pragma unroll
         for (int i = 0; i < XN; ++i) {
-          const int x = threadIdx.x + i * kConsumers;
-          if (x < X) {
-            const int r = row_of(x);
-#pragma unroll 8
-            for (int k = 0; k < nk; ++k) {
-              const float2 u = __ldcg(reinterpret_cast<const float2*>(piece(k0 + k)) + x);
-              v[i].x += u.x * fac[k * R + r];
-              v[i].y += u.y * fac[k * R + r];
+          const int x = min((int)threadIdx.x + i * kConsumers, X - 1);
+          float2 u[KC];
+#pragma unroll
+          for (int k = 0; k < KC; ++k) u[k] = __ldcg(reinterpret_cast<const float2*>(piece(k0 + min(k, nk - 1))) + x);
+          if (i == 0) {
+            named_sync<kConsumers>(1);
+            for (int y = threadIdx.x; y < nk * R; y += kConsumers) {
+              float m = kNone;
+              for (int k = 0; k < nk; ++k) m = fmaxf(m, cm[k * R + y % R]);
+              cf[y] = exp2f(cm[y] - m);
+              if (y < R) cr[y] = m;
             }
+            named_sync<kConsumers>(1);
           }
+          const int r = row_of(x);
+          const float m = fmaxf(jm[i], cr[r]), fo = exp2f(jm[i] - m), fn = exp2f(cr[r] - m);
+          float2 w = make_float2(0.f, 0.f);
+          float wl = 0.f;
+#pragma unroll
+          for (int k = 0; k < KC; ++k)
+            if (k < nk) {
+              const float g = cf[k * R + r];
+              w.x += u[k].x * g;
+              w.y += u[k].y * g;
+              wl += cl[k * R + r] * g;
+            }
+          v[i] = make_float2(v[i].x * fo + w.x * fn, v[i].y * fo + w.y * fn);
+          jl[i] = jl[i] * fo + wl * fn;
+          jm[i] = m;
         }
         named_sync<kConsumers>(1);
       }
 #pragma unroll
-      for (int i = 0; i < XN; ++i)
-        if ((int)threadIdx.x + i * kConsumers < X) store(threadIdx.x + i * kConsumers, v[i]);
+      for (int i = 0; i < XN; ++i) {
+        const int x = threadIdx.x + i * kConsumers;
+        if (x < X) store(x, v[i], jm[i], jl[i]);
+      }
       release();
     }
   }
@@ -1298,9 +1316,8 @@ cudaError_t launch(const DevInfo& d, const KvAttentionArgs& a, cudaStream_t s) {
 template <int MODE, int D>
 cudaError_t launch_rows(const DevInfo& d, const KvAttentionArgs& a, cudaStream_t s) {
   const int64_t rows = (int64_t)a.max_query_len * (a.q_heads / a.cache.kv_heads);
-  if (rows <= 8) return launch<MODE, D, 1>(d, a, s);
-  if (rows <= 16 || D == 256) return launch<MODE, D, 2>(d, a, s);
-  return launch<MODE, D, D == 256 ? 2 : 4>(d, a, s);
+  if (rows <= 8 || D == 256) return launch<MODE, D, 1>(d, a, s);
+  return launch<MODE, D, D == 256 ? 1 : 2>(d, a, s);
 }
 
 }  // namespace
@@ -1313,7 +1330,7 @@ size_t kv_decode_counter_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads,
 
 // Two pieces a CTA, sized for the most rows of a launch with this many.
 size_t kv_decode_ws_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_query_len) {
-  const int64_t rows = max_query_len * (q_heads / kv_heads), R = rows <= 8 ? 8 : rows <= 16 || head_dim == 256 ? 16 : 32;
+  const int64_t rows = max_query_len * (q_heads / kv_heads), R = rows <= 8 || head_dim == 256 ? 8 : 16;
   return kv_decode_counter_bytes(batch, q_heads, kv_heads, max_query_len) +
          (size_t)(2 * kKvDecodeCtas * (R * head_dim + 2 * R) * 4);
 }
