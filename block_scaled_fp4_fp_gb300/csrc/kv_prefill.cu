@@ -14,7 +14,7 @@
 // Scores, P and outputs stay in tensor memory (S: 2 x 128 columns, O: 2 x head_dim): while
 // one tile's softmax runs, the tensor cores work on the other tile.
 //
-// K and V are dequantized once per item and key by four warps into bf16 tiles
+// K and V are dequantized once per item and key by four warps each into bf16 tiles
 // (exact: e2m1 times an E4M3 or E8M0 scale has at most six significant bits): the codes
 // become f16 pairs by the hardware's converter, their exponents move to bf16's place with a
 // shift and two masks, and one multiply by the block scale (two for E8M0, whose range
@@ -29,10 +29,11 @@
 // keys are the most); a warp fetches the next item and its queries while the last one ends.
 //
 //   warps 0-7    softmax and output of tile warp / 4 (lane quadrant warp % 4)
-//   warps 8-11   K and V: codes loaded a tile ahead into registers, dequantized into a
-//                double-buffered tile each; thread t owns key t
-//   warp 12      MMA issue
-//   warps 13-15  items, query tiles
+//   warps 8-11   K: codes loaded a tile ahead into registers, dequantized into a
+//                double-buffered tile; thread t owns key t
+//   warps 12-15  V likewise
+//   warp 16      MMA issue
+//   warps 17-19  items, query tiles
 #include <algorithm>
 #include <cuda.h>
 
@@ -46,7 +47,7 @@ namespace {
 
 constexpr int kRows = 256;      // query rows of an item
 constexpr int kKeys = 128;      // keys of a tile
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr float kLazy = 64.0f;  // a score may pass the row's reference by this (log2) before it moves
 constexpr float kNone = -1e30f;
 
@@ -56,7 +57,7 @@ struct Pre {
   static constexpr uint32_t kKV = kKeys * D * 2;   // one K or V tile
   static constexpr uint32_t kHalf = 128 * 128;     // 64 elements of 128 rows
   static constexpr uint32_t offK = 2 * kQ, offV = offK + 2 * kKV, offBar = offV + 2 * kKV;
-  static constexpr uint32_t kSmem = offBar + 1024 + 5 * 1024;
+  static constexpr uint32_t kSmem = offBar + 1024 + 6 * 1024;
   static constexpr uint32_t kO = 256;              // output columns of tile 0; tile 1 follows
 };
 
@@ -95,22 +96,22 @@ __device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t (&v)[32]) {
 }
 #undef R8
 #define R8(v, o) "r"(v[o]), "r"(v[o + 1]), "r"(v[o + 2]), "r"(v[o + 3]), "r"(v[o + 4]), "r"(v[o + 5]), "r"(v[o + 6]), "r"(v[o + 7])
+__device__ __forceinline__ void tmem_st8(uint32_t a, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               :: "r"(a), R8(v, 0) : "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
       :: "r"(a), R8(v, 0), R8(v, 8) : "memory");
 }
 #undef R8
-__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(a));
-}
 __device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  return pack2(__float_as_uint(lo), __float_as_uint(hi));
+}
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -177,14 +178,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
       mbar_init(&vfull[s], 128);
       mbar_init(&vempty[s], 1);
       mbar_init(&ifull[s], 1);
-      mbar_init(&iempty[s], 16);
+      mbar_init(&iempty[s], 20);
     }
     mbar_init(qfull, 96);
     mbar_init(qempty, 1);
     mbar_init(never, 1);
     fence_barrier_init();
   }
-  if (warp == 12) {
+  if (warp == 16) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                  :: "r"(smem_u32(tmem_slot)), "n"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -229,12 +230,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
   bool failed = false;
   const int page_size = a.cache.page_size, page_shift = 31 - __clz(page_size);
 
-  if (warp >= 13) {
+  if (warp >= 17) {
     // ------------------------------------------------------ items, queries
     const int64_t total_items = prefix[kThreads];
     for (int k = 0;; ++k) {
       Item* it = &items[k & 1];
-      if (warp == 13) {
+      if (warp == 17) {
         if (k >= 2) mbar_wait(&iempty[k & 1], ((k >> 1) - 1) & 1, a.err, failed);
         if (lane == 0) {
           Item x = {};
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
       if (x.stop || failed) break;
       if (k > 0) mbar_wait(qempty, (k - 1) & 1, a.err, failed);
       // 256 rows of D / 8 chunks; rows past the request's are zeros
-      for (int e = threadIdx.x - 13 * 32; e < kRows * (D / 8); e += 96) {
+      for (int e = threadIdx.x - 17 * 32; e < kRows * (D / 8); e += 96) {
         const int r = e / (D / 8), ch = e % (D / 8), rr = x.row0 + r;
         const int tok = rr / group;
         const bool ok = rr < x.rows;
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(qfull)) : "memory");
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == 12) {
+  } else if (warp == 16) {
     // ------------------------------------------------------------ MMA issue
     const uint32_t leader = elect_one_sync();
     if (leader && inject_timeout) {
@@ -369,7 +370,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------- K and V
-    const int t = threadIdx.x - 256;
+    const int t = threadIdx.x & 127;
+    const bool is_v = warp >= 12;
+    const uint32_t* codes = is_v ? a.cache.v_codes : a.cache.k_codes;
+    const uint8_t* scales = is_v ? a.cache.v_scales : a.cache.k_scales;
+    uint64_t* full = is_v ? vfull : kfull;
+    uint64_t* empty = is_v ? vempty : kempty;
+    const uint32_t tiles = base + (is_v ? C::offV : C::offK);
     constexpr int GR = MODE == 2 ? 16 : 32, SB = D / GR, W = D / 8;  // scale bytes, code words of a row
     int g = 0;
     for (int k = 0;; ++k) {
@@ -392,45 +399,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
         }
         return ((page * a.cache.kv_heads + x.h) << page_shift) + (key & (page_size - 1));
       };
-      uint4 kc[W / 4], vc[W / 4];
-      uint32_t ks[(SB + 3) / 4], vs[(SB + 3) / 4];
-      auto load = [&](const uint32_t* codes, const uint8_t* scales, int row, uint4 (&q)[W / 4], uint32_t (&s)[(SB + 3) / 4]) {
+      uint4 q[W / 4];
+      uint32_t sc[(SB + 3) / 4];
+      auto load = [&](int row) {
 #pragma unroll
         for (int i = 0; i < W / 4; ++i)
           q[i] = row >= 0 ? __ldg(reinterpret_cast<const uint4*>(codes + (int64_t)row * W) + i) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < (SB + 3) / 4; ++i)  // (a key no row sees: a scale of zero, or 2^-127, whatever is stored)
-          s[i] = row < 0 ? 0u
-                 : SB >= 4 ? __ldg(reinterpret_cast<const uint32_t*>(scales + (int64_t)row * SB) + i)
-                           : (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(scales + (int64_t)row * SB));
+          sc[i] = row < 0 ? 0u
+                  : SB >= 4 ? __ldg(reinterpret_cast<const uint32_t*>(scales + (int64_t)row * SB) + i)
+                            : (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(scales + (int64_t)row * SB));
       };
-      auto store = [&](uint32_t dst, const uint4 (&q)[W / 4], const uint32_t (&s)[(SB + 3) / 4]) {
-        const uint32_t r = dst + t * 128;
+      int next = row_of(1);
+      load(row_of(0));
+      for (int j = 0; j < n; ++j, ++g) {
+        if (g >= 2) mbar_wait(&empty[g & 1], ((g >> 1) - 1) & 1, a.err, failed);
+        const uint32_t r = tiles + (g & 1) * C::kKV + t * 128;
 #pragma unroll
         for (int i = 0; i < W; ++i) {  // word i: channels 8 i .. 8 i + 7
           const int sb = i * 8 / GR;
           const uint4 v = q[i / 4];
           const uint32_t w = (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
-          const uint4 o = dequant8<MODE>(w, scale_pair<MODE>((s[sb / 4] >> (8 * (sb & 3))) & 0xFFu));
+          const uint4 o = dequant8<MODE>(w, scale_pair<MODE>((sc[sb / 4] >> (8 * (sb & 3))) & 0xFFu));
           asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
                        :: "r"(r + (i >> 3) * C::kHalf + (((i & 7) ^ (t & 7)) << 4)), "r"(o.x), "r"(o.y), "r"(o.z), "r"(o.w)
                        : "memory");
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      };
-      int row = row_of(0), next = row_of(1);
-      load(a.cache.k_codes, a.cache.k_scales, row, kc, ks);
-      for (int j = 0; j < n; ++j, ++g) {
-        load(a.cache.v_codes, a.cache.v_scales, row, vc, vs);
-        if (g >= 2) mbar_wait(&kempty[g & 1], ((g >> 1) - 1) & 1, a.err, failed);
-        store(base + C::offK + (g & 1) * C::kKV, kc, ks);
-        mbar_arrive(&kfull[g & 1]);
-        row = next;
+        mbar_arrive(&full[g & 1]);
+        load(next);
         next = row_of(j + 2);
-        load(a.cache.k_codes, a.cache.k_scales, row, kc, ks);
-        if (g >= 2) mbar_wait(&vempty[g & 1], ((g >> 1) - 1) & 1, a.err, failed);
-        store(base + C::offV + (g & 1) * C::kKV, vc, vs);
-        mbar_arrive(&vfull[g & 1]);
       }
     }
   } else {
@@ -453,22 +452,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
       const int pos = x.total - x.qlen + tok;
       const int hi = real ? max(pos + 1, 0) : INT32_MAX;  // keys lo .. hi - 1 (rows past the request's are not used)
       const int lo = real && a.window > 0 ? max(pos + 1 - a.window, 0) : 0;
-      float m = kNone, l = 0.f;
+      float m = kNone;
+      uint64_t l2 = 0;  // the sum, in two halves
       const int n = x.n[i];
       for (int j = 0; j < n; ++j, ++use) {
         const int key0 = (x.j0 + j) * kKeys;
         const bool mask = __any_sync(0xffffffffu, key0 < lo || key0 + kKeys > hi);
         mbar_wait(&sfull[i], use & 1, a.err, failed);
         tc_fence_after();
-        uint32_t s[32];
-        auto hide = [&](int c) {  // scores of keys the row does not see
+        auto hide = [&](int c, uint32_t (&s)[32]) {  // scores of keys the row does not see
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             const int key = key0 + 32 * c + e;
             if (key >= hi || key < lo) s[e] = 0xFF800000u;
           }
         };
-        auto top = [&]() {
+        auto top = [&](const uint32_t (&s)[32]) {
           float v[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e)
@@ -478,63 +477,81 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
         if (j == 0) {
           float t = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tmem_ld32(ts + 32 * c, s);
+          for (int c = 0; c < 4; c += 2) {
+            uint32_t sa[32], sb[32];
+            tmem_ld32(ts + 32 * c, sa);
+            tmem_ld32(ts + 32 * c + 32, sb);
             ld_wait();
-            if (mask) hide(c);
-            t = fmaxf(t, top());
+            if (mask) hide(c, sa), hide(c + 1, sb);
+            t = fmaxf(t, fmaxf(top(sa), top(sb)));
           }
           m = fmaxf(t * cs, kNone);
         }
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld32(ts + 32 * c, s);
+        auto chunk = [&](int c) {  // thirty-two scores to probabilities
+          uint32_t v[32];
+          tmem_ld32(ts + 32 * c, v);
           ld_wait();
-          if (mask) hide(c);
-          const float t = top() * cs;
+          if (mask) hide(c, v);
+          uint32_t p[16];
+          uint64_t sum;
+          auto exps = [&]() {
+            const uint64_t c2 = pack2(cs, cs), m2 = pack2(-m, -m);
+            uint64_t s0 = 0, s1 = 0;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float p0, p1;
+              unpack2(fma2(pack2(v[2 * e], v[2 * e + 1]), c2, m2), p0, p1);
+              p0 = exp2_approx(p0);
+              p1 = exp2_approx(p1);
+              if (e & 1) s1 = add2(s1, pack2(p0, p1));
+              else s0 = add2(s0, pack2(p0, p1));
+              p[e] = pack_bf16x2_rn(p0, p1);
+            }
+            sum = add2(s0, s1);
+          };
+          exps();  // before the vote: nearly always it passes, and the exponentials need not wait for it
+          const float t = top(v) * cs;
           if (__any_sync(0xffffffffu, t > m + kLazy)) {
-            // move this row's reference: what it has summed so far is scaled down
+            // move this row's reference: what it has summed so far is scaled down, these probabilities start over
             const float nm = t > m + kLazy ? t : m, f = exp2f(m - nm);
             m = nm;
-            l *= f;
-            for (int cc = 0; cc < c; ++cc) {  // probabilities of this tile
-              uint32_t p[16];
-              tmem_ld16(ts + 16 * cc, p);
+            l2 = mul2(l2, pack2(f, f));
+            for (int cc = 0; cc < 2 * c; ++cc) {  // earlier ones of this tile
+              uint32_t o[8];
+              tmem_ld8(ts + 8 * cc, o);
               ld_wait();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) p[e] = pack_bf16x2_rn(bf16_lo(p[e]) * f, bf16_hi(p[e]) * f);
-              tmem_st16(ts + 16 * cc, p);
+              for (int e = 0; e < 8; ++e) o[e] = pack_bf16x2_rn(bf16_lo(o[e]) * f, bf16_hi(o[e]) * f);
+              tmem_st8(ts + 8 * cc, o);
             }
             if (j > 0)  // the output: no MMA is adding to it (this tile's scores were issued after the last that did)
-              for (int cc = 0; cc < D / 16; ++cc) {
-                uint32_t p[16];
-                tmem_ld16(to + 16 * cc, p);
+              for (int cc = 0; cc < D / 8; ++cc) {
+                uint32_t o[8];
+                tmem_ld8(to + 8 * cc, o);
                 ld_wait();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) p[e] = __float_as_uint(__uint_as_float(p[e]) * f);
-                tmem_st16(to + 16 * cc, p);
+                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st8(to + 8 * cc, o);
               }
             st_wait();
+            exps();
           }
-          uint32_t p[16];
-          float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float p0 = exp2_approx(fmaf(__uint_as_float(s[2 * e]), cs, -m));
-            const float p1 = exp2_approx(fmaf(__uint_as_float(s[2 * e + 1]), cs, -m));
-            l0 += p0;
-            l1 += p1;
-            p[e] = pack_bf16x2_rn(p0, p1);
-          }
-          l += l0 + l1;
+          l2 = add2(l2, sum);
           tmem_st16(ts + 16 * c, p);
-        }
+        };
+        chunk(0);
+        chunk(1);
+        chunk(2);
+        chunk(3);
         st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&pfull[i]);
       }
       // ---- output
+      float l, lh;
+      unpack2(l2, l, lh);
+      l += lh;
       const int64_t at = (int64_t)(x.q0 + tok) * a.q_heads + x.h * group + (rr - tok * group);
       const float inv = l == 0.f ? 0.f : gsv / l;
       if (n > 0) {
@@ -570,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 16) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "n"(512) : "memory");
   }
