@@ -33,7 +33,7 @@
 //                double-buffered tile; thread t owns key t
 //   warps 12-15  V likewise
 //   warp 16      MMA issue
-//   warps 17-19  items, query tiles
+//   warps 17-18  items, query tiles
 #include <algorithm>
 #include <cuda.h>
 
@@ -47,8 +47,9 @@ namespace {
 
 constexpr int kRows = 256;      // query rows of an item
 constexpr int kKeys = 128;      // keys of a tile
-constexpr int kThreads = 640;
-constexpr float kLazy = 64.0f;  // a score may pass the row's reference by this (log2) before it moves
+constexpr int kSorted = 64;     // requests of a call that are put in order
+constexpr int kThreads = 608;
+constexpr float kFar = 0x1p64f;  // a row's reference moves when probabilities sum to more than this
 constexpr float kNone = -1e30f;
 
 template <int D>
@@ -161,7 +162,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
   uint64_t* qempty = qfull + 1;                                     // and read
   uint64_t* ifull = qempty + 1;                                     // [2] item known
   uint64_t* iempty = ifull + 2;                                     // [2] and done with
-  uint64_t* never = iempty + 2;                                     // fault injection: nothing arrives here
+  uint64_t* inear = iempty + 2;                                     // the item in work nears its end
+  uint64_t* never = inear + 1;                                     // fault injection: nothing arrives here
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
   Item* items = reinterpret_cast<Item*>(smem + C::offBar + 512);   // [2]
   int64_t* prefix = reinterpret_cast<int64_t*>(smem + C::offBar + 1024);  // [kThreads + 1] items before a thread's requests
@@ -178,10 +180,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
       mbar_init(&vfull[s], 128);
       mbar_init(&vempty[s], 1);
       mbar_init(&ifull[s], 1);
-      mbar_init(&iempty[s], 20);
+      mbar_init(&iempty[s], kThreads / 32);
     }
-    mbar_init(qfull, 96);
+    mbar_init(qfull, 64);
     mbar_init(qempty, 1);
+    mbar_init(inear, 1);
     mbar_init(never, 1);
     fence_barrier_init();
   }
@@ -198,10 +201,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
     if (ql <= 0 || ql > a.max_query_len || q0 < 0 || (int64_t)q0 + ql > a.tokens) return 0;
     return (ql * group + kRows - 1) / kRows;
   };
+  // few requests: the longest first (what is left for the end is then short).  More: as they come.
+  int* order = reinterpret_cast<int*>(smem + C::offBar + 640);  // [kSorted]
+  const bool sorted = a.batch <= kSorted;
+  if (sorted && (int)threadIdx.x < a.batch) {
+    const int mine = __ldg(a.total_lens + threadIdx.x);
+    int rank = 0;
+    for (int b = 0; b < a.batch; ++b) {
+      const int other = __ldg(a.total_lens + b);
+      rank += other > mine || (other == mine && b < (int)threadIdx.x);
+    }
+    order[rank] = threadIdx.x;
+  }
+  __syncthreads();
+  auto request = [&](int b) { return sorted ? order[b] : b; };
   {
     int64_t sum = 0;
     for (int b = min(a.batch, (int)threadIdx.x * per); b < min(a.batch, ((int)threadIdx.x + 1) * per); ++b) {
-      sum += blocks_of(b);
+      sum += blocks_of(request(b));
       if (blockIdx.x == 0) {
         const int ql = __ldg(a.query_start + b + 1) - __ldg(a.query_start + b);
         if (ql < 0 || (ql > 0 && blocks_of(b) == 0) || __ldg(a.total_lens + b) > (int64_t)a.max_pages * a.cache.page_size)
@@ -237,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
       Item* it = &items[k & 1];
       if (warp == 17) {
         if (k >= 2) mbar_wait(&iempty[k & 1], ((k >> 1) - 1) & 1, a.err, failed);
+        if (k >= 1) mbar_wait(inear, (k - 1) & 1, a.err, failed);
         if (lane == 0) {
           Item x = {};
           const int64_t idx = failed ? total_items : (int64_t)atomicAdd(counters, 1);
@@ -254,11 +272,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
               if (prefix[mid] <= idx) lo = mid; else hi = mid;
             }
             int64_t off = idx - prefix[lo];
-            int b = lo * per, nb = blocks_of(b);
+            int b = lo * per, nb = blocks_of(request(b));
             while (off >= (int64_t)nb * a.cache.kv_heads) {
               off -= (int64_t)nb * a.cache.kv_heads;
-              nb = blocks_of(++b);
+              nb = blocks_of(request(++b));
             }
+            b = request(b);
             const int rb = nb - 1 - (int)(off / a.cache.kv_heads);  // longest rows first
             x.b = b;
             x.h = (int)(off % a.cache.kv_heads);
@@ -286,15 +305,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
       if (lane == 0) mbar_arrive(&iempty[k & 1]);
       if (x.stop || failed) break;
       if (k > 0) mbar_wait(qempty, (k - 1) & 1, a.err, failed);
-      // 256 rows of D / 8 chunks; rows past the request's are zeros
-      for (int e = threadIdx.x - 17 * 32; e < kRows * (D / 8); e += 96) {
-        const int r = e / (D / 8), ch = e % (D / 8), rr = x.row0 + r;
-        const int tok = rr / group;
-        const bool ok = rr < x.rows;
-        const uint16_t* src = a.q + (int64_t)(x.q0 + (ok ? tok : 0)) * a.q_token +
-                              (int64_t)(x.h * group + (ok ? rr - tok * group : 0)) * a.q_head + ch * 8;
+      // 256 rows of D / 8 pieces of 16 bytes, rows past the request's as zeros; a thread keeps its piece and steps through
+      // the rows, so that the division by the group is done once
+      constexpr int kPer = 64 / (D / 8);
+      const int t = threadIdx.x - 17 * 32, ch = t % (D / 8);
+      int r = t / (D / 8), head = (x.row0 + r) % group;
+      const uint16_t* src = a.q + (int64_t)(x.q0 + (x.row0 + r) / group) * a.q_token + (int64_t)(x.h * group + head) * a.q_head + ch * 8;
+      const int64_t step = (int64_t)(kPer / group) * a.q_token + (int64_t)(kPer % group) * a.q_head, wrap = a.q_token - group * a.q_head;
+#pragma unroll 4
+      for (; r < kRows; r += kPer) {
+        const bool ok = x.row0 + r < x.rows;
         const uint32_t dst = base + (r >> 7) * C::kQ + (ch >> 3) * C::kHalf + (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(ok ? src : a.q), "r"(ok ? 16 : 0) : "memory");
+        src += step;
+        head += kPer % group;
+        if (head >= group) head -= group, src += wrap;
       }
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(qfull)) : "memory");
     }
@@ -332,7 +357,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
         for (int ks = 0; ks < kKeys / 16; ++ks)
           mma_ts(tmem + C::kO + D * i, tmem + 128 * i + 8 * ks, vd + ks * (2048 >> 4), idesc_o, !first || ks > 0);
       };
-      if (n == 0 && leader) tc_commit(qempty);
+      if (n == 0 && leader) {
+        tc_commit(qempty);
+        mbar_arrive(inear);
+      }
       if (n > 0) {
         mbar_wait(&kfull[g & 1], (g >> 1) & 1, a.err, failed);
         tc_fence_after();
@@ -344,6 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
         }
       }
       for (int j = 0; j < n; ++j, ++g) {
+        if (leader && j == max(n - 4, 0)) mbar_arrive(inear);
         mbar_wait(&vfull[g & 1], (g >> 1) & 1, a.err, failed);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -487,34 +516,35 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
           }
           m = fmaxf(t * cs, kNone);
         }
-        auto chunk = [&](int c) {  // thirty-two scores to probabilities
-          uint32_t v[32];
-          tmem_ld32(ts + 32 * c, v);
-          ld_wait();
+        auto exps = [&](uint32_t (&v)[32], uint32_t (&p)[16]) -> uint64_t {
+          const uint64_t c2 = pack2(cs, cs), m2 = pack2(-m, -m);
+          uint64_t s0 = 0, s1 = 0;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float p0, p1;
+            unpack2(fma2(pack2(v[2 * e], v[2 * e + 1]), c2, m2), p0, p1);
+            p0 = exp2_approx(p0);
+            p1 = exp2_approx(p1);
+            if (e & 1) s1 = add2(s1, pack2(p0, p1));
+            else s0 = add2(s0, pack2(p0, p1));
+            p[e] = pack_bf16x2_rn(p0, p1);
+          }
+          return add2(s0, s1);
+        };
+        auto chunk = [&](int c, uint32_t (&v)[32]) {  // thirty-two scores to probabilities
           if (mask) hide(c, v);
           uint32_t p[16];
-          uint64_t sum;
-          auto exps = [&]() {
-            const uint64_t c2 = pack2(cs, cs), m2 = pack2(-m, -m);
-            uint64_t s0 = 0, s1 = 0;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float p0, p1;
-              unpack2(fma2(pack2(v[2 * e], v[2 * e + 1]), c2, m2), p0, p1);
-              p0 = exp2_approx(p0);
-              p1 = exp2_approx(p1);
-              if (e & 1) s1 = add2(s1, pack2(p0, p1));
-              else s0 = add2(s0, pack2(p0, p1));
-              p[e] = pack_bf16x2_rn(p0, p1);
-            }
-            sum = add2(s0, s1);
-          };
-          exps();  // before the vote: nearly always it passes, and the exponentials need not wait for it
-          const float t = top(v) * cs;
-          if (__any_sync(0xffffffffu, t > m + kLazy)) {
-            // move this row's reference: what it has summed so far is scaled down, these probabilities start over
-            const float nm = t > m + kLazy ? t : m, f = exp2f(m - nm);
-            m = nm;
+          uint64_t sum = exps(v, p);
+          float a0, a1;
+          unpack2(sum, a0, a1);
+          if (__any_sync(0xffffffffu, !(a0 + a1 <= kFar))) {
+            // a score is far above the row's reference: move it; what the row has so far is scaled down,
+            // these probabilities start over
+            tmem_ld32(ts + 32 * c, v);
+            ld_wait();
+            if (mask) hide(c, v);
+            const float t = a0 + a1 <= kFar ? m : fmaxf(top(v) * cs, m), f = exp2f(m - t);
+            m = t;
             l2 = mul2(l2, pack2(f, f));
             for (int cc = 0; cc < 2 * c; ++cc) {  // earlier ones of this tile
               uint32_t o[8];
@@ -534,15 +564,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
                 tmem_st8(to + 8 * cc, o);
               }
             st_wait();
-            exps();
+            sum = exps(v, p);
           }
           l2 = add2(l2, sum);
           tmem_st16(ts + 16 * c, p);
         };
-        chunk(0);
-        chunk(1);
-        chunk(2);
-        chunk(3);
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          tmem_ld32(ts + 32 * c, v);
+          ld_wait();
+          chunk(c, v);
+        }
         st_wait();
         tc_fence_before();
         __syncwarp();
