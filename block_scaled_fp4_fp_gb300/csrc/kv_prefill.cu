@@ -158,9 +158,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
   uint64_t* kempty = kfull + 2;                                     // [2] and read
   uint64_t* vfull = kempty + 2;                                     // [2]
   uint64_t* vempty = vfull + 2;                                     // [2]
-  uint64_t* qfull = vempty + 2;                                     // query tiles landed
-  uint64_t* qempty = qfull + 1;                                     // and read
-  uint64_t* ifull = qempty + 1;                                     // [2] item known
+  uint64_t* qfull = vempty + 2;                                     // [2] query tile landed
+  uint64_t* qempty = qfull + 2;                                     // [2] and read
+  uint64_t* ifull = qempty + 2;                                     // [2] item known
   uint64_t* iempty = ifull + 2;                                     // [2] and done with
   uint64_t* inear = iempty + 2;                                     // the item in work nears its end
   uint64_t* never = inear + 1;                                     // fault injection: nothing arrives here
@@ -175,6 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
       mbar_init(&sfull[s], 1);
       mbar_init(&pfull[s], 4);
       mbar_init(&ofull[s], 1);
+      mbar_init(&qfull[s], 64);
+      mbar_init(&qempty[s], 1);
       mbar_init(&kfull[s], 128);
       mbar_init(&kempty[s], 1);
       mbar_init(&vfull[s], 128);
@@ -182,8 +184,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
       mbar_init(&ifull[s], 1);
       mbar_init(&iempty[s], kThreads / 32);
     }
-    mbar_init(qfull, 64);
-    mbar_init(qempty, 1);
     mbar_init(inear, 1);
     mbar_init(never, 1);
     fence_barrier_init();
@@ -304,24 +304,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
       __syncwarp();
       if (lane == 0) mbar_arrive(&iempty[k & 1]);
       if (x.stop || failed) break;
-      if (k > 0) mbar_wait(qempty, (k - 1) & 1, a.err, failed);
       // 256 rows of D / 8 pieces of 16 bytes, rows past the request's as zeros; a thread keeps its piece and steps through
-      // the rows, so that the division by the group is done once
+      // the rows, so that the division by the group is done once.  Before the tiles are free: into L2.
       constexpr int kPer = 64 / (D / 8);
-      const int t = threadIdx.x - 17 * 32, ch = t % (D / 8);
-      int r = t / (D / 8), head = (x.row0 + r) % group;
-      const uint16_t* src = a.q + (int64_t)(x.q0 + (x.row0 + r) / group) * a.q_token + (int64_t)(x.h * group + head) * a.q_head + ch * 8;
+      const int t = threadIdx.x - 17 * 32, ch = t % (D / 8), r0 = t / (D / 8), head0 = (x.row0 + r0) % group;
+      const uint16_t* src0 = a.q + (int64_t)(x.q0 + (x.row0 + r0) / group) * a.q_token + (int64_t)(x.h * group + head0) * a.q_head + ch * 8;
       const int64_t step = (int64_t)(kPer / group) * a.q_token + (int64_t)(kPer % group) * a.q_head, wrap = a.q_token - group * a.q_head;
+      auto rows = [&](int to, int& r, int& head, const uint16_t*& src, auto each) {
 #pragma unroll 4
-      for (; r < kRows; r += kPer) {
-        const bool ok = x.row0 + r < x.rows;
-        const uint32_t dst = base + (r >> 7) * C::kQ + (ch >> 3) * C::kHalf + (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(ok ? src : a.q), "r"(ok ? 16 : 0) : "memory");
-        src += step;
-        head += kPer % group;
-        if (head >= group) head -= group, src += wrap;
+        for (; r < to; r += kPer) {
+          each(r, src, x.row0 + r < x.rows);
+          src += step;
+          head += kPer % group;
+          if (head >= group) head -= group, src += wrap;
+        }
+      };
+      int r = r0, head = head0;
+      const uint16_t* src = src0;
+      if (k > 0 && (ch & 7) == 0)
+        rows(kRows, r, head, src, [&](int, const uint16_t* p, bool ok) {
+          if (ok) asm volatile("prefetch.global.L2 [%0];" :: "l"(p));
+        });
+      r = r0, head = head0, src = src0;
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        if (k > 0) mbar_wait(&qempty[i], (k - 1) & 1, a.err, failed);
+        rows(128 * (i + 1), r, head, src, [&](int at, const uint16_t* p, bool ok) {
+          const uint32_t dst = base + i * C::kQ + (ch >> 3) * C::kHalf + (at & 127) * 128 + (((ch & 7) ^ (at & 7)) << 4);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(ok ? p : a.q), "r"(ok ? 16 : 0) : "memory");
+        });
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(&qfull[i])) : "memory");
       }
-      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(qfull)) : "memory");
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 16) {
@@ -341,8 +354,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
       if (lane == 0) mbar_arrive(&iempty[k & 1]);
       if (x.stop || failed) break;
       const int n = max(x.n[0], x.n[1]);
-      mbar_wait(qfull, k & 1, a.err, failed);
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the copied queries, for the tensor core
       auto scores = [&](int i, int kb) {
         const uint64_t qd = desc_k(base + i * C::kQ, 1024, 2), kd = desc_k(base + C::offK + kb * C::kKV, 1024, 2);
 #pragma unroll
@@ -357,20 +368,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
         for (int ks = 0; ks < kKeys / 16; ++ks)
           mma_ts(tmem + C::kO + D * i, tmem + 128 * i + 8 * ks, vd + ks * (2048 >> 4), idesc_o, !first || ks > 0);
       };
-      if (n == 0 && leader) {
-        tc_commit(qempty);
-        mbar_arrive(inear);
-      }
-      if (n > 0) {
-        mbar_wait(&kfull[g & 1], (g >> 1) & 1, a.err, failed);
+      if (n == 0 && leader) mbar_arrive(inear);
+      if (n > 0) mbar_wait(&kfull[g & 1], (g >> 1) & 1, a.err, failed);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        mbar_wait(&qfull[i], k & 1, a.err, failed);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the copied queries, for the tensor core
         tc_fence_after();
         if (leader) {
-          for (int i = 0; i < 2; ++i)
-            if (x.n[i] > 0) scores(i, g & 1);
-          tc_commit(&kempty[g & 1]);
-          if (n == 1) tc_commit(qempty);
+          if (x.n[i] > 0) scores(i, g & 1);
+          if (n <= 1) tc_commit(&qempty[i]);
         }
       }
+      if (n > 0 && leader) tc_commit(&kempty[g & 1]);
       for (int j = 0; j < n; ++j, ++g) {
         if (leader && j == max(n - 4, 0)) mbar_arrive(inear);
         mbar_wait(&vfull[g & 1], (g >> 1) & 1, a.err, failed);
@@ -389,11 +399,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
           if (i == 0 && j + 1 < n) mbar_wait(&kfull[(g + 1) & 1], ((g + 1) >> 1) & 1, a.err, failed);
           tc_fence_after();
           if (j + 1 < x.n[i] && leader) scores(i, (g + 1) & 1);
+          if (j + 2 == n && leader) tc_commit(&qempty[i]);
         }
-        if (j + 1 < n && leader) {
-          tc_commit(&kempty[(g + 1) & 1]);
-          if (j + 2 == n) tc_commit(qempty);
-        }
+        if (j + 1 < n && leader) tc_commit(&kempty[(g + 1) & 1]);
         __syncwarp();
       }
     }
