@@ -146,8 +146,12 @@ cudaError_t launch_any(const KvAttentionArgs& args, cudaStream_t s) {
 
 }  // namespace
 
-// Up to 32 query rows a kv head share the few-row kernel's one pass over the cache; more fill the tiles of the
-// many-row kernel.
+// Query rows of a kv head, up to which the few-row kernel runs: it passes over the cache once for every sixteen, the
+// many-row kernel fills a tile of 256 whatever they are.  8 kv heads of 128, 8,000 tokens a request, NVFP4, few-row and
+// many-row in us:  rows     4 requests   16 requests   64 requests
+//                  17..32     36    61    102   121     351   406
+//                  33..48     47    61    143   121     517   408
+//                  64         57    61    184   122     681   408
 constexpr int64_t kFewRows = 32;
 
 bool few_rows(int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_query_len) {
@@ -157,9 +161,11 @@ bool few_rows(int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_q
 
 size_t kv_attention_ws_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                              int64_t max_query_len) {
-  return few_rows(q_heads, kv_heads, head_dim, max_query_len)
-             ? kv_decode_ws_bytes(batch, q_heads, kv_heads, head_dim, max_query_len)
-             : 16;
+  if (few_rows(q_heads, kv_heads, head_dim, max_query_len))
+    return kv_decode_ws_bytes(batch, q_heads, kv_heads, head_dim, max_query_len);
+  if (kv_prefill_supported((int)head_dim))
+    return kv_prefill_ws_bytes(head_dim);
+  return 16;
 }
 
 cudaError_t launch_kv_attention(const DevInfo& d, const KvAttentionArgs& args, cudaStream_t s) {

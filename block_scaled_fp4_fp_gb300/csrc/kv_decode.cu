@@ -1262,6 +1262,11 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
   }
 }
 
+size_t kv_decode_piece_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_query_len) {
+  const int64_t rows = max_query_len * (q_heads / kv_heads), R = rows <= 8 || head_dim == 256 ? 8 : 16;
+  return (size_t)(2 * kKvDecodeCtas * (R * head_dim + 2 * R) * 4);
+}
+
 template <int MODE, int D, int NB>
 cudaError_t launch(const DevInfo& d, const KvAttentionArgs& a, cudaStream_t s) {
   using C = Dec<MODE, D, NB>;
@@ -1283,9 +1288,9 @@ cudaError_t launch(const DevInfo& d, const KvAttentionArgs& a, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
-  const size_t head = kv_decode_counter_bytes(a.batch, a.q_heads, a.cache.kv_heads, a.max_query_len);
+  const size_t pieces = kv_decode_piece_bytes(a.q_heads, a.cache.kv_heads, D, a.max_query_len);
   return cudaLaunchKernelEx(&cfg, kv_decode_kernel<MODE, D, NB>, a, group, max_blocks,
-                            reinterpret_cast<int*>(ws), reinterpret_cast<float*>(ws + head), a.inject_timeout);
+                            reinterpret_cast<int*>(ws + pieces), reinterpret_cast<float*>(ws), a.inject_timeout);
 }
 
 template <int MODE, int D>
@@ -1297,17 +1302,11 @@ cudaError_t launch_rows(const DevInfo& d, const KvAttentionArgs& a, cudaStream_t
 
 }  // namespace
 
-// One counter per (request, kv head, row block of at least 8 rows), zero between calls.
-size_t kv_decode_counter_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t max_query_len) {
-  const int64_t blocks = (max_query_len * (q_heads / kv_heads) + 7) / 8;
-  return (size_t)((batch * kv_heads * blocks * 4 + 255) / 256 * 256);
-}
-
-// Two pieces a CTA, sized for the most rows of a launch with this many.
+// The pieces, two a CTA, then one counter per (request, kv head, row block of at least 8 rows), zero between calls: a
+// workspace sized for a batch serves smaller ones too, whose counters are the first of its own.
 size_t kv_decode_ws_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_query_len) {
-  const int64_t rows = max_query_len * (q_heads / kv_heads), R = rows <= 8 || head_dim == 256 ? 8 : 16;
-  return kv_decode_counter_bytes(batch, q_heads, kv_heads, max_query_len) +
-         (size_t)(2 * kKvDecodeCtas * (R * head_dim + 2 * R) * 4);
+  const int64_t blocks = (max_query_len * (q_heads / kv_heads) + 7) / 8;
+  return kv_decode_piece_bytes(q_heads, kv_heads, head_dim, max_query_len) + (size_t)((batch * kv_heads * blocks * 4 + 255) / 256 * 256);
 }
 
 bool kv_decode_supported(int head_dim) { return head_dim == 64 || head_dim == 128 || head_dim == 256; }

@@ -21,12 +21,25 @@
 // needs it) restores the value.  256 rows an item halve that work a row.
 //
 // Softmax: a thread owns a row.  P is bf16 and so has fp32's range: the reference m_r is the
-// first tile's maximum and moves only when a score passes it by 2^64, so the scores are read
-// once (twice in the first tile) and the output is almost never rescaled; p is rounded
-// to bf16 (2^-9), everything else is fp32.
+// first tile's maximum and moves only when 32 probabilities sum to more than 2^64, so that
+// after the first tile the scores are read once, no maximum is taken of them and the output
+// is almost never rescaled.  p is rounded to bf16 (2^-9); scores, sums and output are fp32.
 //
-// Items are handed out by an atomic counter, the longest rows of a request first (their
-// keys are the most); a warp fetches the next item and its queries while the last one ends.
+// Work: up to 608 items are dealt out: their key tiles, with a fixed cost an item, form one
+// sequence, of which each CTA takes an equal share; a cut near an item's end moves to
+// it, and an item's pieces meet in the workspace, where the last warp to arrive joins its 32 rows'
+// in the pieces' order (the same bits each time).  More items are handed out whole by an atomic
+// counter, near the end of the one before.  The longest come first.
+//   32 query heads on 8, NVFP4: a chunk of 512 tokens over 16,000 takes 132 us dealt out (1030 TFLOP/s) and 196 in
+//   equal pieces handed out by the counter; 576 items (64 heads of 64 on 8, 4 chunks over 0..16k) 420 us either way.
+//
+// What bounds it: for heads of 128 the tensor cores.  Two tiles' four products take 2300 cycles
+// beside the other warps' traffic and a step about 3300, the rest being the ends of items and waits for a softmax
+// (2000 cycles a tile, of which the exponentials 512).  For heads of 64 the softmax: the products take 1750 of 2900.
+//   4096-token prompt, 40 heads of 128, NVFP4:      0.160 ms, 1075 TFLOP/s
+//   4 chunks over 0..16k, 64 heads of 64, MXFP4:    0.420 ms,  734 TFLOP/s
+// Tried and slower on the prompt: 64-key steps with two score buffers (200 us), scores fetched ahead (201), two warps a
+// row (162, and 406 on the chunks), more registers for the softmax by setmaxnreg (186).
 //
 //   warps 0-7    softmax and output of tile warp / 4 (lane quadrant warp % 4)
 //   warps 8-11   K: codes loaded a tile ahead into registers, dequantized into a
@@ -49,6 +62,11 @@ constexpr int kRows = 256;      // query rows of an item
 constexpr int kKeys = 128;      // keys of a tile
 constexpr int kSorted = 64;     // requests of a call that are put in order
 constexpr int kThreads = 608;
+constexpr int kDealt = kThreads;  // calls of up to this many items are dealt out in equal shares (a thread computes an item's length)
+constexpr int kCost = 3;          // what an item costs beside its key tiles, in tiles
+constexpr int kSnap = 8;         // a share's end moves to an item's end that is nearer than this
+constexpr int kShare = 2 * kSnap; // a CTA's share at least
+constexpr int kCtas = 160;        // CTAs of a launch at most (one an SM)
 constexpr float kFar = 0x1p64f;  // a row's reference moves when probabilities sum to more than this
 constexpr float kNone = -1e30f;
 
@@ -58,7 +76,7 @@ struct Pre {
   static constexpr uint32_t kKV = kKeys * D * 2;   // one K or V tile
   static constexpr uint32_t kHalf = 128 * 128;     // 64 elements of 128 rows
   static constexpr uint32_t offK = 2 * kQ, offV = offK + 2 * kKV, offBar = offV + 2 * kKV;
-  static constexpr uint32_t kSmem = offBar + 1024 + 6 * 1024;
+  static constexpr uint32_t offPre = offBar + 1024, offTiles = offPre + 8 * (kThreads + 1), kSmem = offTiles + 8 * (kThreads + 1);
   static constexpr uint32_t kO = 256;              // output columns of tile 0; tile 1 follows
 };
 
@@ -67,8 +85,15 @@ struct Item {
   int row0, rows;             // first row of the item in the request's (token, head) rows; rows of the request
   int j0;                     // first key tile
   int n[2];                   // key tiles of the two row tiles
-  int stop, pad;
+  int stop;
+  int piece, pieces, first;   // this piece of the item's keys, of how many; CTA of the first one
 };
+
+// Workspace: the two counters of the hand-out, arrivals of a split item's pieces (a warp of 32 rows each) -- zero between
+// calls -- and two pieces' results a CTA: outputs [tile][channel / 4][row][4], references and sums [tile][2][row].
+constexpr size_t kArrivals = 64, kResults = kArrivals + (size_t)kCtas * 8 * 4;
+template <int D>
+constexpr size_t kSlotFloats = 256 * (D + 2);
 
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -145,8 +170,11 @@ __device__ __forceinline__ uint32_t scale_pair(uint32_t byte) {
 
 template <int MODE, int D>
 __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttentionArgs a, int group,
-                                                                  int* __restrict__ counters, int inject_timeout) {
+                                                                  uint8_t* __restrict__ ws, int inject_timeout) {
   using C = Pre<D>;
+  int* counters = reinterpret_cast<int*>(ws);
+  int* arrivals = reinterpret_cast<int*>(ws + kArrivals);
+  float* results = reinterpret_cast<float*>(ws + kResults);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -166,7 +194,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
   uint64_t* never = inear + 1;                                     // fault injection: nothing arrives here
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
   Item* items = reinterpret_cast<Item*>(smem + C::offBar + 512);   // [2]
-  int64_t* prefix = reinterpret_cast<int64_t*>(smem + C::offBar + 1024);  // [kThreads + 1] items before a thread's requests
+  int64_t* prefix = reinterpret_cast<int64_t*>(smem + C::offPre);  // [kThreads + 1] items before a thread's requests
+  int64_t* cost_before = reinterpret_cast<int64_t*>(smem + C::offTiles);  // [kThreads + 1] cost of the items before an item
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -194,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // items before each thread's requests; requests outside the contract are reported by the first CTA
+  // Items before each thread's requests; requests outside the contract are reported by the first CTA.
   const int per = (a.batch + kThreads - 1) / kThreads;
   auto blocks_of = [&](int b) {
     const int q0 = __ldg(a.query_start + b), ql = __ldg(a.query_start + b + 1) - q0;
@@ -215,6 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
   }
   __syncthreads();
   auto request = [&](int b) { return sorted ? order[b] : b; };
+  __shared__ int64_t wsum[kThreads / 32];
   {
     int64_t sum = 0;
     for (int b = min(a.batch, (int)threadIdx.x * per); b < min(a.batch, ((int)threadIdx.x + 1) * per); ++b) {
@@ -232,7 +262,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
       const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += u;
     }
-    __shared__ int64_t wsum[kThreads / 32];
     if (lane == 31) wsum[warp] = incl;
     __syncthreads();
     int64_t before = 0;
@@ -240,16 +269,88 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
     prefix[threadIdx.x + 1] = before + incl;
     if (threadIdx.x == 0) prefix[0] = 0;
   }
+  const int page_size = a.cache.page_size, page_shift = 31 - __clz(page_size);
+  __syncthreads();
+  auto describe = [&](int64_t idx) {  // item idx, whole
+    Item x = {};
+    int lo = 0, hi = kThreads;  // the thread whose requests hold the item
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (prefix[mid] <= idx) lo = mid; else hi = mid;
+    }
+    int64_t off = idx - prefix[lo];
+    int r = lo * per, b = request(r), nb = blocks_of(b);
+    while (off >= (int64_t)nb * a.cache.kv_heads) {
+      off -= (int64_t)nb * a.cache.kv_heads;
+      b = request(++r);
+      nb = blocks_of(b);
+    }
+    const int rb = nb - 1 - (int)(off / a.cache.kv_heads);  // longest rows first
+    x.b = b;
+    x.h = (int)(off % a.cache.kv_heads);
+    x.q0 = __ldg(a.query_start + b);
+    x.qlen = __ldg(a.query_start + b + 1) - x.q0;
+    x.total = min(__ldg(a.total_lens + b), a.max_pages * page_size);
+    x.row0 = rb * kRows;
+    x.rows = x.qlen * group;
+    const int pos0 = x.total - x.qlen + x.row0 / group;  // of the first row
+    x.j0 = a.window > 0 ? max(pos0 + 1 - a.window, 0) / kKeys : 0;
+    for (int i = 0; i < 2; ++i) {
+      const int last = min(x.row0 + 128 * (i + 1), x.rows) - 1;  // the tile's last row
+      const int end = last >= x.row0 + 128 * i ? x.total - x.qlen + last / group + 1 : 0;  // keys it sees
+      x.n[i] = max((end + kKeys - 1) / kKeys - x.j0, 0);
+    }
+    x.pieces = 1;
+    return x;
+  };
+  // Few items: their key tiles in one sequence, an equal share of it each CTA.  More: whole items, handed out in turn.
+  const int64_t total_items = prefix[kThreads];
+  const bool dealt = total_items <= kDealt;
+  if (dealt) {
+    int len = 0;
+    if ((int)threadIdx.x < total_items) {
+      const Item x = describe(threadIdx.x);
+      len = kCost + max(x.n[0], x.n[1]);
+    }
+    int64_t incl = len;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) incl += wsum[w];
+    cost_before[threadIdx.x + 1] = incl;
+    if (threadIdx.x == 0) cost_before[0] = 0;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   bool failed = false;
-  const int page_size = a.cache.page_size, page_shift = 31 - __clz(page_size);
 
   if (warp >= 17) {
     // ------------------------------------------------------ items, queries
-    const int64_t total_items = prefix[kThreads];
+    const int64_t cost = dealt ? cost_before[total_items] : 0;
+    const int64_t shares = min((int64_t)gridDim.x, max(max(cost / kShare, total_items), (int64_t)1));
+    auto item_at = [&](int64_t unit) {  // the item that holds a unit of cost
+      int lo = 0, hi = (int)total_items;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cost_before[mid] <= unit) lo = mid; else hi = mid;
+      }
+      return lo;
+    };
+    auto start_of = [&](int64_t c) {  // of a CTA's share
+      const int64_t cut = min(c, shares) * cost / shares;
+      if (cut >= cost) return cost;
+      const int i = item_at(cut);
+      return cut - cost_before[i] < kSnap ? cost_before[i] : cost_before[i + 1] - cut < kSnap ? cost_before[i + 1] : cut;
+    };
+    auto owner_of = [&](int64_t unit) { return (int)(((unit + 1) * shares - 1) / cost); };  // the CTA that has it, before moves
+    int64_t pos = start_of(blockIdx.x);
+    const int64_t end = start_of((int64_t)blockIdx.x + 1);
     for (int k = 0;; ++k) {
       Item* it = &items[k & 1];
       if (warp == 17) {
@@ -257,41 +358,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
         if (k >= 1) mbar_wait(inear, (k - 1) & 1, a.err, failed);
         if (lane == 0) {
           Item x = {};
-          const int64_t idx = failed ? total_items : (int64_t)atomicAdd(counters, 1);
-          x.stop = idx >= total_items;
-          if (x.stop) {
-            // the last CTA to find the work gone leaves the counters ready for the next call
-            if (atomicAdd(counters + 1, 1) == (int)gridDim.x - 1) {
-              counters[0] = 0;
-              counters[1] = 0;
+          if (failed) {
+            x.stop = 1;
+          } else if (dealt) {
+            x.stop = pos >= end;
+            if (!x.stop) {
+              const int i = item_at(pos);
+              const int64_t at = cost_before[i], next = cost_before[i + 1], stop = min(next, end);
+              x = describe(i);
+              x.first = owner_of(min(at + kSnap, next) - 1);
+              x.piece = blockIdx.x - x.first;
+              x.pieces = owner_of(min(next - 1, max(at + kSnap - 1, next - kSnap))) - x.first + 1;
+              const int skip = max((int)(pos - at) - kCost, 0), len = (int)(stop - at) - kCost - skip;
+              x.j0 += skip;
+              for (int e = 0; e < 2; ++e) x.n[e] = min(max(x.n[e] - skip, 0), len);
+              pos = stop;
             }
           } else {
-            int lo = 0, hi = kThreads;  // the thread whose requests hold the item
-            while (hi - lo > 1) {
-              const int mid = (lo + hi) >> 1;
-              if (prefix[mid] <= idx) lo = mid; else hi = mid;
-            }
-            int64_t off = idx - prefix[lo];
-            int b = lo * per, nb = blocks_of(request(b));
-            while (off >= (int64_t)nb * a.cache.kv_heads) {
-              off -= (int64_t)nb * a.cache.kv_heads;
-              nb = blocks_of(request(++b));
-            }
-            b = request(b);
-            const int rb = nb - 1 - (int)(off / a.cache.kv_heads);  // longest rows first
-            x.b = b;
-            x.h = (int)(off % a.cache.kv_heads);
-            x.q0 = __ldg(a.query_start + b);
-            x.qlen = __ldg(a.query_start + b + 1) - x.q0;
-            x.total = min(__ldg(a.total_lens + b), a.max_pages * page_size);
-            x.row0 = rb * kRows;
-            x.rows = x.qlen * group;
-            const int pos0 = x.total - x.qlen + x.row0 / group;  // of the first row
-            x.j0 = a.window > 0 ? max(pos0 + 1 - a.window, 0) / kKeys : 0;
-            for (int i = 0; i < 2; ++i) {
-              const int last = min(x.row0 + 128 * (i + 1), x.rows) - 1;  // the tile's last row
-              const int end = last >= x.row0 + 128 * i ? x.total - x.qlen + last / group + 1 : 0;  // keys it sees
-              x.n[i] = max((end + kKeys - 1) / kKeys - x.j0, 0);
+            const int64_t idx = atomicAdd(counters, 1);
+            if (idx < total_items) {
+              x = describe(idx);
+            } else {
+              x.stop = 1;
+              // the last CTA to find the work gone leaves the counters ready for the next call
+              if (atomicAdd(counters + 1, 1) == (int)gridDim.x - 1) {
+                counters[0] = 0;
+                counters[1] = 0;
+              }
             }
           }
           *it = x;
@@ -304,8 +397,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
       __syncwarp();
       if (lane == 0) mbar_arrive(&iempty[k & 1]);
       if (x.stop || failed) break;
-      // 256 rows of D / 8 pieces of 16 bytes, rows past the request's as zeros; a thread keeps its piece and steps through
-      // the rows, so that the division by the group is done once.  Before the tiles are free: into L2.
+      // 256 rows of D / 8 times 16 bytes, rows past the request's as zeros; a thread keeps its place in a row and steps
+      // through the rows, so that the division by the group is done once.  Before the tiles are free: into L2.
       constexpr int kPer = 64 / (D / 8);
       const int t = threadIdx.x - 17 * 32, ch = t % (D / 8), r0 = t / (D / 8), head0 = (x.row0 + r0) % group;
       const uint16_t* src0 = a.q + (int64_t)(x.q0 + (x.row0 + r0) / group) * a.q_token + (int64_t)(x.h * group + head0) * a.q_head + ch * 8;
@@ -480,20 +573,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
     int use = 0, outs = 0;
     for (int k = 0;; ++k) {
       mbar_wait(&ifull[k & 1], (k >> 1) & 1, a.err, failed);
-      const Item x = items[k & 1];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&iempty[k & 1]);
+      const Item& x = items[k & 1];  // (read again at the item's end, which gives it back)
       if (x.stop || failed) break;
-      const int rr = x.row0 + 128 * i + row, tok = rr / group;
-      const bool real = rr < x.rows;
-      const int pos = x.total - x.qlen + tok;
-      const int hi = real ? max(pos + 1, 0) : INT32_MAX;  // keys lo .. hi - 1 (rows past the request's are not used)
-      const int lo = real && a.window > 0 ? max(pos + 1 - a.window, 0) : 0;
+      int hi = INT32_MAX, lo = 0;  // keys lo .. hi - 1, counted from the piece's first (rows past the request's are not used)
+      {
+        const int rr = x.row0 + 128 * i + row, pos = x.total - x.qlen + rr / group;
+        if (rr < x.rows) {
+          hi = max(pos + 1, 0) - x.j0 * kKeys;
+          lo = (a.window > 0 ? max(pos + 1 - a.window, 0) : 0) - x.j0 * kKeys;
+        }
+      }
       float m = kNone;
       uint64_t l2 = 0;  // the sum, in two halves
       const int n = x.n[i];
       for (int j = 0; j < n; ++j, ++use) {
-        const int key0 = (x.j0 + j) * kKeys;
+        const int key0 = j * kKeys;
         const bool mask = __any_sync(0xffffffffu, key0 < lo || key0 + kKeys > hi);
         mbar_wait(&sfull[i], use & 1, a.err, failed);
         tc_fence_after();
@@ -554,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
             const float t = a0 + a1 <= kFar ? m : fmaxf(top(v) * cs, m), f = exp2f(m - t);
             m = t;
             l2 = mul2(l2, pack2(f, f));
+            st_wait();  // (the earlier ones are in place before they are read back)
             for (int cc = 0; cc < 2 * c; ++cc) {  // earlier ones of this tile
               uint32_t o[8];
               tmem_ld8(ts + 8 * cc, o);
@@ -593,13 +688,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
       float l, lh;
       unpack2(l2, l, lh);
       l += lh;
+      const int rr = x.row0 + 128 * i + row, tok = rr / group;
+      const bool real = rr < x.rows;
       const int64_t at = (int64_t)(x.q0 + tok) * a.q_heads + x.h * group + (rr - tok * group);
-      const float inv = l == 0.f ? 0.f : gsv / l;
       if (n > 0) {
         mbar_wait(&ofull[i], outs & 1, a.err, failed);
         ++outs;
         tc_fence_after();
       }
+      auto sums = [&](int p) { return results + (size_t)(2 * (x.first + p) + (p == 0)) * kSlotFloats<D> + 256 * D + 256 * i + row; };
+      auto outputs = [&](int p, int c) {
+        return reinterpret_cast<float4*>(results + (size_t)(2 * (x.first + p) + (p == 0)) * kSlotFloats<D>) + (i * (D / 4) + 8 * c) * 128 + row;
+      };
+      const bool whole = x.pieces == 1;
+      const float inv = l == 0.f ? 0.f : gsv / l;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
@@ -610,7 +712,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0;
         }
-        if (real) {
+        if (!whole) {
+          uint4* dst = reinterpret_cast<uint4*>(outputs(x.piece, c));
+#pragma unroll
+          for (int e = 0; e < 8; ++e) __stcg(dst + 128 * e, make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+        } else if (real) {
           uint4* dst = reinterpret_cast<uint4*>(a.out + at * D + 32 * c);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -622,7 +728,61 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
           }
         }
       }
-      if (real && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      bool last = whole;
+      if (!whole) {  // the warp whose piece comes last joins the item's pieces of its rows, in their order
+        __stcg(sums(x.piece), m);
+        __stcg(sums(x.piece) + 128, l);
+        __threadfence();
+        __syncwarp();
+        int* arrived = arrivals + 8 * x.first + warp;
+        int before = 0;
+        if (lane == 0) before = atomicAdd(arrived, 1);
+        last = __shfl_sync(0xffffffffu, before, 0) == x.pieces - 1;
+        if (last) {
+          __threadfence();
+          if (lane == 0) *arrived = 0;
+          const int np = x.pieces;
+          m = kNone;
+#pragma unroll 4
+          for (int p = 0; p < np; ++p) m = fmaxf(m, __ldcg(sums(p)));
+          l = 0.f;
+#pragma unroll 4
+          for (int p = 0; p < np; ++p) l += __ldcg(sums(p) + 128) * exp2f(__ldcg(sums(p)) - m);
+          const float join = l == 0.f ? 0.f : gsv / l;
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            float o[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = 0.f;
+#pragma unroll 2
+            for (int p = 0; p < np; ++p) {
+              const float4* src = outputs(p, 0) + 512 * c;
+              const float w = exp2f(__ldcg(sums(p)) - m);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float4 v = __ldcg(src + 128 * e);
+                o[4 * e] += w * v.x;
+                o[4 * e + 1] += w * v.y;
+                o[4 * e + 2] += w * v.z;
+                o[4 * e + 3] += w * v.w;
+              }
+            }
+            if (real) {
+              uint4* dst = reinterpret_cast<uint4*>(a.out + at * D + 16 * c);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                uint32_t v[4];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) v[h] = pack_bf16x2_rn(o[8 * e + 2 * h] * join, o[8 * e + 2 * h + 1] * join);
+                dst[e] = make_uint4(v[0], v[1], v[2], v[3]);
+              }
+            }
+          }
+        }
+      }
+      if (last && real && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&iempty[k & 1]);
       tc_fence_before();
     }
   }
@@ -641,7 +801,7 @@ cudaError_t launch(const DevInfo& d, const KvAttentionArgs& a, cudaStream_t s) {
   const cudaError_t e = allow_smem(d, kv_prefill_kernel<MODE, D>, smem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)d.sm_count);
+  cfg.gridDim = dim3((unsigned)std::min(d.sm_count, kCtas));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
@@ -650,11 +810,13 @@ cudaError_t launch(const DevInfo& d, const KvAttentionArgs& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_prefill_kernel<MODE, D>, a, a.q_heads / a.cache.kv_heads, static_cast<int*>(a.ws),
-                            a.inject_timeout);
+  return cudaLaunchKernelEx(&cfg, kv_prefill_kernel<MODE, D>, a, a.q_heads / a.cache.kv_heads,
+                            static_cast<uint8_t*>(a.ws), a.inject_timeout);
 }
 
 }  // namespace
+
+size_t kv_prefill_ws_bytes(int64_t head_dim) { return kResults + (size_t)(2 * kCtas * 256 * (head_dim + 2) * 4); }
 
 bool kv_prefill_supported(int head_dim) { return head_dim == 64 || head_dim == 128; }
 

@@ -166,11 +166,11 @@ cudaError_t launch_kv_attention(const DevInfo& d, const KvAttentionArgs& args, c
 // kv_decode.cu: a few query rows a request, head_dim 64, 128 or 256
 constexpr int kKvDecodeCtas = 160;  // CTAs of a launch at most (one an SM)
 bool kv_decode_supported(int head_dim);
-size_t kv_decode_counter_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t max_query_len);
 size_t kv_decode_ws_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_query_len);
 cudaError_t launch_kv_decode(const DevInfo& d, const KvAttentionArgs& args, cudaStream_t s);
-// kv_prefill.cu: many query rows a request, head_dim 64 or 128 (workspace: two zeroed ints)
+// kv_prefill.cu: many query rows a request, head_dim 64 or 128
 bool kv_prefill_supported(int head_dim);
+size_t kv_prefill_ws_bytes(int64_t head_dim);
 cudaError_t launch_kv_prefill(const DevInfo& d, const KvAttentionArgs& args, cudaStream_t s);
 
 }  // namespace fp4

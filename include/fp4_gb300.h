@@ -449,6 +449,8 @@ size_t kv_attention_workspace_bytes(int64_t batch, int64_t q_heads, int64_t kv_h
  *                kv_attention_workspace_bytes(batch, q_heads, kv_heads, head_dim,
  *                max_query_len); zero-filled once when allocated, each call leaves it
  *                ready for the next.  Calls that overlap on the GPU must not share one.
+ *                A workspace serves calls with its q_heads, kv_heads, head_dim and
+ *                max_query_len and any batch up to the one it was sized for.
  *   out          bf16[tokens, q_heads, head_dim], 16-byte aligned
  *   lse          fp32[tokens, q_heads] or NULL: log of the sum of exp(score), with which
  *                results over disjoint keys can be merged
@@ -463,7 +465,8 @@ fp4_status kv_attention(const fp4_kv_cache* cache, const fp4_bf16* q, int64_t q_
                         fp4_bf16* out, float* lse, cudaStream_t stream);
 
 /* Test hook, off by default: when `enable` is nonzero the next launches of the
- * tensor-core kernels -- qqmm, qmv's NVFP4/MXFP4 path and gather_qmm -- make
+ * tensor-core kernels -- qqmm, qmv's NVFP4/MXFP4 path, gather_qmm and kv_attention
+ * (head_dim 64, 128 or 256) -- make
  * their MMA-issuing thread wait on a barrier nothing arrives at, with a 1 ms
  * limit, before doing their normal work.  The wait expires, the kernel records
  * FP4_ERR_TIMEOUT and still completes with a correct result; nothing faults or

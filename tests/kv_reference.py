@@ -138,7 +138,7 @@ class Problem:
                     out[t, hs] = p @ v[see] / l
                     lse[t, hs] = (m + np.log(l))[:, 0]
                     ds = 2.0 ** -16 * np.abs(qq).max(-1, keepdims=True) * k1 * scale
-                    bound[t, hs] = 2.0 ** -8 * np.abs(out[t, hs]) + ((1 + 2.0 ** -8) * np.exp(np.minimum(2 * ds, 700)) - 1) * (p @ np.abs(v[see]) / l)
+                    bound[t, hs] = 2.0 ** -8 * np.abs(out[t, hs]) + ((1 + 2.0 ** -8) * np.exp(np.minimum(2 * ds, 700)) - 1) * (p @ np.abs(v[see]) / l) + 2.0 ** -126
         return out, lse, bound
 
     def lse_bound(self, scale=None):

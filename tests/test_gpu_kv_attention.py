@@ -1,14 +1,14 @@
 """kv_attention against a 64-bit implementation over the decoded cache.
 
 Tolerance, element by element, with A = sum_j p_j |v_j| / sum_j p_j:
-    |out - exact| <= 2^-8 |exact| + ((1 + 2^-8) exp(2 ds) - 1) A
+    |out - exact| <= 2^-8 |exact| + ((1 + 2^-8) exp(2 ds) - 1) A + 2^-126
 The first term is the bf16 rounding of the result (2^-9) with room for the
 division; a kernel may hold p in as few as 8 significant bits (2^-9 of every
 p, and of their sum), which moves the result by at most 2^-8 A; and scores may be
 off by ds = 2^-16 max|q| max_j |k_j|_1 scale: the tensor-core form writes q as
 terms that leave 2^-17 of the row's largest element, and fp32 sums add less than as
 much again.  A shift of ds moves every p by a factor within exp(+-ds), the
-quotient by at most exp(2 ds)."""
+quotient by at most exp(2 ds).  Below 2^-126 bf16 has no normal numbers."""
 import numpy as np
 import pytest
 import torch
@@ -201,3 +201,60 @@ def test_contract_violations_on_the_device_are_reported(B):
         B.kv_attention(cache, t["q"], t["query_start"], t["total_lens"], t["block_table"], ws, max_query_len=mq)
         assert B.fp4_check_device_error() == B.FP4_ERR_INVALID_ARG, what
         assert B.fp4_check_device_error() == B.FP4_OK
+
+
+@pytest.mark.parametrize("mode,dim,kv,group", [(2, 128, 1, 4), (1, 64, 2, 4), (2, 64, 1, 9), (1, 128, 3, 1)])
+@pytest.mark.parametrize("window", [0, 3000])
+def test_chunks_over_long_contexts(B, mode, dim, kv, group, window):
+    """Few rows in all, many keys: a request's keys are split over CTAs and joined, beside requests too short for that."""
+    p = R.Problem(mode, dim, kv, group, 64, [6000, 0, 2500, 100], [40, 35, 3, 0], window=window, gs=mode == 2, seed=dim + kv)
+    first, ws = check(B, p)
+    again, _ = check(B, p, ws=ws)
+    assert torch.equal(first, again)
+
+
+@pytest.mark.parametrize("batch,kv", [(320, 2), (700, 1)])
+def test_many_short_chunks(B, batch, kv):
+    """More requests and heads than are dealt out in equal shares; more requests than a block has threads."""
+    cached, new = [(7 * b) % 150 for b in range(batch)], [(b % 6) if b % 50 else 6 for b in range(batch)]
+    p = R.Problem(1 + batch % 2, 64, kv, 8, 16, cached, new, seed=batch)
+    check(B, p)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_sharp_and_rising_scores_of_chunks(B, dim):
+    """The rising scores of the decode test, for the kernel of many rows: its reference has to move."""
+    p = R.Problem(2, dim, 1, 8, 64, [1500, 640], [9, 30], seed=3, q_std=12.0)
+    for b in range(2):
+        j = np.arange(p.total[b])
+        p.scales["k"][p.table[b, j // 64], 0, j % 64] = (0x20 + (24 * j // p.total[b]))[:, None].astype(np.uint8)
+    check(B, p)
+    check(B, p, scale=3.0)
+
+
+@pytest.mark.parametrize("new", [1, 12])
+def test_a_workspace_serves_smaller_batches(B, new):
+    full = R.Problem(2, 128, 2, 4, 64, [3000, 700, 10, 2000, 64], [new] * 5, seed=1)
+    _, ws = check(B, full)
+    for cached in ([4000], [5, 1000], [300, 2, 900]):
+        check(B, R.Problem(2, 128, 2, 4, 64, cached, [new] * len(cached), seed=len(cached)), ws=ws)
+        check(B, full, ws=ws)
+
+
+@pytest.mark.parametrize("new", [1, 12])
+@pytest.mark.parametrize("mode", [2, 1])
+def test_timeout_injection_reports_and_recovers(B, mode, new):
+    p = R.Problem(mode, 128, 2, 4, 64, [700, 90], [new] * 2, seed=1)
+    cache, t = p.cuda(B)
+    ws = B.kv_attention_workspace(cache, 2, p.q_heads, new)
+    run = lambda: B.kv_attention(cache, t["q"], t["query_start"], t["total_lens"], t["block_table"], ws, max_query_len=new)
+    first = run()
+    B.fp4_debug_inject_wait_timeout(True)
+    try:
+        late = run()
+        assert B.fp4_check_device_error() == B.FP4_ERR_TIMEOUT
+        assert torch.equal(first, late)
+    finally:
+        B.fp4_debug_inject_wait_timeout(False)
+    assert torch.equal(first, run())
+    assert B.fp4_check_device_error() == B.FP4_OK
