@@ -258,3 +258,12 @@ def test_timeout_injection_reports_and_recovers(B, mode, new):
         B.fp4_debug_inject_wait_timeout(False)
     assert torch.equal(first, run())
     assert B.fp4_check_device_error() == B.FP4_OK
+
+
+@pytest.mark.parametrize("mode", [2, 1])
+@pytest.mark.parametrize("dim", [32, 96, 160, 192, 224])
+@pytest.mark.parametrize("window", [0, 50])
+def test_other_head_sizes(B, mode, dim, window):
+    """Head sizes without a tensor-core form: one token, a few, a chunk, a request without queries."""
+    p = R.Problem(mode, dim, 2, 3, 16, [0, 31, 257, 600, 12], [1, 3, 40, 1, 0], window=window, gs=mode == 2, seed=dim)
+    check(B, p)
