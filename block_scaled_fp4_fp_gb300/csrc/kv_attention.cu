@@ -199,11 +199,12 @@ cudaError_t launch_any(const KvAttentionArgs& args, cudaStream_t s) {
 }  // namespace
 
 // Query rows of a kv head, up to which the few-row kernel runs: it passes over the cache once for every sixteen, the
-// many-row kernel fills a tile of 256 whatever they are.  8 kv heads of 128, 8,000 tokens a request, NVFP4, few-row and
-// many-row in us:  rows     4 requests   16 requests   64 requests
-//                  17..32     36    61    102   121     351   406
-//                  33..48     47    61    143   121     517   408
-//                  64         57    61    184   122     681   408
+// many-row kernel fills two tiles of 128 whatever they are.  8 kv heads of 128, 8,000 tokens a request, NVFP4, few-row
+// and many-row in us:  rows     4 requests   16 requests   64 requests
+//                      9..16      26    49     60    92     185   298
+//                      17..32     36    49    102    91     351   297
+//                      33..48     47    49    143    91     517   298
+//                      64         57    49    184    91     681   298
 constexpr int64_t kFewRows = 32;
 
 bool few_rows(int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_query_len) {

@@ -12,7 +12,10 @@
 //   O_i += P_i V     P_i in tensor memory, in the columns S_i leaves; V as it is stored, keys as
 //                    rows (an MN-major B operand)
 // Scores, P and outputs stay in tensor memory (S: 2 x 128 columns, O: 2 x head_dim): while
-// one tile's softmax runs, the tensor cores work on the other tile.
+// one tile's softmax runs, the tensor cores work on the other tile.  An item of at most 128 rows is
+// a twin: both tiles hold the same rows and take the key tiles in turn, and as a row's two outputs lie in the same
+// lane of tensor memory, the first tile's warps join them.  (16 requests x 8,000 tokens, 17 to 128 rows of 8
+// heads of 128: 91 us, 121 with the second tile left empty; fetching codes two tiles ahead changes nothing: 91.)
 //
 // K and V are dequantized once per item and key by four warps each into bf16 tiles
 // (exact: e2m1 times an E4M3 or E8M0 scale has at most six significant bits): the codes
@@ -37,7 +40,7 @@
 // beside the other warps' traffic and a step about 3300, the rest being the ends of items and waits for a softmax
 // (2000 cycles a tile, of which the exponentials 512).  For heads of 64 the softmax: the products take 1750 of 2900.
 //   4096-token prompt, 40 heads of 128, NVFP4:      0.160 ms, 1075 TFLOP/s
-//   4 chunks over 0..16k, 64 heads of 64, MXFP4:    0.420 ms,  734 TFLOP/s
+//   4 chunks over 0..16k, 64 heads of 64, MXFP4:    0.424 ms,  727 TFLOP/s
 // Tried and slower on the prompt: 64-key steps with two score buffers (200 us), scores fetched ahead (201), two warps a
 // row (162, and 406 on the chunks), more registers for the softmax by setmaxnreg (186).
 //
@@ -76,7 +79,7 @@ struct Pre {
   static constexpr uint32_t kKV = kKeys * D * 2;   // one K or V tile
   static constexpr uint32_t kHalf = 128 * 128;     // 64 elements of 128 rows
   static constexpr uint32_t offK = 2 * kQ, offV = offK + 2 * kKV, offBar = offV + 2 * kKV;
-  static constexpr uint32_t offPre = offBar + 1024, offTiles = offPre + 8 * (kThreads + 1), kSmem = offTiles + 8 * (kThreads + 1);
+  static constexpr uint32_t offPre = offBar + 1024, offTiles = offPre + 8 * (kThreads + 1), offX = (offTiles + 8 * (kThreads + 1) + 15) / 16 * 16, kSmem = offX + 1024;
   static constexpr uint32_t kO = 256;              // output columns of tile 0; tile 1 follows
 };
 
@@ -85,6 +88,7 @@ struct Item {
   int row0, rows;             // first row of the item in the request's (token, head) rows; rows of the request
   int j0;                     // first key tile
   int n[2];                   // key tiles of the two row tiles
+  int tiles, twin;            // key tiles in all; both row tiles hold the same rows and take them in turn
   int stop;
   int piece, pieces, first;   // this piece of the item's keys, of how many; CTA of the first one
 };
@@ -191,11 +195,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
   uint64_t* ifull = qempty + 2;                                     // [2] item known
   uint64_t* iempty = ifull + 2;                                     // [2] and done with
   uint64_t* inear = iempty + 2;                                     // the item in work nears its end
-  uint64_t* never = inear + 1;                                     // fault injection: nothing arrives here
+  uint64_t* xgive = inear + 1;                                      // [4] twins: a quadrant's second output complete
+  uint64_t* xtake = xgive + 4;                                      // [4] and read
+  uint64_t* never = xtake + 4;                                     // fault injection: nothing arrives here
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
   Item* items = reinterpret_cast<Item*>(smem + C::offBar + 512);   // [2]
   int64_t* prefix = reinterpret_cast<int64_t*>(smem + C::offPre);  // [kThreads + 1] items before a thread's requests
   int64_t* cost_before = reinterpret_cast<int64_t*>(smem + C::offTiles);  // [kThreads + 1] cost of the items before an item
+
+  float* xch = reinterpret_cast<float*>(smem + C::offX);  // [4][2][32] references and sums of the second outputs
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -214,6 +222,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
       mbar_init(&iempty[s], kThreads / 32);
     }
     mbar_init(inear, 1);
+    for (int w = 0; w < 4; ++w) {
+      mbar_init(&xgive[w], 1);
+      mbar_init(&xtake[w], 1);
+    }
     mbar_init(never, 1);
     fence_barrier_init();
   }
@@ -387,6 +399,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
               }
             }
           }
+          x.tiles = max(x.n[0], x.n[1]);
+          x.twin = x.row0 + 128 >= x.rows;  // no rows for the second tile: it takes every other key tile of the first's
+          if (x.twin) {
+            x.n[0] = (x.tiles + 1) / 2;
+            x.n[1] = x.tiles / 2;
+          }
           *it = x;
           mbar_arrive(&ifull[k & 1]);
         }
@@ -446,9 +464,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
       __syncwarp();
       if (lane == 0) mbar_arrive(&iempty[k & 1]);
       if (x.stop || failed) break;
-      const int n = max(x.n[0], x.n[1]);
+      const int n = x.tiles;
       auto scores = [&](int i, int kb) {
-        const uint64_t qd = desc_k(base + i * C::kQ, 1024, 2), kd = desc_k(base + C::offK + kb * C::kKV, 1024, 2);
+        const uint64_t qd = desc_k(base + (x.twin ? 0 : i) * C::kQ, 1024, 2), kd = desc_k(base + C::offK + kb * C::kKV, 1024, 2);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
           mma_ss(tmem + 128 * i, qd + (ks >> 2) * (C::kHalf >> 4) + 2 * (ks & 3), kd + (ks >> 2) * (C::kHalf >> 4) + 2 * (ks & 3),
@@ -462,6 +480,49 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
           mma_ts(tmem + C::kO + D * i, tmem + 128 * i + 8 * ks, vd + ks * (2048 >> 4), idesc_o, !first || ks > 0);
       };
       if (n == 0 && leader) mbar_arrive(inear);
+      if (x.twin) {
+        for (int i = 0; i < 2; ++i) {
+          mbar_wait(&qfull[i], k & 1, a.err, failed);
+          if (i < n) mbar_wait(&kfull[(g + i) & 1], ((g + i) >> 1) & 1, a.err, failed);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the copied queries, for the tensor core
+          tc_fence_after();
+          if (leader && i < n) {
+            scores(i, (g + i) & 1);
+            tc_commit(&kempty[(g + i) & 1]);
+          }
+        }
+        if (leader && n <= 2) {
+          tc_commit(&qempty[0]);
+          tc_commit(&qempty[1]);
+        }
+        for (int j = 0; j < n; ++j, ++g) {
+          const int i = j & 1;
+          if (leader && j == max(n - 4, 0)) mbar_arrive(inear);
+          mbar_wait(&vfull[g & 1], (g >> 1) & 1, a.err, failed);
+          mbar_wait(&pfull[i], u[i] & 1, a.err, failed);
+          ++u[i];
+          tc_fence_after();
+          if (leader) {
+            values(i, g & 1, j < 2);
+            if (j + 2 >= n) tc_commit(&ofull[i]);
+            tc_commit(&vempty[g & 1]);
+          }
+          if (j + 2 < n) {
+            mbar_wait(&kfull[g & 1], ((g + 2) >> 1) & 1, a.err, failed);
+            tc_fence_after();
+            if (leader) {
+              scores(i, g & 1);
+              tc_commit(&kempty[g & 1]);
+              if (j + 3 == n) {
+                tc_commit(&qempty[0]);
+                tc_commit(&qempty[1]);
+              }
+            }
+          }
+          __syncwarp();
+        }
+        continue;
+      }
       if (n > 0) mbar_wait(&kfull[g & 1], (g >> 1) & 1, a.err, failed);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -515,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
       __syncwarp();
       if (lane == 0) mbar_arrive(&iempty[k & 1]);
       if (x.stop || failed) break;
-      const int n = max(x.n[0], x.n[1]);
+      const int n = x.tiles;
       const int32_t* table = a.block_table + (int64_t)x.b * a.table_stride;
       const int lo = a.window > 0 ? max(x.total - x.qlen + x.row0 / group + 1 - a.window, 0) : 0;
       const int hi = min(x.total, (x.j0 + n) * kKeys);
@@ -570,14 +631,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
     const float gsk = (MODE == 2 && a.cache.gs_k) ? __ldg(a.cache.gs_k) : 1.0f;
     const float gsv = (MODE == 2 && a.cache.gs_v) ? __ldg(a.cache.gs_v) : 1.0f;
     const float cs = a.scale * 1.4426950408889634f * gsk;
-    int use = 0, outs = 0;
+    int use = 0, outs = 0, twins = 0;
     for (int k = 0;; ++k) {
       mbar_wait(&ifull[k & 1], (k >> 1) & 1, a.err, failed);
       const Item& x = items[k & 1];  // (read again at the item's end, which gives it back)
       if (x.stop || failed) break;
       int hi = INT32_MAX, lo = 0;  // keys lo .. hi - 1, counted from the piece's first (rows past the request's are not used)
       {
-        const int rr = x.row0 + 128 * i + row, pos = x.total - x.qlen + rr / group;
+        const int rr = x.row0 + (x.twin ? 0 : 128 * i) + row, pos = x.total - x.qlen + rr / group;
         if (rr < x.rows) {
           hi = max(pos + 1, 0) - x.j0 * kKeys;
           lo = (a.window > 0 ? max(pos + 1 - a.window, 0) : 0) - x.j0 * kKeys;
@@ -585,9 +646,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
       }
       float m = kNone;
       uint64_t l2 = 0;  // the sum, in two halves
-      const int n = x.n[i];
+      const int n = x.n[i], first = x.twin ? i * kKeys : 0, step = x.twin ? 2 * kKeys : kKeys;
       for (int j = 0; j < n; ++j, ++use) {
-        const int key0 = j * kKeys;
+        const int key0 = first + j * step;
         const bool mask = __any_sync(0xffffffffu, key0 < lo || key0 + kKeys > hi);
         mbar_wait(&sfull[i], use & 1, a.err, failed);
         tc_fence_after();
@@ -688,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
       float l, lh;
       unpack2(l2, l, lh);
       l += lh;
-      const int rr = x.row0 + 128 * i + row, tok = rr / group;
+      const int rr = x.row0 + (x.twin ? 0 : 128 * i) + row, tok = rr / group;
       const bool real = rr < x.rows;
       const int64_t at = (int64_t)(x.q0 + tok) * a.q_heads + x.h * group + (rr - tok * group);
       if (n > 0) {
@@ -696,6 +757,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
         ++outs;
         tc_fence_after();
       }
+      float w0 = 1.f, w1 = 0.f;
+      if (x.twin) {  // both outputs of a row lie in the same lane: the first tile's warp joins them
+        float* xc = xch + 64 * (warp & 3) + lane;
+        if (i == 1) {
+          xc[0] = m;
+          xc[32] = l;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&xgive[warp & 3]);
+          mbar_wait(&xtake[warp & 3], twins & 1, a.err, failed);
+          tc_fence_after();
+        } else {
+          mbar_wait(&xgive[warp & 3], twins & 1, a.err, failed);
+          tc_fence_after();
+          const float top1 = xc[0], l1 = xc[32], t = fmaxf(m, top1);
+          w0 = exp2f(m - t);
+          w1 = exp2f(top1 - t);
+          m = t;
+          l = l * w0 + l1 * w1;
+        }
+        ++twins;
+      }
+      if (!x.twin || i == 0) {
       auto sums = [&](int p) { return results + (size_t)(2 * (x.first + p) + (p == 0)) * kSlotFloats<D> + 256 * D + 256 * i + row; };
       auto outputs = [&](int p, int c) {
         return reinterpret_cast<float4*>(results + (size_t)(2 * (x.first + p) + (p == 0)) * kSlotFloats<D>) + (i * (D / 4) + 8 * c) * 128 + row;
@@ -708,6 +792,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
         if (n > 0) {
           tmem_ld32(to + 32 * c, o);
           ld_wait();
+          if (x.twin) {
+            const bool both = x.n[1] > 0;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              uint32_t p[8];
+              if (both) {
+                tmem_ld8(to + D + 32 * c + 8 * h, p);
+                ld_wait();
+              }
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float v = __uint_as_float(o[8 * h + e]) * w0;
+                o[8 * h + e] = __float_as_uint(both ? fmaf(__uint_as_float(p[e]), w1, v) : v);
+              }
+            }
+          }
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0;
@@ -727,6 +827,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
             dst[e] = make_uint4(v[0], v[1], v[2], v[3]);
           }
         }
+      }
+      if (x.twin) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&xtake[warp & 3]);
       }
       bool last = whole;
       if (!whole) {  // the warp whose piece comes last joins the item's pieces of its rows, in their order
@@ -781,6 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
         }
       }
       if (last && real && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&iempty[k & 1]);
       tc_fence_before();

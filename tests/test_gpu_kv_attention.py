@@ -267,3 +267,15 @@ def test_other_head_sizes(B, mode, dim, window):
     """Head sizes without a tensor-core form: one token, a few, a chunk, a request without queries."""
     p = R.Problem(mode, dim, 2, 3, 16, [0, 31, 257, 600, 12], [1, 3, 40, 1, 0], window=window, gs=mode == 2, seed=dim)
     check(B, p)
+
+
+@pytest.mark.parametrize("mode,dim,kv,group", [(2, 128, 2, 4), (1, 64, 1, 8)])
+@pytest.mark.parametrize("window", [0, 200])
+def test_chunks_at_the_tiles_edges(B, mode, dim, kv, group, window):
+    """127, 128, 129, 256 and 257 rows of a kv head in one call: items whose second tile has no rows, some, all; contexts of
+    one, two and three key tiles."""
+    rows = [127, 128, 129, 256, 257, 40]
+    new = [-(-r // group) for r in rows]
+    total = [130, 128, 300, 257, 129, 11]
+    p = R.Problem(mode, dim, kv, group, 32, [max(t - n, 0) for t, n in zip(total, new)], new, window=window, gs=mode == 2, seed=kv + window)
+    check(B, p)
