@@ -1099,18 +1099,23 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
         if (lane == 0) set_l[set * R + r] = v;
       }
       named_sync<kConsumers>(1);
-      if (threadIdx.x < R) {
+      float* set_f = reinterpret_cast<float*>(smem + offP);  // a set's factor to the joint reference, over the joint sum
+      if (threadIdx.x < SETS * R) {
+        const int r = threadIdx.x % R;
         float m = -INFINITY, v = 0.f;
 #pragma unroll
-        for (int k = 0; k < SETS; ++k) m = fmaxf(m, set_m[k * R + threadIdx.x]);
+        for (int k = 0; k < SETS; ++k) m = fmaxf(m, set_m[k * R + r]);
 #pragma unroll
-        for (int k = 0; k < SETS; ++k) {
-          v += set_l[k * R + threadIdx.x] * exp2f(set_m[k * R + threadIdx.x] - m);
+        for (int k = 0; k < SETS; ++k) v += set_l[k * R + r] * exp2f(set_m[k * R + r] - m);
+        set_f[threadIdx.x] = v == 0.f ? 0.f : exp2f(set_m[threadIdx.x] - m) / v;
+        if (threadIdx.x < R) {
+          join_m[r] = m;
+          join_l[r] = v;
         }
-        join_m[threadIdx.x] = m;
-        join_l[threadIdx.x] = v;
       }
-      // outputs on the joint reference; the second half of the sets hands its own to the first (half the space)
+      named_sync<kConsumers>(1);
+      // Outputs on the joint reference, divided by the joint sum (V may be near fp32's largest values, whose undivided
+      // sums would pass it); the second half of the sets hands its own to the first (half the space).
       float2* dump = reinterpret_cast<float2*>(smem + offOut) + (set % (SETS / 2)) * (C::kPieces * 32) + lane;
       const float ve = MODE == 1 ? exp2i_f32(vexp) : 1.0f;
 #pragma unroll
@@ -1118,10 +1123,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int r = 8 * nb + 2 * c + h;
-          float m = -INFINITY;
-#pragma unroll
-          for (int k = 0; k < SETS; ++k) m = fmaxf(m, set_m[k * R + r]);
-          const float f = exp2f(set_m[set * R + r] - m) * ve;
+          const float f = set_f[set * R + r] * ve;
 #pragma unroll
           for (int i = 0; i < CH / 2; ++i) {
             acc[i][nb][h] *= f;
@@ -1160,8 +1162,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
         const int r = row_of(x), ch = CH * ((x & 31) >> 2) + 2 * ((x >> 6) / NB);
         const int64_t at = row_out[qb * R + r];
         if (at < 0) return;
-        const float inv = ls == 0.f ? 0.f : gsv / ls;
-        *reinterpret_cast<uint32_t*>(a.out + at * D + ch) = pack_bf16x2_rn(v.x * inv, v.y * inv);
+        *reinterpret_cast<uint32_t*>(a.out + at * D + ch) = pack_bf16x2_rn(v.x * gsv, v.y * gsv);
         if (a.lse && ch == 0) a.lse[at] = ls == 0.f ? -INFINITY : (jm + log2f(ls)) * 0.6931471805599453f;
       };
       auto release = [&]() {  // the segment's query rows, key ranges and output rows are done with
@@ -1205,7 +1206,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
       static_assert(3 * KC * R * 4 + R * 4 <= (int)C::kPBytes, "a chunk's m, l and factors fit the probabilities' space");
       float* cm = reinterpret_cast<float*>(smem + offP);
       float* cl = cm + KC * R;
-      float* cf = cl + KC * R;  // factors to the chunk's reference
+      float* cf = cl + KC * R;  // weights: the sums on the chunk's reference, times 2^-24 (against overflow, as above)
       float* cr = cf + KC * R;  // that reference
       float2 v[XN] = {};
       float jm[XN], jl[XN];
@@ -1228,8 +1229,9 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
             named_sync<kConsumers>(1);
             for (int y = threadIdx.x; y < nk * R; y += kConsumers) {
               float m = kNone;
+#pragma unroll 8
               for (int k = 0; k < nk; ++k) m = fmaxf(m, cm[k * R + y % R]);
-              cf[y] = exp2f(cm[y] - m);
+              cf[y] = cl[y] * exp2f(cm[y] - m) * 0x1p-24f;
               if (y < R) cr[y] = m;
             }
             named_sync<kConsumers>(1);
@@ -1244,7 +1246,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
               const float g = cf[k * R + r];
               w.x += u[k].x * g;
               w.y += u[k].y * g;
-              wl += cl[k * R + r] * g;
+              wl += g;
             }
           v[i] = make_float2(v[i].x * fo + w.x * fn, v[i].y * fo + w.y * fn);
           jl[i] = jl[i] * fo + wl * fn;
@@ -1255,7 +1257,8 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
 #pragma unroll
       for (int i = 0; i < XN; ++i) {
         const int x = threadIdx.x + i * kConsumers;
-        if (x < X) store(x, v[i], jm[i], jl[i]);
+        const float inv = jl[i] == 0.f ? 0.f : 1.0f / jl[i];
+        if (x < X) store(x, make_float2(v[i].x * inv, v[i].y * inv), jm[i], jl[i] * 0x1p24f);
       }
       release();
     }

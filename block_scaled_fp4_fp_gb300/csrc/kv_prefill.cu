@@ -24,7 +24,7 @@
 // needs it) restores the value.  256 rows an item halve that work a row.
 //
 // Softmax: a thread owns a row.  P is bf16 and so has fp32's range: the reference m_r is the
-// first tile's maximum and moves only when 32 probabilities sum to more than 2^64, so that
+// first tile's maximum and moves only when 32 probabilities sum to more than 2^24, so that
 // after the first tile the scores are read once, no maximum is taken of them and the output
 // is almost never rescaled.  p is rounded to bf16 (2^-9); scores, sums and output are fp32.
 //
@@ -40,7 +40,7 @@
 // beside the other warps' traffic and a step about 3300, the rest being the ends of items and waits for a softmax
 // (2000 cycles a tile, of which the exponentials 512).  For heads of 64 the softmax: the products take 1750 of 2900.
 //   4096-token prompt, 40 heads of 128, NVFP4:      0.160 ms, 1075 TFLOP/s
-//   4 chunks over 0..16k, 64 heads of 64, MXFP4:    0.424 ms,  727 TFLOP/s
+//   4 chunks over 0..16k, 64 heads of 64, MXFP4:    0.430 ms,  716 TFLOP/s
 // Tried and slower on the prompt: 64-key steps with two score buffers (200 us), scores fetched ahead (201), two warps a
 // row (162, and 406 on the chunks), more registers for the softmax by setmaxnreg (186).
 //
@@ -70,7 +70,7 @@ constexpr int kCost = 3;          // what an item costs beside its key tiles, in
 constexpr int kSnap = 8;         // a share's end moves to an item's end that is nearer than this
 constexpr int kShare = 2 * kSnap; // a CTA's share at least
 constexpr int kCtas = 160;        // CTAs of a launch at most (one an SM)
-constexpr float kFar = 0x1p64f;  // a row's reference moves when probabilities sum to more than this
+constexpr float kFar = 0x1p24f;  // a row's reference moves when probabilities sum to more than this
 constexpr float kNone = -1e30f;
 
 template <int D>
@@ -148,8 +148,8 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Eight codes of a scale group -> eight bf16 (16 bytes).  `sc`: the scale times 2^112 (NVFP4), or
-// the scale times 2^12 (MXFP4), as a bf16 pair.
+// Eight codes of a scale group -> eight bf16 (16 bytes).  `sc`: the scale (MXFP4), or the scale times 2^112 (NVFP4), as a
+// bf16 pair.
 template <int MODE>
 __device__ __forceinline__ uint4 dequant8(uint32_t w, uint32_t sc) {
   uint32_t h[4];
@@ -161,14 +161,18 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w, uint32_t sc) {
   for (int i = 0; i < 4; ++i) {
     // f16 bits moved to bf16's exponent place: the value times 2^-112
     uint32_t v = (h[i] & 0x80008000u) | ((h[i] >> 3) & 0x0FFF0FFFu);
-    if (MODE == 1) v = mul_bf16x2(v, 0x71807180u);  // 2^100
+    if (MODE == 1) v = mul_bf16x2(v, 0x77807780u);  // 2^112
     h[i] = mul_bf16x2(v, sc);
   }
   return make_uint4(h[0], h[1], h[2], h[3]);
 }
 template <int MODE>
 __device__ __forceinline__ uint32_t scale_pair(uint32_t byte) {
-  const float s = MODE == 2 ? e4m3_to_f32(byte) * 0x1p112f : exp2i_f32(min((int)byte - 127 + 12, 127));
+  if (MODE == 1) {  // 2^(byte - 127), 2^-127 as a subnormal number
+    const uint32_t s = max(byte << 7, 0x40u);
+    return __byte_perm(s, s, 0x1010);
+  }
+  const float s = e4m3_to_f32(byte) * 0x1p112f;
   return pack_bf16x2_rn(s, s);
 }
 

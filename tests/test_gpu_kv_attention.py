@@ -279,3 +279,17 @@ def test_chunks_at_the_tiles_edges(B, mode, dim, kv, group, window):
     total = [130, 128, 300, 257, 129, 11]
     p = R.Problem(mode, dim, kv, group, 32, [max(t - n, 0) for t, n in zip(total, new)], new, window=window, gs=mode == 2, seed=kv + window)
     check(B, p)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 96])
+@pytest.mark.parametrize("new", [1, 9])
+def test_mxfp4_scales_at_the_ends_of_their_range(B, dim, new):
+    """V blocks scaled by up to 2^119 and down to 2^-127, K blocks by 2^-127: any E8M0 scale counts for what it is."""
+    p = R.Problem(1, dim, 1, 8, 16, [20 - new, 0], [new, new], seed=dim + new, q_std=0.05)
+    g = np.random.RandomState(dim)
+    p.scales["v"][:] = g.randint(236, 247, p.scales["v"].shape)
+    p.scales["v"][..., -1] = g.randint(0, 4, p.scales["v"].shape[:-1])
+    p.scales["k"][..., -1] = 0
+    p.scales["v"][p.unseen()] = 0xFF
+    p.scales["k"][p.unseen()] = 0xFF
+    check(B, p)
