@@ -410,8 +410,8 @@ def kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slot_map: torch.
 
 
 def kv_attention_workspace(cache: KvCache, batch: int, q_heads: int, max_query_len: int = 1, device="cuda"):
-    """A zero-filled workspace for kv_attention: allocate once, reuse for calls with these heads, this head_dim and
-    max_query_len, and up to `batch` requests."""
+    """A zero-filled workspace for kv_attention: allocate once, with the longest max_query_len, for calls of any batch and
+    any max_query_len up to it."""
     n = lib().kv_attention_workspace_bytes(batch, q_heads, cache.kv_heads, cache.head_dim, max_query_len)
     return torch.zeros(n, dtype=torch.uint8, device=device)
 

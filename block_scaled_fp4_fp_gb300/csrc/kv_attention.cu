@@ -212,10 +212,9 @@ bool few_rows(int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_q
          (max_query_len * (q_heads / kv_heads) <= kFewRows || !kv_prefill_supported((int)head_dim));
 }
 
-size_t kv_attention_ws_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
-                             int64_t max_query_len) {
+size_t kv_attention_ws_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_query_len) {
   if (few_rows(q_heads, kv_heads, head_dim, max_query_len))
-    return kv_decode_ws_bytes(batch, q_heads, kv_heads, head_dim, max_query_len);
+    return kv_decode_ws_bytes(q_heads, kv_heads, head_dim, max_query_len);
   if (kv_prefill_supported((int)head_dim))
     return kv_prefill_ws_bytes(head_dim);
   return 16;

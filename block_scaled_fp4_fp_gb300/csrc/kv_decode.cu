@@ -393,7 +393,7 @@ __device__ __forceinline__ void query_rows(const KvAttentionArgs& a, uint8_t* ds
 
 template <int MODE, int D, int NB>
 __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_kernel(
-    const KvAttentionArgs a, int group, int max_blocks, int* __restrict__ counters, float* __restrict__ pieces, int inject_timeout) {
+    const KvAttentionArgs a, int group, int* __restrict__ arrivals, float* __restrict__ pieces, int inject_timeout) {
   using C = Dec<MODE, D, NB>;
   constexpr int R = C::kR, SK = C::kStK, SV = C::kStV, BUFS = C::kBufs, SETS = C::kSets;
   constexpr int kThreads = C::kThreads, kConsumers = C::kConsumers;
@@ -1189,10 +1189,10 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
       named_sync<kConsumers>(1);
       if (threadIdx.x == 0) {
         __threadfence();  // the barrier has ordered every thread's stores before it
-        int* ctr = counters + ((int64_t)e.b * a.cache.kv_heads + e.h) * max_blocks + e.rb;
-        const int n = atomicAdd(ctr, 1);
+        int* arrived = arrivals + 8 * c0;
+        const int n = atomicAdd(arrived, 1);
         *last_flag = n == c1 - c0;
-        if (n == c1 - c0) *ctr = 0;  // ready for the next call
+        if (n == c1 - c0) *arrived = 0;  // ready for the next call
         __threadfence();
       }
       named_sync<kConsumers>(1);
@@ -1272,23 +1272,16 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
   }
 }
 
-size_t kv_decode_piece_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_query_len) {
-  const int64_t rows = max_query_len * (q_heads / kv_heads), R = rows <= 8 || head_dim == 256 ? 8 : 16;
-  return (size_t)(2 * kKvDecodeCtas * (R * head_dim + 2 * R) * 4);
-}
-
 template <int MODE, int D, int NB>
 cudaError_t launch(const DevInfo& d, const KvAttentionArgs& a, cudaStream_t s) {
   using C = Dec<MODE, D, NB>;
   const int group = a.q_heads / a.cache.kv_heads;
-  const int64_t rows = (int64_t)std::min<int64_t>(a.max_query_len, a.tokens) * group;
-  const int max_blocks = (int)((rows + C::kR - 1) / C::kR);
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(d, kv_decode_kernel<MODE, D, NB>, (int)C::kSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  static_assert(kKvDecodeCtas <= 160, "share() and owner() multiply by the CTA count in 32 bits");
-  cfg.gridDim = dim3((unsigned)std::min(kKvDecodeCtas, d.sm_count));
+  static_assert(kKvCtas <= 160, "share() and owner() multiply by the CTA count in 32 bits");
+  cfg.gridDim = dim3((unsigned)std::min(kKvCtas, d.sm_count));
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
@@ -1298,9 +1291,8 @@ cudaError_t launch(const DevInfo& d, const KvAttentionArgs& a, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
-  const size_t pieces = kv_decode_piece_bytes(a.q_heads, a.cache.kv_heads, D, a.max_query_len);
-  return cudaLaunchKernelEx(&cfg, kv_decode_kernel<MODE, D, NB>, a, group, max_blocks,
-                            reinterpret_cast<int*>(ws + pieces), reinterpret_cast<float*>(ws), a.inject_timeout);
+  return cudaLaunchKernelEx(&cfg, kv_decode_kernel<MODE, D, NB>, a, group, reinterpret_cast<int*>(ws + kKvArrivals),
+                            reinterpret_cast<float*>(ws + kKvResults), a.inject_timeout);
 }
 
 template <int MODE, int D>
@@ -1312,11 +1304,10 @@ cudaError_t launch_rows(const DevInfo& d, const KvAttentionArgs& a, cudaStream_t
 
 }  // namespace
 
-// The pieces, two a CTA, then one counter per (request, kv head, row block of at least 8 rows), zero between calls: a
-// workspace sized for a batch serves smaller ones too, whose counters are the first of its own.
-size_t kv_decode_ws_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_query_len) {
-  const int64_t blocks = (max_query_len * (q_heads / kv_heads) + 7) / 8;
-  return kv_decode_piece_bytes(q_heads, kv_heads, head_dim, max_query_len) + (size_t)((batch * kv_heads * blocks * 4 + 255) / 256 * 256);
+// Two pieces a CTA, of 8 or 16 rows.
+size_t kv_decode_ws_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_query_len) {
+  const int64_t rows = max_query_len * (q_heads / kv_heads), R = rows <= 8 || head_dim == 256 ? 8 : 16;
+  return kKvResults + (size_t)(2 * kKvCtas * (R * head_dim + 2 * R) * 4);
 }
 
 bool kv_decode_supported(int head_dim) { return head_dim == 64 || head_dim == 128 || head_dim == 256; }

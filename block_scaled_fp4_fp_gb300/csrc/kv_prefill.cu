@@ -69,7 +69,6 @@ constexpr int kDealt = kThreads;  // calls of up to this many items are dealt ou
 constexpr int kCost = 3;          // what an item costs beside its key tiles, in tiles
 constexpr int kSnap = 8;         // a share's end moves to an item's end that is nearer than this
 constexpr int kShare = 2 * kSnap; // a CTA's share at least
-constexpr int kCtas = 160;        // CTAs of a launch at most (one an SM)
 constexpr float kFar = 0x1p24f;  // a row's reference moves when probabilities sum to more than this
 constexpr float kNone = -1e30f;
 
@@ -93,9 +92,8 @@ struct Item {
   int piece, pieces, first;   // this piece of the item's keys, of how many; CTA of the first one
 };
 
-// Workspace: the two counters of the hand-out, arrivals of a split item's pieces (a warp of 32 rows each) -- zero between
-// calls -- and two pieces' results a CTA: outputs [tile][channel / 4][row][4], references and sums [tile][2][row].
-constexpr size_t kArrivals = 64, kResults = kArrivals + (size_t)kCtas * 8 * 4;
+// In the workspace an arrival word for each warp's 32 rows of a split item, and two pieces' results a CTA: outputs
+// [tile][channel / 4][row][4], references and sums [tile][2][row].
 template <int D>
 constexpr size_t kSlotFloats = 256 * (D + 2);
 
@@ -181,8 +179,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
                                                                   uint8_t* __restrict__ ws, int inject_timeout) {
   using C = Pre<D>;
   int* counters = reinterpret_cast<int*>(ws);
-  int* arrivals = reinterpret_cast<int*>(ws + kArrivals);
-  float* results = reinterpret_cast<float*>(ws + kResults);
+  int* arrivals = reinterpret_cast<int*>(ws + kKvArrivals);
+  float* results = reinterpret_cast<float*>(ws + kKvResults);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -911,7 +909,7 @@ cudaError_t launch(const DevInfo& d, const KvAttentionArgs& a, cudaStream_t s) {
   const cudaError_t e = allow_smem(d, kv_prefill_kernel<MODE, D>, smem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min(d.sm_count, kCtas));
+  cfg.gridDim = dim3((unsigned)std::min(d.sm_count, kKvCtas));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
@@ -926,7 +924,7 @@ cudaError_t launch(const DevInfo& d, const KvAttentionArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t kv_prefill_ws_bytes(int64_t head_dim) { return kResults + (size_t)(2 * kCtas * 256 * (head_dim + 2) * 4); }
+size_t kv_prefill_ws_bytes(int64_t head_dim) { return kKvResults + (size_t)(2 * kKvCtas * 256 * (head_dim + 2) * 4); }
 
 bool kv_prefill_supported(int head_dim) { return head_dim == 64 || head_dim == 128; }
 

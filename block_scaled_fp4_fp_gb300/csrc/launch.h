@@ -161,12 +161,17 @@ struct KvAttentionArgs {
   int inject_timeout = 0;
 };
 // the attention's dispatch (kv_attention.cu) and its workspace
-size_t kv_attention_ws_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_query_len);
+size_t kv_attention_ws_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_query_len);
 cudaError_t launch_kv_attention(const DevInfo& d, const KvAttentionArgs& args, cudaStream_t s);
+// The workspace, the same for both tensor-core kernels and whatever the call's sizes, so that calls of different kinds may
+// take turns on one: the two counters of the prompt kernel's hand-out; the arrivals of split items' pieces, eight words for
+// the CTA that holds an item's first piece (a CTA begins at most one item that it does not end) -- zero between calls --
+// and then results of the pieces, which mean nothing between calls.
+constexpr int kKvCtas = 160;  // CTAs of a launch at most (one an SM)
+constexpr size_t kKvArrivals = 64, kKvResults = kKvArrivals + (size_t)kKvCtas * 8 * 4;
 // kv_decode.cu: a few query rows a request, head_dim 64, 128 or 256
-constexpr int kKvDecodeCtas = 160;  // CTAs of a launch at most (one an SM)
 bool kv_decode_supported(int head_dim);
-size_t kv_decode_ws_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_query_len);
+size_t kv_decode_ws_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_query_len);
 cudaError_t launch_kv_decode(const DevInfo& d, const KvAttentionArgs& args, cudaStream_t s);
 // kv_prefill.cu: many query rows a request, head_dim 64 or 128
 bool kv_prefill_supported(int head_dim);

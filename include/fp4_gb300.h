@@ -449,8 +449,8 @@ size_t kv_attention_workspace_bytes(int64_t batch, int64_t q_heads, int64_t kv_h
  *                kv_attention_workspace_bytes(batch, q_heads, kv_heads, head_dim,
  *                max_query_len); zero-filled once when allocated, each call leaves it
  *                ready for the next.  Calls that overlap on the GPU must not share one.
- *                A workspace serves calls with its q_heads, kv_heads, head_dim and
- *                max_query_len and any batch up to the one it was sized for.
+ *                Calls of any kind may take turns on one workspace that has the bytes each
+ *                needs: one sized for the longest max_query_len serves shorter ones.
  *   out          bf16[tokens, q_heads, head_dim], 16-byte aligned
  *   lse          fp32[tokens, q_heads] or NULL: log of the sum of exp(score), with which
  *                results over disjoint keys can be merged

@@ -293,3 +293,17 @@ def test_mxfp4_scales_at_the_ends_of_their_range(B, dim, new):
     p.scales["v"][p.unseen()] = 0xFF
     p.scales["k"][p.unseen()] = 0xFF
     check(B, p)
+
+
+@pytest.mark.parametrize("mode,dim,group", [(2, 128, 8), (1, 64, 4), (2, 256, 2)])
+def test_calls_of_every_kind_take_turns_on_one_workspace(B, mode, dim, group):
+    """Single tokens, a few, prompts, and the reverse, over contexts long enough that items are split: each call leaves the
+    workspace ready for any other, whatever kernel and piece size it takes."""
+    cases = {n: R.Problem(mode, dim, 2, group, 64, [12000] * 5, [n] * 5, seed=n) for n in (1, 2, 4, 12)}
+    cache, _ = cases[12].cuda(B)
+    ws = B.kv_attention_workspace(cache, 5, cases[12].q_heads, 12)
+    for n in (4, 1, 12, 1, 4, 12, 2, 12, 4, 1):
+        check(B, cases[n], ws=ws)
+    small = R.Problem(mode, dim, 1, 2 * group, 64, [2500], [4], seed=9)  # other heads, another batch
+    check(B, small, ws=ws)
+    check(B, cases[1], ws=ws)
