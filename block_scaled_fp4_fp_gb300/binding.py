@@ -336,6 +336,24 @@ def qmm(x: torch.Tensor, w: torch.Tensor, scales: torch.Tensor, biases=None, glo
     return out
 
 
+def _need(name: str, t: torch.Tensor, dtype, shape, rows: bool = False):
+    """Refuses a tensor whose type, shape or layout the kernels would misread: contiguous, or with `rows` its rows."""
+    if t.dtype is not dtype or t.shape != shape or not (t.is_contiguous() or rows and t.stride(-1) == 1):
+        raise ValueError(f"{name}: a {dtype} tensor of shape {tuple(shape)} with {'contiguous rows' if rows else 'contiguous elements'} "
+                         f"is needed, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}")
+
+
+def _need_vector(name: str, t: torch.Tensor, dtype, n: int):
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: {n} contiguous {dtype} are needed, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}")
+
+
+def _need_gpu(*tensors):
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise ValueError(f"a tensor of shape {tuple(t.shape)} is on {t.device}: the kernels read GPU memory")
+
+
 class KvCache(c.Structure):
     """fp4_kv_cache: one layer's paged 4-bit cache (make it with kv_cache, which keeps the tensors alive)."""
     _fields_ = [("k_codes", c.c_void_p), ("k_scales", c.c_void_p), ("v_codes", c.c_void_p), ("v_scales", c.c_void_p),
@@ -354,9 +372,10 @@ def kv_cache(k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tenso
     for name, t, shape, dt in (("k_codes", k_codes, tuple(k_codes.shape), torch.int32),
                                ("v_codes", v_codes, tuple(k_codes.shape), torch.int32),
                                ("k_scales", k_scales, want, torch.uint8), ("v_scales", v_scales, want, torch.uint8)):
-        if tuple(t.shape) != shape or t.dtype != dt or not t.is_contiguous():
-            raise ValueError(f"{name}: a contiguous {dt} tensor of shape {shape} is needed, got {t.dtype} "
-                             f"{tuple(t.shape)}")
+        _need(name, t, dt, shape)
+    for name, t in (("global_scale_k", global_scale_k), ("global_scale_v", global_scale_v)):
+        if t is not None and (t.dtype is not torch.float32 or t.numel() != 1):
+            raise ValueError(f"{name}: one float32 is needed, got {t.dtype} {tuple(t.shape)}")
     cache = KvCache(_p(k_codes), _p(k_scales), _p(v_codes), _p(v_scales), _p(global_scale_k), _p(global_scale_v),
                     pages, page, heads, words * 8, mode)
     cache.tensors = (k_codes, k_scales, v_codes, v_scales, global_scale_k, global_scale_v)
@@ -386,27 +405,44 @@ def kv_plan(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch
             page_size: int, tokens: int, plan: KvPlan = None, stream=None) -> KvPlan:
     """Places a step's tokens: completes block_table [batch, max_pages] in place from free_pages and returns the
     lengths, slots and positions of up to `tokens` tokens (entries past the step's own are -1)."""
-    batch = cached_lens.numel()
+    batch, i32 = cached_lens.numel(), torch.int32
+    if not (plan is None and cached_lens.dtype is i32 and cached_lens.is_cuda and cached_lens.is_contiguous() and new_lens.dtype is i32 and new_lens.is_cuda
+            and new_lens.is_contiguous() and new_lens.numel() == batch and free_pages.dtype is i32 and free_pages.is_cuda
+            and free_pages.is_contiguous() and block_table.dtype is i32 and block_table.is_cuda and block_table.dim() == 2
+            and block_table.shape[0] == batch and block_table.stride(1) == 1):
+        _need_vector("cached_lens", cached_lens, i32, batch)
+        _need_vector("new_lens", new_lens, i32, batch)
+        _need_vector("free_pages", free_pages, i32, free_pages.numel())
+        _need("block_table", block_table, i32, (batch, *block_table.shape[-1:]), rows=True)
+        if plan is not None:
+            for name, t, dt, n in zip(plan._fields, plan, (i32, i32, torch.int64, i32, i32), (batch, batch + 1, tokens, tokens, 1)):
+                _need_vector(name, t, dt, n)
+        _need_gpu(cached_lens, new_lens, free_pages, block_table, *(plan or ()))
     if plan is None:
-        dev, i32 = cached_lens.device, torch.int32
+        dev = cached_lens.device
         plan = KvPlan(torch.empty(batch, dtype=i32, device=dev), torch.empty(batch + 1, dtype=i32, device=dev),
                       torch.empty(tokens, dtype=torch.int64, device=dev), torch.empty(tokens, dtype=i32, device=dev),
                       torch.empty((), dtype=i32, device=dev))
     _check(lib().kv_plan(_p(cached_lens), _p(new_lens), batch, page_size, _p(free_pages), free_pages.numel(),
                          _p(block_table), block_table.stride(0), block_table.shape[1], _p(plan.total_lens),
-                         _p(plan.query_start), _p(plan.slot_map), _p(plan.positions), plan.slot_map.numel(),
+                         _p(plan.query_start), _p(plan.slot_map), _p(plan.positions), tokens,
                          _p(plan.pages_taken), _s(stream)), "kv_plan")
     return plan
 
 
 def kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, stream=None):
     """Quantizes k and v [tokens, kv_heads, head_dim] (views with strides are read in place) into their slots."""
-    for name, t in (("k", k), ("v", v)):
-        if t.shape[1:] != (cache.kv_heads, cache.head_dim) or t.shape[0] != slot_map.numel() or t.stride(2) != 1:
-            raise ValueError(f"{name}: [{slot_map.numel()}, {cache.kv_heads}, {cache.head_dim}] with unit stride in a "
-                             f"row is needed, got {tuple(t.shape)}, strides {t.stride()}")
-    _check(lib().kv_append(c.byref(cache), _p(k), k.stride(0), k.stride(1), _p(v), v.stride(0), v.stride(1),
-                           _p(slot_map), k.shape[0], _s(stream)), "kv_append")
+    tokens = slot_map.numel()
+    bf16, shape, ks, vs = torch.bfloat16, (tokens, cache.kv_heads, cache.head_dim), k.stride(), v.stride()
+    if not (slot_map.dtype is torch.int64 and slot_map.is_cuda and slot_map.is_contiguous() and k.dtype is bf16 and k.is_cuda
+            and k.shape == shape and ks[2] == 1 and v.dtype is bf16 and v.is_cuda and v.shape == shape and vs[2] == 1
+            and cache.tensors[0].is_cuda):
+        _need_vector("slot_map", slot_map, torch.int64, tokens)
+        for name, t in (("k", k), ("v", v)):
+            _need(name, t, bf16, shape, rows=True)
+        _need_gpu(k, v, slot_map, cache.tensors[0])
+    _check(lib().kv_append(c.byref(cache), k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], slot_map.data_ptr(), tokens,
+                           _s(stream)), "kv_append")
 
 
 def kv_attention_workspace(cache: KvCache, batch: int, q_heads: int, max_query_len: int = 1, device="cuda"):
@@ -422,17 +458,30 @@ def kv_attention(cache: KvCache, q: torch.Tensor, query_start: torch.Tensor, tot
     """Causal attention of q [tokens, q_heads, head_dim] over the paged 4-bit cache; scale defaults to
     head_dim ** -0.5."""
     tokens, heads, dim = q.shape
-    batch = total_lens.numel()
-    if dim != cache.head_dim or q.stride(2) != 1 or query_start.numel() != batch + 1 or block_table.shape[0] != batch:
-        raise ValueError(f"q {tuple(q.shape)} (strides {q.stride()}), query_start {tuple(query_start.shape)}, total_lens "
-                         f"{tuple(total_lens.shape)} and block_table {tuple(block_table.shape)} do not belong together "
-                         f"for head_dim {cache.head_dim}")
+    batch, i32 = total_lens.numel(), torch.int32
+    bf16, qs, pages = torch.bfloat16, q.stride(), block_table.shape
+    if not (q.dtype is bf16 and q.is_cuda and dim == cache.head_dim and qs[2] == 1 and total_lens.dtype is i32 and total_lens.is_cuda
+            and total_lens.is_contiguous() and query_start.dtype is i32 and query_start.is_cuda and query_start.is_contiguous()
+            and query_start.numel() == batch + 1 and block_table.dtype is i32 and block_table.is_cuda and len(pages) == 2
+            and pages[0] == batch and block_table.stride(1) == 1 and ws.is_cuda and ws.is_contiguous() and out is None and lse is None
+            and cache.tensors[0].is_cuda):
+        _need("q", q, bf16, (tokens, heads, cache.head_dim), rows=True)
+        _need_vector("total_lens", total_lens, i32, batch)
+        _need_vector("query_start", query_start, i32, batch + 1)
+        _need("block_table", block_table, i32, (batch, *pages[-1:]), rows=True)
+        if out is not None:
+            _need("out", out, bf16, (tokens, heads, dim))
+        if lse is not None:
+            _need("lse", lse, torch.float32, (tokens, heads))
+        if not ws.is_contiguous():
+            raise ValueError(f"ws: a contiguous tensor is needed, got strides {ws.stride()}")
+        _need_gpu(q, total_lens, query_start, block_table, ws, out, lse, cache.tensors[0])
     if out is None:
         out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=q.device)
-    _check(lib().kv_attention(c.byref(cache), _p(q), q.stride(0), q.stride(1), tokens, heads, _p(query_start),
-                              _p(total_lens), batch, _p(block_table), block_table.stride(0),
-                              block_table.shape[1], max_query_len, dim ** -0.5 if scale is None else scale, window,
-                              _p(ws), ws.numel() * ws.element_size(), _p(out), _p(lse), _s(stream)), "kv_attention")
+    _check(lib().kv_attention(c.byref(cache), q.data_ptr(), qs[0], qs[1], tokens, heads, query_start.data_ptr(),
+                              total_lens.data_ptr(), batch, block_table.data_ptr(), block_table.stride(0), pages[1], max_query_len,
+                              dim ** -0.5 if scale is None else scale, window, ws.data_ptr(), ws.numel() * ws.element_size(),
+                              out.data_ptr(), _p(lse), _s(stream)), "kv_attention")
     return out
 
 

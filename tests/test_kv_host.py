@@ -117,3 +117,57 @@ def test_binding_refuses_tensors_that_do_not_belong_together(B):
     i = torch.zeros(4, dtype=torch.int32)
     with pytest.raises(ValueError):
         B.kv_attention(c, k[..., :64], i, i[:3], i.view(1, 4), i)
+
+
+def refused(name, call, good, **bad):
+    """`call` with one argument exchanged is refused, and the message names it."""
+    with pytest.raises(ValueError, match=name):
+        call(**{**good, **bad})
+
+
+def test_binding_refuses_tensors_the_kernels_would_misread(B):
+    """Types, shapes and layouts are looked at before memory: what is right in all of them but lies on the host is refused last."""
+    i32, i64, bf = torch.int32, torch.int64, torch.bfloat16
+    ints = lambda *n, dtype=i32: torch.zeros(n, dtype=dtype)  # noqa: E731
+
+    good = dict(cached_lens=ints(4), new_lens=ints(4), free_pages=ints(9), block_table=ints(4, 8), page_size=64, tokens=6)
+    with pytest.raises(ValueError, match="GPU"):
+        B.kv_plan(**good)
+    plan = B.KvPlan(ints(4), ints(5), ints(6, dtype=i64), ints(6), ints())
+    with pytest.raises(ValueError, match="GPU"):
+        B.kv_plan(**good, plan=plan)
+    for name, t in (("cached_lens", ints(4, dtype=i64)), ("new_lens", ints(3)), ("new_lens", ints(4, dtype=i64)),
+                    ("new_lens", ints(8)[::2]), ("free_pages", ints(9, dtype=i64)), ("free_pages", ints(9)[::3]), ("block_table", ints(3, 8)),
+                    ("block_table", ints(4, 8, dtype=i64)), ("block_table", ints(8, 4).t()), ("block_table", ints(4, 16)[:, ::2])):
+        refused(name, B.kv_plan, good, **{name: t})
+    for name, t in (("total_lens", ints(3)), ("total_lens", ints(4, dtype=i64)), ("query_start", ints(4)),
+                    ("slot_map", ints(6)), ("slot_map", ints(5, dtype=i64)), ("positions", ints(7)), ("pages_taken", ints(2)),
+                    ("pages_taken", ints(dtype=i64))):
+        refused(name, B.kv_plan, good, plan=plan._replace(**{name: t}))
+
+    codes, scales = torch.zeros((4, 2, 64, 16), dtype=i32), torch.zeros((4, 2, 64, 8), dtype=torch.uint8)
+    cache = B.kv_cache(codes, scales, codes, scales)
+    refused("global_scale_k", B.kv_cache, dict(k_codes=codes, k_scales=scales, v_codes=codes, v_scales=scales),
+            global_scale_k=torch.ones(2))
+    refused("global_scale_v", B.kv_cache, dict(k_codes=codes, k_scales=scales, v_codes=codes, v_scales=scales),
+            global_scale_v=torch.ones((), dtype=torch.float64))
+
+    good = dict(cache=cache, k=torch.zeros((3, 2, 128), dtype=bf), v=torch.zeros((3, 2, 128), dtype=bf), slot_map=ints(3, dtype=i64))
+    with pytest.raises(ValueError, match="GPU"):
+        B.kv_append(**good)
+    for name, t in (("slot_map", ints(3)), ("slot_map", ints(6, dtype=i64)[::2]), ("k", torch.zeros((3, 2, 128), dtype=torch.float16)),
+                    ("v", torch.zeros((3, 2, 128))), ("v", torch.zeros((3, 1, 128), dtype=bf)),
+                    ("k", torch.zeros((3, 2, 256), dtype=bf)[..., ::2]), ("k", torch.zeros((3, 256), dtype=bf))):
+        refused(name, B.kv_append, good, **{name: t})
+
+    good = dict(cache=cache, q=torch.zeros((3, 4, 128), dtype=bf), query_start=ints(3), total_lens=ints(2), block_table=ints(2, 8),
+                ws=torch.zeros(64, dtype=torch.uint8), out=torch.zeros((3, 4, 128), dtype=bf), lse=torch.zeros((3, 4)))
+    with pytest.raises(ValueError, match="GPU"):
+        B.kv_attention(**good)
+    for name, t in (("q", torch.zeros((3, 4, 128), dtype=torch.float16)), ("q", torch.zeros((3, 4, 64), dtype=bf)),
+                    ("q", torch.zeros((3, 4, 256), dtype=bf)[..., ::2]), ("query_start", ints(3, dtype=i64)), ("query_start", ints(2)),
+                    ("total_lens", ints(2, dtype=i64)), ("total_lens", ints(4)[::2]), ("block_table", ints(1, 8)),
+                    ("block_table", ints(8, 2).t()), ("block_table", ints(2, 8, dtype=i64)), ("ws", torch.zeros(64)[::2]),
+                    ("out", torch.zeros((3, 4, 128))), ("out", torch.zeros((2, 4, 128), dtype=bf)),
+                    ("out", torch.zeros((3, 4, 256), dtype=bf)[..., ::2]), ("lse", torch.zeros((3, 4), dtype=bf)), ("lse", torch.zeros((4, 3)))):
+        refused(name, B.kv_attention, good, **{name: t})
