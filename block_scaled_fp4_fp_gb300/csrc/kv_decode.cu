@@ -272,12 +272,12 @@ __device__ __forceinline__ Req load_req(const KvAttentionArgs& a, int b, int gro
   r.q0 = __ldg(a.query_start + b);
   r.qlen = __ldg(a.query_start + b + 1) - r.q0;
   r.total = __ldg(a.total_lens + b);
-  r.total = min(r.total, a.max_pages * a.cache.page_size);
+  r.total = max(min(r.total, a.max_pages * a.cache.page_size), 0);
   if (r.qlen > a.max_query_len || r.q0 < 0 || (int64_t)r.q0 + r.qlen > a.tokens) r.qlen = 0;
   r.first = a.window > 0 ? max(0, r.total - r.qlen + 1 - a.window) : 0;
   r.lo_tile = r.first / kTile;
   r.blocks = r.qlen > 0 ? (int)((unsigned)(r.qlen * group + R - 1) / (unsigned)R) : 0;
-  r.tiles = (r.total > 0 && r.qlen > 0) ? (r.total + kTile - 1) / kTile - r.lo_tile : 0;
+  r.tiles = r.total > 0 && r.qlen > 0 ? (r.total + kTile - 1) / kTile - r.lo_tile : 0;
   r.cost = r.tiles + item_cost;
   return r;
 }

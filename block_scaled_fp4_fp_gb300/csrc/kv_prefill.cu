@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
     x.h = (int)(off % a.cache.kv_heads);
     x.q0 = __ldg(a.query_start + b);
     x.qlen = __ldg(a.query_start + b + 1) - x.q0;
-    x.total = min(__ldg(a.total_lens + b), a.max_pages * page_size);
+    x.total = max(min(__ldg(a.total_lens + b), a.max_pages * page_size), 0);  // (the differences below stay within 32 bits)
     x.row0 = rb * kRows;
     x.rows = x.qlen * group;
     const int pos0 = x.total - x.qlen + x.row0 / group;  // of the first row

@@ -436,7 +436,7 @@ size_t kv_attention_workspace_bytes(int64_t batch, int64_t q_heads, int64_t kv_h
  * for token t of request b (query_start[b] <= t < query_start[b+1]) at position
  * pos = total_lens[b] - (query_start[b+1] - t), over the keys j with 0 <= j <= pos
  * and, when window > 0, j > pos - window, of kv head h / (q_heads / kv_heads).
- * A row that sees no key gives zeros (lse = -inf).
+ * A row that sees no key gives zeros (lse = -inf); a negative total counts as 0.
  *   q            bf16[tokens, q_heads, head_dim], 16-byte aligned; strides in elements,
  *                multiples of 8;  q_heads a multiple of kv_heads
  *   query_start  int32[batch+1], total_lens int32[batch] (kv_plan's outputs, after

@@ -307,3 +307,24 @@ def test_calls_of_every_kind_take_turns_on_one_workspace(B, mode, dim, group):
     small = R.Problem(mode, dim, 1, 2 * group, 64, [2500], [4], seed=9)  # other heads, another batch
     check(B, small, ws=ws)
     check(B, cases[1], ws=ws)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 96])
+@pytest.mark.parametrize("new", [1, 12])
+@pytest.mark.parametrize("window", [0, 40])
+def test_a_negative_total_counts_as_no_keys(B, dim, new, window):
+    """Down to the lowest 32-bit number, whose difference to a query count is no 32-bit number: zeros, and the others' results."""
+    p = R.Problem(2, dim, 1, 8, 64, [300, 20, 700], [new] * 3, window=window, seed=dim + new)
+    cache, t = p.cuda(B)
+    ws = B.kv_attention_workspace(cache, 3, p.q_heads, new)
+    call = lambda lse: B.kv_attention(cache, t["q"], t["query_start"], t["total_lens"], t["block_table"], ws, max_query_len=new,  # noqa: E731
+                                      window=window, lse=lse)
+    sums = torch.empty((3 * new, p.q_heads), device="cuda")
+    want = call(None)
+    for total in (-1, -2 ** 31 + 1, -2 ** 31):
+        t["total_lens"][1] = total
+        got = call(sums)
+        assert B.fp4_check_device_error() == B.FP4_OK
+        mine = slice(new, 2 * new)
+        assert not got[mine].any() and torch.isneginf(sums[mine]).all()
+        assert torch.equal(got[:new], want[:new]) and torch.equal(got[2 * new:], want[2 * new:])
