@@ -58,6 +58,14 @@ __device__ __forceinline__ void tmem_ld8(uint32_t a, uint32_t (&r)[8]) {
                : "r"(a));
 }
 
+// A call whose wait expired gives up: its counts in the workspace may be short, and a later call that finds them so would
+// leave rows unwritten without a word.  It therefore leaves a mark there, which every later call reports until the workspace
+// is zeroed.  (Marked at the kernel's end: in the waits themselves it made every case 2 to 3 % slower.)
+__device__ __forceinline__ void mark_expired(const KvAttentionArgs& a) { __stcg(static_cast<int*>(a.ws) + kKvExpired, 1); }
+__device__ __forceinline__ void report_expired(const KvAttentionArgs& a) {  // (one thread of a call)
+  if (__ldcg(static_cast<const int*>(a.ws) + kKvExpired)) record_error(a.err, kErrTimeout);
+}
+
 // two fp32 values in a register pair, and the packed add and multiply-add (each lane rounded to nearest)
 __device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
   uint64_t r;

@@ -724,6 +724,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
   } else if (warp == C::kWarps + 3) {
 
     // ------------------------------------------------------------ queries
+    if (blockIdx.x == 0 && lane == 0) report_expired(a);
     Walk w;
     w.begin(a, group, R, C::kItemCost, plan_at[0], plan_at[1], plan_at[2], f0, f1);
     for (int seg = 0;; ++seg) {
@@ -1263,6 +1264,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
       release();
     }
   }
+  if (failed) mark_expired(a);
   tc_fence_before();
   __syncthreads();
   if (warp == C::kWarps + 2) {

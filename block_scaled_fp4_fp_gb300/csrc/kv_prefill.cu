@@ -346,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
 
   if (warp >= 17) {
     // ------------------------------------------------------ items, queries
+    if (blockIdx.x == 0 && threadIdx.x == 17 * 32) report_expired(a);
     const int64_t cost = dealt ? cost_before[total_items] : 0;
     const int64_t shares = min((int64_t)gridDim.x, max(max(cost / kShare, total_items), (int64_t)1));
     auto item_at = [&](int64_t unit) {  // the item that holds a unit of cost
@@ -894,6 +895,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
       tc_fence_before();
     }
   }
+  if (failed) mark_expired(a);
   tc_fence_before();
   __syncthreads();
   if (warp == 16) {

@@ -164,10 +164,12 @@ struct KvAttentionArgs {
 size_t kv_attention_ws_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_query_len);
 cudaError_t launch_kv_attention(const DevInfo& d, const KvAttentionArgs& args, cudaStream_t s);
 // The workspace, the same for both tensor-core kernels and whatever the call's sizes, so that calls of different kinds may
-// take turns on one: the two counters of the prompt kernel's hand-out; the arrivals of split items' pieces, eight words for
+// take turns on one: the two counters of the prompt kernel's hand-out, and a word that is set when a wait expired (what
+// is counted here may then be left short, so later calls report it); the arrivals of split items' pieces, eight words for
 // the CTA that holds an item's first piece (a CTA begins at most one item that it does not end) -- zero between calls --
 // and then results of the pieces, which mean nothing between calls.
 constexpr int kKvCtas = 160;  // CTAs of a launch at most (one an SM)
+constexpr int kKvExpired = 2;  // that word
 constexpr size_t kKvArrivals = 64, kKvResults = kKvArrivals + (size_t)kKvCtas * 8 * 4;
 // kv_decode.cu: a few query rows a request, head_dim 64, 128 or 256
 bool kv_decode_supported(int head_dim);

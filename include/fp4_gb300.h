@@ -448,7 +448,10 @@ size_t kv_attention_workspace_bytes(int64_t batch, int64_t q_heads, int64_t kv_h
  *   ws           device workspace, 16-byte aligned, ws_bytes >=
  *                kv_attention_workspace_bytes(batch, q_heads, kv_heads, head_dim,
  *                max_query_len); zero-filled once when allocated, each call leaves it
- *                ready for the next.  Calls that overlap on the GPU must not share one.
+ *                ready for the next, but for one whose wait expired (FP4_ERR_TIMEOUT):
+ *                it sets the workspace's third 32-bit word, and later calls report
+ *                FP4_ERR_TIMEOUT too until the workspace is zero-filled again.
+ *                Calls that overlap on the GPU must not share one.
  *                Calls of any kind may take turns on one workspace that has the bytes each
  *                needs: one sized for the longest max_query_len serves shorter ones.
  *   out          bf16[tokens, q_heads, head_dim], 16-byte aligned

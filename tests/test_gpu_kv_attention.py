@@ -328,3 +328,19 @@ def test_a_negative_total_counts_as_no_keys(B, dim, new, window):
         mine = slice(new, 2 * new)
         assert not got[mine].any() and torch.isneginf(sums[mine]).all()
         assert torch.equal(got[:new], want[:new]) and torch.equal(got[2 * new:], want[2 * new:])
+
+
+@pytest.mark.parametrize("new", [1, 12])
+def test_a_workspace_left_by_an_expired_wait_is_reported(B, new):
+    """The mark of such a call: every later one reports it, until the workspace is zeroed."""
+    p = R.Problem(2, 128, 2, 4, 64, [700, 90], [new] * 2, seed=1)
+    cache, t = p.cuda(B)
+    _, ws = check(B, p)
+    run = lambda: B.kv_attention(cache, t["q"], t["query_start"], t["total_lens"], t["block_table"], ws, max_query_len=new)  # noqa: E731
+    ws.view(torch.int32)[2] = 1
+    for _ in range(2):
+        run()
+        assert B.fp4_check_device_error() == B.FP4_ERR_TIMEOUT
+    ws.zero_()
+    check(B, p, ws=ws)
+    assert not ws.view(torch.int32)[:16].any()
