@@ -10,14 +10,16 @@
 // Scores on the 5th-generation tensor cores, K never dequantized: a tile of 128
 // keys is the block-scaled FP4 A operand of tcgen05.mma.kind::mxf4nvf4 (one key per
 // accumulator lane, its E4M3/E8M0 scales applied by the hardware), and the R query
-// rows are the B operand, each written as kTerms = 6 FP4 terms in radix 8,
+// rows are the B operand, each written as kTerms = 8 FP4 terms in radix 8,
 //     q = 2^e0 (sum_t d_t 2^(6-3t) + rest),  d_t in {-4..4},  max|q| / 2^e0 in [128, 256),
-// exact but for |rest| <= 2^-10, 2^-17 of the row's largest element.  Terms t and t + 3 of row r
-// add up in column (t mod 3) R + r (two MMAs a step of 64 channels, ~143 cycles each whatever
-// N is), so the thread that owns a key sums a row's three columns in registers: no
-// score crosses a lane.  (Six columns and one MMA cost the consumers 27 more instructions per 32
-// keys and eight rows; one column and six MMAs would take the tensor cores longer than
-// the tile's DRAM time.)  Dequantizing K instead would cost an instruction stream as long as
+// exact but for |rest| <= 2^-16, 2^-23 of the row's largest element, fp32's own precision of it.
+// (With six, 2^-17, a channel of q a thousand times its others moved scores by 0.05.)
+// Terms t and t + 3, t < 3, of row r add up in column t R + r, terms 6 and 7 in column 3 R + r,
+// in units of 2^-18 (E4M3 has no scale small enough for them): two MMAs a step of 64 channels,
+// ~143 cycles each whatever N is.  The thread that owns a key sums a row's four columns in
+// registers: no score crosses a lane.  (A column a term and one MMA cost the consumers 27 more
+// instructions per 32 keys and eight rows; one column and an MMA a term would take the tensor
+// cores longer than the tile's DRAM time.)  Dequantizing K instead would cost an instruction stream as long as
 // V's, the larger half of what the SM issues.
 //
 // Values in registers: a warp owns 32 keys of the tile (its tensor-memory lane
@@ -79,9 +81,12 @@
 namespace fp4 {
 namespace {
 
-constexpr int kTerms = 6;
-constexpr int kCols = 3;                 // score columns of a row
+constexpr int kTerms = 8;
+constexpr int kCols = 4;                 // score columns of a row
 constexpr int kChains = kTerms / kCols;  // terms added into each
+constexpr float kLastUnit = 0x1p-18f;    // unit of the last column
+// term of chain ch in column c
+__host__ __device__ constexpr int term_of(int ch, int c) { return c < 3 ? 3 * ch + c : 6 + ch; }
 constexpr int kTile = 128;  // keys per tile: the MMA's M
 constexpr int kMaxStages = 12;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -149,10 +154,10 @@ struct Dec {
   static constexpr int kSlot = kR * D + 2 * kR;              // floats of a workspace piece (output, m, l)
 };
 
-// byte of the term scale 2^(7-3t) (see the FP4 GEMV's terms: exact in both formats)
+// byte of the term scale 2^(7-3t), of terms 6 and 7 times 2^18 (see the FP4 GEMV's terms: exact in both formats)
 template <int MODE>
 __device__ __forceinline__ uint32_t term_scale(int t) {
-  const int e = 7 - 3 * t;
+  const int e = 7 - 3 * (t < 6 ? t : t - 6);
   if (MODE == 1) return (uint32_t)(127 + e);
   return e >= -6 ? (uint32_t)((e + 7) << 3) : (1u << (e + 9));
 }
@@ -336,8 +341,20 @@ struct Seg {
   int64_t start;  // where the item's tile 0 sits in the sequence
 };
 
-// Query rows r0 .. r0 + N - 1 of a segment as FP4 terms in the B operands' order (a warp): term t of row r is
-// row (t mod kCols) R + r of chain t / kCols.  Writes each row's score factor.
+// |v| < 256 -> v's eight radix-8 digits in -4..4 as e2m1 codes of half of each, the lowest, of 2^-15, in the lowest nibble.
+// With four added to every digit they are three bits each (the highest four) of an integer; spread to a nibble each,
+// a digit below 4 (u) is the code of -(4 - u), one from 4 on that of u - 4.
+__device__ __forceinline__ uint32_t radix8_codes(float v) {
+  uint32_t w = (uint32_t)__float2int_rn(v * 32768.0f) + 04444'4444u;
+  w = (w & 0xFFFu) | ((w & 0x1FFF000u) << 4);
+  w = (w & 0x003F003Fu) | ((w & 0x1FC00FC0u) << 2);
+  w = (w & 0x07070707u) | ((w & 0x78383838u) << 1);
+  const uint32_t below = ~((w >> 2) | (w >> 3)) & 0x11111111u;  // 4 - u = (u ^ 3) + 1; 8 for the sign
+  return ((w & 0x33333333u) ^ (3u * below)) + 9u * below + ((w >> 1) & 0x40000000u);
+}
+
+// Query rows r0 .. r0 + N - 1 of a segment as FP4 terms in the B operands' order (a warp): term term_of(ch, c) of row r is
+// row c R + r of chain ch.  Writes each row's score factor.
 template <int MODE, int D, int NB, int N>
 __device__ __forceinline__ void query_rows(const KvAttentionArgs& a, uint8_t* dst, const int64_t* row_q, float* row_c,
                                            int r0, int lane) {
@@ -363,30 +380,25 @@ __device__ __forceinline__ void query_rows(const KvAttentionArgs& a, uint8_t* ds
     const float pre = __uint_as_float((261u - min(E, 254u)) << 23);  // 2^-e0, e0 = E - 134
     if (lane == 0)
       row_c[r0 + k] = mb < 0x7F80u ? mult * (E >= 8u ? __uint_as_float((E - 7u) << 23) : 0x1p-127f) : __int_as_float(0x7FC00000);
-    float v[EL];
+    uint32_t even[EL / 2], odd[EL / 2];  // digits 0, 2, 4, 6 and 1, 3, 5, 7 of a pair of elements, a byte each
 #pragma unroll
     for (int e = 0; e < EL / 2; ++e) {
-      v[2 * e] = bf16_lo(x[k][e]) * pre;
-      v[2 * e + 1] = bf16_hi(x[k][e]) * pre;
+      const uint32_t d0 = radix8_codes(bf16_lo(x[k][e]) * pre), d1 = radix8_codes(bf16_hi(x[k][e]) * pre);
+      even[e] = (d0 & 0x0F0F0F0Fu) | ((d1 << 4) & 0xF0F0F0F0u);
+      odd[e] = ((d0 >> 4) & 0x0F0F0F0Fu) | (d1 & 0xF0F0F0F0u);
     }
+    const uint32_t at = (uint32_t)((r0 + k) * C::kRowB + lane * (EL / 2));
+    uint8_t* row = dst + (at ^ ((at >> 3) & C::kSwz));
+    static_assert(((C::kR * C::kRowB) & (C::kSwz << 3 | ((C::kSwz << 3) - 1))) == 0, "a column starts at the same place of the swizzle");
 #pragma unroll
     for (int t = 0; t < kTerms; ++t) {
-      // d / 2 = rint(v 2^(3t-6)) / 2 by adding and subtracting 1.5 * 2^22; v keeps the rest
-      const float inv = __int_as_float((127 + 3 * t - 7) << 23), sc = __int_as_float((127 + 7 - 3 * t) << 23);
-      uint32_t codes = 0;
-#pragma unroll
-      for (int e = 0; e < EL / 2; ++e) {
-        const float d0 = __fsub_rn(__fmaf_rn(v[2 * e], inv, 6291456.0f), 6291456.0f);
-        const float d1 = __fsub_rn(__fmaf_rn(v[2 * e + 1], inv, 6291456.0f), 6291456.0f);
-        v[2 * e] = __fmaf_rn(-sc, d0, v[2 * e]);
-        v[2 * e + 1] = __fmaf_rn(-sc, d1, v[2 * e + 1]);
-        codes |= e2m1x2_rn(d0, d1) << (8 * e);
-      }
-      uint32_t off = (uint32_t)(((t % kCols) * C::kR + r0 + k) * C::kRowB + lane * (EL / 2));
-      off = (off ^ ((off >> 3) & C::kSwz)) + (t / kCols) * C::kQChain;
-      if (EL == 2) dst[off] = (uint8_t)codes;
-      else if (EL == 4) *reinterpret_cast<uint16_t*>(dst + off) = (uint16_t)codes;
-      else *reinterpret_cast<uint32_t*>(dst + off) = codes;
+      const int i = (7 - t) >> 1;  // term t is digit 7 - t
+      const uint32_t* by = t & 1 ? even : odd;
+      uint8_t* to = row + (t < 6 ? t % 3 : 3) * (C::kR * C::kRowB) + (t < 6 ? t / 3 : t - 6) * C::kQChain;
+      const uint32_t two = __byte_perm(by[0], by[1 % (EL / 2)], i | (i + 4) << 4);
+      if (EL == 2) *to = (uint8_t)(by[0] >> (8 * i));
+      else if (EL == 4) *reinterpret_cast<uint16_t*>(to) = (uint16_t)two;
+      else *reinterpret_cast<uint32_t*>(to) = __byte_perm(two, __byte_perm(by[2 % (EL / 2)], by[3 % (EL / 2)], i | (i + 4) << 4), 0x5410);
     }
   }
 }
@@ -641,7 +653,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int n = 32 * c + lane;
-        v[c] = n < kCols * R ? term_scale<MODE>(ch * kCols + n / R) * 0x01010101u : 0u;
+        v[c] = n < kCols * R ? term_scale<MODE>(term_of(ch, n / R)) * 0x01010101u : 0u;
       }
       reinterpret_cast<uint4*>(smem + offOut)[32 * ch + lane] = make_uint4(v[0], v[1], v[2], v[3]);
     }
@@ -787,6 +799,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
     const uint32_t vc0 = vc ^ ((vc >> 3) & C::kSwz), vc1 = (vc0 + 128) ^ 16;
     const uint32_t vsc = (uint32_t)((32 * quad + key_of<D>(c, 0)) * C::kSB + g * CH / C::kGroup);
     constexpr int KSTEP = 128 / C::kRowB;  // keys between i = 0 and i = 1
+    const uint64_t unit2 = pack2(__float_as_uint(kLastUnit), __float_as_uint(kLastUnit));
     float* mn = set_n + set * R;
     const uint32_t mn_a = smem_u32(mn);
     // the first segment's query terms
@@ -869,7 +882,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               t2[r] = add2(add2(pack2(d[0][2 * r], d[0][2 * r + 1]), pack2(d[1][2 * r], d[1][2 * r + 1])),
-                           pack2(d[2][2 * r], d[2][2 * r + 1]));
+                           fma2(pack2(d[3][2 * r], d[3][2 * r + 1]), unit2, pack2(d[2][2 * r], d[2][2 * r + 1])));
               x2[r] = fma2(t2[r], f2[r], n2[r]);
             }
           }

@@ -457,7 +457,9 @@ size_t kv_attention_workspace_bytes(int64_t batch, int64_t q_heads, int64_t kv_h
  *   out          bf16[tokens, q_heads, head_dim], 16-byte aligned
  *   lse          fp32[tokens, q_heads] or NULL: log of the sum of exp(score), with which
  *                results over disjoint keys can be merged
- * Scores, softmax statistics and sums are fp32.  Slots that no query of the call
+ * Scores, softmax statistics and sums are fp32; with few query rows (up to 32 a kv
+ * head, or head_dim 256) what lies below 2^-23 of a query row's largest element
+ * is not seen by its scores.  Slots that no query of the call
  * sees may hold anything; a value of V that is NaN for one query of a request
  * (a NaN scale) may make the request's other queries of the same call NaN too,
  * those before it among them (their probability of it is 0, and 0 NaN is NaN).

@@ -1,0 +1,73 @@
+"""kv_attention's scores, against 64 bits, where a channel of the queries is far above the others.
+
+The scores are claimed to be fp32 sums of the exact products, but for what the few-row kernel leaves of a query,
+2^-23 of the row's largest element.  A sum of at most 64 rounded partial sums (the tensor cores add 16 or 64 products at a
+time, the other kernel one by one in groups of at most 32) is within 64 2^-24 of the sum of the magnitudes, so
+    ds = scale (2^-18 max_j sum_d |q_d k_jd| + 2^-23 max|q| max_j |k_j|_1)
+bounds a score's error, and, with A = sum_j p_j |v_j| / sum_j p_j and p in at least 8 significant bits,
+    |out - exact| <= 2^-8 |exact| + ((1 + 2^-8) exp(2 ds) - 1) A + 2^-126
+    |lse - exact| <= ds + 2^-14
+(what exp2, the sums of p and the last logarithm add is below 2^-14)."""
+import numpy as np
+import pytest
+import torch
+
+import kv_reference as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def B():
+    from block_scaled_fp4_fp_gb300 import build, binding
+    build.build()
+    binding.fp4_init(0)
+    return binding
+
+
+def check_tight(B, p, scale=None):
+    cache, t = p.cuda(B)
+    scale = p.dim ** -0.5 if scale is None else scale
+    ws = B.kv_attention_workspace(cache, len(p.new), p.q_heads, max(p.new))
+    sums = torch.empty((p.q.shape[0], p.q_heads), device="cuda")
+    out = B.kv_attention(cache, t["q"], t["query_start"], t["total_lens"], t["block_table"], ws, max_query_len=max(p.new), scale=scale,
+                         lse=sums)
+    assert B.fp4_check_device_error() == B.FP4_OK
+    got, lse = out.double().cpu().numpy(), sums.double().cpu().numpy()
+    want, wlse, _ = p.attention(scale)
+    group = p.q_heads // p.kv_heads
+    q = p.q.double().numpy()
+    for b, n in enumerate(p.total):
+        j = np.arange(n)
+        pg, sl = p.table[b, j // p.page], j % p.page
+        for h in range(p.kv_heads):
+            k, v = (np.abs(R.values(p.codes[w][pg, h, sl], p.scales[w][pg, h, sl], p.mode, np.float64(np.float32(gs or 1))))
+                    for w, gs in (("k", p.gs_k), ("v", p.gs_v)))
+            kv = R.values(p.codes["k"][pg, h, sl], p.scales["k"][pg, h, sl], p.mode, np.float64(np.float32(p.gs_k or 1)))
+            for i in range(p.new[b]):
+                t_, hs, see = p.starts[b] + i, slice(h * group, (h + 1) * group), n - p.new[b] + i + 1
+                qq = q[t_, hs]
+                ds = scale * (2.0 ** -18 * (np.abs(qq) @ k[:see].T).max(-1) + 2.0 ** -23 * np.abs(qq).max(-1) * k[:see].sum(-1).max())
+                s = qq @ kv[:see].T * scale
+                pr = np.exp(s - wlse[t_, hs][:, None])
+                bound = (2.0 ** -8 * np.abs(want[t_, hs]) + ((1 + 2.0 ** -8) * np.exp(2 * ds)[:, None] - 1) * (pr @ v[:see]) + 2.0 ** -126)
+                assert (np.abs(got[t_, hs] - want[t_, hs]) <= bound).all(), \
+                    f"token {t_}, kv head {h}: off by {np.abs(got[t_, hs] - want[t_, hs]).max():.3g} of {bound.max():.3g}"
+                assert (np.abs(lse[t_, hs] - wlse[t_, hs]) <= ds + 2.0 ** -14).all()
+
+
+KERNELS = [  # dim, kv heads, group, queries: few rows (one block of eight, two), prompts, other head sizes
+    (128, 2, 4, 1), (128, 1, 8, 2), (128, 1, 8, 9), (64, 2, 8, 1), (64, 1, 8, 3), (64, 1, 4, 20), (256, 1, 4, 1), (256, 1, 2, 9), (96, 1, 4, 2),
+]
+
+
+@pytest.mark.parametrize("mode", [2, 1])
+@pytest.mark.parametrize("dim,kv,group,new", KERNELS)
+@pytest.mark.parametrize("large", [0.0, 2.0 ** 7, 2.0 ** 10, 2.0 ** 12, 2.0 ** 14])
+def test_one_channel_of_the_queries_far_above_the_others(B, mode, dim, kv, group, new, large):
+    """The keys are zero in that channel, so that the others decide."""
+    p = R.Problem(mode, dim, kv, group, 64, [400, 33, 700], [new] * 3, gs=mode == 2, seed=dim + new)
+    if large:
+        p.q[..., 13] = torch.where(p.q[..., 13] < 0, -large, large).to(torch.bfloat16)
+        p.codes["k"][..., 1] &= np.uint32(0xFF0FFFFF)
+    check_tight(B, p)
