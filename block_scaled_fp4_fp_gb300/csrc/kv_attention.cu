@@ -4,14 +4,14 @@
 //   o_i = sum_j p_ij v_j / sum_j p_ij,   p_ij = exp(scale q_i . k_j - m_i),
 //   over the keys j <= pos_i (causal), j > pos_i - window, j < total_len.
 // A block owns one (query token, query head); its warps take the visible keys 32 at a
-// time, each with its own running maximum m, sum l and output.  Scores: a lane owns a key
+// time, each with its own running maximum m, sum l and mean output.  Scores: a lane owns a key
 // and reads its whole row (q is broadcast from shared memory), so that no score
 // crosses a lane.  Outputs: a lane owns eight channels (one word of codes) of every
 // KP-th of those keys, KP = 32 / (head_dim / 8), whose probabilities and rows come
 // by shuffle.  The block joins the warps' (m, l, o) at the end.  All sums in fp32.
 // Bound by instructions: about 5 an element of K and V for every query head (no group shares them).
-// 8 requests of 4,000 tokens, 64 query heads on 8, NVFP4: heads of 96 127 us, of 32 48 us (a whole warp a key, with a
-// five-step reduction of its score: 803 and 609); a 512-token prompt, 32 heads of 96 on 8: 239 us (1220).
+// 8 requests of 4,000 tokens, 64 query heads on 8, NVFP4: heads of 96 129 us, of 32 50 us (a whole warp a key, with a
+// five-step reduction of its score: 803 and 609); a 512-token prompt, 32 heads of 96 on 8: 245 us (1220).
 #include <cuda.h>
 
 #include "../../include/fp4_gb300.h"
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_attention_any_kernel(KvAttenti
   __syncthreads();
   const int word = lane % W, sub = lane / W;  // (lanes from KP W on add nothing up)
   float o[8] = {};
-  float m = -INFINITY, l = 0.f;  // l: of this lane's keys
+  float m = -INFINITY, l = 0.f;
   for (int64_t j0 = begin + 32 * warp; j0 < end; j0 += 32 * kWarps) {
     const int n = (int)min((int64_t)32, end - j0);
     int row = 0;
@@ -121,11 +121,17 @@ __global__ void __launch_bounds__(kWarps * 32) kv_attention_any_kernel(KvAttenti
 #pragma unroll
     for (int x = 16; x; x >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
     const float ref = mn == -INFINITY ? 0.f : mn;
-    const float alpha = exp2f(m - ref), p = exp2f(s - ref);
-    m = mn;
-    l = l * alpha + p;
+    float p = exp2f(s - ref), sum = p;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] *= alpha;
+    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    const float old = l * exp2f(m - ref);
+    m = mn;
+    l = old + sum;
+    // o is the mean of the values so far, never their sum: V may be near fp32's largest numbers
+    const float inv = l == 0.f ? 0.f : 1.0f / l, keep = old * inv;
+    p *= inv;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] *= keep;
 #pragma unroll 4
     for (int k = 0; k < n; k += KP) {
       const int key = k + sub;
@@ -140,8 +146,6 @@ __global__ void __launch_bounds__(kWarps * 32) kv_attention_any_kernel(KvAttenti
       }
     }
   }
-#pragma unroll
-  for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
   if (lane == 0) {
     sm[warp] = m;
     sl[warp] = l;
@@ -156,16 +160,16 @@ __global__ void __launch_bounds__(kWarps * 32) kv_attention_any_kernel(KvAttenti
   const float ref = mm == -INFINITY ? 0.f : mm;
   float ll = 0.f;
   for (int w = 0; w < kWarps; ++w) ll += sl[w] * exp2f(sm[w] - ref);
+  const float inv = ll == 0.f ? 0.f : 1.0f / ll;
   if (threadIdx.x < D) {
     float v = 0.f;
     for (int w = 0; w < kWarps; ++w) {
       float u = 0.f;
 #pragma unroll
       for (int k = 0; k < KP; ++k) u += so[w][k * D + threadIdx.x];
-      v += u * exp2f(sm[w] - ref);
+      v += u * (sl[w] * exp2f(sm[w] - ref) * inv);
     }
-    v = ll == 0.f ? 0.f : v / ll * gsv;
-    a.out[(t * a.q_heads + head) * D + threadIdx.x] = (uint16_t)f32_to_bf16_rn(v);
+    a.out[(t * a.q_heads + head) * D + threadIdx.x] = (uint16_t)f32_to_bf16_rn(v * gsv);
   }
   if (a.lse && threadIdx.x == 0)
     a.lse[t * a.q_heads + head] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;

@@ -344,3 +344,28 @@ def test_a_workspace_left_by_an_expired_wait_is_reported(B, new):
     ws.zero_()
     check(B, p, ws=ws)
     assert not ws.view(torch.int32)[:16].any()
+
+
+def huge_values(B, dim, new):
+    """4096 keys whose V is near bf16's largest numbers: their weighted mean is one of bf16's, their weighted sum is none of fp32's.
+    All equal; of different sizes; under scores that rise by about 20 in log2 along the context."""
+    for what in ("equal", "different", "rising"):
+        p = R.Problem(1, dim, 1, 8, 64, [4096 - new, 70, 0], [new] * 3, seed=dim + new, q_std=0.3)
+        g = np.random.RandomState(dim)
+        if what == "equal":
+            p.codes["v"][:], p.scales["v"][:] = 0x22222222, 127 + 120  # code 2 is 1
+        else:
+            p.scales["v"][:] = g.randint(240, 252, p.scales["v"].shape)
+        if what == "rising":
+            j = np.arange(4096)
+            p.codes["k"][p.table[0, j // 64], 0, j % 64, 0] = 0x00000007  # channel 0 is 6 times a scale that grows
+            p.scales["k"][p.table[0, j // 64], 0, j % 64, 0] = 120 + (7 * j // 4096)
+            p.q[..., 0] = 1.75 * (dim / 64) ** 0.5
+        for w, bad in (("v", 0xFF), ("k", 0xFF)):
+            p.scales[w][p.unseen()] = bad
+        check(B, p)
+
+
+@pytest.mark.parametrize("dim,new", [(96, 1), (96, 9), (32, 1), (128, 1), (64, 2)])
+def test_values_near_the_largest_numbers(B, dim, new):
+    huge_values(B, dim, new)
