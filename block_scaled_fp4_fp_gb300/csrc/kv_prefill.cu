@@ -27,6 +27,9 @@
 // first tile's maximum and moves only when 32 probabilities sum to more than 2^24, so that
 // after the first tile the scores are read once, no maximum is taken of them and the output
 // is almost never rescaled.  p is rounded to bf16 (2^-9); scores, sums and output are fp32.
+// MXFP4's V reaches fp32's largest numbers, whose sums do not fit although their quotient does: an item whose output
+// is not finite is done again with p 2^60 smaller.  (Found at its end: watching the sum beside V's scales tile by tile took
+// the chunks below from 423 to 440 us, this to 433.)
 //
 // Work: up to 608 items are dealt out: their key tiles, with a fixed cost an item, form one
 // sequence, of which each CTA takes an equal share; a cut near an item's end moves to
@@ -40,7 +43,7 @@
 // beside the other warps' traffic and a step about 3300, the rest being the ends of items and waits for a softmax
 // (2000 cycles a tile, of which the exponentials 512).  For heads of 64 the softmax: the products take 1750 of 2900.
 //   4096-token prompt, 40 heads of 128, NVFP4:      0.160 ms, 1075 TFLOP/s
-//   4 chunks over 0..16k, 64 heads of 64, MXFP4:    0.430 ms,  716 TFLOP/s
+//   4 chunks over 0..16k, 64 heads of 64, MXFP4:    0.433 ms,  712 TFLOP/s
 // Tried and slower on the prompt: 64-key steps with two score buffers (200 us), scores fetched ahead (201), two warps a
 // row (162, and 406 on the chunks), more registers for the softmax by setmaxnreg (186).
 //
@@ -71,6 +74,9 @@ constexpr int kSnap = 8;         // a share's end moves to an item's end that is
 constexpr int kShare = 2 * kSnap; // a CTA's share at least
 constexpr float kFar = 0x1p24f;  // a row's reference moves when probabilities sum to more than this
 constexpr float kNone = -1e30f;
+// MXFP4's V may be so large that a sum of p V passes fp32 where the quotient does not.  A warp that finds it so has the item
+// done again with p at most 2^-60, and moving at 2^-32: no context has the keys to pass it then.
+constexpr float kLow = 60.f, kLowFar = 0x1p-32f;
 
 template <int D>
 struct Pre {
@@ -89,6 +95,7 @@ struct Item {
   int n[2];                   // key tiles of the two row tiles
   int tiles, twin;            // key tiles in all; both row tiles hold the same rows and take them in turn
   int stop;
+  int again;                  // done again with small p, for the softmax warps of these bits
   int piece, pieces, first;   // this piece of the item's keys, of how many; CTA of the first one
 };
 
@@ -202,6 +209,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
   uint64_t* never = xtake + 4;                                     // fault injection: nothing arrives here
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
   Item* items = reinterpret_cast<Item*>(smem + C::offBar + 512);   // [2]
+  int* again = reinterpret_cast<int*>(smem + C::offBar + 912);     // [2] warps whose output passed fp32
+  static_assert(512 + 2 * sizeof(Item) <= 656 && 656 + 4 * kSorted <= 912, "the small areas");
   int64_t* prefix = reinterpret_cast<int64_t*>(smem + C::offPre);  // [kThreads + 1] items before a thread's requests
   int64_t* cost_before = reinterpret_cast<int64_t*>(smem + C::offTiles);  // [kThreads + 1] cost of the items before an item
 
@@ -229,6 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
       mbar_init(&xtake[w], 1);
     }
     mbar_init(never, 1);
+    again[0] = again[1] = 0;
     fence_barrier_init();
   }
   if (warp == 16) {
@@ -245,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
     return (ql * group + kRows - 1) / kRows;
   };
   // few requests: the longest first (what is left for the end is then short).  More: as they come.
-  int* order = reinterpret_cast<int*>(smem + C::offBar + 640);  // [kSorted]
+  int* order = reinterpret_cast<int*>(smem + C::offBar + 656);  // [kSorted]
   const bool sorted = a.batch <= kSorted;
   if (sorted && (int)threadIdx.x < a.batch) {
     const int mine = __ldg(a.total_lens + threadIdx.x);
@@ -366,15 +376,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
     auto owner_of = [&](int64_t unit) { return (int)(((unit + 1) * shares - 1) / cost); };  // the CTA that has it, before moves
     int64_t pos = start_of(blockIdx.x);
     const int64_t end = start_of((int64_t)blockIdx.x + 1);
+    bool over = false;  // no item left
     for (int k = 0;; ++k) {
       Item* it = &items[k & 1];
       if (warp == 17) {
         if (k >= 2) mbar_wait(&iempty[k & 1], ((k >> 1) - 1) & 1, a.err, failed);
         if (k >= 1) mbar_wait(inear, (k - 1) & 1, a.err, failed);
+        Item x = {};
+        int redo = 0;
         if (lane == 0) {
-          Item x = {};
-          if (failed) {
+          if (MODE == 1 && k >= 2) redo = again[k & 1];  // item k - 2
+          if (failed || over) {
             x.stop = 1;
+          } else if (redo) {
           } else if (dealt) {
             x.stop = pos >= end;
             if (!x.stop) {
@@ -402,12 +416,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
               }
             }
           }
+          over = x.stop;
           x.tiles = max(x.n[0], x.n[1]);
           x.twin = x.row0 + 128 >= x.rows;  // no rows for the second tile: it takes every other key tile of the first's
           if (x.twin) {
             x.n[0] = (x.tiles + 1) / 2;
             x.n[1] = x.tiles / 2;
           }
+        }
+        if (MODE == 1) {
+          int at = k & 1;
+          if (k >= 1 && __shfl_sync(0xffffffffu, (int)(x.stop && !redo), 0)) {  // the last item may have to be done again
+            mbar_wait(&iempty[(k - 1) & 1], ((k - 1) >> 1) & 1, a.err, failed);
+            at = (k - 1) & 1;
+            redo = again[at];
+          }
+          if (lane == 0 && redo && !failed) {
+            x = items[at];
+            x.again = redo;
+            again[at] = 0;
+          }
+        }
+        if (lane == 0) {
           *it = x;
           mbar_arrive(&ifull[k & 1]);
         }
@@ -650,6 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
       float m = kNone;
       uint64_t l2 = 0;  // the sum, in two halves
       const int n = x.n[i], first = x.twin ? i * kKeys : 0, step = x.twin ? 2 * kKeys : kKeys;
+      const float low = MODE == 1 && x.again ? kLow : 0.f, far = MODE == 1 && x.again ? kLowFar : kFar;
       for (int j = 0; j < n; ++j, ++use) {
         const int key0 = first + j * step;
         const bool mask = __any_sync(0xffffffffu, key0 < lo || key0 + kKeys > hi);
@@ -680,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
             if (mask) hide(c, sa), hide(c + 1, sb);
             t = fmaxf(t, fmaxf(top(sa), top(sb)));
           }
-          m = fmaxf(t * cs, kNone);
+          m = fmaxf(t * cs, kNone) + low;
         }
         auto exps = [&](uint32_t (&v)[32], uint32_t (&p)[16]) -> uint64_t {
           const uint64_t c2 = pack2(cs, cs), m2 = pack2(-m, -m);
@@ -703,13 +734,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
           uint64_t sum = exps(v, p);
           float a0, a1;
           unpack2(sum, a0, a1);
-          if (__any_sync(0xffffffffu, !(a0 + a1 <= kFar))) {
+          if (__any_sync(0xffffffffu, !(a0 + a1 <= far))) {
             // a score is far above the row's reference: move it; what the row has so far is scaled down,
             // these probabilities start over
             tmem_ld32(ts + 32 * c, v);
             ld_wait();
             if (mask) hide(c, v);
-            const float t = a0 + a1 <= kFar ? m : fmaxf(top(v) * cs, m), f = exp2f(m - t);
+            const float t = a0 + a1 <= far ? m : fmaxf(top(v) * cs + low, m), f = exp2f(m - t);
             m = t;
             l2 = mul2(l2, pack2(f, f));
             st_wait();  // (the earlier ones are in place before they are read back)
@@ -787,35 +818,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
       auto outputs = [&](int p, int c) {
         return reinterpret_cast<float4*>(results + (size_t)(2 * (x.first + p) + (p == 0)) * kSlotFloats<D>) + (i * (D / 4) + 8 * c) * 128 + row;
       };
+      // Outputs are divided by the sum before anything is added to them.
       const bool whole = x.pieces == 1;
-      const float inv = l == 0.f ? 0.f : gsv / l;
+      const float inv = l == 0.f ? 0.f : (whole ? gsv : 1.0f) / l;
+      w0 *= inv;
+      w1 *= inv;
+      uint64_t seen = 0;  // 0 times every output: NaN where one is not a number or passed fp32
+      const bool mine = MODE != 1 || !x.again || (x.again >> warp & 1);  // (done again for another warp's rows)
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
         if (n > 0) {
           tmem_ld32(to + 32 * c, o);
           ld_wait();
-          if (x.twin) {
-            const bool both = x.n[1] > 0;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * w0);
+          if (x.twin && x.n[1] > 0)
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
               uint32_t p[8];
-              if (both) {
-                tmem_ld8(to + D + 32 * c + 8 * h, p);
-                ld_wait();
-              }
+              tmem_ld8(to + D + 32 * c + 8 * h, p);
+              ld_wait();
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float v = __uint_as_float(o[8 * h + e]) * w0;
-                o[8 * h + e] = __float_as_uint(both ? fmaf(__uint_as_float(p[e]), w1, v) : v);
-              }
+              for (int e = 0; e < 8; ++e) o[8 * h + e] = __float_as_uint(fmaf(__uint_as_float(p[e]), w1, __uint_as_float(o[8 * h + e])));
             }
-          }
+          if (MODE == 1)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) seen = fma2(pack2(o[e], o[e + 1]), 0ull, seen);
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0;
         }
-        if (!whole) {
+        if (!mine) {
+        } else if (!whole) {
           uint4* dst = reinterpret_cast<uint4*>(outputs(x.piece, c));
 #pragma unroll
           for (int e = 0; e < 8; ++e) __stcg(dst + 128 * e, make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
@@ -826,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
             uint32_t v[4];
 #pragma unroll
             for (int h = 0; h < 4; ++h)
-              v[h] = pack_bf16x2_rn(__uint_as_float(o[8 * e + 2 * h]) * inv, __uint_as_float(o[8 * e + 2 * h + 1]) * inv);
+              v[h] = pack_bf16x2_rn(__uint_as_float(o[8 * e + 2 * h]), __uint_as_float(o[8 * e + 2 * h + 1]));
             dst[e] = make_uint4(v[0], v[1], v[2], v[3]);
           }
         }
@@ -836,8 +871,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
         __syncwarp();
         if (lane == 0) mbar_arrive(&xtake[warp & 3]);
       }
-      bool last = whole;
-      if (!whole) {  // the warp whose piece comes last joins the item's pieces of its rows, in their order
+      bool done = mine;
+      if (MODE == 1 && !x.again) {
+        float s0, s1;
+        unpack2(seen, s0, s1);
+        done = !__any_sync(0xffffffffu, real && l < INFINITY && !(s0 + s1 == 0.f));
+        if (!done && lane == 0) atomicOr(&again[k & 1], 1 << warp);
+      }
+      bool last = whole && done;
+      if (!whole && done) {  // the warp whose piece comes last joins the item's pieces of its rows, in their order
         __stcg(sums(x.piece), m);
         __stcg(sums(x.piece) + 128, l);
         __threadfence();
@@ -865,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
 #pragma unroll 2
             for (int p = 0; p < np; ++p) {
               const float4* src = outputs(p, 0) + 512 * c;
-              const float w = exp2f(__ldcg(sums(p)) - m);
+              const float w = __ldcg(sums(p) + 128) * exp2f(__ldcg(sums(p)) - m) * join;
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const float4 v = __ldcg(src + 128 * e);
@@ -881,7 +923,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
               for (int e = 0; e < 2; ++e) {
                 uint32_t v[4];
 #pragma unroll
-                for (int h = 0; h < 4; ++h) v[h] = pack_bf16x2_rn(o[8 * e + 2 * h] * join, o[8 * e + 2 * h + 1] * join);
+                for (int h = 0; h < 4; ++h) v[h] = pack_bf16x2_rn(o[8 * e + 2 * h], o[8 * e + 2 * h + 1]);
                 dst[e] = make_uint4(v[0], v[1], v[2], v[3]);
               }
             }

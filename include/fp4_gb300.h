@@ -459,7 +459,9 @@ size_t kv_attention_workspace_bytes(int64_t batch, int64_t q_heads, int64_t kv_h
  *                results over disjoint keys can be merged
  * Scores, softmax statistics and sums are fp32; with few query rows (up to 32 a kv
  * head, or head_dim 256) what lies below 2^-23 of a query row's largest element
- * is not seen by its scores.  Slots that no query of the call
+ * is not seen by its scores.  With more rows, where a sum of p V passes fp32 the
+ * rows concerned are summed again with p 2^60 smaller (MXFP4), so that beside such
+ * channels those below about 2^-66 are lost.  Slots that no query of the call
  * sees may hold anything; a value of V that is NaN for one query of a request
  * (a NaN scale) may make the request's other queries of the same call NaN too,
  * those before it among them (their probability of it is 0, and 0 NaN is NaN).

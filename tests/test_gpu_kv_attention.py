@@ -369,3 +369,20 @@ def huge_values(B, dim, new):
 @pytest.mark.parametrize("dim,new", [(96, 1), (96, 9), (32, 1), (128, 1), (64, 2)])
 def test_values_near_the_largest_numbers(B, dim, new):
     huge_values(B, dim, new)
+
+
+@pytest.mark.parametrize("dim,new", [(64, 12), (128, 9), (128, 20), (64, 130)])
+def test_values_near_the_largest_numbers_in_prompts(B, dim, new):
+    huge_values(B, dim, new)
+
+
+def test_values_near_the_largest_numbers_in_many_short_chunks(B):
+    """Items handed out one by one, of which most have to be done again; twice, on one workspace."""
+    batch = 320
+    cached, new = [60 + (7 * b) % 150 for b in range(batch)], [(b % 6) if b % 50 else 6 for b in range(batch)]
+    p = R.Problem(1, 64, 2, 8, 16, cached, new, seed=5, q_std=0.3)
+    p.scales["v"][:] = np.random.RandomState(1).randint(236, 252, p.scales["v"].shape)
+    p.scales["v"][p.unseen()] = 0xFF
+    first, ws = check(B, p)
+    again, _ = check(B, p, ws=ws)
+    assert torch.equal(first, again)
