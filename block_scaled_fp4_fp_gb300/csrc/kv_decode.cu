@@ -37,13 +37,12 @@
 // Every quadrant of every group keeps its own running reference m, sum and output:
 // they meet only at the end of a (request, kv head).
 //
-// Range.  p = 2^(s - m) is rounded to f16 (2^-11).  m is set kHead below the largest
-// score and moves only when a score passes it by kMax: p stays between f16's
-// largest value and, for scores within 2^23 of m, its rounding error stays below
-// 2^-9 of p.  A warp whose tile holds a smaller p (not zero: down to 2^-126) multiplies that
-// tile in bf16 instead: codes to bf16 by shifts and masks (twice the instructions
-// of the converter), p with bf16's range.  Sharp score distributions pay this; no
-// probability is lost in either.
+// Range.  p = 2^(s - m) is rounded to f16 (2^-11, while p is at least 2^-14; 2^-9 at 2^-16, where f16 is
+// subnormal).  m is set kHead below the largest score and moves only when a score passes it by kMax,
+// so that p stays below f16's largest value.  A warp whose tile holds a p below 2^-kTiny (not zero: down to
+// 2^-126) multiplies that tile in bf16 instead: codes to bf16 by shifts and masks (twice the
+// instructions of the converter), p with bf16's range.  Sharp score distributions pay this; every p counts with
+// eight bits in either, also where V is zero at the keys of the large ones.
 // MXFP4's E8M0 scales have the range of fp32, f16 has not: a thread's V values are
 // held relative to 2^E, E the largest scale exponent so far of the channel group it owns;
 // a tile with scales 2^20 below it takes the bf16 form too.
@@ -96,7 +95,7 @@ constexpr int kSnap = 6;
 constexpr int kMinShare = 8;  // units of a CTA at least (of all requests together, before boundaries move)
 constexpr float kHead = 7.0f;   // a new reference m is the largest score less this (log2)
 constexpr float kMax = 15.0f;   // and moves when a score passes it by this: p <= 2^15
-constexpr float kTiny = 23.0f;  // scores further below m than this need bf16's range
+constexpr float kTiny = 16.0f;  // scores further below m than this need bf16's range
 constexpr float kNone = -1e30f; // m before any score: exp2 of a hidden key's -inf less this is 0, of this less a score too
 
 template <int MODE, int D, int NB>

@@ -71,3 +71,21 @@ def test_one_channel_of_the_queries_far_above_the_others(B, mode, dim, kv, group
         p.q[..., 13] = torch.where(p.q[..., 13] < 0, -large, large).to(torch.bfloat16)
         p.codes["k"][..., 1] &= np.uint32(0xFF0FFFFF)
     check_tight(B, p)
+
+
+@pytest.mark.parametrize("mode", [2, 1])
+@pytest.mark.parametrize("dim,new", [(128, 1), (64, 1), (256, 1), (128, 2), (128, 12), (64, 20), (96, 1)])
+@pytest.mark.parametrize("below", [10.0, 20.0, 24.0, 28.5, 40.0, 100.0])
+def test_small_probabilities_count_with_eight_bits(B, mode, dim, new, below):
+    """One key `below` above the others in log2 has zeros for values in some channels: there the others decide, however small
+    their probabilities are."""
+    p = R.Problem(mode, dim, 1, 8, 64, [31 - new], [new], seed=dim + new)
+    p.codes["k"][:] = 0
+    p.scales["k"][..., 0] = 0x38 if mode == 2 else 127  # 1
+    p.codes["k"][p.table[0, 0], 0, 0, 0] = 0x7  # 6 in channel 0 of key 0
+    p.codes["v"][p.table[0, 0], 0, 0, 1:] = 0
+    for w in "kv":
+        p.scales[w][p.unseen()] = 0x7F if mode == 2 else 0xFF
+    p.q[:] = 0
+    p.q[..., 0] = below / 6 / 1.4426950408889634 * dim ** 0.5
+    check_tight(B, p)
