@@ -437,6 +437,7 @@ size_t kv_attention_workspace_bytes(int64_t batch, int64_t q_heads, int64_t kv_h
  * pos = total_lens[b] - (query_start[b+1] - t), over the keys j with 0 <= j <= pos
  * and, when window > 0, j > pos - window, of kv head h / (q_heads / kv_heads).
  * A row that sees no key gives zeros (lse = -inf); a negative total counts as 0.
+ * softmax_scale is positive and finite.
  *   q            bf16[tokens, q_heads, head_dim], 16-byte aligned; strides in elements,
  *                multiples of 8;  q_heads a multiple of kv_heads
  *   query_start  int32[batch+1], total_lens int32[batch] (kv_plan's outputs, after
@@ -457,14 +458,22 @@ size_t kv_attention_workspace_bytes(int64_t batch, int64_t q_heads, int64_t kv_h
  *   out          bf16[tokens, q_heads, head_dim], 16-byte aligned
  *   lse          fp32[tokens, q_heads] or NULL: log of the sum of exp(score), with which
  *                results over disjoint keys can be merged
- * Scores, softmax statistics and sums are fp32; with few query rows (up to 32 a kv
- * head, or head_dim 256) what lies below 2^-23 of a query row's largest element
- * is not seen by its scores.  With more rows, where a sum of p V passes fp32 the
- * rows concerned are summed again with p 2^60 smaller (MXFP4), so that beside such
- * channels those below about 2^-66 are lost.  Slots that no query of the call
- * sees may hold anything; a value of V that is NaN for one query of a request
- * (a NaN scale) may make the request's other queries of the same call NaN too,
- * those before it among them (their probability of it is 0, and 0 NaN is NaN).
+ * What is held in fewer bits than fp32: the probabilities, of which the product with
+ * V takes bf16's 8 bits or, with few query rows, where its range allows f16's 9 to
+ * 11; their sum takes them unrounded.
+ * Scores, softmax statistics and sums are fp32, a score within fp32's rounding of
+ * the sum of its products.  With few query rows (up to 32 a kv head, or head_dim
+ * 256) what lies below 2^-23 of a query row's largest element is not seen by its
+ * scores.  A score's size is to stay below 2^30 (fp32 rounds larger ones by whole
+ * powers of e: rows may then be zeros or NaN), and with few rows the scales of an
+ * MXFP4 K between 2^-100 and 2^110 (a row's products are formed with its largest
+ * element brought to between 128 and 256).  With more rows, where a sum of p V
+ * passes fp32 (MXFP4), the rows concerned are summed again with p 2^60 smaller, and
+ * beside such channels those below about 2^-66 are lost.
+ * Slots that no query of the call sees may hold anything; a value of V that is NaN
+ * for one query of a request (a NaN scale) may make the request's other queries of
+ * the same call NaN too, those before it among them (their probability of it is 0,
+ * and 0 NaN is NaN).
  * A page id outside [0, num_pages),
  * a request with more than max_query_len queries or more tokens than its table
  * row holds makes the next fp4_check_device_error return FP4_ERR_INVALID_ARG
