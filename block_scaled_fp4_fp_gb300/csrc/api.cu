@@ -572,7 +572,7 @@ fp4_status kv_append(const fp4_kv_cache* cache, const fp4_bf16* k, int64_t k_tok
 size_t kv_attention_workspace_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                                     int64_t max_query_len) {
   if (batch < 1 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || head_dim < 32 || head_dim > 256 ||
-      max_query_len < 1)
+      head_dim % 32 != 0 || max_query_len < 1)
     return 0;
   return kv_attention_ws_bytes(q_heads, kv_heads, head_dim, max_query_len);
 }

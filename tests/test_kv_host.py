@@ -171,3 +171,8 @@ def test_binding_refuses_tensors_the_kernels_would_misread(B):
                     ("out", torch.zeros((3, 4, 128))), ("out", torch.zeros((2, 4, 128), dtype=bf)),
                     ("out", torch.zeros((3, 4, 256), dtype=bf)[..., ::2]), ("lse", torch.zeros((3, 4), dtype=bf)), ("lse", torch.zeros((4, 3)))):
         refused(name, B.kv_attention, good, **{name: t})
+
+
+def test_workspace_bytes_of_a_head_size_no_call_takes(B):
+    f = B.lib().kv_attention_workspace_bytes
+    assert f(1, 8, 8, 40, 1) == 0 and f(1, 8, 8, 100, 700) == 0 and f(1, 8, 8, 96, 1) > 0
