@@ -14,7 +14,7 @@ namespace fp4 {
 namespace {
 
 // ----------------------------------------------------------------- kv_plan --
-//   old_b  = ceil(cached_b / P),  need_b = ceil((cached_b + new_b) / P)
+//   old_b  = ceil(cached_b / P),  need_b = ceil((cached_b + new_b) / P), both at most the entries of a table row
 //   page j of request b, old_b <= j < need_b, is free[first_b + j - old_b],
 //   first_b = sum over b' < b of (need - old);  query_start = exclusive sum of new
 //   token t of request r sits at position p = cached_r + t - query_start[r], slot
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(
     }
     const int64_t old = (c + pmask) >> page_shift, need = (c + n + pmask) >> page_shift;
     bad |= need > max_pages;
-    int64_t v[2] = {n, need - old}, incl[2];
+    int64_t v[2] = {n, min(need, (int64_t)max_pages) - min(old, (int64_t)max_pages)}, incl[2];  // (no page without an entry)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       incl[k] = warp_scan_incl(v[k], lane);
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(
     const int r = owner_of(first, B, (int)f);
     const int c = max(__ldg(cached + r), 0);
     const int64_t j = (((int64_t)c + pmask) >> page_shift) + f - first[r];
-    if (j < max_pages) table[r * table_stride + j] = __ldg(free_pages + f);
+    table[r * table_stride + j] = __ldg(free_pages + f);
   }
 }
 

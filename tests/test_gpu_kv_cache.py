@@ -155,3 +155,20 @@ def test_the_cache_reads_as_matrices_of_the_library(B):
     xq, xs = B.fp4_quantize(k.reshape(-1, 128), B.MODE_MXFP4)
     assert torch.equal(got.reshape(-1, 128), B.fp4_dequantize(xq, xs, mode=B.MODE_MXFP4))
     assert torch.equal(dk, -dv)
+
+
+def test_plan_takes_no_page_that_no_row_holds(B):
+    """Where a table row is full, the pages it has no entry for stay free: the next request's are the next of the list, and
+    pages_taken counts what the rows hold."""
+    table = torch.full((4, 3), -7, dtype=torch.int32, device="cuda")
+    table[:, 0] = torch.arange(4)
+    free = torch.arange(100, 109, dtype=torch.int32, device="cuda")
+    # one page too many by three; exactly full; past its row already; one that fits
+    pl = B.kv_plan(ints([16, 16, 100, 16]), ints([80, 32, 30, 16]), free, table, 16, 158)
+    assert B.fp4_check_device_error() == B.FP4_ERR_INVALID_ARG
+    assert table.tolist() == [[0, 100, 101], [1, 102, 103], [2, -7, -7], [3, 104, -7]]
+    assert int(pl.pages_taken) == 5
+    slots = pl.slot_map.tolist()
+    assert slots[:32] == list(range(1600, 1632)) and slots[32:80] == [-1] * 48
+    assert slots[80:112] == list(range(1632, 1664)) and slots[112:142] == [-1] * 30
+    assert slots[142:] == list(range(1664, 1680))
