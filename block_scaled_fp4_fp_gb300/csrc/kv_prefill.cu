@@ -26,7 +26,7 @@
 // Softmax: a thread owns a row.  P is bf16 and so has fp32's range: the reference m_r is the
 // first tile's maximum and moves only when 32 probabilities sum to more than 2^24, so that
 // after the first tile the scores are read once, no maximum is taken of them and the output
-// is almost never rescaled.  p is rounded to bf16 (2^-9), once; scores, sums and output are fp32.
+// is almost never rescaled.  p is rounded to bf16 (2^-8), once; scores, sums and output are fp32.
 // MXFP4's V reaches fp32's largest numbers, whose sums do not fit although their quotient does: an item whose output
 // is not finite is done again with p 2^60 smaller.  (Found at its end: watching the sum beside V's scales tile by tile took
 // the chunks below from 423 to 440 us, this to 433.)

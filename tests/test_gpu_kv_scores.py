@@ -5,9 +5,10 @@ The scores are claimed to be fp32 sums of the exact products, but for what the f
 time, the other kernel one by one in groups of at most 32) is within 64 2^-24 of the sum of the magnitudes, so
     ds = scale (2^-18 max_j sum_d |q_d k_jd| + 2^-23 max|q| max_j |k_j|_1)
 bounds a score's error, and, with A = sum_j p_j |v_j| / sum_j p_j and p in at least 8 significant bits,
-    |out - exact| <= 2^-8 |exact| + ((1 + 2^-8) exp(2 ds) - 1) A + 2^-126
+    |out - exact| <= 2^-8 |exact| + ((1 + 2^-8) exp(2 ds) - 1) A + 2^-126 (1 + sum_j |v_j|)
     |lse - exact| <= ds + 2^-14
-(what exp2, the sums of p and the last logarithm add is below 2^-14)."""
+(what exp2, the sums of p and the last logarithm add is below 2^-14; 2^-126 is fp32's and bf16's smallest normal number,
+below which outputs, and the p of the row's sum of at least 1, may be 0)."""
 import numpy as np
 import pytest
 import torch
@@ -36,6 +37,7 @@ def check_tight(B, p, scale=None):
     got, lse = out.double().cpu().numpy(), sums.double().cpu().numpy()
     want, wlse, _ = p.attention(scale)
     group = p.q_heads // p.kv_heads
+    bounds = np.zeros_like(want)
     q = p.q.double().numpy()
     for b, n in enumerate(p.total):
         j = np.arange(n)
@@ -50,10 +52,13 @@ def check_tight(B, p, scale=None):
                 ds = scale * (2.0 ** -18 * (np.abs(qq) @ k[:see].T).max(-1) + 2.0 ** -23 * np.abs(qq).max(-1) * k[:see].sum(-1).max())
                 s = qq @ kv[:see].T * scale
                 pr = np.exp(s - wlse[t_, hs][:, None])
-                bound = (2.0 ** -8 * np.abs(want[t_, hs]) + ((1 + 2.0 ** -8) * np.exp(2 * ds)[:, None] - 1) * (pr @ v[:see]) + 2.0 ** -126)
+                bound = (2.0 ** -8 * np.abs(want[t_, hs]) + ((1 + 2.0 ** -8) * np.exp(2 * ds)[:, None] - 1) * (pr @ v[:see])
+                         + 2.0 ** -126 * (1 + v[:see].sum(0)))
+                bounds[t_, hs] = bound
                 assert (np.abs(got[t_, hs] - want[t_, hs]) <= bound).all(), \
                     f"token {t_}, kv head {h}: off by {np.abs(got[t_, hs] - want[t_, hs]).max():.3g} of {bound.max():.3g}"
                 assert (np.abs(lse[t_, hs] - wlse[t_, hs]) <= ds + 2.0 ** -14).all()
+    return np.median(bounds / np.abs(want).mean())
 
 
 KERNELS = [  # dim, kv heads, group, queries: few rows (one block of eight, two), prompts, other head sizes
@@ -89,3 +94,16 @@ def test_small_probabilities_count_with_eight_bits(B, mode, dim, new, below):
     p.q[:] = 0
     p.q[..., 0] = below / 6 / 1.4426950408889634 * dim ** 0.5
     check_tight(B, p)
+
+
+@pytest.mark.parametrize("mode", [2, 1])
+@pytest.mark.parametrize("dim,new", [(128, 1), (64, 1), (256, 1), (128, 2), (64, 9), (128, 30), (96, 2)])
+@pytest.mark.parametrize("scale", [None, 3.0])
+def test_sharp_and_rising_scores_closely(B, mode, dim, new, scale):
+    """Scores that grow along the context, so that the references move, and that leave a few keys or one."""
+    p = R.Problem(mode, dim, 1, 8, 64, [1500, 640], [new] * 2, seed=3, q_std=12.0)
+    for b in range(2):
+        j = np.arange(p.total[b])
+        grow = 0x20 + 24 * j // p.total[b] if mode == 2 else 124 + 4 * j // p.total[b]
+        p.scales["k"][p.table[b, j // 64], 0, j % 64] = grow[:, None].astype(np.uint8)
+    assert check_tight(B, p, scale) < 0.5  # of the outputs' mean size: zeros would not pass
