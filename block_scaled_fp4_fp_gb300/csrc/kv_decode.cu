@@ -75,6 +75,7 @@
 #include "../../include/fp4_gb300.h"
 #include "common.cuh"
 #include "kv_common.cuh"
+#include "kv_split.h"
 #include "launch.h"
 
 namespace fp4 {
@@ -89,10 +90,6 @@ __host__ __device__ constexpr int term_of(int ch, int c) { return c < 3 ? 3 * ch
 constexpr int kTile = 128;  // keys per tile: the MMA's M
 constexpr int kMaxStages = 12;
 constexpr float kLog2e = 1.4426950408889634f;
-// Boundaries between the CTAs' shares within this many units of an item's end are moved there: a piece costs
-// two CTAs and its join more than the tiles it moves.
-constexpr int kSnap = 6;
-constexpr int kMinShare = 8;  // units of a CTA at least (of all requests together, before boundaries move)
 constexpr float kHead = 7.0f;   // a new reference m is the largest score less this (log2)
 constexpr float kMax = 15.0f;   // and moves when a score passes it by this: p <= 2^15
 constexpr float kTiny = 16.0f;  // scores further below m than this need bf16's range
@@ -239,16 +236,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 }
 template <int N>
 __device__ __forceinline__ void named_sync(int id) { asm volatile("bar.sync %0, %1;" :: "r"(id), "n"(N) : "memory"); }
-
-// Where CTA k of n starts in a sequence of `all`.
-__device__ __forceinline__ int64_t share(int64_t all, int k, int n) {
-  return all <= INT32_MAX / 160 ? (int64_t)((unsigned)all * (unsigned)k / (unsigned)n) : all * k / n;
-}
-// The CTA whose share holds position `at`.
-__device__ __forceinline__ int owner(int64_t all, int64_t at, int n) {
-  return all <= INT32_MAX / 160 ? (int)(((unsigned)(at + 1) * (unsigned)n - 1) / (unsigned)all)
-                                : (int)(((at + 1) * n - 1) / all);
-}
 
 // The keys of a thread's fragment column pair c, of the slab's 16: base(c) + offset(i), i = 0..3
 // (columns 2c, 2c + 1, 2c + 8, 2c + 9).  Any order serves as long as the probabilities
@@ -496,7 +483,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
       all += scan[w];
     }
     before += incl - sum;
-    const int64_t ctas = max((int64_t)1, min((int64_t)gridDim.x, all / kMinShare));
+    const int64_t ctas = FewSplit::ctas(all, (int)gridDim.x);
     const bool has = (int64_t)blockIdx.x < ctas && all > 0;
     if (threadIdx.x == 0) {
       plan[0] = plan[1] = 0;
@@ -506,7 +493,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < 2; ++e) {  // the share's two boundaries; the thread whose requests hold one places it
-      const int64_t f = has ? share(all, blockIdx.x + e, (int)ctas) : -1;
+      const int64_t f = has ? FewSplit::share(all, blockIdx.x + e, (int)ctas) : -1;
       if (e == 1 && f == all && threadIdx.x == 0) plan[1] = all;
       if (f >= before && f < before + sum) {
         int64_t off = f - before;
@@ -518,9 +505,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
             int item = (int)((unsigned)off / (unsigned)r.cost), at = 0;  // (off < 2^31: at most 16 million keys a request)
             if (n > INT32_MAX) item = (int)(off / r.cost);
             at = (int)(off - (int64_t)item * r.cost);
-            int move = 0;  // to an end of the item, if one is near
-            if (at <= kSnap && at <= r.cost - at) move = -at;
-            else if (r.cost - at <= kSnap) move = r.cost - at;
+            const int move = FewSplit::move(at, r.cost);  // to an end of the item, if one is near
             plan[e] = f + move;
             if (e == 0) {
               plan_at[0] = b;
@@ -1189,9 +1174,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
       }
       // A piece: into the workspace; the CTA that completes the item's count joins its pieces.  A CTA
       // starts inside at most one item (its piece 0) and ends inside at most one that it began (piece 1).
-      // (boundaries within kSnap of the item's ends have moved there)
-      const int c0 = owner(all_units, e.start + kSnap, ctas);
-      const int c1 = owner(all_units, e.start + min(e.tiles - 1, e.tiles + C::kItemCost - kSnap - 1), ctas);
+      const int c0 = FewSplit::first(all_units, e.start, ctas), c1 = FewSplit::last(all_units, e.start, e.tiles, C::kItemCost, ctas);
       auto piece = [&](int k) { return pieces + (int64_t)(2 * k + (k == c0)) * C::kSlot; };
       float* mine = piece(blockIdx.x);
       for (int x = threadIdx.x; x < X; x += kConsumers) __stcg(reinterpret_cast<float2*>(mine) + x, total(x));
@@ -1294,7 +1277,7 @@ cudaError_t launch(const DevInfo& d, const KvAttentionArgs& a, cudaStream_t s) {
   const cudaError_t e = allow_smem(d, kv_decode_kernel<MODE, D, NB>, (int)C::kSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  static_assert(kKvCtas <= 160, "share() and owner() multiply by the CTA count in 32 bits");
+  static_assert(kKvCtas <= 160, "FewSplit multiplies by the CTA count in 32 bits");
   cfg.gridDim = dim3((unsigned)std::min(kKvCtas, d.sm_count));
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;

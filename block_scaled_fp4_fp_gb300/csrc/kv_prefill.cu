@@ -59,6 +59,7 @@
 #include "../../include/fp4_gb300.h"
 #include "common.cuh"
 #include "kv_common.cuh"
+#include "kv_split.h"
 #include "launch.h"
 
 namespace fp4 {
@@ -69,9 +70,6 @@ constexpr int kKeys = 128;      // keys of a tile
 constexpr int kSorted = 64;     // requests of a call that are put in order
 constexpr int kThreads = 608;
 constexpr int kDealt = kThreads;  // calls of up to this many items are dealt out in equal shares (a thread computes an item's length)
-constexpr int kCost = 3;          // what an item costs beside its key tiles, in tiles
-constexpr int kSnap = 8;         // a share's end moves to an item's end that is nearer than this
-constexpr int kShare = 2 * kSnap; // a CTA's share at least
 constexpr float kFar = 0x1p24f;  // a row's reference moves when probabilities sum to more than this
 constexpr float kNone = -1e30f;
 // MXFP4's V may be so large that a sum of p V passes fp32 where the quotient does not.  A warp that finds it so has the item
@@ -334,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
     int len = 0;
     if ((int)threadIdx.x < total_items) {
       const Item x = describe(threadIdx.x);
-      len = kCost + max(x.n[0], x.n[1]);
+      len = PromptSplit::kCost + max(x.n[0], x.n[1]);
     }
     int64_t incl = len;
 #pragma unroll
@@ -358,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
     // ------------------------------------------------------ items, queries
     if (blockIdx.x == 0 && threadIdx.x == 17 * 32) report_expired(a);
     const int64_t cost = dealt ? cost_before[total_items] : 0;
-    const int64_t shares = min((int64_t)gridDim.x, max(max(cost / kShare, total_items), (int64_t)1));
+    const int64_t shares = PromptSplit::shares(cost, total_items, (int)gridDim.x);
     auto item_at = [&](int64_t unit) {  // the item that holds a unit of cost
       int lo = 0, hi = (int)total_items;
       while (hi - lo > 1) {
@@ -368,12 +366,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
       return lo;
     };
     auto start_of = [&](int64_t c) {  // of a CTA's share
-      const int64_t cut = min(c, shares) * cost / shares;
+      const int64_t cut = PromptSplit::cut(c, shares, cost);
       if (cut >= cost) return cost;
       const int i = item_at(cut);
-      return cut - cost_before[i] < kSnap ? cost_before[i] : cost_before[i + 1] - cut < kSnap ? cost_before[i + 1] : cut;
+      return PromptSplit::moved(cut, cost_before[i], cost_before[i + 1]);
     };
-    auto owner_of = [&](int64_t unit) { return (int)(((unit + 1) * shares - 1) / cost); };  // the CTA that has it, before moves
     int64_t pos = start_of(blockIdx.x);
     const int64_t end = start_of((int64_t)blockIdx.x + 1);
     bool over = false;  // no item left
@@ -395,10 +392,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttenti
               const int i = item_at(pos);
               const int64_t at = cost_before[i], next = cost_before[i + 1], stop = min(next, end);
               x = describe(i);
-              x.first = owner_of(min(at + kSnap, next) - 1);
+              x.first = PromptSplit::first(at, next, shares, cost);
               x.piece = blockIdx.x - x.first;
-              x.pieces = owner_of(min(next - 1, max(at + kSnap - 1, next - kSnap))) - x.first + 1;
-              const int skip = max((int)(pos - at) - kCost, 0), len = (int)(stop - at) - kCost - skip;
+              x.pieces = PromptSplit::last(at, next, shares, cost) - x.first + 1;
+              const int skip = PromptSplit::skip(pos, at), len = PromptSplit::length(stop, at, skip);
               x.j0 += skip;
               for (int e = 0; e < 2; ++e) x.n[e] = min(max(x.n[e] - skip, 0), len);
               pos = stop;
