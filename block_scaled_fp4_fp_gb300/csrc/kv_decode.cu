@@ -130,7 +130,7 @@ struct Dec {
   // score factors, key ranges and output rows x 2, m, -m and l of the sets, joined m and l, factors of moved
   // references, segments x 2
   static constexpr uint32_t kRowBytes =
-      2 * 3 * kR * 4 + 2 * kR * 16 + kSets * kR * 12 + 2 * kR * 4 + kSets * kR * 4 + 128;  // (a multiple of 8)
+      2 * 3 * kR * 4 + 2 * kR * 16 + kSets * kR * 12 + 2 * kR * 4 + kSets * kR * 4 + 80;  // (a multiple of 8)
   static constexpr uint32_t kFixed =
       2 * kQBytes + kBufs * kSfaBytes + kOutBytes + kPBytes + kRowBytes + 1024 + 1024;
   static constexpr uint32_t kBudget = 226u * 1024u;
@@ -320,10 +320,9 @@ struct Walk {
 
 // A segment as the query warp hands it to the MMA warp and the consumers (in shared memory).
 struct Seg {
-  int b, h, rb, ta, tb;        // ta = tb: the CTA's share is done
-  int q0, qlen, total, first;  // the request's
+  int ta, tb;                  // ta = tb: the CTA's share is done
+  int total, first;            // the request's
   int lo_tile, tiles, lo_max, hi_min;
-  int pad;
   int64_t start;  // where the item's tile 0 sits in the sequence
 };
 
@@ -414,7 +413,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
   float* join_l = join_m + R;                                     // [R]
   float* set_f = join_l + R;                                      // [SETS][R] a moved reference's factors
   Seg* segs = reinterpret_cast<Seg*>(set_f + SETS * R);           // [2]
-  static_assert(sizeof(Seg) == 64 && (C::kRowBytes - 128) % 8 == 0 && offRow % 16 == 0, "segment records");
+  static_assert(2 * sizeof(Seg) == 80 && (C::kRowBytes - 80) % 8 == 0 && offRow % 16 == 0, "segment records");
   uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + offBar);   // a K tile has landed
   uint64_t* kempty = kfull + SK;                                  // and is done with
   uint64_t* vfull = kempty + SK;                                  // a V tile
@@ -748,8 +747,7 @@ __global__ void __launch_bounds__((Dec<MODE, D, NB>::kThreads), 1) kv_decode_ker
           row_q[qb * R + lane] = real ? (int64_t)(w.r.q0 + i) * a.q_token + (int64_t)head * a.q_head : -1;
         }
         const int hi_min = __reduce_min_sync(0xffffffffu, hi), lo_max = __reduce_max_sync(0xffffffffu, lo);
-        if (lane == 0) segs[qb] = Seg{w.b, w.h, w.rb, w.ta, w.tb, w.r.q0, w.r.qlen, w.r.total, w.r.first, w.r.lo_tile,
-                                      w.r.tiles, lo_max, hi_min, 0, w.start};
+        if (lane == 0) segs[qb] = Seg{w.ta, w.tb, w.r.total, w.r.first, w.r.lo_tile, w.r.tiles, lo_max, hi_min, w.start};
       }
       __syncwarp();
       if (seg == 0) {

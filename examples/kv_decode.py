@@ -113,15 +113,17 @@ def main():
         want = block.exact(keep["q"], keep["plan"])
         worst = max(worst, float((keep["out"].double() - want).norm() / want.norm()))
 
+    # one workspace for prompts and tokens
+    ws = block.workspace(max(a.prompts))
     # prompts
     x = torch.randn((sum(a.prompts), a.hidden), device="cuda").bfloat16()
     keep = {}
-    block.step(x, torch.tensor(a.prompts, dtype=torch.int32, device="cuda"), block.workspace(max(a.prompts)), max(a.prompts), keep)
+    block.step(x, torch.tensor(a.prompts, dtype=torch.int32, device="cuda"), ws, max(a.prompts), keep)
     if a.check:
         check(keep)
     # tokens: one step runs eagerly, the others from a graph
     x = torch.randn((n, a.hidden), device="cuda").bfloat16()
-    one, ws = torch.ones(n, dtype=torch.int32, device="cuda"), block.workspace(1)
+    one = torch.ones(n, dtype=torch.int32, device="cuda")
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
