@@ -61,9 +61,10 @@
 //   MMA         moves a tile's K scales into the 32x16-byte order tcgen05.cp reads, issues that copy and the MMAs
 //   queries     query rows as FP4 terms, one segment ahead
 //
-// Bound by HBM: 2 D (1/2 + 1/g) bytes a key and kv head; at many requests 69 % of the copy rate, the rest being the
-// consumers' instructions (a tile 473 ns of 410), and at one request the chain of plan, first queries, first
-// tiles and joins (about 10 us).  Measured, heads of 128:
+// Bound by HBM: 2 D (1/2 + 1/g) bytes a key and kv head.  Of the 96 requests below the tiles take 225 of 268 us (473 ns
+// each; their bytes take 410; issue active 53 %, no unit near its limit), the rest are the items' ends (about 4 us each,
+// five a CTA) and the chain of plan, first queries, first tiles and joins (about 10 us), which is what one request
+// pays.  Measured, heads of 128:
 //   96 requests of 4k..20k, 40 query heads on 8, MXFP4    268 us, 4.7 TB/s
 //   32 requests of 1..8k, 64 on 8, NVFP4                   46 us, 3.3 TB/s
 //   1 request of 131k, 64 on 8, NVFP4                      40 us, 3.8 TB/s

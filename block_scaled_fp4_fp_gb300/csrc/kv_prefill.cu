@@ -29,21 +29,23 @@
 // is almost never rescaled.  p is rounded to bf16 (2^-8), once; scores, sums and output are fp32.
 // MXFP4's V reaches fp32's largest numbers, whose sums do not fit although their quotient does: an item whose output
 // is not finite is done again with p 2^60 smaller.  (Found at its end: watching the sum beside V's scales tile by tile took
-// the chunks below from 423 to 440 us, this to 433.)
+// the chunks below from 423 to 440 us, this to 430.)
 //
 // Work: up to 608 items are dealt out: their key tiles, with a fixed cost an item, form one
 // sequence, of which each CTA takes an equal share; a cut near an item's end moves to
 // it, and an item's pieces meet in the workspace, where the last warp to arrive joins its 32 rows'
 // in the pieces' order (the same bits each time).  More items are handed out whole by an atomic
-// counter, near the end of the one before.  The longest come first.
-//   32 query heads on 8, NVFP4: a chunk of 512 tokens over 16,000 takes 132 us dealt out (1030 TFLOP/s) and 196 in
-//   equal pieces handed out by the counter; 576 items (64 heads of 64 on 8, 4 chunks over 0..16k) 420 us either way.
+// counter, near the end of the one before; up to 64 requests the longest come first.
+//   32 query heads on 8, NVFP4: a chunk of 512 tokens over 16,000 takes 130 us dealt out (1050 TFLOP/s) and 196 in
+//   equal pieces handed out by the counter; 576 items of similar lengths (64 heads of 64 on 8, 4 chunks over 0..16k) take
+//   as long either way.  Handed out whole, one long context among many short ones is its CTA's alone: 80 tokens of
+//   which one has 131k keys, beside one chunk of 512, are 648 items and take 1.4 ms.
 //
 // What bounds it: for heads of 128 the tensor cores.  Two tiles' four products take 2300 cycles
 // beside the other warps' traffic and a step about 3300, the rest being the ends of items and waits for a softmax
 // (2000 cycles a tile, of which the exponentials 512).  For heads of 64 the softmax: the products take 1750 of 2900.
-//   4096-token prompt, 40 heads of 128, NVFP4:      0.160 ms, 1075 TFLOP/s
-//   4 chunks over 0..16k, 64 heads of 64, MXFP4:    0.433 ms,  712 TFLOP/s
+//   4096-token prompt, 40 heads of 128, NVFP4:      0.159 ms, 1082 TFLOP/s
+//   4 chunks over 0..16k, 64 heads of 64, MXFP4:    0.430 ms,  717 TFLOP/s
 // Tried and slower on the prompt: 64-key steps with two score buffers (200 us), scores fetched ahead (201), two warps a
 // row (162, and 406 on the chunks), more registers for the softmax by setmaxnreg (186).
 //
