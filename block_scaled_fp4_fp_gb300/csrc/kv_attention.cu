@@ -205,11 +205,11 @@ cudaError_t launch_any(const KvAttentionArgs& args, cudaStream_t s) {
 // Query rows of a kv head, up to which the few-row kernel runs: it passes over the cache once for every sixteen, the
 // many-row kernel fills two tiles of 128 whatever they are.  8 kv heads of 128, 8,000 tokens a request, NVFP4, few-row
 // and many-row in us:  rows     4 requests   16 requests   64 requests
-//                      9..16      26    48     62    90     198   296
-//                      17..32     37    48    106    90     367   296
+//                      9..16      26    48     61    90     192   296
+//                      17..32     37    48    105    90     366   296
 //                      33..48     48    48    148    91     543   297
 //                      64         59    48    199    90     719   297
-// The rule asks for the rows only: at 17..32 it is right for few requests and 18 to 24 % slow for many.
+// The rule asks for the rows only: at 17..32 it is right for few requests and 17 to 24 % slow for many.
 constexpr int64_t kFewRows = 32;
 
 bool few_rows(int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_query_len) {

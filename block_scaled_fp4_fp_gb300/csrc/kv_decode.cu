@@ -37,12 +37,13 @@
 // Every quadrant of every group keeps its own running reference m, sum and output:
 // they meet only at the end of a (request, kv head).
 //
-// Range.  p = 2^(s - m) is rounded to f16 (2^-11, while p is at least 2^-14; 2^-9 at 2^-16, where f16 is
+// Range.  p = 2^(s - m) is rounded to f16 (2^-11, while p is at least 2^-14; 2^-8, as in bf16, at 2^-17, where f16 is
 // subnormal).  m is set kHead below the largest score and moves only when a score passes it by kMax,
 // so that p stays below f16's largest value.  A warp whose tile holds a p below 2^-kTiny (not zero: down to
 // 2^-126) multiplies that tile in bf16 instead: codes to bf16 by shifts and masks (twice the
 // instructions of the converter), p with bf16's range.  Sharp score distributions pay this; every p counts with
-// eight bits in either, also where V is zero at the keys of the large ones.
+// eight bits in either, also where V is zero at the keys of the large ones.  (64 requests x 8,000, 16 rows a head:
+// 192 us; 197 with a reference one power of two higher and the bound at 2^-16, 193 with that and 2^-23.)
 // MXFP4's E8M0 scales have the range of fp32, f16 has not: a thread's V values are
 // held relative to 2^E, E the largest scale exponent so far of the channel group it owns;
 // a tile with scales 2^20 below it takes the bf16 form too.
@@ -91,9 +92,9 @@ __host__ __device__ constexpr int term_of(int ch, int c) { return c < 3 ? 3 * ch
 constexpr int kTile = 128;  // keys per tile: the MMA's M
 constexpr int kMaxStages = 12;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kHead = 7.0f;   // a new reference m is the largest score less this (log2)
+constexpr float kHead = 8.0f;   // a new reference m is the largest score less this (log2)
 constexpr float kMax = 15.0f;   // and moves when a score passes it by this: p <= 2^15
-constexpr float kTiny = 16.0f;  // scores further below m than this need bf16's range
+constexpr float kTiny = 17.0f;  // scores further below m than this need bf16's range
 constexpr float kNone = -1e30f; // m before any score: exp2 of a hidden key's -inf less this is 0, of this less a score too
 
 template <int MODE, int D, int NB>

@@ -459,7 +459,7 @@ size_t kv_attention_workspace_bytes(int64_t batch, int64_t q_heads, int64_t kv_h
  *   lse          fp32[tokens, q_heads] or NULL: log of the sum of exp(score), with which
  *                results over disjoint keys can be merged
  * What is held in fewer bits than fp32: the probabilities, of which the product with
- * V takes bf16's 8 bits or, with few query rows, where its range allows f16's 9 to
+ * V takes bf16's 8 bits or, with few query rows, where its range allows f16's 8 to
  * 11; their sum takes them unrounded.
  * Scores, softmax statistics and sums are fp32, a score within fp32's rounding of
  * the sum of its products.  With few query rows (up to 32 a kv head, or head_dim

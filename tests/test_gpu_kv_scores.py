@@ -84,6 +84,17 @@ def test_one_channel_of_the_queries_far_above_the_others(B, mode, dim, kv, group
 def test_small_probabilities_count_with_eight_bits(B, mode, dim, new, below):
     """One key `below` above the others in log2 has zeros for values in some channels: there the others decide, however small
     their probabilities are."""
+    one_key_above(B, mode, dim, new, below)
+
+
+@pytest.mark.parametrize("mode", [2, 1])
+@pytest.mark.parametrize("dim,new", [(128, 1), (64, 1), (256, 1), (128, 2)])
+@pytest.mark.parametrize("below", [23.3, 23.6, 24.3, 24.6, 24.9, 25.1, 25.6])
+def test_small_probabilities_at_the_end_of_f16(B, mode, dim, new, below):
+    one_key_above(B, mode, dim, new, below)
+
+
+def one_key_above(B, mode, dim, new, below):
     p = R.Problem(mode, dim, 1, 8, 64, [31 - new], [new], seed=dim + new)
     p.codes["k"][:] = 0
     p.scales["k"][..., 0] = 0x38 if mode == 2 else 127  # 1
