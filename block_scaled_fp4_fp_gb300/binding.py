@@ -62,6 +62,15 @@ SIGNATURES = {
     "kv_attention": (_INT, [_VP, _VP, _I64, _I64, _I64, _I64, _VP, _VP, _I64, _VP, _I64, _I64, _I64, _F, _I64, _VP,
                             c.c_size_t, _VP, _VP, _VP]),
     "fp4_amax_global_scale_noalloc": (_INT, [_VP, _I64, _VP, _VP, _VP]),
+    "rms_norm": (_INT, [_VP, _I64, _VP, _I64, _VP, _F, _I64, _I64, _VP, _I64, _VP, _INT, _VP, _VP, _VP, _INT, _VP]),
+    "rope_frequencies": (_INT, [_INT, c.c_double, _INT, c.c_double, _I64, c.c_double, c.c_double, _VP, _VP]),
+    "rope_table": (_INT, [_VP, _INT, c.c_double, _I64, _VP, _VP]),
+    "rope": (_INT, [_VP, _VP, _I64, _I64, _VP, _I64, _I64, _I64, _INT, _VP, _I64, _I64, _VP]),
+    "kv_append_rope": (_INT, [_VP, _VP, _VP, _I64, _I64, _VP, _I64, _I64, _VP, _VP, _I64, _VP, _I64, _I64, _I64, _VP, _I64,
+                              _I64, _VP]),
+    "moe_sort": (_INT, [_VP, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP]),
+    "moe_combine": (_INT, [_VP, _I64, _VP, _VP, _VP, _I64, _I64, _I64, _VP, _VP]),
+    "moe_combine_backward": (_INT, [_VP, _VP, _VP, _VP, _I64, _I64, _I64, _I64, _VP, _VP, _VP, _VP]),
 }
 
 
@@ -483,6 +492,281 @@ def kv_attention(cache: KvCache, q: torch.Tensor, query_start: torch.Tensor, tot
                               dim ** -0.5 if scale is None else scale, window, ws.data_ptr(), ws.numel() * ws.element_size(),
                               out.data_ptr(), _p(lse), _s(stream)), "kv_attention")
     return out
+
+
+def _need_here(*tensors):
+    """Refuses tensors that the current device's kernels cannot take: host memory, or another GPU's."""
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            _need_gpu(t)
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"a tensor of shape {tuple(t.shape)} is on {t.device}, the current device is cuda:{here}")
+
+
+def _empty(shape, dtype, like, stream):
+    """An output, from the memory pool of the stream that writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+class RmsNorm(NamedTuple):
+    """rms_norm's outputs (None where not asked for)."""
+    out: torch.Tensor     # bf16 [rows, cols]
+    sum: torch.Tensor     # bf16 [rows, cols]: x + residual
+    xq: torch.Tensor      # int32 [rows, cols / 8]
+    scales: torch.Tensor  # uint8, linear or tiled
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor = None, eps: float = 1e-6, residual: torch.Tensor = None, mode: int = None,
+             global_scale=None, layout: int = SCALES_LINEAR, sum_out=None, out=None, xq=None, scales=None,
+             stream=None) -> RmsNorm:
+    """Root-mean-square norm of the rows of x [rows, cols] (+ residual; their sum is returned too, and written in place
+    with sum_out=residual).  Without a mode the result is bf16; with MODE_NVFP4 or MODE_MXFP4 it is codes and scales as
+    fp4_quantize makes them, and bf16 as well where out is given."""
+    bf16 = torch.bfloat16
+    if x.dim() != 2:
+        raise ValueError(f"x: [rows, cols] is needed, got {tuple(x.shape)}")
+    rows, cols = x.shape
+    _need("x", x, bf16, (rows, cols), rows=True)
+    for name, t in (("residual", residual), ("sum_out", sum_out)):
+        if t is not None:
+            _need(name, t, bf16, (rows, cols), rows=True)
+    if out is not None:
+        _need("out", out, bf16, (rows, cols))
+    if weight is not None:
+        _need_vector("weight", weight, bf16, cols)
+    group = shape = None
+    if mode is not None:
+        if mode not in (MODE_NVFP4, MODE_MXFP4):
+            raise ValueError(f"mode: MODE_NVFP4 or MODE_MXFP4 is needed, got {mode}")
+        group = GROUP[mode]
+        shape = scales_shape(rows, cols, group, layout)
+        if xq is not None:
+            _need("xq", xq, torch.int32, (rows, cols // 8))
+        if scales is not None:
+            _need("scales", scales, torch.uint8, shape)
+        if global_scale is not None:
+            _need_vector("global_scale", global_scale, torch.float32, 1)
+    elif global_scale is not None or xq is not None or scales is not None:
+        raise ValueError("mode: global_scale, xq and scales belong to a 4-bit output")
+    _need_here(x, residual, weight, sum_out, out, global_scale, xq, scales)
+    if residual is not None and sum_out is None:
+        sum_out = _empty((rows, cols), bf16, x, stream)
+    if mode is None:
+        if out is None:
+            out = _empty((rows, cols), bf16, x, stream)
+    else:
+        if xq is None:
+            xq = _empty((rows, cols // 8), torch.int32, x, stream)
+        if scales is None:
+            scales = _empty(shape, torch.uint8, x, stream)
+    _check(lib().rms_norm(_p(x), x.stride(0) if rows > 1 else cols, _p(residual), _row_stride(residual), _p(weight), eps, rows,
+                          cols, _p(sum_out), _row_stride(sum_out), _p(out), mode or 0, _p(global_scale), _p(xq), _p(scales),
+                          layout, _s(stream)), "rms_norm")
+    return RmsNorm(out, sum_out, xq, scales)
+
+
+def _row_stride(t):
+    """Elements between the rows of a matrix (of one row: any; its width)."""
+    return 0 if t is None else t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _view_strides(t):
+    """(token, head) strides of a [tokens, heads, dim] view; those of a single token or head say nothing."""
+    tokens, heads, dim = t.shape
+    head = t.stride(1) if heads > 1 else dim
+    return t.stride(0) if tokens > 1 else max(heads * dim, heads * head), head
+
+
+class Rope(c.Structure):
+    """fp4_rope: a table of cosines and sines (make it with rope_table or rope_from_table, which keep the tensor alive)."""
+    _fields_ = [("table", c.c_void_p), ("positions", c.c_int64), ("rotary_dim", c.c_int32), ("interleaved", c.c_int32)]
+
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "wavelength": 3, "ramp": 4}
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_positions: int = 1, low: float = 1.0, high: float = 32.0):
+    """(radians a position for each pair as a list, what cos and sin are multiplied by)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling: one of {', '.join(ROPE_SCALINGS)} is needed, got {scaling!r}")
+    f, scale = (c.c_double * max(1, rotary_dim // 2))(), c.c_double()
+    _check(lib().rope_frequencies(rotary_dim, base, ROPE_SCALINGS[scaling], factor, original_positions, low, high, f,
+                                  c.byref(scale)), "rope_frequencies")
+    return list(f), scale.value
+
+
+def rope_from_table(table: torch.Tensor, interleaved: bool = False) -> Rope:
+    """Rotary positions over the caller's table, float32 [positions, rotary_dim / 2, 2]: cos and sin."""
+    if table.dim() != 3 or table.shape[2] != 2:
+        raise ValueError(f"table: [positions, rotary_dim / 2, 2] is needed, got {tuple(table.shape)}")
+    _need("table", table, torch.float32, tuple(table.shape))
+    r = Rope(_p(table), table.shape[0], 2 * table.shape[1], 1 if interleaved else 0)
+    r.tensor = table
+    return r
+
+
+def rope_table(positions: int, rotary_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+               factor: float = 1.0, original_positions: int = 1, low: float = 1.0, high: float = 32.0, frequencies=None,
+               scale: float = None, device="cuda", stream=None) -> Rope:
+    """The table of a model's positions 0 .. positions - 1, once: from the base and scaling (as rope_frequencies takes
+    them), or from the caller's own frequencies (radians a position, rotary_dim / 2 of them) and scale."""
+    if frequencies is None:
+        frequencies, own = rope_frequencies(rotary_dim, base, scaling, factor, original_positions, low, high)
+        scale = own if scale is None else scale
+    elif len(frequencies) != rotary_dim // 2:
+        raise ValueError(f"frequencies: {rotary_dim // 2} are needed, got {len(frequencies)}")
+    f = (c.c_double * max(1, len(frequencies)))(*frequencies)
+    like = torch.empty(0, device=device)
+    _need_here(like)
+    table = _empty((positions, rotary_dim // 2, 2), torch.float32, like, stream)
+    _check(lib().rope_table(f, rotary_dim, 1.0 if scale is None else scale, positions, _p(table), _s(stream)), "rope_table")
+    return rope_from_table(table, interleaved)
+
+
+def _need_view(name: str, t: torch.Tensor, shape):
+    if t.dim() != 3:
+        raise ValueError(f"{name}: [tokens, heads, head_dim] is needed, got {tuple(t.shape)}")
+    _need(name, t, torch.bfloat16, shape, rows=True)
+
+
+def rope(rope: Rope, x: torch.Tensor, positions: torch.Tensor, backward: bool = False, out=None, stream=None):
+    """x [tokens, heads, head_dim] (views with strides are read in place) rotated by its tokens' positions; backward: the
+    transposed rotation.  out=x rotates in place; rows of negative positions are not written."""
+    _need_view("x", x, tuple(x.shape))
+    tokens, heads, dim = x.shape
+    _need_vector("positions", positions, torch.int32, tokens)
+    if out is not None:
+        _need_view("out", out, (tokens, heads, dim))
+    _need_here(x, positions, out, rope.tensor)
+    if out is None:
+        out = _empty((tokens, heads, dim), torch.bfloat16, x, stream)
+    _check(lib().rope(c.byref(rope), _p(x), *_view_strides(x), _p(positions), tokens, heads, dim, 1 if backward else 0,
+                      _p(out), *_view_strides(out), _s(stream)), "rope")
+    return out
+
+
+def kv_append_rope(cache: KvCache, rope: Rope, k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor,
+                   positions: torch.Tensor, q: torch.Tensor = None, q_out=None, stream=None):
+    """kv_append with K rotated by its tokens' positions; q [tokens, q_heads, head_dim], where given, is rotated by the
+    same launch into q_out (q_out=q: in place), which is returned.  Views with strides are read in place."""
+    tokens = slot_map.numel()
+    shape = (tokens, cache.kv_heads, cache.head_dim)
+    _need_vector("slot_map", slot_map, torch.int64, tokens)
+    _need_vector("positions", positions, torch.int32, tokens)
+    _need_view("k", k, shape)
+    _need_view("v", v, shape)
+    if q is not None:
+        _need_view("q", q, (tokens, q.shape[1] if q.dim() == 3 else 0, cache.head_dim))
+        if q_out is not None:
+            _need_view("q_out", q_out, tuple(q.shape))
+    elif q_out is not None:
+        raise ValueError("q_out: there is no q to rotate")
+    _need_here(k, v, slot_map, positions, q, q_out, cache.tensors[0], rope.tensor)
+    if q is not None and q_out is None:
+        q_out = _empty(tuple(q.shape), torch.bfloat16, q, stream)
+    qs, os_ = (0, 0) if q is None else _view_strides(q), (0, 0) if q is None else _view_strides(q_out)
+    _check(lib().kv_append_rope(c.byref(cache), c.byref(rope), _p(k), *_view_strides(k), _p(v), *_view_strides(v),
+                                _p(slot_map), _p(positions), tokens, _p(q), *qs, 0 if q is None else q.shape[1], _p(q_out),
+                                *os_, _s(stream)), "kv_append_rope")
+    return q_out
+
+
+class MoeSort(NamedTuple):
+    """moe_sort's outputs (device tensors)."""
+    lhs_idx: torch.Tensor  # int32 [rows]: token of each sorted row
+    rhs_idx: torch.Tensor  # int32 [rows]: its expert
+    slot: torch.Tensor     # int32 [tokens, k]: sorted row of each routed row, -1 if dropped
+    offsets: torch.Tensor  # int32 [experts + 1]: first sorted row of each expert; the number kept
+
+
+def moe_sort(ids: torch.Tensor, num_experts: int, plan: MoeSort = None, stream=None) -> MoeSort:
+    """The routed rows of ids int32 [tokens, k] in order of their experts: lhs_idx and rhs_idx are what gather_rows and
+    gather_qmm take, slot what moe_combine takes.  Negative ids are dropped."""
+    i32 = torch.int32
+    if ids.dim() != 2:
+        raise ValueError(f"ids: [tokens, k] is needed, got {tuple(ids.shape)}")
+    _need("ids", ids, i32, tuple(ids.shape))
+    tokens, k = ids.shape
+    if plan is not None:
+        _need_vector("lhs_idx", plan.lhs_idx, i32, tokens * k)
+        _need_vector("rhs_idx", plan.rhs_idx, i32, tokens * k)
+        _need("slot", plan.slot, i32, (tokens, k))
+        _need_vector("offsets", plan.offsets, i32, num_experts + 1)
+    _need_here(ids, *(plan or ()))
+    if plan is None:
+        plan = MoeSort(_empty(tokens * k, i32, ids, stream), _empty(tokens * k, i32, ids, stream),
+                       _empty((tokens, k), i32, ids, stream), _empty(num_experts + 1, i32, ids, stream))
+    _check(lib().moe_sort(_p(ids), tokens, k, num_experts, _p(plan.lhs_idx), _p(plan.rhs_idx), _p(plan.slot),
+                          _p(plan.offsets), _s(stream)), "moe_sort")
+    return plan
+
+
+def _need_routing(slot, weights):
+    if slot.dim() != 2:
+        raise ValueError(f"slot: [tokens, k] is needed, got {tuple(slot.shape)}")
+    _need("slot", slot, torch.int32, tuple(slot.shape))
+    if weights is not None:
+        _need("weights", weights, torch.float32, tuple(slot.shape))
+
+
+def moe_combine(y: torch.Tensor, slot: torch.Tensor, weights: torch.Tensor = None, residual: torch.Tensor = None, out=None,
+                stream=None):
+    """The experts' rows y [rows, cols] back to their tokens: residual + sum of weights * y[slot] (weights None: 1, which
+    with the sorted rows' gradient as y is the gradient of their gather).  out=residual adds in place."""
+    bf16 = torch.bfloat16
+    _need_routing(slot, weights)
+    if y.dim() != 2:
+        raise ValueError(f"y: [rows, cols] is needed, got {tuple(y.shape)}")
+    _need("y", y, bf16, tuple(y.shape))
+    (tokens, k), (rows, cols) = slot.shape, y.shape
+    for name, t in (("residual", residual), ("out", out)):
+        if t is not None:
+            _need(name, t, bf16, (tokens, cols))
+    _need_here(y, slot, weights, residual, out)
+    if out is None:
+        out = _empty((tokens, cols), bf16, y, stream)
+    _check(lib().moe_combine(_p(y), rows, _p(slot), _p(weights), _p(residual), tokens, k, cols, _p(out), _s(stream)),
+           "moe_combine")
+    return out
+
+
+def moe_combine_backward(dout: torch.Tensor, slot: torch.Tensor, weights: torch.Tensor = None, y: torch.Tensor = None,
+                         offsets: torch.Tensor = None, dy=None, dweights=None, stream=None):
+    """(dy [rows, cols], dweights [tokens, k]) from dout [tokens, cols].  dweights needs y (None without it); rows is y's,
+    or dy's, or every routed row's.  offsets (moe_sort's): rows of dy that no slot names are zeros; without it they are
+    not written."""
+    bf16 = torch.bfloat16
+    _need_routing(slot, weights)
+    tokens, k = slot.shape
+    if dout.dim() != 2:
+        raise ValueError(f"dout: [tokens, cols] is needed, got {tuple(dout.shape)}")
+    cols = dout.shape[1]
+    _need("dout", dout, bf16, (tokens, cols))
+    rows = y.shape[0] if y is not None else dy.shape[0] if dy is not None else tokens * k
+    for name, t in (("y", y), ("dy", dy)):
+        if t is not None:
+            _need(name, t, bf16, (rows, cols))
+    if dweights is not None:
+        _need("dweights", dweights, torch.float32, (tokens, k))
+        if y is None:
+            raise ValueError("dweights: y is needed for it")
+    if offsets is not None:
+        _need_vector("offsets", offsets, torch.int32, offsets.numel())
+    _need_here(dout, slot, weights, y, offsets, dy, dweights)
+    if dy is None:
+        dy = _empty((rows, cols), bf16, dout, stream)
+    if y is not None and dweights is None:
+        dweights = _empty((tokens, k), torch.float32, dout, stream)
+    used = None if offsets is None else offsets.data_ptr() + 4 * (offsets.numel() - 1)
+    _check(lib().moe_combine_backward(_p(dout), _p(y), _p(slot), _p(weights), tokens, k, cols, rows, used, _p(dy),
+                                      _p(dweights), _s(stream)), "moe_combine_backward")
+    return dy, dweights
 
 
 def fp4_debug_stream_weights(wq: torch.Tensor, scales: torch.Tensor, stream=None):

@@ -1,6 +1,7 @@
 // api.cu -- the C ABI of libfp4gb300: host-side validation, per-device state
 // and launches.  No entry point throws, allocates or keeps a pointer.
 #include <atomic>
+#include <cmath>
 #include <cstdio>
 #include <mutex>
 
@@ -550,10 +551,12 @@ fp4_status kv_plan(const int32_t* cached_lens, const int32_t* new_lens, int64_t 
                                   pages_taken, stream));
 }
 
-fp4_status kv_append(const fp4_kv_cache* cache, const fp4_bf16* k, int64_t k_token_stride, int64_t k_head_stride,
-                     const fp4_bf16* v, int64_t v_token_stride, int64_t v_head_stride, const int64_t* slot_map,
-                     int64_t tokens, cudaStream_t stream) {
-  fp4_status st = check_kv_cache(cache);
+namespace {
+// what kv_append and kv_append_rope take alike
+fp4_status check_append(const fp4_kv_cache* cache, const fp4_bf16* k, int64_t k_token_stride, int64_t k_head_stride,
+                        const fp4_bf16* v, int64_t v_token_stride, int64_t v_head_stride, const int64_t* slot_map,
+                        int64_t tokens) {
+  const fp4_status st = check_kv_cache(cache);
   if (st != FP4_OK) return st;
   if (!k || !v || !slot_map || tokens < 1 || tokens > INT32_MAX) return FP4_ERR_INVALID_ARG;
   if (!view_ok(k_token_stride, k_head_stride, cache->kv_heads, cache->head_dim) ||
@@ -562,6 +565,15 @@ fp4_status kv_append(const fp4_kv_cache* cache, const fp4_bf16* k, int64_t k_tok
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slot_map, 8) || k_token_stride % 8 || k_head_stride % 8 ||
       v_token_stride % 8 || v_head_stride % 8)
     return FP4_ERR_ALIGNMENT;
+  return FP4_OK;
+}
+}  // namespace
+
+fp4_status kv_append(const fp4_kv_cache* cache, const fp4_bf16* k, int64_t k_token_stride, int64_t k_head_stride,
+                     const fp4_bf16* v, int64_t v_token_stride, int64_t v_head_stride, const int64_t* slot_map,
+                     int64_t tokens, cudaStream_t stream) {
+  fp4_status st = check_append(cache, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, slot_map, tokens);
+  if (st != FP4_OK) return st;
   const DevInfo* d = nullptr;
   st = current(&d);
   if (st != FP4_OK) return st;
@@ -623,6 +635,233 @@ fp4_status kv_attention(const fp4_kv_cache* cache, const fp4_bf16* q, int64_t q_
   a.err = d->err;
   a.inject_timeout = g_inject_timeout.load();
   return from_cuda(launch_kv_attention(*d, a, stream));
+}
+
+fp4_status rms_norm(const fp4_bf16* x, int64_t x_stride, const fp4_bf16* residual, int64_t residual_stride,
+                    const fp4_bf16* weight, float eps, int64_t rows, int64_t cols, fp4_bf16* sum_out,
+                    int64_t sum_stride, fp4_bf16* out, fp4_mode mode, const float* global_scale, uint32_t* xq,
+                    uint8_t* scales, fp4_scale_layout layout, cudaStream_t stream) {
+  if (!x || (!out && !xq) || rows <= 0 || cols <= 0 || cols % 8 != 0 || cols > 32768 || rows > INT32_MAX / 2)
+    return FP4_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f) || eps > 1.0f) return FP4_ERR_INVALID_ARG;
+  if (x_stride < cols || (residual && residual_stride < cols) || (sum_out && sum_stride < cols)) return FP4_ERR_INVALID_ARG;
+  if (x_stride > INT32_MAX || (residual && residual_stride > INT32_MAX) || (sum_out && sum_stride > INT32_MAX))
+    return FP4_ERR_INVALID_ARG;
+  // what is written in place has its input's rows; out and the sum are two buffers
+  if ((sum_out && sum_out == residual && sum_stride != residual_stride) || (sum_out && sum_out == x && sum_stride != x_stride) ||
+      (out && out == x && x_stride != cols) || (out && out == residual && residual_stride != cols) || (out && out == sum_out))
+    return FP4_ERR_INVALID_ARG;
+  if (xq) {
+    if (mode != FP4_MODE_NVFP4 && mode != FP4_MODE_MXFP4) return FP4_ERR_UNSUPPORTED;
+    if (!scales || cols % (mode == FP4_MODE_NVFP4 ? 16 : 32) != 0) return FP4_ERR_INVALID_ARG;
+    if (global_scale && mode != FP4_MODE_NVFP4) return FP4_ERR_INVALID_ARG;
+    if (layout != FP4_SCALES_LINEAR && layout != FP4_SCALES_TILED_128x4) return FP4_ERR_INVALID_ARG;
+    if (!aligned(xq, 4) || !aligned(global_scale, 4)) return FP4_ERR_ALIGNMENT;
+  }
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(sum_out, 16) || !aligned(out, 16) ||
+      x_stride % 8 || (residual && residual_stride % 8) || (sum_out && sum_stride % 8))
+    return FP4_ERR_ALIGNMENT;
+  const DevInfo* d = nullptr;
+  const fp4_status st = current(&d);
+  if (st != FP4_OK) return st;
+  RmsNormArgs a;
+  a.x = x;
+  a.x_stride = x_stride;
+  a.residual = residual;
+  a.residual_stride = residual_stride;
+  a.weight = weight;
+  a.eps = eps;
+  a.rows = (int)rows;
+  a.cols = (int)cols;
+  a.sum_out = sum_out;
+  a.sum_stride = sum_stride;
+  a.out = out;
+  a.mode = xq ? (int)mode : 0;
+  a.gs = global_scale;
+  a.xq = xq;
+  a.scales = scales;
+  a.tiled = layout == FP4_SCALES_TILED_128x4;
+  return from_cuda(launch_rms_norm(*d, a, stream));
+}
+
+namespace {
+fp4_status check_rope(const fp4_rope* r) {
+  if (!r || !r->table || r->positions < 1 || r->positions > INT32_MAX || r->rotary_dim < 2 || r->rotary_dim > 256 ||
+      r->rotary_dim % 2 != 0)
+    return FP4_ERR_INVALID_ARG;
+  return aligned(r->table, 8) ? FP4_OK : FP4_ERR_ALIGNMENT;
+}
+
+RopeDesc rope_desc(const fp4_rope* r) {
+  RopeDesc d;
+  d.table = reinterpret_cast<const float2*>(r->table);
+  d.positions = (int)r->positions;
+  d.rotary_dim = r->rotary_dim;
+  d.interleaved = r->interleaved != 0;
+  return d;
+}
+
+// a rotated view: where it is read and where it is written
+fp4_status check_heads(const fp4_bf16* in, int64_t in_token, int64_t in_head, const fp4_bf16* out, int64_t out_token,
+                       int64_t out_head, int64_t heads, int64_t dim) {
+  if (!in || !out || heads < 1 || heads > 65535) return FP4_ERR_INVALID_ARG;
+  if (!view_ok(in_token, in_head, heads, dim) || !view_ok(out_token, out_head, heads, dim)) return FP4_ERR_INVALID_ARG;
+  if (in == out && (in_token != out_token || in_head != out_head)) return FP4_ERR_INVALID_ARG;
+  if (!aligned(in, 16) || !aligned(out, 16) || in_token % 8 || in_head % 8 || out_token % 8 || out_head % 8)
+    return FP4_ERR_ALIGNMENT;
+  return FP4_OK;
+}
+
+HeadsView heads_view(const fp4_bf16* in, int64_t in_token, int64_t in_head, fp4_bf16* out, int64_t out_token,
+                     int64_t out_head, int64_t heads, int64_t dim) {
+  HeadsView v;
+  v.in = in;
+  v.in_token = in_token;
+  v.in_head = in_head;
+  v.out = out;
+  v.out_token = out_token;
+  v.out_head = out_head;
+  v.heads = (int)heads;
+  v.dim = (int)dim;
+  return v;
+}
+}  // namespace
+
+fp4_status rope_frequencies(int rotary_dim, double base, fp4_rope_scaling scaling, double factor,
+                            int64_t original_positions, double low, double high, double* frequencies, double* scale) {
+  const bool blend = scaling == FP4_ROPE_WAVELENGTH || scaling == FP4_ROPE_RAMP;
+  if (scaling < FP4_ROPE_NONE || scaling > FP4_ROPE_RAMP) return FP4_ERR_UNSUPPORTED;
+  if (rotary_dim < 2 || rotary_dim > 256 || rotary_dim % 2 != 0 || !frequencies || !scale) return FP4_ERR_INVALID_ARG;
+  if (!(base > 1.0) || !std::isfinite(base)) return FP4_ERR_INVALID_ARG;
+  if (scaling != FP4_ROPE_NONE && (!(factor >= 1.0) || !std::isfinite(factor))) return FP4_ERR_INVALID_ARG;
+  if (blend && (original_positions < 1 || !(low < high) || !std::isfinite(low) || !std::isfinite(high))) return FP4_ERR_INVALID_ARG;
+  if (scaling == FP4_ROPE_RAMP && !(low > 0.0)) return FP4_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586, d = rotary_dim, L = (double)original_positions;
+  if (scaling == FP4_ROPE_BASE && rotary_dim > 2) base *= std::pow(factor, d / (d - 2.0));
+  double first = 0.0, last = 0.0;
+  if (scaling == FP4_ROPE_RAMP) {
+    const double per = d / (2.0 * std::log(base));
+    first = std::fmax(std::floor(per * std::log(L / (high * two_pi))), 0.0);
+    last = std::fmin(std::ceil(per * std::log(L / (low * two_pi))), d - 1.0);
+  }
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    const double f = std::pow(base, -2.0 * i / d);
+    double s = 1.0;  // the share of f that stays
+    if (scaling == FP4_ROPE_LINEAR) s = 0.0;
+    if (scaling == FP4_ROPE_WAVELENGTH) s = (L * f / two_pi - low) / (high - low);
+    if (scaling == FP4_ROPE_RAMP) s = 1.0 - (i - first) / std::fmax(last - first, 0.001);
+    s = std::fmin(std::fmax(s, 0.0), 1.0);
+    frequencies[i] = s == 1.0 ? f : (1.0 - s) * f / factor + s * f;
+  }
+  *scale = scaling == FP4_ROPE_RAMP ? 0.1 * std::log(factor) + 1.0 : 1.0;
+  return FP4_OK;
+}
+
+fp4_status rope_table(const double* frequencies, int rotary_dim, double scale, int64_t positions, float* table,
+                      cudaStream_t stream) {
+  if (!frequencies || !table || rotary_dim < 2 || rotary_dim > 256 || rotary_dim % 2 != 0 || positions < 1 ||
+      positions > INT32_MAX || !std::isfinite(scale))
+    return FP4_ERR_INVALID_ARG;
+  for (int i = 0; i < rotary_dim / 2; ++i)
+    if (!std::isfinite(frequencies[i])) return FP4_ERR_INVALID_ARG;
+  if (!aligned(table, 8)) return FP4_ERR_ALIGNMENT;
+  const DevInfo* d = nullptr;
+  const fp4_status st = current(&d);
+  if (st != FP4_OK) return st;
+  return from_cuda(launch_rope_table(*d, frequencies, rotary_dim, scale, positions, table, stream));
+}
+
+fp4_status rope(const fp4_rope* r, const fp4_bf16* x, int64_t x_token_stride, int64_t x_head_stride,
+                const int32_t* positions, int64_t tokens, int64_t heads, int64_t head_dim, int backward, fp4_bf16* out,
+                int64_t out_token_stride, int64_t out_head_stride, cudaStream_t stream) {
+  fp4_status st = check_rope(r);
+  if (st != FP4_OK) return st;
+  if (!positions || tokens < 1 || tokens > INT32_MAX || head_dim < r->rotary_dim || head_dim > 256 || head_dim % 8 != 0)
+    return FP4_ERR_INVALID_ARG;
+  st = check_heads(x, x_token_stride, x_head_stride, out, out_token_stride, out_head_stride, heads, head_dim);
+  if (st != FP4_OK) return st;
+  if (!aligned(positions, 4)) return FP4_ERR_ALIGNMENT;
+  const DevInfo* d = nullptr;
+  st = current(&d);
+  if (st != FP4_OK) return st;
+  return from_cuda(launch_rope(*d, rope_desc(r),
+                               heads_view(x, x_token_stride, x_head_stride, out, out_token_stride, out_head_stride, heads, head_dim),
+                               positions, tokens, backward != 0, stream));
+}
+
+fp4_status kv_append_rope(const fp4_kv_cache* cache, const fp4_rope* r, const fp4_bf16* k, int64_t k_token_stride,
+                          int64_t k_head_stride, const fp4_bf16* v, int64_t v_token_stride, int64_t v_head_stride,
+                          const int64_t* slot_map, const int32_t* positions, int64_t tokens, const fp4_bf16* q,
+                          int64_t q_token_stride, int64_t q_head_stride, int64_t q_heads, fp4_bf16* q_out,
+                          int64_t q_out_token_stride, int64_t q_out_head_stride, cudaStream_t stream) {
+  fp4_status st = check_append(cache, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, slot_map, tokens);
+  if (st == FP4_OK) st = check_rope(r);
+  if (st != FP4_OK) return st;
+  if (!positions || r->rotary_dim > cache->head_dim) return FP4_ERR_INVALID_ARG;
+  if (!aligned(positions, 4)) return FP4_ERR_ALIGNMENT;
+  HeadsView view;
+  if (q || q_out || q_heads != 0) {
+    st = check_heads(q, q_token_stride, q_head_stride, q_out, q_out_token_stride, q_out_head_stride, q_heads, cache->head_dim);
+    if (st != FP4_OK) return st;
+    view = heads_view(q, q_token_stride, q_head_stride, q_out, q_out_token_stride, q_out_head_stride, q_heads, cache->head_dim);
+  }
+  const DevInfo* d = nullptr;
+  st = current(&d);
+  if (st != FP4_OK) return st;
+  return from_cuda(launch_kv_append_rope(*d, kv_desc(cache), rope_desc(r), k, k_token_stride, k_head_stride, v,
+                                         v_token_stride, v_head_stride, slot_map, positions, tokens, view, stream));
+}
+
+fp4_status moe_sort(const int32_t* ids, int64_t tokens, int64_t k, int64_t num_experts, int32_t* lhs_idx,
+                    int32_t* rhs_idx, int32_t* slot, int32_t* offsets, cudaStream_t stream) {
+  if (!ids || !lhs_idx || !rhs_idx || !slot || !offsets || tokens < 1 || k < 1 || k > 1024 || num_experts < 1 ||
+      num_experts > 1024 || tokens > ((int64_t)1 << 30) / k)
+    return FP4_ERR_INVALID_ARG;
+  if (slot == ids || lhs_idx == ids || rhs_idx == ids) return FP4_ERR_INVALID_ARG;  // (ids are read twice)
+  if (!aligned(ids, 4) || !aligned(lhs_idx, 4) || !aligned(rhs_idx, 4) || !aligned(slot, 4) || !aligned(offsets, 4))
+    return FP4_ERR_ALIGNMENT;
+  const DevInfo* d = nullptr;
+  const fp4_status st = current(&d);
+  if (st != FP4_OK) return st;
+  return from_cuda(launch_moe_sort(*d, ids, tokens, (int)k, (int)num_experts, lhs_idx, rhs_idx, slot, offsets, stream));
+}
+
+namespace {
+fp4_status check_combine(const void* a, const void* b, const int32_t* slot, const float* weights, const void* c,
+                         const void* e, int64_t tokens, int64_t k, int64_t cols, int64_t rows) {
+  if (!a || !b || !slot || tokens < 1 || tokens > INT32_MAX / 2 || k < 1 || k > 1024 || cols < 8 || cols % 8 != 0 ||
+      cols > (1 << 24) || rows < 1 || rows > INT32_MAX)
+    return FP4_ERR_INVALID_ARG;
+  if (!aligned(a, 16) || !aligned(b, 16) || !aligned(c, 16) || !aligned(slot, 4) || !aligned(weights, 4) || !aligned(e, 4))
+    return FP4_ERR_ALIGNMENT;
+  return FP4_OK;
+}
+}  // namespace
+
+fp4_status moe_combine(const fp4_bf16* y, int64_t rows, const int32_t* slot, const float* weights,
+                       const fp4_bf16* residual, int64_t tokens, int64_t k, int64_t cols, fp4_bf16* out,
+                       cudaStream_t stream) {
+  fp4_status st = check_combine(y, out, slot, weights, residual, nullptr, tokens, k, cols, rows);
+  if (st != FP4_OK) return st;
+  if (out == y) return FP4_ERR_INVALID_ARG;  // (rows of y are read by several tokens' threads)
+  const DevInfo* d = nullptr;
+  st = current(&d);
+  if (st != FP4_OK) return st;
+  return from_cuda(launch_moe_combine(*d, y, rows, slot, weights, residual, tokens, (int)k, (int)cols, out, stream));
+}
+
+fp4_status moe_combine_backward(const fp4_bf16* dout, const fp4_bf16* y, const int32_t* slot, const float* weights,
+                                int64_t tokens, int64_t k, int64_t cols, int64_t rows, const int32_t* rows_used,
+                                fp4_bf16* dy, float* dweights, cudaStream_t stream) {
+  fp4_status st = check_combine(dout, dy, slot, weights, y, dweights, tokens, k, cols, rows);
+  if (st != FP4_OK) return st;
+  if ((dweights != nullptr) != (y != nullptr) || dy == dout || dy == y) return FP4_ERR_INVALID_ARG;
+  if (!aligned(rows_used, 4)) return FP4_ERR_ALIGNMENT;
+  const DevInfo* d = nullptr;
+  st = current(&d);
+  if (st != FP4_OK) return st;
+  return from_cuda(launch_moe_combine_backward(*d, dout, y, slot, weights, tokens, (int)k, (int)cols, rows, rows_used, dy,
+                                               dweights, stream));
 }
 
 fp4_status fp4_debug_stream_weights(const uint32_t* w, const uint8_t* scales, int64_t N, int64_t K,

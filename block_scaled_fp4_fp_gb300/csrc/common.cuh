@@ -201,6 +201,23 @@ __device__ __forceinline__ void block_scale_rule(uint32_t mb, float gs, float& m
   block_scale_rule<MODE>(mb, gs, nvfp4_div(gs), mul, sbyte, sval);
 }
 
+// The block rule for a block maximum b >= 0 that is any fp32 number (block_scale_rule takes bf16's); p = fl(6 gs).
+template <int MODE>
+__device__ __forceinline__ void block_scale_rule_f32(float b, float p, float gs, float& mul, uint32_t& sbyte) {
+  if (MODE == 2) {
+    sbyte = e4m3_rn(b == 0.0f ? 0.0f : __fdiv_rn(b, p));
+    const float dd = __fmul_rn(e4m3_to_f32(sbyte), gs);
+    mul = dd == 0.0f ? 0.0f : __frcp_rn(dd);
+  } else {
+    const uint32_t u = __float_as_uint(b);
+    const int E = (int)(u >> 23);
+    const int e = E == 0 ? 31 - __clz((int)u) - 149 : E - 127;  // floor(log2 b), b > 0
+    const int se = u == 0 ? -127 : min(max(e - 2, -127), 127);
+    sbyte = (uint32_t)(se + 127);
+    mul = exp2i_f32(-se);
+  }
+}
+
 // Largest bf16 magnitude (bits) of the eight values of a 16-byte piece.
 __device__ __forceinline__ uint32_t max_mag8(uint4 v) {
   uint32_t m2 = __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu);

@@ -160,6 +160,57 @@ struct KvAttentionArgs {
   unsigned* err = nullptr;
   int inject_timeout = 0;
 };
+// norm.cu: the root-mean-square norm (mode 0: no 4-bit output)
+struct RmsNormArgs {
+  const uint16_t* x = nullptr;  // row strides in elements
+  int64_t x_stride = 0;
+  const uint16_t* residual = nullptr;  // nullptr: none
+  int64_t residual_stride = 0;
+  const uint16_t* weight = nullptr;  // nullptr: 1
+  float eps = 0.f;
+  int rows = 0, cols = 0;
+  uint16_t* sum_out = nullptr;  // nullptr: not wanted, as out and xq
+  int64_t sum_stride = 0;
+  uint16_t* out = nullptr;
+  int mode = 0;
+  const float* gs = nullptr;
+  uint32_t* xq = nullptr;
+  uint8_t* scales = nullptr;
+  int tiled = 0;
+};
+cudaError_t launch_rms_norm(const DevInfo& d, const RmsNormArgs& a, cudaStream_t s);
+
+// rope.cu: rotary positions, on their own and on the way into the cache
+struct RopeDesc {
+  const float2* table = nullptr;  // [positions, rotary_dim / 2]: cos, sin
+  int positions = 0, rotary_dim = 0, interleaved = 0;
+};
+struct HeadsView {  // bf16 [tokens, heads, head_dim]; strides in elements
+  const uint16_t* in = nullptr;
+  int64_t in_token = 0, in_head = 0;
+  uint16_t* out = nullptr;
+  int64_t out_token = 0, out_head = 0;
+  int heads = 0, dim = 0;
+};
+cudaError_t launch_rope_table(const DevInfo& d, const double* frequencies, int rotary_dim, double scale,
+                              int64_t positions, float* table, cudaStream_t s);
+cudaError_t launch_rope(const DevInfo& d, const RopeDesc& r, const HeadsView& x, const int32_t* positions, int64_t T,
+                        int backward, cudaStream_t s);
+cudaError_t launch_kv_append_rope(const DevInfo& d, const KvCacheDesc& c, const RopeDesc& r, const uint16_t* k,
+                                  int64_t k_token, int64_t k_head, const uint16_t* v, int64_t v_token, int64_t v_head,
+                                  const int64_t* slot_map, const int32_t* positions, int64_t T, const HeadsView& q,
+                                  cudaStream_t s);
+
+// moe.cu: routed rows by expert and back
+cudaError_t launch_moe_sort(const DevInfo& d, const int32_t* ids, int64_t T, int k, int E, int32_t* lhs, int32_t* rhs,
+                            int32_t* slot, int32_t* offsets, cudaStream_t s);
+cudaError_t launch_moe_combine(const DevInfo& d, const uint16_t* y, int64_t rows, const int32_t* slot,
+                               const float* weights, const uint16_t* residual, int64_t T, int k, int cols,
+                               uint16_t* out, cudaStream_t s);
+cudaError_t launch_moe_combine_backward(const DevInfo& d, const uint16_t* dout, const uint16_t* y, const int32_t* slot,
+                                        const float* weights, int64_t T, int k, int cols, int64_t rows,
+                                        const int32_t* rows_used, uint16_t* dy, float* dweights, cudaStream_t s);
+
 // the attention's dispatch (kv_attention.cu) and its workspace
 size_t kv_attention_ws_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_query_len);
 cudaError_t launch_kv_attention(const DevInfo& d, const KvAttentionArgs& args, cudaStream_t s);

@@ -484,6 +484,146 @@ fp4_status kv_attention(const fp4_kv_cache* cache, const fp4_bf16* q, int64_t q_
                         int64_t max_query_len, float softmax_scale, int64_t window, void* ws, size_t ws_bytes,
                         fp4_bf16* out, float* lse, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Around a decoder layer's products: the norm in front of one, the positions'
+ * rotation between the projection and the cache, the experts' rows and back. */
+
+/* rms_norm: root-mean-square norm of the rows of x, after the residual's addition,
+ * out in bf16, in 4 bits, or both.
+ *   h[r, c] = x[r, c] + residual[r, c]        (residual NULL: h = x; fp32)
+ *   rstd[r] = 1 / sqrt(mean over c of h[r, c]^2 + eps)
+ *   y[r, c] = (h[r, c] * rstd[r]) * weight[c] (weight NULL: h * rstd; fp32)
+ *   sum_out = bf16(h), out = bf16(y), xq and scales = fp4_quantize's rule on the fp32
+ *   y: b is the block's largest |y| in fp32, nothing is rounded to bf16 on the way.
+ *   x        bf16[rows, cols], 16-byte aligned; row strides in elements, multiples of 8
+ *   residual bf16[rows, cols] or NULL, as x;  weight bf16[cols] or NULL, 16-byte aligned
+ *   sum_out  bf16[rows, cols] or NULL, as x; may be residual or x itself (same stride)
+ *   out      bf16[rows, cols] or NULL, contiguous, 16-byte aligned; may be x itself
+ *   xq       uint32[rows, cols/8] or NULL (at least one of out and xq), 4-byte aligned;
+ *            mode, global_scale, scales, layout: as for fp4_quantize, read only with xq
+ * rstd is held in fp32 from a sum of squares of at least fp32's precision; it holds
+ * over bf16's whole range (squares that fp32 cannot hold are summed in fp64).  A row
+ * of zeros gives zeros also where eps is 0.  An infinity or a NaN in a row gives what the
+ * formula gives in out (NaN), and unspecified codes.
+ * Requires cols a multiple of 8 (with xq, of 16 or 32, the group), at most 32768;
+ * eps in [0, 1]. */
+fp4_status rms_norm(const fp4_bf16* x, int64_t x_stride, const fp4_bf16* residual, int64_t residual_stride,
+                    const fp4_bf16* weight, float eps, int64_t rows, int64_t cols, fp4_bf16* sum_out,
+                    int64_t sum_stride, fp4_bf16* out, fp4_mode mode, const float* global_scale, uint32_t* xq,
+                    uint8_t* scales, fp4_scale_layout layout, cudaStream_t stream);
+
+/* Rotary positions.  Pair i of a head (0 <= i < rotary_dim / 2) is turned by an angle
+ * that grows with the position, and scaled:
+ *   (a, b) -> (a cos - b sin, b cos + a sin),  cos and sin: table[position][i]
+ * Pair i is channels (i, i + rotary_dim/2), or (2 i, 2 i + 1) when interleaved is not
+ * 0; channels from rotary_dim on stay as they are.
+ *   table      fp32[positions, rotary_dim/2, 2]: cos and sin, 8-byte aligned (rope_table
+ *              fills one; a caller's own is as good)
+ *   rotary_dim even, 2 .. 256 */
+typedef struct fp4_rope {
+  const float* table;
+  int64_t positions;
+  int32_t rotary_dim;
+  int32_t interleaved;
+} fp4_rope;
+
+/* How the angles are scaled for contexts longer than the trained one.  f_i = base^(-2 i / rotary_dim)
+ * radians a position, L = original_positions:
+ *   NONE        f_i
+ *   LINEAR      f_i / factor
+ *   BASE        base * factor^(rotary_dim / (rotary_dim - 2)) in place of base (rotary_dim 2: base)
+ *   WAVELENGTH  with t = L f_i / 2 pi, the pair's turns over L, and s = (t - low) / (high - low) held to
+ *               [0, 1]:  (1 - s) f_i / factor + s f_i
+ *   RAMP        the same blend over the pairs' numbers: with n(t) = rotary_dim ln(L / (2 pi t)) / (2 ln base),
+ *               first = max(floor n(high), 0), last = min(ceil n(low), rotary_dim - 1),
+ *               s = 1 - (i - first) / max(last - first, 0.001) held to [0, 1]; and cos and sin are multiplied
+ *               by 0.1 ln(factor) + 1 */
+typedef enum {
+  FP4_ROPE_NONE = 0,
+  FP4_ROPE_LINEAR = 1,
+  FP4_ROPE_BASE = 2,
+  FP4_ROPE_WAVELENGTH = 3,
+  FP4_ROPE_RAMP = 4
+} fp4_rope_scaling;
+
+/* rope_frequencies (host only): frequencies[i], i < rotary_dim / 2, in radians a position, and what cos and sin
+ * are multiplied by, in fp64.  base > 1; factor >= 1 (NONE: not read); low < high and original_positions >= 1
+ * for WAVELENGTH and RAMP (else not read), low > 0 for RAMP.  frequencies and scale: HOST memory. */
+fp4_status rope_frequencies(int rotary_dim, double base, fp4_rope_scaling scaling, double factor,
+                            int64_t original_positions, double low, double high, double* frequencies, double* scale);
+
+/* rope_table: cos and sin of positions 0 .. positions - 1, each scale * cos(position * frequency) and
+ * scale * sin(...) rounded once from fp64.  The angle is formed as a 64-bit fraction of a turn, so it is exact
+ * to 2^-33 of a turn at any position.
+ *   frequencies  HOST array of rotary_dim / 2 finite values (copied before the call returns)
+ *   table        device fp32[positions, rotary_dim/2, 2], 8-byte aligned
+ * positions in [1, 2^31). */
+fp4_status rope_table(const double* frequencies, int rotary_dim, double scale, int64_t positions, float* table,
+                      cudaStream_t stream);
+
+/* rope: the rotation of a [tokens, heads, head_dim] view, or (backward != 0) its transpose: the gradient by x of
+ * the gradient by the result.  fp32 products, one rounding to bf16.
+ *   x, out     bf16[tokens, heads, head_dim], 16-byte aligned; strides in elements, multiples of 8; out may be x
+ *              itself (same strides), else they do not overlap
+ *   positions  int32[tokens]; a token with a negative position (padding) is not written; one past the table is not
+ *              written and makes the next fp4_check_device_error return FP4_ERR_INVALID_ARG
+ * Requires head_dim a multiple of 8, at most 256, rotary_dim <= head_dim. */
+fp4_status rope(const fp4_rope* rope, const fp4_bf16* x, int64_t x_token_stride, int64_t x_head_stride,
+                const int32_t* positions, int64_t tokens, int64_t heads, int64_t head_dim, int backward, fp4_bf16* out,
+                int64_t out_token_stride, int64_t out_head_stride, cudaStream_t stream);
+
+/* kv_append_rope: kv_append with K rotated on the way (fp32; not rounded to bf16 between rotation and
+ * quantization), and the step's queries rotated by the same launch.
+ *   cache, k, v, slot_map, tokens: as for kv_append;  rope, positions: as for rope
+ *   q, q_out   bf16[tokens, q_heads, head_dim], as rope's x and out (q_out may be q), or both NULL (q_heads 0)
+ * A token with a negative position is skipped altogether; one with a negative slot has its q rotated only.  A
+ * position past the table skips the token, a slot past the cache its K and V, and either makes the next
+ * fp4_check_device_error return FP4_ERR_INVALID_ARG. */
+fp4_status kv_append_rope(const fp4_kv_cache* cache, const fp4_rope* rope, const fp4_bf16* k, int64_t k_token_stride,
+                          int64_t k_head_stride, const fp4_bf16* v, int64_t v_token_stride, int64_t v_head_stride,
+                          const int64_t* slot_map, const int32_t* positions, int64_t tokens, const fp4_bf16* q,
+                          int64_t q_token_stride, int64_t q_head_stride, int64_t q_heads, fp4_bf16* q_out,
+                          int64_t q_out_token_stride, int64_t q_out_head_stride, cudaStream_t stream);
+
+/* moe_sort: the routed rows in order of their experts, as gather_rows and gather_qmm take them, in one launch
+ * without workspace (capturable: the routing stays on the device).  R = tokens * k routed rows; entry (t, j) of ids
+ * is routed row t * k + j.
+ *   ids      int32[tokens, k] expert of each; a negative one is dropped, one that is num_experts or more is dropped
+ *            and makes the next fp4_check_device_error return FP4_ERR_INVALID_ARG
+ *   lhs_idx  int32[R] out: token of each sorted row, by expert and within an expert by routed row (stable)
+ *   rhs_idx  int32[R] out: its expert
+ *   slot     int32[tokens, k] out: where each routed row went, -1 if it was dropped
+ *   offsets  int32[num_experts + 1] out: first sorted row of each expert, then the number of rows kept
+ * Sorted rows from offsets[num_experts] on (as many as were dropped) get token 0 and the last expert, so that the
+ * lists stay what gather_qmm wants; no slot names them.
+ * num_experts and k in [1, 1024], R <= 2^30. */
+fp4_status moe_sort(const int32_t* ids, int64_t tokens, int64_t k, int64_t num_experts, int32_t* lhs_idx,
+                    int32_t* rhs_idx, int32_t* slot, int32_t* offsets, cudaStream_t stream);
+
+/* moe_combine: the experts' rows back to their tokens, weighted.
+ *   out[t] = residual[t] + sum over j of weights[t, j] * y[slot[t, j]]    (fp32, in order of j; one rounding to bf16)
+ *   y         bf16[rows, cols], 16-byte aligned;  slot int32[tokens, k] (moe_sort's); a negative slot adds nothing,
+ *             one that is rows or more adds nothing and makes the next fp4_check_device_error return FP4_ERR_INVALID_ARG
+ *   weights   fp32[tokens, k] or NULL (1: with the gradient of the sorted rows as y, the gradient of their gather)
+ *   residual  bf16[tokens, cols] or NULL (0), 16-byte aligned
+ *   out       bf16[tokens, cols], 16-byte aligned; may be residual itself
+ * Requires cols a multiple of 8, k in [1, 1024]. */
+fp4_status moe_combine(const fp4_bf16* y, int64_t rows, const int32_t* slot, const float* weights,
+                       const fp4_bf16* residual, int64_t tokens, int64_t k, int64_t cols, fp4_bf16* out,
+                       cudaStream_t stream);
+
+/* moe_combine_backward: the gradients of moe_combine (that of residual is dout).
+ *   dy[slot[t, j]] = bf16(weights[t, j] * dout[t]);   dweights[t, j] = dout[t] . y[slot[t, j]]   (fp32, in a fixed order)
+ *   dout      bf16[tokens, cols];  slot: as for moe_combine, no row named twice;  weights: fp32 or NULL (1)
+ *   y         bf16[rows, cols], read only for dweights (NULL without it)
+ *   rows_used device int32 or NULL: rows of dy from *rows_used on are set to zero (moe_sort's offsets + num_experts:
+ *             the rows that no slot names); without it rows that no slot names are left as they were
+ *   dy        bf16[rows, cols];  dweights fp32[tokens, k] or NULL; 0 where the slot is negative
+ * All bf16 tensors 16-byte aligned.  Requires cols a multiple of 8, k in [1, 1024]. */
+fp4_status moe_combine_backward(const fp4_bf16* dout, const fp4_bf16* y, const int32_t* slot, const float* weights,
+                                int64_t tokens, int64_t k, int64_t cols, int64_t rows, const int32_t* rows_used,
+                                fp4_bf16* dy, float* dweights, cudaStream_t stream);
+
 /* Test hook, off by default: when `enable` is nonzero the next launches of the
  * tensor-core kernels -- qqmm, qmv's NVFP4/MXFP4 path, gather_qmm and kv_attention
  * (head_dim 64, 128 or 256) -- make
