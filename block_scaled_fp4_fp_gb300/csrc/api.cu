@@ -656,7 +656,7 @@ fp4_status rms_norm(const fp4_bf16* x, int64_t x_stride, const fp4_bf16* residua
     if (!scales || cols % (mode == FP4_MODE_NVFP4 ? 16 : 32) != 0) return FP4_ERR_INVALID_ARG;
     if (global_scale && mode != FP4_MODE_NVFP4) return FP4_ERR_INVALID_ARG;
     if (layout != FP4_SCALES_LINEAR && layout != FP4_SCALES_TILED_128x4) return FP4_ERR_INVALID_ARG;
-    if (!aligned(xq, 4) || !aligned(global_scale, 4)) return FP4_ERR_ALIGNMENT;
+    if (!aligned(xq, 8) || !aligned(global_scale, 4)) return FP4_ERR_ALIGNMENT;
   }
   if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(sum_out, 16) || !aligned(out, 16) ||
       x_stride % 8 || (residual && residual_stride % 8) || (sum_out && sum_stride % 8))
@@ -666,15 +666,15 @@ fp4_status rms_norm(const fp4_bf16* x, int64_t x_stride, const fp4_bf16* residua
   if (st != FP4_OK) return st;
   RmsNormArgs a;
   a.x = x;
-  a.x_stride = x_stride;
+  a.x_stride = (int)x_stride;
   a.residual = residual;
-  a.residual_stride = residual_stride;
+  a.residual_stride = (int)residual_stride;
   a.weight = weight;
   a.eps = eps;
   a.rows = (int)rows;
   a.cols = (int)cols;
   a.sum_out = sum_out;
-  a.sum_stride = sum_stride;
+  a.sum_stride = (int)sum_stride;
   a.out = out;
   a.mode = xq ? (int)mode : 0;
   a.gs = global_scale;

@@ -201,13 +201,43 @@ __device__ __forceinline__ void block_scale_rule(uint32_t mb, float gs, float& m
   block_scale_rule<MODE>(mb, gs, nvfp4_div(gs), mul, sbyte, sval);
 }
 
-// The block rule for a block maximum b >= 0 that is any fp32 number (block_scale_rule takes bf16's); p = fl(6 gs).
+// The block rule for a block maximum b >= 0 that is any fp32 number (block_scale_rule takes bf16's), in fewer
+// instructions.  For divisors whose quotients and reciprocals stay far from fp32's ends (quick), NVFP4's quotient is
+// nvfp4_block_div's without its range tests (1024 stands for what is larger: both round to 448, or to 0 where b / p is
+// small), and the reciprocal of d = fl(s8 gs) is the hardware's approximation r and one Newton step, fl(r + r (1 - d r)),
+// which is off from 1 / d by some 2^-46 of it before its one rounding.
+struct BlockScale {
+  Nvfp4Div div;
+  float gs;
+  bool quick;
+};
+
 template <int MODE>
-__device__ __forceinline__ void block_scale_rule_f32(float b, float p, float gs, float& mul, uint32_t& sbyte) {
+__device__ __forceinline__ BlockScale block_scale(const float* gs) {
+  BlockScale s;
   if (MODE == 2) {
-    sbyte = e4m3_rn(b == 0.0f ? 0.0f : __fdiv_rn(b, p));
-    const float dd = __fmul_rn(e4m3_to_f32(sbyte), gs);
-    mul = dd == 0.0f ? 0.0f : __frcp_rn(dd);
+    s.gs = gs ? __ldg(gs) : 1.0f;
+    s.div = nvfp4_div(s.gs);
+    s.quick = s.div.p >= 0x1p-80f && s.div.p < 0x1p100f;
+  }
+  return s;
+}
+
+template <int MODE>
+__device__ __forceinline__ void block_scale_rule_f32(float b, const BlockScale& s, float& mul, uint32_t& sbyte) {
+  if (MODE == 2) {
+    if (s.quick) {
+      const float q0 = fminf(__fmul_rn(b, s.div.r), 1024.0f);
+      sbyte = e4m3_rn(__fmaf_rn(__fmaf_rn(-q0, s.div.p, b), s.div.r, q0));
+      const float d = __fmul_rn(e4m3_to_f32(sbyte), s.gs);
+      float r;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+      mul = d == 0.0f ? 0.0f : __fmaf_rn(r, __fmaf_rn(-d, r, 1.0f), r);
+    } else {
+      sbyte = e4m3_rn(b == 0.0f ? 0.0f : __fdiv_rn(b, s.div.p));
+      const float d = __fmul_rn(e4m3_to_f32(sbyte), s.gs);
+      mul = d == 0.0f ? 0.0f : __frcp_rn(d);
+    }
   } else {
     const uint32_t u = __float_as_uint(b);
     const int E = (int)(u >> 23);

@@ -163,14 +163,14 @@ struct KvAttentionArgs {
 // norm.cu: the root-mean-square norm (mode 0: no 4-bit output)
 struct RmsNormArgs {
   const uint16_t* x = nullptr;  // row strides in elements
-  int64_t x_stride = 0;
+  int x_stride = 0;
   const uint16_t* residual = nullptr;  // nullptr: none
-  int64_t residual_stride = 0;
+  int residual_stride = 0;
   const uint16_t* weight = nullptr;  // nullptr: 1
   float eps = 0.f;
   int rows = 0, cols = 0;
   uint16_t* sum_out = nullptr;  // nullptr: not wanted, as out and xq
-  int64_t sum_stride = 0;
+  int sum_stride = 0;
   uint16_t* out = nullptr;
   int mode = 0;
   const float* gs = nullptr;

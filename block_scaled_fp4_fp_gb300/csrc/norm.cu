@@ -27,14 +27,28 @@ __device__ __forceinline__ void group_sum(float& hi, float& lo, int width) {
   }
 }
 
-// 1 / sqrt((hi + lo) / n + eps): the hardware's approximation and one Newton step whose residual 1 - m r^2 is formed
-// in two parts, which leaves little but the rounding of the result
-__device__ __forceinline__ float inv_rms(float hi, float lo, float n, float eps) {
-  const float q = __fdiv_rn(hi, n);
-  const float rest = __fdividef(__fadd_rn(__fmaf_rn(-q, n, hi), lo), n);
-  float m, e;
-  two_sum(q, eps, m, e);
-  e = __fadd_rn(e, rest);
+// The same over a whole warp in two reductions instead of five steps of eleven instructions: the lanes' sums (>= 0, without
+// a second part) as whole numbers of 2^-26 of the largest's power of two, added as integers.  Each is off by half a unit, as
+// much as 2^-27 of the largest one; the sum of 32 of about the same size by some 2^-30.
+__device__ __forceinline__ void warp_sum(float s, float& hi, float& lo) {
+  const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(s));
+  if (most >= 0x7f800000u) {  // overflown, or NaN
+    hi = __uint_as_float(most);
+    lo = 0.0f;
+    return;
+  }
+  const int e = max((int)(most >> 23) - 127, -90);  // sums of this size say nothing (out_of_range, or a large eps)
+  const uint32_t t = __reduce_add_sync(0xffffffffu, __float2uint_rn(__fmul_rn(s, exp2i_f32(26 - e))));
+  hi = __uint2float_rz(t);
+  lo = (float)(int)(t - __float2uint_rz(hi));
+  const float unit = exp2i_f32(e - 26);
+  hi *= unit;
+  lo *= unit;
+}
+
+// 1 / sqrt(m + e), e small beside m: the hardware's approximation and one Newton step whose residual 1 - (m + e) r^2 is
+// formed in two parts, which leaves little but the rounding of the result
+__device__ __forceinline__ float inv_sqrt(float m, float e) {
   const float r = rsqrtf(m);
   const float p = __fmul_rn(m, r), pe = __fmaf_rn(m, r, -p);
   float d = __fmaf_rn(-p, r, 1.0f);
@@ -43,207 +57,314 @@ __device__ __forceinline__ float inv_rms(float hi, float lo, float n, float eps)
   return __fmaf_rn(__fmul_rn(0.5f, r), d, r);
 }
 
-// A row belongs to `tpr` threads: a power of two of a warp's lanes (then a warp holds several rows), or a whole CTA.
-// A thread's 16-byte pieces of the row are tpr pieces apart, so neighbouring lanes hold neighbouring pieces, and a
-// scale group is 2 (NVFP4) or 4 (MXFP4) neighbouring lanes.  The row stays in registers from its one reading to its
-// last writing; between them the sum of squares goes through the CTA.
-//
-// Precision: a thread's up to 32 squares are added in fp32, the threads' sums in pairs hi + lo, so that rstd is the
-// rounding of its exact value but for a few rows in a hundred.  Elements next to a border of the 4-bit formats move
-// by a whole step with rstd's last bit; the pairs cost six additions a step of the reduction.
-// Squares outside fp32's range (|h| near 2^63 and above, or sums below 2^-80 beside an eps that does not hide them):
-// the row is summed and scaled in fp64.
-template <int V, int MODE>
-__global__ void __launch_bounds__(1024) rms_norm_kernel(const RmsNormArgs a, int tpr, int padded_rows, int padded_cols,
-                                                        int word_scales) {
-  constexpr int G = MODE == 2 ? 2 : 4;  // pieces of a scale group
-  __shared__ float2 part[32];
-  __shared__ double part64[32];
-  __shared__ double rstd64;
-  __shared__ float rstd_sh;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int rpb = tpr > 32 ? 1 : (int)blockDim.x / tpr;
-  const int sub = tpr > 32 ? 0 : (int)threadIdx.x / tpr;
-  const int l = (int)threadIdx.x - sub * tpr;
-  const int64_t row = (int64_t)blockIdx.x * rpb + sub;
-  const int pieces = a.cols >> 3;
-  const bool live = row < a.rows;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// 1 / sqrt((hi + lo) / n + eps) (inv_n: 1 / n, whose rounding the remainder makes good)
+__device__ __forceinline__ float inv_rms(float hi, float lo, float n, float inv_n, float eps) {
+  const float q = __fmul_rn(hi, inv_n);
+  const float rest = __fmul_rn(__fadd_rn(__fmaf_rn(-q, n, hi), lo), inv_n);
+  float m, e;
+  two_sum(q, eps, m, e);
+  return inv_sqrt(m, __fadd_rn(e, rest));
+}
 
-  float h[V][8];
-  uint4 xv[V], rv[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int p = v * tpr + l;
-    const bool in = live && p < pieces;
-    xv[v] = in ? *reinterpret_cast<const uint4*>(a.x + row * a.x_stride + 8 * p) : make_uint4(0, 0, 0, 0);
-    if (a.residual)
-      rv[v] = in ? *reinterpret_cast<const uint4*>(a.residual + row * a.residual_stride + 8 * p) : make_uint4(0, 0, 0, 0);
+// 1 / sqrt(m) = r 2^k of any m >= 0 in fp64 (0 for m = 0): r in [1/2, 1], k in two halves that fp32 holds as powers
+__device__ __forceinline__ void inv_sqrt_wide(double m, float& r, float& p0, float& p1) {
+  p0 = p1 = 1.0f;
+  r = 0.0f;  // (an infinite m too)
+  if (m != m) r = __int_as_float(0x7fffffff);
+  if (!(m > 0.0) || m > 1.0e300) return;
+  const int e = ((__double2hiint(m) >> 20) - 1023) & ~1;  // even; m 2^-e is in [1, 4)
+  const double f = m * __hiloint2double((1023 - e) << 20, 0);
+  const float hi = (float)f;
+  r = inv_sqrt(hi, (float)(f - hi));
+  const int k = -(e / 2);
+  p0 = exp2i_f32(k / 2);
+  p1 = exp2i_f32(k - k / 2);
+}
+
+// Sums of squares that say nothing: overflown (or NaN), or made of squares that may have vanished, with no eps above them.
+__device__ __forceinline__ bool out_of_range(float sum, float eps) {
+  return !(sum <= 0x1p120f) || (sum < 0x1p-80f && eps < 0x1p-50f);
+}
+
+// two fp32 values in a register pair, each lane's operation rounded to nearest as the scalar one
+__device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair_of(float v) { return pair_of(__float_as_uint(v), __float_as_uint(v)); }
+__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t widen(uint32_t bf16x2) { return pair_of(bf16x2 << 16, bf16x2 & 0xFFFF0000u); }
+__device__ __forceinline__ uint4 narrow(const uint64_t* h) {
+  return make_uint4(pack_bf16x2_rn(lo_of(h[0]), hi_of(h[0])), pack_bf16x2_rn(lo_of(h[1]), hi_of(h[1])),
+                    pack_bf16x2_rn(lo_of(h[2]), hi_of(h[2])), pack_bf16x2_rn(lo_of(h[3]), hi_of(h[3])));
+}
+
+// ------------------------------------------------------------------ the row --
+// A row belongs to `tpr` threads: a power of two of a warp's lanes (then a warp holds several rows), or a whole CTA.
+// A thread holds U chunks of 16 elements, tpr chunks apart, so neighbouring lanes hold neighbouring chunks; a
+// chunk is a scale group of NVFP4, two lanes' chunks are one of MXFP4.  The row stays in registers from its one reading
+// to its last writing; between them the sum of squares goes through the CTA.
+//
+// Precision: a thread's up to 32 squares are added in fp32, the threads' sums as integers or in pairs hi + lo, so that rstd
+// is the rounding of its exact value but for a few rows in a hundred.  Elements next to a border of the 4-bit formats move
+// by a whole step with rstd's last bit.
+// Squares outside fp32's range (|h| near 2^60 and above, or sums below 2^-80 beside an eps that does not hide them):
+// the row is summed again in fp64.
+struct Shared {
+  float2 part[32];
+  double part64[32];
+  double sum64;
+};
+
+template <int U>
+struct Row {
+  uint64_t h[U][8];
+
+  __device__ __forceinline__ void set(int u, int i, uint4 v) {  // elements 8 i .. 8 i + 7 of chunk u
+    h[u][4 * i] = widen(v.x);
+    h[u][4 * i + 1] = widen(v.y);
+    h[u][4 * i + 2] = widen(v.z);
+    h[u][4 * i + 3] = widen(v.w);
   }
-  float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const uint32_t xw[4] = {xv[v].x, xv[v].y, xv[v].z, xv[v].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      h[v][2 * j] = bf16_lo(xw[j]);
-      h[v][2 * j + 1] = bf16_hi(xw[j]);
-    }
-    if (a.residual) {
-      const uint32_t rw[4] = {rv[v].x, rv[v].y, rv[v].z, rv[v].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        h[v][2 * j] = __fadd_rn(h[v][2 * j], bf16_lo(rw[j]));
-        h[v][2 * j + 1] = __fadd_rn(h[v][2 * j + 1], bf16_hi(rw[j]));
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      s0 = __fmaf_rn(h[v][2 * j], h[v][2 * j], s0);
-      s1 = __fmaf_rn(h[v][2 * j + 1], h[v][2 * j + 1], s1);
-    }
+  __device__ __forceinline__ void add(int u, int i, uint4 v) {
+    h[u][4 * i] = add2(h[u][4 * i], widen(v.x));
+    h[u][4 * i + 1] = add2(h[u][4 * i + 1], widen(v.y));
+    h[u][4 * i + 2] = add2(h[u][4 * i + 2], widen(v.z));
+    h[u][4 * i + 3] = add2(h[u][4 * i + 3], widen(v.w));
   }
-  if (a.sum_out) {
+  // the thread's sum of squares
+  __device__ __forceinline__ float squares() const {
+    uint64_t s = 0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int p = v * tpr + l;
-      if (live && p < pieces)
-        *reinterpret_cast<uint4*>(a.sum_out + row * a.sum_stride + 8 * p) =
-            make_uint4(pack_bf16x2_rn(h[v][0], h[v][1]), pack_bf16x2_rn(h[v][2], h[v][3]),
-                       pack_bf16x2_rn(h[v][4], h[v][5]), pack_bf16x2_rn(h[v][6], h[v][7]));
-    }
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s = fma2(h[u][j], h[u][j], s);
+    return __fadd_rn(lo_of(s), hi_of(s));
   }
-  // the row's sum of squares and 1 / rms
-  float hi, lo;
-  two_sum(s0, s1, hi, lo);
-  group_sum(hi, lo, min(tpr, 32));
-  float rstd;
-  if (tpr > 32) {
-    const int nw = (int)blockDim.x >> 5;
-    if (lane == 0) part[warp] = make_float2(hi, lo);
-    __syncthreads();
-    if (warp == 0) {
-      const float2 t = lane < nw ? part[lane] : make_float2(0.f, 0.f);
-      hi = t.x;
-      lo = t.y;
-      group_sum(hi, lo, 32);
-      if (lane == 0) {
-        const bool wide = !(hi <= 0x1p120f) || (hi < 0x1p-80f && a.eps < 0x1p-50f);
-        rstd_sh = wide ? -1.0f : inv_rms(hi, lo, (float)a.cols, a.eps);
-      }
-    }
-    __syncthreads();
-    rstd = rstd_sh;
-  } else {
-    const bool wide = !(hi <= 0x1p120f) || (hi < 0x1p-80f && a.eps < 0x1p-50f);
-    rstd = wide ? -1.0f : inv_rms(hi, lo, (float)a.cols, a.eps);
-  }
-  // (a CTA's threads agree on their row's rstd; of rows in one warp, any wide one takes the warp along)
-  const bool wide = rstd < 0.0f;
-  if (tpr > 32 ? wide : __any_sync(0xffffffffu, wide)) {
+  // rstd (or, in fp64, a row that fp32's squares do not hold: then scaled by its power of two) for this thread's row
+  template <bool CTA>
+  __device__ __forceinline__ float scale(float rstd, const RmsNormArgs& a, int tpr, double inv_n, Shared& sh) {
+    // (a CTA's threads agree on their row's rstd; of rows in one warp, any wide one takes the warp along)
+    const bool wide = rstd < 0.0f;
+    if (!(CTA ? wide : __any_sync(0xffffffffu, wide))) return rstd;
     double s = 0.0;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s += (double)h[v][j] * (double)h[v][j];
+      for (int j = 0; j < 8; ++j) {
+        const double p = lo_of(h[u][j]), q = hi_of(h[u][j]);
+        s += p * p + q * q;
+      }
     for (int o = min(tpr, 32) >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (tpr > 32) {
-      if (lane == 0) part64[warp] = s;
+    if (CTA) {
+      if ((threadIdx.x & 31) == 0) sh.part64[threadIdx.x >> 5] = s;
       __syncthreads();
       if (threadIdx.x == 0) {
         s = 0.0;
-        for (int w = 0; w < (int)blockDim.x >> 5; ++w) s += part64[w];
-        rstd64 = s;
+        for (int w = 0; w < (int)blockDim.x >> 5; ++w) s += sh.part64[w];
+        sh.sum64 = s;
       }
       __syncthreads();
-      s = rstd64;
+      s = sh.sum64;
     }
-    const double m = s / a.cols + (double)a.eps;
-    const double r = m == 0.0 ? 0.0 : 1.0 / sqrt(m);
+    if (!wide) return rstd;
+    float r, p0, p1;
+    inv_sqrt_wide(s * inv_n + (double)a.eps, r, p0, p1);
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) h[v][j] = wide ? (float)((double)h[v][j] * r) : __fmul_rn(h[v][j], rstd);
-  } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[v][j] = __fmul_rn(h[v][j], rstd);
+      for (int j = 0; j < 8; ++j) h[u][j] = mul2(mul2(h[u][j], pair_of(p0)), pair_of(p1));
+    return r;
   }
-  const float gs = (MODE == 2 && a.gs) ? __ldg(a.gs) : 1.0f;
-  const float div = __fmul_rn(6.0f, gs);
+  __device__ __forceinline__ void write_sum(const RmsNormArgs& a, int row, bool live, int l, int tpr, int pieces) const {
+    uint4* sr = reinterpret_cast<uint4*>(a.sum_out + (int64_t)row * a.sum_stride);
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int p = v * tpr + l;
-    const bool in = live && p < pieces;
-    if (a.weight && p < pieces) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(a.weight) + p);
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        h[v][2 * j] = __fmul_rn(h[v][2 * j], bf16_lo(ww[j]));
-        h[v][2 * j + 1] = __fmul_rn(h[v][2 * j + 1], bf16_hi(ww[j]));
-      }
+    for (int u = 0; u < U; ++u) {
+      const int p = 2 * (u * tpr + l);
+      if (live && p < pieces) sr[p] = narrow(h[u]);
+      if (live && p + 1 < pieces) sr[p + 1] = narrow(h[u] + 4);
     }
-    if (a.out && in)
-      *reinterpret_cast<uint4*>(a.out + row * a.cols + 8 * p) =
-          make_uint4(pack_bf16x2_rn(h[v][0], h[v][1]), pack_bf16x2_rn(h[v][2], h[v][3]), pack_bf16x2_rn(h[v][4], h[v][5]),
-                     pack_bf16x2_rn(h[v][6], h[v][7]));
-    if (MODE != 0) {
-      float b = 0.0f;
+  }
+  // y, and what is wanted of it
+  template <int MODE>
+  __device__ __forceinline__ void write(const RmsNormArgs& a, float rstd, const BlockScale& rule, int row,
+                                        bool live, int l, int tpr, int pieces, int padded_rows, int padded_cols,
+                                        int word_scales) {
+    constexpr int G = MODE == 1 ? 2 : 1;  // chunks of a scale group
+    const uint64_t r2 = pair_of(rstd);
+    uint4* out = reinterpret_cast<uint4*>(a.out + (int64_t)row * a.cols);
+    uint32_t* codes = a.xq + (int64_t)row * pieces;
+    uint8_t* scales = a.tiled ? a.scales + (int64_t)(row >> 7) * (padded_cols << 7) + ((row & 31) << 4) + ((row & 127) >> 5 << 2)
+                              : a.scales + (int64_t)row * padded_cols;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) b = fmaxf(b, fabsf(h[v][j]));
+    for (int u = 0; u < U; ++u) {
+      const int ch = u * tpr + l, p = 2 * ch;
+      const bool in = live && p < pieces;
 #pragma unroll
-      for (int o = 1; o < G; o <<= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
-      float mul;
-      uint32_t sbyte;
-      block_scale_rule_f32<MODE>(b, div, gs, mul, sbyte);
-      float f[8];
+      for (int j = 0; j < 8; ++j) h[u][j] = mul2(h[u][j], r2);
+      if (a.weight) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(h[v][j], mul);
-      if (in) a.xq[row * pieces + p] = e2m1x8_rn(f);
-      // scale bytes: four groups' in one word by their first lane, where the buffer allows words
-      const int c = p / G;  // scale column
-      if (!in) sbyte = 0;   // (the padding's bytes are 0)
-      if (word_scales) {
-        uint32_t w = sbyte | __shfl_down_sync(0xffffffffu, sbyte, G) << 8;
-        w |= __shfl_down_sync(0xffffffffu, w, 2 * G) << 16;
-        if ((l & (4 * G - 1)) == 0 && c < padded_cols && row < padded_rows) {
-          const int64_t at = a.tiled ? tiled_scale_offset(row, c, padded_cols) : row * padded_cols + c;
-          *reinterpret_cast<uint32_t*>(a.scales + at) = w;
+        for (int i = 0; i < 2; ++i)
+          if (p + i < pieces) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(a.weight) + p + i);
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[u][4 * i + j] = mul2(h[u][4 * i + j], widen(ww[j]));
+          }
+      }
+      if (a.out) {
+        if (in) out[p] = narrow(h[u]);
+        if (live && p + 1 < pieces) out[p + 1] = narrow(h[u] + 4);
+      }
+      if (MODE != 0) {
+        float b = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) b = max_abs3(b, lo_of(h[u][j]), hi_of(h[u][j]));
+        if (MODE == 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 1));
+        float mul;
+        uint32_t sbyte;
+        block_scale_rule_f32<MODE>(b, rule, mul, sbyte);
+        const uint64_t m2 = pair_of(mul);
+        float f[2][8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint64_t v = mul2(h[u][j], m2);
+          f[j >> 2][2 * (j & 3)] = lo_of(v);
+          f[j >> 2][2 * (j & 3) + 1] = hi_of(v);
         }
-      } else if ((l & (G - 1)) == 0 && c < padded_cols && row < padded_rows) {
-        a.scales[a.tiled ? tiled_scale_offset(row, c, padded_cols) : row * padded_cols + c] = (uint8_t)sbyte;
+        if (in) *reinterpret_cast<uint2*>(codes + p) = make_uint2(e2m1x8_rn(f[0]), e2m1x8_rn(f[1]));  // (4-bit rows are whole chunks)
+        // scale bytes: four groups' in one word by their first lane, where the buffer allows words
+        const int c = ch / G;  // scale column
+        if (!in) sbyte = 0;    // (the padding's bytes are 0)
+        if (word_scales) {
+          uint32_t w = sbyte | __shfl_down_sync(0xffffffffu, sbyte, G) << 8;
+          w |= __shfl_down_sync(0xffffffffu, w, 2 * G) << 16;
+          if ((l & (4 * G - 1)) == 0 && c < padded_cols && row < padded_rows)
+            *reinterpret_cast<uint32_t*>(scales + (a.tiled ? c << 7 : c)) = w;
+        } else if ((l & (G - 1)) == 0 && c < padded_cols && row < padded_rows) {
+          scales[a.tiled ? ((c >> 2) << 9) + (c & 3) : c] = (uint8_t)sbyte;
+        }
       }
     }
   }
+};
+
+// Bound by HBM in bf16; with 4-bit results by some 24 instructions an element between the loads and the stores; one row
+// by latency.
+template <int U, int MODE, bool CTA>
+__global__ void __launch_bounds__(CTA ? 1024 : 128) rms_norm_kernel(const RmsNormArgs a, int tpr, int padded_rows, int padded_cols,
+                                                        int word_scales, double inv_n) {
+  __shared__ Shared sh;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int sub = CTA ? 0 : (int)threadIdx.x / tpr, l = (int)threadIdx.x - sub * tpr;
+  const int row = CTA ? (int)blockIdx.x : (int)blockIdx.x * ((int)blockDim.x / tpr) + sub;
+  const int pieces = a.cols >> 3;  // of 16 bytes
+  const bool live = row < a.rows;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+
+  Row<U> r;
+  {
+    const uint4* xr = reinterpret_cast<const uint4*>(a.x + (int64_t)row * a.x_stride);
+    const uint4* rr = reinterpret_cast<const uint4*>(a.residual + (int64_t)row * a.residual_stride);
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    uint4 xv[U][2], rv[U][2];
+    if (CTA && live && pieces == 2 * U * tpr) {  // (no select a load)
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) xv[u][i] = xr[2 * (u * tpr + l) + i];
+      if (a.residual) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) rv[u][i] = rr[2 * (u * tpr + l) + i];
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int p = 2 * (u * tpr + l) + i;
+          const bool in = live && p < pieces;
+          xv[u][i] = in ? xr[p] : none;
+          rv[u][i] = a.residual && in ? rr[p] : none;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        r.set(u, i, xv[u][i]);
+        if (a.residual) r.add(u, i, rv[u][i]);
+      }
+  }
+  float hi = r.squares(), lo = 0.0f;
+  if (a.sum_out) r.write_sum(a, row, live, l, tpr, pieces);
+  if (CTA || tpr == 32)
+    warp_sum(hi, hi, lo);
+  else
+    group_sum(hi, lo, tpr);
+  if (CTA) {  // every warp adds the warps' sums up for itself, each aligned group of lanes all of them: one barrier
+    const int nw = (int)blockDim.x >> 5, width = nw <= 4 ? 4 : nw <= 8 ? 8 : nw <= 16 ? 16 : 32, w = lane & (width - 1);
+    if (lane == 0) sh.part[warp] = make_float2(hi, lo);
+    __syncthreads();
+    const float2 t = w < nw ? sh.part[w] : make_float2(0.f, 0.f);
+    hi = t.x;
+    lo = t.y;
+    group_sum(hi, lo, width);
+  }
+  float rstd = out_of_range(hi, a.eps) ? -1.0f : inv_rms(hi, lo, (float)a.cols, (float)inv_n, a.eps);
+  rstd = r.template scale<CTA>(rstd, a, tpr, inv_n, sh);
+  r.template write<MODE>(a, rstd, block_scale<MODE>(a.gs), row, live, l, tpr, pieces, padded_rows, padded_cols, word_scales);
 }
 
-template <int V>
-cudaError_t launch_v(const cudaLaunchConfig_t& cfg, const RmsNormArgs& a, int tpr, int prows, int pcols, int words) {
-  if (!a.xq) return cudaLaunchKernelEx(&cfg, rms_norm_kernel<V, 0>, a, tpr, prows, pcols, words);
-  if (a.mode == FP4_MODE_NVFP4) return cudaLaunchKernelEx(&cfg, rms_norm_kernel<V, 2>, a, tpr, prows, pcols, words);
-  return cudaLaunchKernelEx(&cfg, rms_norm_kernel<V, 1>, a, tpr, prows, pcols, words);
+template <int U, bool CTA>
+cudaError_t launch_u(const cudaLaunchConfig_t& cfg, const RmsNormArgs& a, int tpr, int prows, int pcols, int words) {
+  const double inv_n = 1.0 / a.cols;
+  if (!a.xq) return cudaLaunchKernelEx(&cfg, rms_norm_kernel<U, 0, CTA>, a, tpr, prows, pcols, words, inv_n);
+  if (a.mode == FP4_MODE_NVFP4) return cudaLaunchKernelEx(&cfg, rms_norm_kernel<U, 2, CTA>, a, tpr, prows, pcols, words, inv_n);
+  return cudaLaunchKernelEx(&cfg, rms_norm_kernel<U, 1, CTA>, a, tpr, prows, pcols, words, inv_n);
 }
 
 }  // namespace
 
 cudaError_t launch_rms_norm(const DevInfo& d, const RmsNormArgs& a, cudaStream_t s) {
-  (void)d;
-  const int group = a.mode == FP4_MODE_NVFP4 ? 16 : 32;
-  int pieces = a.cols / 8, prows = a.rows, pcols = 0, words = 0, least = 4;
+  int chunks = (a.cols + 15) / 16, prows = a.rows, pcols = 0, words = 0, least = 1;
   if (a.xq) {
-    const int scols = a.cols / group;
+    const int scols = a.cols / (a.mode == FP4_MODE_NVFP4 ? 16 : 32);
     pcols = a.tiled ? (scols + 3) / 4 * 4 : scols;
     prows = a.tiled ? (a.rows + 127) / 128 * 128 : a.rows;
     words = pcols % 4 == 0 && (reinterpret_cast<uintptr_t>(a.scales) & 3) == 0;
-    least = group / 8 * 4;                            // the lanes of four scales
-    pieces = (pieces + least - 1) / least * least;    // (whole words of scales, and the padding's)
+    least = a.mode == FP4_MODE_NVFP4 ? 4 : 8;       // the lanes of four scales
+    chunks = (chunks + least - 1) / least * least;  // (whole words of scales, and the padding's)
   }
-  int V = 1;
-  while (V < 4 && pieces > 1024 * V) V *= 2;
-  const int need = (pieces + V - 1) / V;
+  // Two chunks a thread where the rows fill the GPU anyway (4096 x 5120: 27.6 us against 28.9 in bf16, 26.5 against 31.8 to
+  // NVFP4), one where latency counts (1 x 5120: 2.4 us against 2.7, 2.8 against 3.3); more than 1024 chunks need two.
+  const int U = chunks > 1024 || (int64_t)chunks * prows >= (int64_t)d.sm_count * 1024 ? 2 : 1;
+  const int need = (chunks + U - 1) / U;
   int tpr = (need + 31) / 32 * 32;
   if (need <= 32)
     for (tpr = least; tpr < need;) tpr *= 2;
@@ -257,9 +378,9 @@ cudaError_t launch_rms_norm(const DevInfo& d, const RmsNormArgs& a, cudaStream_t
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (V == 1) return launch_v<1>(cfg, a, tpr, prows, pcols, words);
-  if (V == 2) return launch_v<2>(cfg, a, tpr, prows, pcols, words);
-  return launch_v<4>(cfg, a, tpr, prows, pcols, words);
+  if (tpr > 32)
+    return U == 1 ? launch_u<1, true>(cfg, a, tpr, prows, pcols, words) : launch_u<2, true>(cfg, a, tpr, prows, pcols, words);
+  return U == 1 ? launch_u<1, false>(cfg, a, tpr, prows, pcols, words) : launch_u<2, false>(cfg, a, tpr, prows, pcols, words);
 }
 
 }  // namespace fp4

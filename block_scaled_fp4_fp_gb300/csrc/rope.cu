@@ -282,10 +282,9 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_rope_kernel(
     for (int j = 0; j < 8; ++j) b = fmaxf(b, fabsf(f[i][j]));
   }
   const float* gsp = is_v ? c.gs_v : c.gs_k;
-  const float gs = (MODE == 2 && gsp) ? __ldg(gsp) : 1.0f;
   float mul;
   uint32_t sbyte;
-  block_scale_rule_f32<MODE>(b, __fmul_rn(6.0f, gs), gs, mul, sbyte);
+  block_scale_rule_f32<MODE>(b, block_scale<MODE>(gsp), mul, sbyte);
   uint32_t words[kGroup / 8];
 #pragma unroll
   for (int i = 0; i < kGroup / 8; ++i) {

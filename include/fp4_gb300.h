@@ -499,7 +499,7 @@ fp4_status kv_attention(const fp4_kv_cache* cache, const fp4_bf16* q, int64_t q_
  *   residual bf16[rows, cols] or NULL, as x;  weight bf16[cols] or NULL, 16-byte aligned
  *   sum_out  bf16[rows, cols] or NULL, as x; may be residual or x itself (same stride)
  *   out      bf16[rows, cols] or NULL, contiguous, 16-byte aligned; may be x itself
- *   xq       uint32[rows, cols/8] or NULL (at least one of out and xq), 4-byte aligned;
+ *   xq       uint32[rows, cols/8] or NULL (at least one of out and xq), 8-byte aligned;
  *            mode, global_scale, scales, layout: as for fp4_quantize, read only with xq
  * rstd is held in fp32 from a sum of squares of at least fp32's precision; it holds
  * over bf16's whole range (squares that fp32 cannot hold are summed in fp64).  A row
