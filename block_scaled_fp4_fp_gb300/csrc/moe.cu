@@ -26,139 +26,212 @@ __device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
 }
 
 // ---------------------------------------------------------------- moe_sort --
-// A stable counting sort.  Every warp owns a run of routed rows, in order of the CTA's rank in its cluster and the
-// warp's in its CTA, and counts its run's rows by expert: lanes with the same expert find one another
-// (match) and the first of them adds their number, so nothing is atomic and the order is fixed.  Sums of the counts
-// over the warps before (shared memory), the CTAs before (distributed shared memory) and the experts before give every
-// (warp, expert) its first place; the second pass over the run hands the places out.
-// Bound by latency.  One CTA up to kSortOne rows, above a cluster of eight: its counts need no workspace and no second launch.
-constexpr int kSortBatch = 4;  // loads in flight a lane
+// A stable counting sort in one launch: one CTA, or a cluster whose CTAs hold the routed rows in order of their ranks.
+//   1. Each CTA counts its rows by expert; the counts of the CTAs before (distributed shared memory) and the experts
+//      before give the place of its first row of each expert.
+//   2. Tile by tile of up to kTileRows rows, a run of them a warp: lanes with the same expert find one another by a
+//      vote on each bit of its number (nothing is atomic, so the order is fixed), which with the counts of the warps
+//      before gives each row its place in the tile's own order.  The tile is put into that order in shared memory and
+//      written from there, neighbouring places by neighbouring lanes.
+// A CTA of one tile takes its counts from 2.  No workspace, no second launch.  Bound by latency, and by what one SM issues.
+// Tried, for 131,072 rows of 256 experts on eight CTAs: the match instruction in place of the votes (41 us against 31),
+// rows written straight to their places (31 against 22: a sector a lane; a tile of one row a lane still does).
+constexpr int kRunRows = 8;                        // a lane's rows of a tile
+constexpr int kTileRows = 32 * 32 * kRunRows;      // of a CTA of 32 warps: 13 bits
+constexpr int kExpertBits = 10;
 
-__global__ void __launch_bounds__(1024) moe_sort_kernel(const int32_t* __restrict__ ids, int R, int k, int E, int run,
-                                                        int32_t* __restrict__ lhs, int32_t* __restrict__ rhs,
-                                                        int32_t* __restrict__ slot, int32_t* __restrict__ offsets,
-                                                        unsigned* __restrict__ err) {
-  extern __shared__ int sort_smem[];
-  const int W = (int)blockDim.x >> 5, pitch = E + 1;  // (odd pitch of counts for even E: a column's words lie in different banks)
-  int* count = sort_smem;             // [W][pitch]: rows of the warp, then of the warps before it
-  int* total = sort_smem + W * pitch; // [E] of this CTA
-  int* first = total + E;             // [E]: place of this CTA's first row of the expert
-  __shared__ int warp_sum[32];
-  __shared__ int kept_sh;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int ctas = (int)gridDim.x;  // one cluster
-  const uint32_t rank = cluster_rank();
-  for (int i = t; i < W * pitch; i += (int)blockDim.x) count[i] = 0;
-  __syncthreads();
-  // R <= 2^30 and at most 8 * 32 runs of R / 256 + 31 rows: no overflow
-  const int lo = ((int)rank * W + warp) * run, hi = min(lo + run, R);
-  int* mine = count + warp * pitch;
-  bool bad = false;
-  for (int i0 = lo; i0 < hi; i0 += 32 * kSortBatch) {
-    int e[kSortBatch];
-#pragma unroll
-    for (int u = 0; u < kSortBatch; ++u) {
-      const int i = i0 + 32 * u + lane;
-      e[u] = i < hi ? __ldg(ids + i) : -1;
-      bad |= e[u] >= E;
-      if ((unsigned)e[u] >= (unsigned)E) e[u] = E;  // dropped
-    }
-#pragma unroll
-    for (int u = 0; u < kSortBatch; ++u) {
-      const unsigned peers = __match_any_sync(0xffffffffu, e[u]);
-      if (e[u] < E && lane == __ffs((int)peers) - 1) mine[e[u]] += __popc(peers);
-      __syncwarp();
-    }
-  }
-  if (bad) record_error(err, kErrIndex);
-  __syncthreads();
-  // over the CTA's warps: a warp an expert, a lane a warp
-  for (int e = warp; e < E; e += W) {
-    const int c = lane < W ? count[lane * pitch + e] : 0;
-    int s = c;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += u;
-    }
-    if (lane < W) count[lane * pitch + e] = s - c;
-    if (lane == 31) total[e] = s;
-  }
-  if (ctas > 1) {
-    cluster_arrive();
-    cluster_wait();
-  } else {
-    __syncthreads();
-  }
-  // over the CTAs, then over the experts (a thread an expert: the block has at least E threads)
-  int before = 0, all = 0;
-  if (t < E) {
-    if (ctas == 1) {
-      all = total[t];
-    } else {
-      for (int c = 0; c < ctas; ++c) {
-        const int v = ld_cluster(total + t, (uint32_t)c);
-        all += v;
-        if (c < (int)rank) before += v;
-      }
-    }
-  }
-  if (ctas > 1) cluster_arrive();  // this CTA has read the others' totals (waited for at the end)
-  int s = all;
+// exclusive sum over the block of one value a thread (all threads; `part`: 33 ints)
+__device__ __forceinline__ int block_scan(int v, int* part, int& all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = (int)blockDim.x >> 5;
+  int s = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int u = __shfl_up_sync(0xffffffffu, s, o);
     if (lane >= o) s += u;
   }
-  if (lane == 31) warp_sum[warp] = s;
+  if (lane == 31) part[warp] = s;
   __syncthreads();
   if (warp == 0) {
-    const int v = lane < W ? warp_sum[lane] : 0;
-    int i = v;
+    const int w = lane < W ? part[lane] : 0;
+    int i = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, i, o);
       if (lane >= o) i += u;
     }
-    if (lane < W) warp_sum[lane] = i - v;
-    if (lane == 31) kept_sh = i;
+    if (lane < W) part[lane] = i - w;
+    if (lane == 31) part[32] = i;
   }
   __syncthreads();
-  const int kept = kept_sh;
-  if (t < E) {
-    const int at = warp_sum[warp] + s - all;
-    first[t] = at + before;
-    if (rank == 0) offsets[t] = at;
-  }
-  if (rank == 0 && t == 0) offsets[E] = kept;
-  __syncthreads();
-  for (int i0 = lo; i0 < hi; i0 += 32 * kSortBatch) {
-    int e[kSortBatch];
+  all = part[32];
+  return part[warp] + s - v;
+}
+
+__global__ void __launch_bounds__(1024) moe_sort_kernel(const int32_t* __restrict__ ids, int R, int k, int E, int bits,
+                                                        int rows_cta, int run, int32_t* __restrict__ lhs,
+                                                        int32_t* __restrict__ rhs, int32_t* __restrict__ slot,
+                                                        int32_t* __restrict__ offsets, unsigned* __restrict__ err) {
+  extern __shared__ int sort_smem[];
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, W = (int)blockDim.x >> 5;
+  int* count = sort_smem;                                // [W][E]: rows of the warp, then of the warps before it
+  int* total = count + W * E;                            // [E] rows of this CTA
+  int* delta = total + E;                                // [E] from a place in the tile's order to one in the list
+  int* start = delta + E;                                // [E] the expert's first place in the tile's order
+  uint32_t* stage = reinterpret_cast<uint32_t*>(start + E);  // [tile]: row of the tile and expert
+  __shared__ int part[33];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int ctas = (int)gridDim.x;  // one cluster
+  const uint32_t rank = cluster_rank();
+  const int tile = run * W;
+  // rows [begin, end) of this CTA (R <= 2^30: no overflow)
+  const int begin = min((int)rank * rows_cta, R), end = min(begin + rows_cta, R);
+  const bool one_tile = rows_cta <= tile;
+  int e[kRunRows], at[kRunRows];
+  bool bad = false;
+
+  auto load = [&](int i0) {
 #pragma unroll
-    for (int u = 0; u < kSortBatch; ++u) {
-      const int i = i0 + 32 * u + lane;
-      e[u] = i < hi ? __ldg(ids + i) : -1;
-      if ((unsigned)e[u] >= (unsigned)E) e[u] = E;
+    for (int u = 0; u < kRunRows; ++u) {
+      const int i = i0 + warp * run + 32 * u + lane;
+      e[u] = 32 * u < run && i < end ? __ldg(ids + i) : -1;
     }
 #pragma unroll
-    for (int u = 0; u < kSortBatch; ++u) {
-      const int i = i0 + 32 * u + lane;
-      const unsigned peers = __match_any_sync(0xffffffffu, e[u]);
-      const unsigned ahead = peers & ((1u << lane) - 1);
-      int at = -1;
-      if (e[u] < E) {
-        at = first[e[u]] + mine[e[u]] + __popc(ahead);
-        lhs[at] = (int)((unsigned)i / (unsigned)k);
-        rhs[at] = e[u];
+    for (int u = 0; u < kRunRows; ++u) {
+      bad |= e[u] >= E;
+      if (e[u] >= E) e[u] = -1;  // dropped
+    }
+  };
+  // at: a row's place among its warp's of the same expert; count: the warps' numbers of rows, then of those before
+  auto places = [&]() -> int {  // returns (thread t) the tile's rows of expert t
+    for (int i = t; i < W * E; i += (int)blockDim.x) count[i] = 0;
+    __syncthreads();
+    int* mine = count + warp * E;
+#pragma unroll
+    for (int u = 0; u < kRunRows; ++u) {
+      if (32 * u >= run) break;
+      const bool kept = e[u] >= 0;
+      unsigned peers = __ballot_sync(0xffffffffu, kept);
+#pragma unroll
+      for (int b = 0; b < kExpertBits; ++b) {
+        if (b >= bits) break;
+        const bool one = (e[u] >> b) & 1;
+        const unsigned v = __ballot_sync(0xffffffffu, one);
+        peers &= one ? v : ~v;
       }
-      if (i < hi) slot[i] = at;
+      const unsigned ahead = peers & ((1u << lane) - 1);
+      const int base = kept ? mine[e[u]] : 0;
+      at[u] = base + __popc(ahead);
       __syncwarp();
-      if (e[u] < E && ahead == 0) mine[e[u]] += __popc(peers);
+      if (kept && ahead == 0) mine[e[u]] = base + __popc(peers);
       __syncwarp();
     }
+    __syncthreads();
+    int s = 0;
+    if (t < E) {  // a thread an expert (the block has at least E)
+      for (int w0 = 0; w0 < W; w0 += 8) {
+        int c[8];
+#pragma unroll
+        for (int w = 0; w < 8; ++w) c[w] = w0 + w < W ? count[(w0 + w) * E + t] : 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+          if (w0 + w < W) count[(w0 + w) * E + t] = s;
+          s += c[w];
+        }
+      }
+    }
+    return s;
+  };
+
+  int in_tile = 0;  // (thread t < E) the tile's rows of expert t
+  load(begin);
+  if (one_tile) {
+    in_tile = places();
+    if (t < E) total[t] = in_tile;
+  } else {
+    if (t < E) total[t] = 0;
+    __syncthreads();
+    for (int i0 = begin;;) {
+#pragma unroll
+      for (int u = 0; u < kRunRows; ++u)
+        if (e[u] >= 0) atomicAdd(total + e[u], 1);
+      i0 += tile;
+      if (i0 >= end) break;
+      load(i0);
+    }
   }
+  int before = 0, all = 0;
+  if (ctas > 1) {
+    cluster_arrive();
+    cluster_wait();
+    if (t < E)
+      for (int c = 0; c < ctas; ++c) {
+        const int v = ld_cluster(total + t, (uint32_t)c);
+        all += v;
+        if (c < (int)rank) before += v;
+      }
+    cluster_arrive();  // this CTA has read the others' totals (waited for at the end)
+  } else {
+    __syncthreads();
+    if (t < E) all = total[t];
+  }
+  int kept;
+  int first = block_scan(all, part, kept);  // (thread t < E) place of the expert's first row, then of this CTA's next
+  if (rank == 0) {
+    if (t < E) offsets[t] = first;
+    if (t == 0) offsets[E] = kept;
+  }
+  first += before;
+  if (one_tile && run == 32) {  // a row a lane: straight to its place
+    if (t < E) start[t] = first;
+    __syncthreads();
+    const int i = begin + warp * 32 + lane;
+    if (i < end) {
+      int to = -1;
+      if (e[0] >= 0) {
+        to = start[e[0]] + count[warp * E + e[0]] + at[0];
+        lhs[to] = (int)((unsigned)i / (unsigned)k);
+        rhs[to] = e[0];
+      }
+      slot[i] = to;
+    }
+  } else for (int i0 = begin; i0 < end; i0 += tile) {
+    if (!one_tile) {
+      load(i0);
+      in_tile = places();
+    }
+    __syncthreads();  // (part is free again)
+    int staged;
+    const int s = block_scan(t < E ? in_tile : 0, part, staged);
+    if (t < E) {
+      start[t] = s;
+      delta[t] = first - s;
+      first += in_tile;
+    }
+    __syncthreads();
+    const int* mine = count + warp * E;
+#pragma unroll
+    for (int u = 0; u < kRunRows; ++u) {
+      const int j = warp * run + 32 * u + lane, i = i0 + j;
+      if (32 * u >= run || i >= end) break;
+      int to = -1;
+      if (e[u] >= 0) {
+        to = start[e[u]] + mine[e[u]] + at[u];
+        stage[to] = (uint32_t)j << kExpertBits | (uint32_t)e[u];
+        to += delta[e[u]];
+      }
+      slot[i] = to;
+    }
+    __syncthreads();
+    for (int j = t; j < staged; j += (int)blockDim.x) {
+      const uint32_t v = stage[j];
+      const int x = (int)(v & ((1u << kExpertBits) - 1)), to = j + delta[x];
+      lhs[to] = (int)(((unsigned)i0 + (v >> kExpertBits)) / (unsigned)k);
+      rhs[to] = x;
+    }
+    if (!one_tile) __syncthreads();  // count, delta and stage have been read
+  }
+  if (bad) record_error(err, kErrIndex);
   for (int64_t i = (int64_t)kept + (int)rank * (int)blockDim.x + t; i < R; i += (int64_t)ctas * (int)blockDim.x) {
     lhs[i] = 0;
     rhs[i] = E - 1;
@@ -334,30 +407,39 @@ void pdl(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int64_t grid, int b
 
 }  // namespace
 
-constexpr int kSortOne = 4096;  // rows that one CTA sorts
+// Rows that one CTA sorts (2048 of 32 experts: 4.5 us, with a cluster 4.4; 4096: 5.7 against 4.4), and the CTAs of a
+// cluster above: 16, the most there is (131,072 rows of 256 experts: 12.5 us, with eight 22).
+constexpr int kSortOne = 2048, kSortCtas = 16;
 
 cudaError_t launch_moe_sort(const DevInfo& d, const int32_t* ids, int64_t T, int k, int E, int32_t* lhs, int32_t* rhs,
                             int32_t* slot, int32_t* offsets, cudaStream_t s) {
   const int64_t R = T * k;
-  const int ctas = R > kSortOne ? 8 : 1;
-  int64_t threads = std::max<int64_t>((E + 31) / 32 * 32, std::min<int64_t>((R + 31) / 32 * 32, 1024));
-  if (ctas > 1) threads = 1024;
-  const int warps = (int)threads / 32;
-  const int64_t per = (R + (int64_t)ctas * warps - 1) / ((int64_t)ctas * warps);
-  const int run = (int)((per + 31) / 32 * 32);
-  const int smem = (warps * (E + 1) + 2 * E) * 4;
-  static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(d, moe_sort_kernel, (32 * 1025 + 2 * 1024) * 4, done);
+  const int ctas = R > kSortOne ? kSortCtas : 1;
+  const int64_t whole = std::max<int64_t>((E + 31) / 32 * 32, std::min<int64_t>((R + 31) / 32 * 32, 1024));
+  const int threads = ctas > 1 ? 1024 : (int)whole, warps = threads / 32;
+  const int64_t rows_cta = (R + ctas - 1) / ctas;
+  const int run = (int)std::min<int64_t>((rows_cta + threads - 1) / threads, kRunRows) * 32;
+  int bits = 0;
+  while ((1 << bits) < E) ++bits;
+  const int smem = ((warps + 3) * E + run * warps) * 4;
+  static std::atomic<uint64_t> done{0}, wide{0};
+  cudaError_t e = allow_smem(d, moe_sort_kernel, (35 * 1024 + kTileRows) * 4, done);
   if (e != cudaSuccess) return e;
+  if (const uint64_t bit = 1ull << (d.device & 63); !(wide.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(moe_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    wide.fetch_or(bit, std::memory_order_release);
+  }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
-  pdl(cfg, attr, ctas, (int)threads, (size_t)smem, s);
+  pdl(cfg, attr, ctas, threads, (size_t)smem, s);
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = (unsigned)ctas;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, moe_sort_kernel, ids, (int)R, k, E, run, lhs, rhs, slot, offsets, d.err);
+  return cudaLaunchKernelEx(&cfg, moe_sort_kernel, ids, (int)R, k, E, bits, (int)rows_cta, run, lhs, rhs, slot, offsets,
+                            d.err);
 }
 
 cudaError_t launch_moe_combine(const DevInfo& d, const uint16_t* y, int64_t rows, const int32_t* slot,
