@@ -48,6 +48,20 @@ __device__ __forceinline__ uint32_t pack_bf16x2_rn(float lo, float hi) {
   return r;
 }
 
+// eight bf16 values of a 16-byte piece <-> fp32
+__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f[2 * j] = bf16_lo(w[j]);
+    f[2 * j + 1] = bf16_hi(w[j]);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2_rn(f[0], f[1]), pack_bf16x2_rn(f[2], f[3]), pack_bf16x2_rn(f[4], f[5]),
+                    pack_bf16x2_rn(f[6], f[7]));
+}
+
 // --------------------------------------------------------- 4-bit codecs ----
 // Two fp32 values -> one byte of two e2m1 codes: `lo` in bits 0..3, `hi` in
 // bits 4..7 (round to nearest even, saturate to +-6, sign kept).

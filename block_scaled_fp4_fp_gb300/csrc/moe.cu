@@ -240,77 +240,88 @@ __global__ void __launch_bounds__(1024) moe_sort_kernel(const int32_t* __restric
 }
 
 // ------------------------------------------------------------- moe_combine --
-// A thread a 16-byte piece of a token's row: its k rows are read with up to eight loads in flight, added in fp32 in
-// order of j, rounded once.  Bound by HBM.
+// A thread has P 16-byte pieces of tokens' rows, K rows of each in flight: eight loads whatever k is (bytes in flight are
+// what the rate goes by: 2048 x 4 of 2880 took 17.9 us with four).  Added in fp32 in order of j, rounded once.
+// Bound by HBM.
 constexpr int kCombineThreads = 128;
 
+template <int K, int P>
 __global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(
     const uint16_t* __restrict__ y, int rows, const int32_t* __restrict__ slot, const float* __restrict__ weights,
     const uint16_t* residual, int64_t T, int k, int pieces, uint16_t* out, unsigned* __restrict__ err) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int64_t base = (int64_t)blockIdx.x * kCombineThreads;
+  const int64_t base = (int64_t)blockIdx.x * (kCombineThreads * P);
   const int64_t t0 = base <= UINT32_MAX ? (int64_t)((unsigned)base / (unsigned)pieces) : base / pieces;
   const unsigned rem = (unsigned)(base - t0 * pieces) + threadIdx.x;
-  const int64_t t = t0 + rem / (unsigned)pieces;
-  const int p = (int)(rem % (unsigned)pieces);
-  if (t >= T) return;
-  float acc[8];
+  int64_t t[P];
+  int p[P];
+  float acc[P][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+  for (int q = 0; q < P; ++q) {
+    const unsigned r = rem + (unsigned)(q * kCombineThreads), n = r / (unsigned)pieces;
+    t[q] = t0 + n;
+    p[q] = (int)(r - n * (unsigned)pieces);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[q][i] = 0.f;
+  }
   if (residual) {
-    const uint4 r = *(reinterpret_cast<const uint4*>(residual) + t * pieces + p);
-    const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
+    uint4 r[P];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      acc[2 * i] = bf16_lo(rw[i]);
-      acc[2 * i + 1] = bf16_hi(rw[i]);
-    }
+    for (int q = 0; q < P; ++q)
+      if (t[q] < T) r[q] = *(reinterpret_cast<const uint4*>(residual) + t[q] * pieces + p[q]);
+#pragma unroll
+    for (int q = 0; q < P; ++q)
+      if (t[q] < T) unpack8(r[q], acc[q]);
   }
-  const int32_t* sl = slot + t * k;
-  for (int j0 = 0; j0 < k; j0 += 8) {
-    uint4 v[8];
-    int at[8];
+  for (int j0 = 0; j0 < k; j0 += K) {
+    uint4 v[P][K];
+    int at[P][K];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      at[j] = j0 + j < k ? __ldg(sl + j0 + j) : -1;
-      if (at[j] >= rows) {
-        if (p == 0) record_error(err, kErrIndex);
-        at[j] = -1;
+    for (int q = 0; q < P; ++q)
+#pragma unroll
+      for (int j = 0; j < K; ++j) at[q][j] = t[q] < T && j0 + j < k ? __ldg(slot + t[q] * k + j0 + j) : -1;
+#pragma unroll
+    for (int q = 0; q < P; ++q)
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        if (at[q][j] >= rows) {
+          if (p[q] == 0) record_error(err, kErrIndex);
+          at[q][j] = -1;
+        }
+        if (at[q][j] >= 0) v[q][j] = ld_stream_v4(reinterpret_cast<const uint4*>(y) + (int64_t)at[q][j] * pieces + p[q]);
       }
-    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (at[j] >= 0) v[j] = ld_stream_v4(reinterpret_cast<const uint4*>(y) + (int64_t)at[j] * pieces + p);
+    for (int q = 0; q < P; ++q)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (at[j] < 0) continue;
-      const float w = weights ? __ldg(weights + t * k + j0 + j) : 1.0f;
-      const uint32_t vw[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+      for (int j = 0; j < K; ++j) {
+        if (at[q][j] < 0) continue;
+        const float w = weights ? __ldg(weights + t[q] * k + j0 + j) : 1.0f;
+        float f[8];
+        unpack8(v[q][j], f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[2 * i] = __fmaf_rn(w, bf16_lo(vw[i]), acc[2 * i]);
-        acc[2 * i + 1] = __fmaf_rn(w, bf16_hi(vw[i]), acc[2 * i + 1]);
+        for (int i = 0; i < 8; ++i) acc[q][i] = __fmaf_rn(w, f[i], acc[q][i]);
       }
-    }
   }
-  *(reinterpret_cast<uint4*>(out) + t * pieces + p) =
-      make_uint4(pack_bf16x2_rn(acc[0], acc[1]), pack_bf16x2_rn(acc[2], acc[3]), pack_bf16x2_rn(acc[4], acc[5]),
-                 pack_bf16x2_rn(acc[6], acc[7]));
+#pragma unroll
+  for (int q = 0; q < P; ++q)
+    if (t[q] < T) *(reinterpret_cast<uint4*>(out) + t[q] * pieces + p[q]) = pack8(acc[q]);
 }
 
 // ---------------------------------------------------- moe_combine_backward --
-// A CTA a token: dout's row is read once (again from L1 for each further eight of the k rows), a row of dy written and a
-// row of y multiplied with it for each j.  The dot products of eight rows are reduced together: each step of the
-// butterfly halves the number of sums a lane holds, nine shuffles instead of forty.  The CTAs from T on clear the rows that no slot names.
-// Bound by HBM.
+// A CTA a token: dout's row is read (again from L1 for each further K of the k rows), a row of dy written and a row of y
+// multiplied with it for each j; two pieces of K rows are in flight a thread.  The dot products of the K rows are
+// reduced together: each step of the butterfly halves the number of sums a lane holds, nine shuffles instead of forty for eight.
+// The CTAs from T on clear the rows that no slot names.  Bound by HBM.
 constexpr int kTailCtas = 64, kBackwardThreads = 512;
 
-__global__ void __launch_bounds__(kBackwardThreads) moe_combine_backward_kernel(
+template <int K>
+__global__ void __launch_bounds__(kBackwardThreads, 1) moe_combine_backward_kernel(
     const uint16_t* __restrict__ dout, const uint16_t* __restrict__ y, const int32_t* __restrict__ slot,
     const float* __restrict__ weights, int64_t T, int k, int pieces, int64_t rows, const int32_t* __restrict__ rows_used,
     uint16_t* __restrict__ dy, float* __restrict__ dweights, unsigned* __restrict__ err) {
-  __shared__ float part[kBackwardThreads / 32][8];
+  constexpr int P = 2;
+  __shared__ float part[kBackwardThreads / 32][K];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t t = blockIdx.x;
@@ -321,14 +332,15 @@ __global__ void __launch_bounds__(kBackwardThreads) moe_combine_backward_kernel(
         *(reinterpret_cast<uint4*>(dy) + r * pieces + p) = make_uint4(0, 0, 0, 0);
     return;
   }
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, step = (int)blockDim.x;
   const uint4* g4 = reinterpret_cast<const uint4*>(dout) + t * pieces;
-  for (int j0 = 0; j0 < k; j0 += 8) {
-    int at[8];
-    float w[8], dot[8];
+  for (int j0 = 0; j0 < k; j0 += K) {
+    int at[K];
+    float w[K], dot[K];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      at[j] = j0 + j < k ? __ldg(slot + t * k + j0 + j) : -1;
+    for (int j = 0; j < K; ++j) at[j] = j0 + j < k ? __ldg(slot + t * k + j0 + j) : -1;
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
       if (at[j] >= rows) {
         if (threadIdx.x == 0) record_error(err, kErrIndex);
         at[j] = -1;
@@ -336,42 +348,44 @@ __global__ void __launch_bounds__(kBackwardThreads) moe_combine_backward_kernel(
       w[j] = at[j] >= 0 && weights ? __ldg(weights + t * k + j0 + j) : 1.0f;
       dot[j] = 0.f;
     }
-    for (int p = threadIdx.x; p < pieces; p += (int)blockDim.x) {
-      const uint4 gv = __ldg(g4 + p);
-      const uint32_t gw[4] = {gv.x, gv.y, gv.z, gv.w};
-      uint4 v[8];
-      if (dweights) {
+    for (int p0 = threadIdx.x; p0 < pieces; p0 += P * step) {
+      uint4 gv[P], v[P][K];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (at[j] >= 0) v[j] = ld_stream_v4(reinterpret_cast<const uint4*>(y) + (int64_t)at[j] * pieces + p);
-      }
-      float g[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        g[2 * i] = bf16_lo(gw[i]);
-        g[2 * i + 1] = bf16_hi(gw[i]);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (at[j] < 0) continue;
-        uint32_t o[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2_rn(__fmul_rn(w[j], g[2 * i]), __fmul_rn(w[j], g[2 * i + 1]));
-        *(reinterpret_cast<uint4*>(dy) + (int64_t)at[j] * pieces + p) = make_uint4(o[0], o[1], o[2], o[3]);
+      for (int q = 0; q < P; ++q) {
+        const int p = p0 + q * step;
+        if (p >= pieces) continue;
+        gv[q] = __ldg(g4 + p);
         if (dweights) {
-          const uint32_t vw[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            dot[j] = __fmaf_rn(g[2 * i], bf16_lo(vw[i]), dot[j]);
-            dot[j] = __fmaf_rn(g[2 * i + 1], bf16_hi(vw[i]), dot[j]);
+          for (int j = 0; j < K; ++j)
+            if (at[j] >= 0) v[q][j] = ld_stream_v4(reinterpret_cast<const uint4*>(y) + (int64_t)at[j] * pieces + p);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < P; ++q) {
+        const int p = p0 + q * step;
+        if (p >= pieces) continue;
+        float g[8];
+        unpack8(gv[q], g);
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+          if (at[j] < 0) continue;
+          float f[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(w[j], g[i]);
+          *(reinterpret_cast<uint4*>(dy) + (int64_t)at[j] * pieces + p) = pack8(f);
+          if (dweights) {
+            unpack8(v[q][j], f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dot[j] = __fmaf_rn(g[i], f[i], dot[j]);
           }
         }
       }
     }
     if (!dweights) continue;
-    // lane bits 4, 3, 2 pick the half of the sums that the lane keeps
+    // the lane's top bits pick the half of the sums that it keeps: lane / (32 / K) is then j
 #pragma unroll
-    for (int n = 4, o = 16; n > 0; n >>= 1, o >>= 1) {
+    for (int n = K / 2, o = 16; n > 0; n >>= 1, o >>= 1) {
       const bool upper = lane & o;
 #pragma unroll
       for (int i = 0; i < n; ++i) {
@@ -380,11 +394,11 @@ __global__ void __launch_bounds__(kBackwardThreads) moe_combine_backward_kernel(
       }
     }
     float d = dot[0];
-    d = __fadd_rn(d, __shfl_xor_sync(0xffffffffu, d, 2));
-    d = __fadd_rn(d, __shfl_xor_sync(0xffffffffu, d, 1));
-    if ((lane & 3) == 0) part[warp][lane >> 2] = d;  // lane >> 2 is j: its bits picked the halves
+#pragma unroll
+    for (int o = 16 / K; o > 0; o >>= 1) d = __fadd_rn(d, __shfl_xor_sync(0xffffffffu, d, o));
+    if (lane % (32 / K) == 0) part[warp][lane / (32 / K)] = d;
     __syncthreads();
-    if (threadIdx.x < 8 && j0 + (int)threadIdx.x < k) {
+    if (threadIdx.x < K && j0 + (int)threadIdx.x < k) {
       float sum = 0.f;
       for (int i = 0; i < (int)blockDim.x >> 5; ++i) sum = __fadd_rn(sum, part[i][threadIdx.x]);
       const int s = __ldg(slot + t * k + j0 + threadIdx.x);
@@ -442,16 +456,28 @@ cudaError_t launch_moe_sort(const DevInfo& d, const int32_t* ids, int64_t T, int
                             d.err);
 }
 
-cudaError_t launch_moe_combine(const DevInfo& d, const uint16_t* y, int64_t rows, const int32_t* slot,
-                               const float* weights, const uint16_t* residual, int64_t T, int k, int cols,
-                               uint16_t* out, cudaStream_t s) {
-  const int pieces = cols / 8;
-  const int64_t grid = (T * pieces + kCombineThreads - 1) / kCombineThreads;
+namespace {
+template <int K, int P>
+cudaError_t combine(const DevInfo& d, const uint16_t* y, int64_t rows, const int32_t* slot, const float* weights,
+                    const uint16_t* residual, int64_t T, int k, int pieces, uint16_t* out, cudaStream_t s) {
+  const int64_t grid = (T * pieces + kCombineThreads * P - 1) / (kCombineThreads * P);
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   pdl(cfg, attr, grid, kCombineThreads, 0, s);
-  return cudaLaunchKernelEx(&cfg, moe_combine_kernel, y, (int)rows, slot, weights, residual, T, k, pieces, out, d.err);
+  return cudaLaunchKernelEx(&cfg, moe_combine_kernel<K, P>, y, (int)rows, slot, weights, residual, T, k, pieces, out, d.err);
+}
+}  // namespace
+
+cudaError_t launch_moe_combine(const DevInfo& d, const uint16_t* y, int64_t rows, const int32_t* slot,
+                               const float* weights, const uint16_t* residual, int64_t T, int k, int cols,
+                               uint16_t* out, cudaStream_t s) {
+  const int pieces = cols / 8;
+  // several pieces a thread only where there are threads enough for the GPU (96 x 4 of 5120: see the document's table)
+  const bool many = T * pieces >= (int64_t)d.sm_count * 2048;
+  if (!many || k > 4) return combine<8, 1>(d, y, rows, slot, weights, residual, T, k, pieces, out, s);
+  if (k > 2) return combine<4, 2>(d, y, rows, slot, weights, residual, T, k, pieces, out, s);
+  return combine<2, 4>(d, y, rows, slot, weights, residual, T, k, pieces, out, s);
 }
 
 cudaError_t launch_moe_combine_backward(const DevInfo& d, const uint16_t* dout, const uint16_t* y, const int32_t* slot,
@@ -462,9 +488,17 @@ cudaError_t launch_moe_combine_backward(const DevInfo& d, const uint16_t* dout, 
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  pdl(cfg, attr, grid, std::min(kBackwardThreads, (pieces + 31) / 32 * 32), 0, s);
-  return cudaLaunchKernelEx(&cfg, moe_combine_backward_kernel, dout, y, slot, weights, T, k, pieces, rows, rows_used, dy,
-                            dweights, d.err);
+  // short rows in one go; else many tokens share an SM, and few take it whole
+  const int most = T >= 4 * d.sm_count ? 128 : kBackwardThreads;
+  pdl(cfg, attr, grid, std::min(most, (pieces + 31) / 32 * 32), 0, s);
+  if (k > 4)
+    return cudaLaunchKernelEx(&cfg, moe_combine_backward_kernel<8>, dout, y, slot, weights, T, k, pieces, rows, rows_used,
+                              dy, dweights, d.err);
+  if (k > 2)
+    return cudaLaunchKernelEx(&cfg, moe_combine_backward_kernel<4>, dout, y, slot, weights, T, k, pieces, rows, rows_used,
+                              dy, dweights, d.err);
+  return cudaLaunchKernelEx(&cfg, moe_combine_backward_kernel<2>, dout, y, slot, weights, T, k, pieces, rows, rows_used,
+                            dy, dweights, d.err);
 }
 
 }  // namespace fp4

@@ -41,19 +41,6 @@ __device__ __forceinline__ void turn(float a, float b, float2 cs, float& u, floa
   v = __fadd_rn(__fmul_rn(b, cs.x), __fmul_rn(a, cs.y));
 }
 
-__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    f[2 * j] = bf16_lo(w[j]);
-    f[2 * j + 1] = bf16_hi(w[j]);
-  }
-}
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2_rn(f[0], f[1]), pack_bf16x2_rn(f[2], f[3]), pack_bf16x2_rn(f[4], f[5]),
-                    pack_bf16x2_rn(f[6], f[7]));
-}
-
 // n table entries from an 8-byte aligned address (16-byte where the address allows)
 template <int N>
 __device__ __forceinline__ void load_cs(const float2* p, bool wide, float2 (&cs)[N]) {
