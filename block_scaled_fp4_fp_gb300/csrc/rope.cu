@@ -9,6 +9,7 @@
 #include "../../include/fp4_gb300.h"
 #include "common.cuh"
 #include "launch.h"
+#include "packed.cuh"
 
 namespace fp4 {
 namespace {
@@ -35,16 +36,10 @@ __global__ void __launch_bounds__(256) rope_table_kernel(const RopeSteps s, int 
   }
 }
 
-// (a, b) turned; sgn -1: the transpose
-__device__ __forceinline__ void turn(float a, float b, float2 cs, float& u, float& v) {
-  u = __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y));
-  v = __fadd_rn(__fmul_rn(b, cs.x), __fmul_rn(a, cs.y));
-}
-
 // n table entries from an 8-byte aligned address (16-byte where the address allows)
 template <int N>
-__device__ __forceinline__ void load_cs(const float2* p, bool wide, float2 (&cs)[N]) {
-  if (wide) {
+__device__ __forceinline__ void load_cs(const float2* p, float2 (&cs)[N]) {
+  if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
       const float4 v = __ldg(reinterpret_cast<const float4*>(p + i));
@@ -57,61 +52,97 @@ __device__ __forceinline__ void load_cs(const float2* p, bool wide, float2 (&cs)
   }
 }
 
-// Whether the rotated channels of a head are whole 16-byte pieces (and, in halves, a pair's two lie in two pieces).
-__host__ __device__ inline bool whole_pieces(const RopeDesc& r) {
-  return r.interleaved ? r.rotary_dim % 8 == 0 : r.rotary_dim % 16 == 0;
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) { return pair_of(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ uint64_t swapped(uint64_t v) { return pair_of((uint32_t)(v >> 32), (uint32_t)v); }
+__device__ __forceinline__ float bf16_at(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
+
+// Largest vector (8, 4 channels; 1: none) of which the rotated channels of a head are whole vectors and, in halves, a
+// pair's two channels lie at the same place of two vectors.
+__host__ __device__ inline int vector_of(const RopeDesc& r) {
+  const int n = r.interleaved ? r.rotary_dim : r.rotary_dim / 2;
+  return n % 8 == 0 ? 8 : n % 4 == 0 ? 4 : 1;
 }
 
 // -------------------------------------------------------------------- rope --
-// What one thread does of a token's heads [first, heads) in steps of `step`, unit `u` of each head.  Whole pieces: a unit
-// is two pieces of a head's halves (eight pairs), or an interleaved piece (four pairs), then the pieces that stay as
-// they are.  Its cosines are loaded once for all its heads, and kBatch heads are in flight.  Otherwise a unit is a pair
-// (two-byte accesses), then a channel that stays.
-constexpr int kBatch = 4;
+// What one thread does of a token's heads first, first + step, ..: unit `u` of each.  A unit is two vectors of a head's
+// halves, or an interleaved vector, then the vectors that stay as they are; its cosines are loaded once for all its
+// heads, and several heads' loads are in flight.  Rotations that are no whole vectors (rotary/2 or, interleaved, rotary
+// no multiple of 4) are done a pair at a time.  Whatever is written was read by the same thread before: in place is fine.
+// Bound by HBM.
+template <int N>
+struct VecOf;
+template <>
+struct VecOf<8> {
+  using T = uint4;
+};
+template <>
+struct VecOf<4> {
+  using T = uint2;
+};
 
-template <bool INTERLEAVED>
-__device__ __forceinline__ void rope_pieces(const HeadsView& x, const uint16_t* in, uint16_t* out, const float2* row,
-                                            bool wide, float sign, int rotary, int u, int first, int step) {
-  constexpr int N = INTERLEAVED ? 4 : 8;  // pairs of the unit
-  const int turned = rotary / (INTERLEAVED ? 8 : 16);
-  if (u >= turned) {  // a piece that stays
-    const int c = rotary + 8 * (u - turned);
-    for (int h = first; h < x.heads; h += step)
-      *reinterpret_cast<uint4*>(out + h * x.out_head + c) = *reinterpret_cast<const uint4*>(in + h * x.in_head + c);
-    return;
+template <bool INTERLEAVED, int N>
+__device__ __forceinline__ void rope_vectors(const HeadsView& x, const uint16_t* in, uint16_t* out, const float2* row,
+                                             float sign, int rotary, int u, int first, int step) {
+  using T = typename VecOf<N>::T;
+  constexpr int NW = N / 2, B = INTERLEAVED ? 8 : 4;  // words of a vector; heads in flight
+  const int turned = rotary / (INTERLEAVED ? N : 2 * N);
+  const bool stays = u >= turned;
+  const int c0 = stays ? rotary + N * (u - turned) : N * u, c1 = c0 + rotary / 2;
+  uint64_t C[NW], S[NW];
+  if (!stays) {
+    float2 cs[INTERLEAVED ? NW : N];
+    load_cs(row + (INTERLEAVED ? NW : N) * u, cs);
+#pragma unroll
+    for (int j = 0; j < NW; ++j) {
+      if (INTERLEAVED) {
+        C[j] = pair_of(cs[j].x);
+        S[j] = pair_of(-sign * cs[j].y, sign * cs[j].y);
+      } else {
+        C[j] = pair_of(cs[2 * j].x, cs[2 * j + 1].x);
+        S[j] = pair_of(sign * cs[2 * j].y, sign * cs[2 * j + 1].y);
+      }
+    }
   }
-  const int c0 = 8 * u, c1 = c0 + rotary / 2;
-  float2 cs[N];
-  load_cs<N>(row + N * u, wide, cs);
+  for (int h0 = first; h0 < x.heads; h0 += B * step) {
+    T a[B], b[B];
 #pragma unroll
-  for (int i = 0; i < N; ++i) cs[i].y *= sign;
-  for (int h0 = first; h0 < x.heads; h0 += kBatch * step) {
-    uint4 a[kBatch], b[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
+    for (int i = 0; i < B; ++i) {
       const int h = h0 + i * step;
       if (h < x.heads) {
-        a[i] = *reinterpret_cast<const uint4*>(in + h * x.in_head + c0);
-        if (!INTERLEAVED) b[i] = *reinterpret_cast<const uint4*>(in + h * x.in_head + c1);
+        a[i] = *reinterpret_cast<const T*>(in + h * x.in_head + c0);
+        if (!INTERLEAVED && !stays) b[i] = *reinterpret_cast<const T*>(in + h * x.in_head + c1);
       }
     }
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
+    for (int i = 0; i < B; ++i) {
       const int h = h0 + i * step;
-      if (h < x.heads) {
-        float fa[8], fb[8], ga[8], gb[8];
-        unpack8(a[i], fa);
-        if (INTERLEAVED) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) turn(fa[2 * j], fa[2 * j + 1], cs[j], ga[2 * j], ga[2 * j + 1]);
-        } else {
-          unpack8(b[i], fb);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) turn(fa[j], fb[j], cs[j], ga[j], gb[j]);
-          *reinterpret_cast<uint4*>(out + h * x.out_head + c1) = pack8(gb);
-        }
-        *reinterpret_cast<uint4*>(out + h * x.out_head + c0) = pack8(ga);
+      if (h >= x.heads) continue;
+      T* o0 = reinterpret_cast<T*>(out + h * x.out_head + c0);
+      T* o1 = reinterpret_cast<T*>(out + h * x.out_head + c1);
+      if (stays) {
+        *o0 = a[i];
+        continue;
       }
+      const uint32_t* aw = reinterpret_cast<const uint32_t*>(&a[i]);
+      const uint32_t* bw = reinterpret_cast<const uint32_t*>(&b[i]);
+      T ya, yb;
+      uint32_t* yaw = reinterpret_cast<uint32_t*>(&ya);
+      uint32_t* ybw = reinterpret_cast<uint32_t*>(&yb);
+#pragma unroll
+      for (int j = 0; j < NW; ++j) {
+        const uint64_t p = widen(aw[j]);
+        if (INTERLEAVED) {
+          const uint64_t y = add2(mul2(p, C[j]), mul2(swapped(p), S[j]));
+          yaw[j] = pack_bf16x2_rn(lo_of(y), hi_of(y));
+        } else {
+          const uint64_t q = widen(bw[j]), minus = pair_of(-lo_of(S[j]), -hi_of(S[j]));
+          const uint64_t y0 = add2(mul2(p, C[j]), mul2(q, minus)), y1 = add2(mul2(q, C[j]), mul2(p, S[j]));
+          yaw[j] = pack_bf16x2_rn(lo_of(y0), hi_of(y0));
+          ybw[j] = pack_bf16x2_rn(lo_of(y1), hi_of(y1));
+        }
+      }
+      *o0 = ya;
+      if (!INTERLEAVED) *o1 = yb;
     }
   }
 }
@@ -125,19 +156,16 @@ __device__ __forceinline__ void rope_pairs(const RopeDesc& r, const HeadsView& x
     return;
   }
   const int c0 = r.interleaved ? 2 * u : u, c1 = r.interleaved ? c0 + 1 : u + half;
-  float2 cs = __ldg(row + u);
-  cs.y *= sign;
+  const float2 cs = __ldg(row + u);
+  const float sn = sign * cs.y;
   for (int h = first; h < x.heads; h += step) {
-    const float a = __uint_as_float((uint32_t)in[h * x.in_head + c0] << 16);
-    const float b = __uint_as_float((uint32_t)in[h * x.in_head + c1] << 16);
-    float p, q;
-    turn(a, b, cs, p, q);
-    out[h * x.out_head + c0] = (uint16_t)f32_to_bf16_rn(p);
-    out[h * x.out_head + c1] = (uint16_t)f32_to_bf16_rn(q);
+    const float a = bf16_at(in + h * x.in_head + c0), b = bf16_at(in + h * x.in_head + c1);
+    out[h * x.out_head + c0] = (uint16_t)f32_to_bf16_rn(__fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, sn)));
+    out[h * x.out_head + c1] = (uint16_t)f32_to_bf16_rn(__fadd_rn(__fmul_rn(b, cs.x), __fmul_rn(a, sn)));
   }
 }
 
-// Thread `i` of the rotation's: unit fastest, so that neighbouring lanes hold neighbouring pieces of a head, then
+// Thread `i` of the rotation's: unit fastest, so that neighbouring lanes hold neighbouring vectors of a head, then
 // `lanes` threads that take every lanes-th head, then the token.
 __device__ __forceinline__ void rope_item(const RopeDesc& r, const HeadsView& x, const int32_t* positions, int64_t T,
                                           float sign, int units, int lanes, int64_t i, unsigned* err) {
@@ -155,20 +183,18 @@ __device__ __forceinline__ void rope_item(const RopeDesc& r, const HeadsView& x,
   const float2* row = r.table + (int64_t)pos * (r.rotary_dim / 2);
   const uint16_t* in = x.in + t * x.in_token;
   uint16_t* out = x.out + t * x.out_token;
-  if (whole_pieces(r)) {
-    const bool wide = (reinterpret_cast<uintptr_t>(row) & 15) == 0;
-    if (r.interleaved)
-      rope_pieces<true>(x, in, out, row, wide, sign, r.rotary_dim, u, hl, lanes);
-    else
-      rope_pieces<false>(x, in, out, row, wide, sign, r.rotary_dim, u, hl, lanes);
-  } else {
-    rope_pairs(r, x, in, out, row, sign, u, hl, lanes);
+  switch (vector_of(r) * 2 + r.interleaved) {
+    case 16: return rope_vectors<false, 8>(x, in, out, row, sign, r.rotary_dim, u, hl, lanes);
+    case 17: return rope_vectors<true, 8>(x, in, out, row, sign, r.rotary_dim, u, hl, lanes);
+    case 8: return rope_vectors<false, 4>(x, in, out, row, sign, r.rotary_dim, u, hl, lanes);
+    case 9: return rope_vectors<true, 4>(x, in, out, row, sign, r.rotary_dim, u, hl, lanes);
+    default: return rope_pairs(r, x, in, out, row, sign, u, hl, lanes);
   }
 }
 
 constexpr int kRopeThreads = 128;
 
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeDesc r, const HeadsView x,
+__global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(const RopeDesc r, const HeadsView x,
                                                             const int32_t* __restrict__ positions, int64_t T, float sign,
                                                             int units, int lanes, unsigned* __restrict__ err) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -177,122 +203,299 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeDesc r, co
 }
 
 // ----------------------------------------------------------- kv_append_rope --
-// The first blocks append, a thread a scale group as in kv_append: it reads its group and, of a K group, the channels
-// that its own are paired with (which another thread of the same warp or its neighbour reads as its own: they
-// come from L1), rotates in fp32, and applies the block rule to the fp32 values.  The blocks behind them rotate q.
-// Channels [c0, c0 + 8) of a K head, rotated.
-__device__ __forceinline__ void rotated8(const RopeDesc& r, const uint16_t* head, const float2* row, bool pieces, bool wide,
-                                         int c0, float (&f)[8]) {
-  const int half = r.rotary_dim / 2;
-  unpack8(__ldg(reinterpret_cast<const uint4*>(head + c0)), f);
-  if (c0 >= r.rotary_dim) return;
-  if (pieces && r.interleaved) {
-    float2 cs[4];
-    load_cs<4>(row + c0 / 2, wide, cs);
+// The first blocks append, the blocks behind them rotate q.  An appending thread has a unit of every lanes-th kv head
+// of a token, of K and of V, its cosines loaded once for all its heads.  A unit is
+//   kPairs   (halves of whole scale groups): two pieces of 8 channels of K's halves, which turn each other.  The lanes that
+//            share two groups (2 of NVFP4, 4 of MXFP4) do the rule of one of them each and exchange multipliers;
+//   kChunks  (interleaved): 16 channels of K;  both: 16 channels of V, and of K where it stays;
+//   kPieces  (any other rotation): 8 channels; what they are paired with is read beside them.
+// Bound by HBM, and to NVFP4 by instructions (some 8 an element).
+constexpr int kAppendThreads = 128, kAppendBatch = 2;
+enum AppendKind { kPairs, kChunks, kPieces };
+
+// eight values' codes, their largest size
+__device__ __forceinline__ uint32_t codes8(const uint64_t* f, float mul) {
+  const uint64_t m2 = pair_of(mul);
+  float y[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float u, v;
-      turn(f[2 * j], f[2 * j + 1], cs[j], u, v);
-      f[2 * j] = u;
-      f[2 * j + 1] = v;
-    }
-  } else if (pieces) {
-    const bool first = c0 < half;
-    float g[8];
-    float2 cs[8];
-    unpack8(__ldg(reinterpret_cast<const uint4*>(head + (first ? c0 + half : c0 - half))), g);
-    load_cs<8>(row + (first ? c0 : c0 - half), wide, cs);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float s = first ? -cs[j].y : cs[j].y;  // a cos - b sin, or b cos + a sin
-      f[j] = __fadd_rn(__fmul_rn(f[j], cs[j].x), __fmul_rn(g[j], s));
-    }
-  } else {
-    for (int j = 0; j < 8; ++j) {
-      const int c = c0 + j;
-      if (c >= r.rotary_dim) break;
-      const bool first = r.interleaved ? !(c & 1) : c < half;
-      const int i = r.interleaved ? c >> 1 : (first ? c : c - half);
-      const int other = r.interleaved ? c ^ 1 : (first ? c + half : c - half);
-      const float2 cs = __ldg(row + i);
-      const float g = __uint_as_float((uint32_t)__ldg(head + other) << 16);
-      f[j] = __fadd_rn(__fmul_rn(f[j], cs.x), __fmul_rn(g, first ? -cs.y : cs.y));
-    }
+  for (int j = 0; j < 4; ++j) {
+    const uint64_t p = mul2(f[j], m2);
+    y[2 * j] = lo_of(p);
+    y[2 * j + 1] = hi_of(p);
   }
+  return e2m1x8_rn(y);
+}
+__device__ __forceinline__ float largest8(const uint64_t* f) {
+  float m = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) m = max_abs3(m, lo_of(f[j]), hi_of(f[j]));
+  return m;
+}
+__device__ __forceinline__ void widen8(uint4 v, uint64_t* f) {
+  f[0] = widen(v.x);
+  f[1] = widen(v.y);
+  f[2] = widen(v.z);
+  f[3] = widen(v.w);
 }
 
-constexpr int kAppendThreads = 128;
+// one cached row's codes and scales
+struct CacheRow {
+  uint32_t* codes;
+  uint8_t* scales;
+};
 
+// 16 channels, the u-th of the row: a scale group of NVFP4, half of one of MXFP4 (the lane beside has the other)
 template <int MODE>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_rope_kernel(
+__device__ __forceinline__ void store_chunk(const CacheRow& row, int u, const uint64_t (&f)[8], const BlockScale& rule,
+                                            unsigned peers) {
+  float m = fmaxf(largest8(f), largest8(f + 4)), mul;
+  if (MODE == 1) m = fmaxf(m, __shfl_xor_sync(peers, m, 1));
+  uint32_t sbyte;
+  block_scale_rule_f32<MODE>(m, rule, mul, sbyte);
+  reinterpret_cast<uint2*>(row.codes)[u] = make_uint2(codes8(f, mul), codes8(f + 4, mul));
+  if (MODE == 2)
+    row.scales[u] = (uint8_t)sbyte;
+  else if (!(u & 1))
+    row.scales[u >> 1] = (uint8_t)sbyte;
+}
+
+// pieces u and u + half / 8 of the row: lanes of even u do the rule of the first's group, of odd u of the second's
+template <int MODE>
+__device__ __forceinline__ void store_pair(const CacheRow& row, int u, int half, const uint64_t (&fa)[4],
+                                           const uint64_t (&fb)[4], const BlockScale& rule, unsigned peers) {
+  constexpr int G = MODE == 2 ? 16 : 32;
+  const float ma = largest8(fa), mb = largest8(fb);
+  const bool odd = u & 1;
+  float m = fmaxf(odd ? mb : ma, __shfl_xor_sync(peers, odd ? ma : mb, 1)), mul;
+  if (MODE == 1) m = fmaxf(m, __shfl_xor_sync(peers, m, 2));
+  uint32_t sbyte;
+  block_scale_rule_f32<MODE>(m, rule, mul, sbyte);
+  const float other = __shfl_xor_sync(peers, mul, 1);
+  row.codes[u] = codes8(fa, odd ? other : mul);
+  row.codes[u + half / 8] = codes8(fb, odd ? mul : other);
+  if (MODE == 2 || !(u & 2)) row.scales[(u * 8 + (odd ? half : 0)) / G] = (uint8_t)sbyte;
+}
+
+// How the channels [c0, c0 + 8) of a K head are turned: y = own C + other S
+struct PieceTurn {
+  enum Kind { kStays, kPartner, kSwap, kGather } kind;
+  int c0, partner;  // the paired piece (kPartner)
+  uint64_t C[4], S[4];
+
+  __device__ __forceinline__ PieceTurn(const RopeDesc& r, const float2* row, int c) : kind(kStays), c0(c), partner(c) {
+    if (c >= r.rotary_dim) return;
+    const int half = r.rotary_dim / 2;
+    if (vector_of(r) != 8) {
+      kind = kGather;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float c2[2], s2[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int ch = c0 + 2 * j + k;
+          const bool first = r.interleaved ? k == 0 : ch < half;
+          const float2 cs = ch < r.rotary_dim ? __ldg(row + (r.interleaved ? ch >> 1 : first ? ch : ch - half))
+                                              : make_float2(1.0f, first ? 0.0f : -0.0f);
+          c2[k] = cs.x;
+          s2[k] = first ? -cs.y : cs.y;  // (a channel that stays: a 1 + 0 (-0), its zero's sign too)
+        }
+        C[j] = pair_of(c2[0], c2[1]);
+        S[j] = pair_of(s2[0], s2[1]);
+      }
+    } else if (r.interleaved) {
+      kind = kSwap;
+      float2 cs[4];
+      load_cs(row + c0 / 2, cs);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        C[j] = pair_of(cs[j].x);
+        S[j] = pair_of(-cs[j].y, cs[j].y);
+      }
+    } else {
+      kind = kPartner;
+      const bool first = c0 < half;
+      partner = first ? c0 + half : c0 - half;
+      float2 cs[8];
+      load_cs(row + (first ? c0 : c0 - half), cs);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        C[j] = pair_of(cs[2 * j].x, cs[2 * j + 1].x);
+        S[j] = first ? pair_of(-cs[2 * j].y, -cs[2 * j + 1].y) : pair_of(cs[2 * j].y, cs[2 * j + 1].y);
+      }
+    }
+  }
+  // the channels that a head's own are paired with, where they are not its own
+  __device__ __forceinline__ uint4 others(const RopeDesc& r, const uint16_t* head) const {
+    if (kind == kPartner) return __ldg(reinterpret_cast<const uint4*>(head + partner));
+    uint32_t w[4] = {0, 0, 0, 0};
+    if (kind == kGather) {
+      const int half = r.rotary_dim / 2;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int ch = c0 + j, at = r.interleaved ? ch ^ 1 : ch < half ? ch + half : ch - half;
+        if (ch < r.rotary_dim) w[j >> 1] |= (uint32_t)__ldg(head + at) << (16 * (j & 1));
+      }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ void apply(uint64_t (&h)[4], uint4 other) const {
+    if (kind == kStays) return;
+    const uint32_t w[4] = {other.x, other.y, other.z, other.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = add2(mul2(h[j], C[j]), mul2(kind == kSwap ? swapped(h[j]) : widen(w[j]), S[j]));
+  }
+};
+
+template <int MODE, int KIND>
+__global__ void __launch_bounds__(kAppendThreads, 5) kv_append_rope_kernel(
     const KvCacheDesc c, const RopeDesc r, const uint16_t* __restrict__ k, int64_t k_token, int64_t k_head,
     const uint16_t* __restrict__ v, int64_t v_token, int64_t v_head, const int64_t* __restrict__ slot_map,
-    const int32_t* __restrict__ positions, int64_t T, const HeadsView q, int units, int lanes, unsigned append_blocks,
-    unsigned* __restrict__ err) {
-  constexpr int kGroup = MODE == 2 ? 16 : 32;
+    const int32_t* __restrict__ positions, int64_t T, int append_lanes, const HeadsView q, int units, int lanes,
+    unsigned append_blocks, unsigned* __restrict__ err) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // k, v and q may come from the previous kernel
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x >= append_blocks) {
     rope_item(r, q, positions, T, 1.0f, units, lanes, (int64_t)(blockIdx.x - append_blocks) * kAppendThreads + threadIdx.x, err);
     return;
   }
-  const unsigned groups = (unsigned)(c.head_dim / kGroup), per_token = groups * (unsigned)c.kv_heads * 2u;
+  constexpr int kUnit = KIND == kPieces ? 8 : 16;  // channels
+  const unsigned U = (unsigned)c.head_dim / kUnit, per_token = U * (unsigned)append_lanes;
   const int64_t idx = (int64_t)blockIdx.x * kAppendThreads + threadIdx.x;
   const int64_t t = idx <= UINT32_MAX ? (int64_t)((unsigned)idx / per_token) : idx / per_token;
   if (t >= T) return;
-  unsigned rem = (unsigned)(idx - t * per_token);
-  const unsigned g = rem % groups;
-  rem /= groups;
-  const bool is_v = rem >= (unsigned)c.kv_heads;
-  const unsigned h = is_v ? rem - (unsigned)c.kv_heads : rem;
+  const unsigned rem = (unsigned)(idx - t * per_token);
+  const int hl = (int)(rem / U), u = (int)(rem - (unsigned)hl * U);
   const int64_t slot = __ldg(slot_map + t);
   const int pos = __ldg(positions + t);
   if (slot < 0 || pos < 0) return;  // a padding token
-  const int64_t page = (unsigned)slot / (unsigned)c.page_size;
+  const unsigned page = (unsigned)slot / (unsigned)c.page_size;
   if (slot > INT32_MAX || page >= c.num_pages || pos >= r.positions) {
-    if (rem == 0 && g == 0) record_error(err, kErrIndex);
+    if (rem == 0) record_error(err, kErrIndex);
     return;
   }
-  const uint16_t* head = is_v ? v + t * v_token + h * v_head : k + t * k_token + h * k_head;
-  const float2* row = r.table + (int64_t)pos * (r.rotary_dim / 2);
-  const bool pieces = whole_pieces(r), wide = (reinterpret_cast<uintptr_t>(row) & 15) == 0;
-  float f[kGroup / 8][8];
-  float b = 0.0f;
+  const int heads = c.kv_heads, half = r.rotary_dim / 2;
+  const float2* row = r.table + (int64_t)pos * half;
+  const BlockScale rule_k = block_scale<MODE>(c.gs_k), rule_v = block_scale<MODE>(c.gs_v);
+  // (num_pages * kv_heads * page_size < 2^31)
+  const int at0 = (int)page * heads * c.page_size + (int)((unsigned)slot - page * (unsigned)c.page_size);
+  const int words = c.head_dim / 8, groups = c.head_dim / (MODE == 2 ? 16 : 32);
+  const uint16_t* kt = k + t * k_token;
+  const uint16_t* vt = v + t * v_token;
+  auto cached = [&](uint32_t* codes, uint8_t* scales, int h) {
+    const int64_t at = at0 + h * c.page_size;
+    return CacheRow{codes + at * words, scales + at * groups};
+  };
+  if (KIND == kPieces) {
+    constexpr int kLanes = MODE == 2 ? 2 : 4;  // of a scale group
+    const unsigned peers = ((1u << kLanes) - 1) << ((threadIdx.x & 31) & ~(kLanes - 1));
+    const PieceTurn turn(r, row, 8 * u);
+    for (int h0 = hl; h0 < heads; h0 += kAppendBatch * append_lanes) {
+      uint4 own[kAppendBatch][2], other[kAppendBatch];
 #pragma unroll
-  for (int i = 0; i < kGroup / 8; ++i) {
-    const int c0 = (int)g * kGroup + 8 * i;
-    if (is_v)
-      unpack8(__ldg(reinterpret_cast<const uint4*>(head + c0)), f[i]);
-    else
-      rotated8(r, head, row, pieces, wide, c0, f[i]);
+      for (int i = 0; i < kAppendBatch; ++i) {
+        const int h = h0 + i * append_lanes;
+        if (h >= heads) continue;
+        own[i][0] = __ldg(reinterpret_cast<const uint4*>(kt + h * k_head) + u);
+        own[i][1] = __ldg(reinterpret_cast<const uint4*>(vt + h * v_head) + u);
+        other[i] = turn.others(r, kt + h * k_head);
+      }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) b = fmaxf(b, fabsf(f[i][j]));
+      for (int i = 0; i < kAppendBatch; ++i) {
+        const int h = h0 + i * append_lanes;
+        if (h >= heads) continue;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+          uint64_t f[4];
+          widen8(own[i][which], f);
+          if (!which) turn.apply(f, other[i]);
+          float m = largest8(f), mul;
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(peers, m, o));
+          uint32_t sbyte;
+          block_scale_rule_f32<MODE>(m, which ? rule_v : rule_k, mul, sbyte);
+          const CacheRow to = which ? cached(c.v_codes, c.v_scales, h) : cached(c.k_codes, c.k_scales, h);
+          to.codes[u] = codes8(f, mul);
+          if (u % kLanes == 0) to.scales[u / kLanes] = (uint8_t)sbyte;
+        }
+      }
+    }
+    return;
   }
-  const float* gsp = is_v ? c.gs_v : c.gs_k;
-  float mul;
-  uint32_t sbyte;
-  block_scale_rule_f32<MODE>(b, block_scale<MODE>(gsp), mul, sbyte);
-  uint32_t words[kGroup / 8];
+  // (the lanes that share a group are neighbours with the same token and heads: they come to its exchange together)
+  constexpr int kLanes = MODE == 2 ? 2 : 4;
+  const unsigned peers = ((1u << kLanes) - 1) << ((threadIdx.x & 31) & ~(kLanes - 1));
+  const unsigned two = 3u << ((threadIdx.x & 31) & ~1);
+  const bool turned = u < r.rotary_dim / 16;
+  const int p0 = KIND == kPairs && turned ? u : 2 * u, p1 = KIND == kPairs && turned ? u + half / 8 : 2 * u + 1;  // K's pieces
+  float2 cs[8];
+  uint64_t C[4], S[4], M[4];
+  if (turned) {
+    load_cs(row + 8 * u, cs);
+    if (KIND == kPairs) {
 #pragma unroll
-  for (int i = 0; i < kGroup / 8; ++i) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[i][j] = __fmul_rn(f[i][j], mul);
-    words[i] = e2m1x8_rn(f[i]);
+      for (int j = 0; j < 4; ++j) {
+        C[j] = pair_of(cs[2 * j].x, cs[2 * j + 1].x);
+        S[j] = pair_of(cs[2 * j].y, cs[2 * j + 1].y);
+        M[j] = pair_of(-cs[2 * j].y, -cs[2 * j + 1].y);
+      }
+    }
   }
-  const int64_t at = (page * c.kv_heads + h) * c.page_size + (slot - page * c.page_size);
-  uint32_t* codes = (is_v ? c.v_codes : c.k_codes) + at * (c.head_dim / 8) + g * (kGroup / 8);
-  if (MODE == 2)
-    *reinterpret_cast<uint2*>(codes) = make_uint2(words[0], words[1]);
-  else
-    *reinterpret_cast<uint4*>(codes) = make_uint4(words[0], words[1], words[kGroup / 8 - 2], words[kGroup / 8 - 1]);
-  (is_v ? c.v_scales : c.k_scales)[at * groups + g] = (uint8_t)sbyte;
+  for (int h0 = hl; h0 < heads; h0 += kAppendBatch * append_lanes) {
+    uint4 ka[kAppendBatch][2], va[kAppendBatch][2];
+#pragma unroll
+    for (int i = 0; i < kAppendBatch; ++i) {
+      const int h = h0 + i * append_lanes;
+      if (h >= heads) continue;
+      const uint4* kh = reinterpret_cast<const uint4*>(kt + h * k_head);
+      const uint4* vh = reinterpret_cast<const uint4*>(vt + h * v_head);
+      ka[i][0] = __ldg(kh + p0);
+      ka[i][1] = __ldg(kh + p1);
+      va[i][0] = __ldg(vh + 2 * u);
+      va[i][1] = __ldg(vh + 2 * u + 1);
+    }
+#pragma unroll
+    for (int i = 0; i < kAppendBatch; ++i) {
+      const int h = h0 + i * append_lanes;
+      if (h >= heads) continue;
+      const CacheRow to = cached(c.k_codes, c.k_scales, h);
+      uint64_t f[8];
+      widen8(ka[i][0], f);
+      widen8(ka[i][1], f + 4);
+      if (KIND == kPairs && turned) {
+        uint64_t fa[4], fb[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          fa[j] = add2(mul2(f[j], C[j]), mul2(f[4 + j], M[j]));
+          fb[j] = add2(mul2(f[4 + j], C[j]), mul2(f[j], S[j]));
+        }
+        store_pair<MODE>(to, u, half, fa, fb, rule_k, peers);
+      } else {
+        if (turned) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            f[j] = add2(mul2(f[j], pair_of(cs[j].x)), mul2(swapped(f[j]), pair_of(-cs[j].y, cs[j].y)));
+        }
+        store_chunk<MODE>(to, u, f, rule_k, two);
+      }
+      widen8(va[i][0], f);
+      widen8(va[i][1], f + 4);
+      store_chunk<MODE>(cached(c.v_codes, c.v_scales, h), u, f, rule_v, two);
+    }
+  }
 }
 
-// How many threads share a token's heads: one for every kBatch heads, as long as there are then threads enough for the
-// GPU; else one a head.
-int head_lanes(const DevInfo& d, int64_t T, int units, int heads) {
-  const int some = (heads + kBatch - 1) / kBatch;
-  return T * units * some >= (int64_t)d.sm_count * 1024 ? some : heads;
+// The kind of append: see kv_append_rope_kernel.  (A warp holds whole groups of four units where a head has them.)
+AppendKind append_kind(const KvCacheDesc& c, const RopeDesc& r) {
+  const int group = c.mode == FP4_MODE_NVFP4 ? 16 : 32;
+  if (r.interleaved) return r.rotary_dim % 16 == 0 ? kChunks : kPieces;
+  return r.rotary_dim / 2 % group == 0 && c.head_dim % (2 * group) == 0 ? kPairs : kPieces;
+}
+
+// How many threads share a token's heads: one for every `batch` heads where there are then threads enough for the GPU, up to
+// one a head where there are not.
+int head_lanes(const DevInfo& d, int64_t T, int units, int heads, int batch) {
+  const int64_t some = (heads + batch - 1) / batch, wanted = (int64_t)d.sm_count * 512 / (T * units);
+  return (int)std::max<int64_t>(some, std::min<int64_t>(heads, wanted));
 }
 
 void pdl(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int64_t grid, int block, cudaStream_t s) {
@@ -305,10 +508,11 @@ void pdl(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int64_t grid, int b
   cfg.numAttrs = 1;
 }
 
-int host_units(const RopeDesc& r, int dim, bool keep) {
-  const int rest = keep ? dim - r.rotary_dim : 0;
-  if (whole_pieces(r)) return r.rotary_dim / (r.interleaved ? 8 : 16) + rest / 8;
-  return r.rotary_dim / 2 + rest;
+// units of a head that the rotation of a view is made of (rope_item), and the threads that share a token's heads
+void rope_shape(const DevInfo& d, const RopeDesc& r, const HeadsView& x, int64_t T, int& units, int& lanes) {
+  const int rest = x.in != x.out ? x.dim - r.rotary_dim : 0, n = vector_of(r);
+  units = n == 1 ? r.rotary_dim / 2 + rest : r.rotary_dim / (r.interleaved ? n : 2 * n) + rest / n;
+  lanes = head_lanes(d, T, units, x.heads, r.interleaved ? 8 : 4);
 }
 
 }  // namespace
@@ -336,8 +540,8 @@ cudaError_t launch_rope_table(const DevInfo& d, const double* frequencies, int r
 
 cudaError_t launch_rope(const DevInfo& d, const RopeDesc& r, const HeadsView& x, const int32_t* positions, int64_t T,
                         int backward, cudaStream_t s) {
-  const int units = host_units(r, x.dim, x.in != x.out);
-  const int lanes = head_lanes(d, T, units, x.heads);
+  int units, lanes;
+  rope_shape(d, r, x, T, units, lanes);
   const int64_t grid = (T * units * lanes + kRopeThreads - 1) / kRopeThreads;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
@@ -350,24 +554,31 @@ cudaError_t launch_kv_append_rope(const DevInfo& d, const KvCacheDesc& c, const 
                                   int64_t k_token, int64_t k_head, const uint16_t* v, int64_t v_token, int64_t v_head,
                                   const int64_t* slot_map, const int32_t* positions, int64_t T, const HeadsView& q,
                                   cudaStream_t s) {
-  const int group = c.mode == FP4_MODE_NVFP4 ? 16 : 32;
-  const int64_t append = (T * (int64_t)(c.head_dim / group) * c.kv_heads * 2 + kAppendThreads - 1) / kAppendThreads;
+  const AppendKind kind = append_kind(c, r);
+  const int per_head = c.head_dim / (kind == kPieces ? 8 : 16);
+  const int append_lanes = head_lanes(d, T, per_head, c.kv_heads, kAppendBatch);
+  const int64_t append = (T * per_head * append_lanes + kAppendThreads - 1) / kAppendThreads;
   int units = 0, lanes = 0;
   int64_t rotate = 0;
   if (q.heads > 0) {
-    units = host_units(r, q.dim, q.in != q.out);
-    lanes = head_lanes(d, T, units, q.heads);
+    rope_shape(d, r, q, T, units, lanes);
     rotate = (T * units * lanes + kAppendThreads - 1) / kAppendThreads;
   }
   if (append + rotate > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   pdl(cfg, attr, append + rotate, kAppendThreads, s);
+  auto go = [&](auto kernel) {
+    return cudaLaunchKernelEx(&cfg, kernel, c, r, k, k_token, k_head, v, v_token, v_head, slot_map, positions, T,
+                              append_lanes, q, units, lanes, (unsigned)append, d.err);
+  };
   if (c.mode == FP4_MODE_NVFP4)
-    return cudaLaunchKernelEx(&cfg, kv_append_rope_kernel<2>, c, r, k, k_token, k_head, v, v_token, v_head, slot_map,
-                              positions, T, q, units, lanes, (unsigned)append, d.err);
-  return cudaLaunchKernelEx(&cfg, kv_append_rope_kernel<1>, c, r, k, k_token, k_head, v, v_token, v_head, slot_map,
-                            positions, T, q, units, lanes, (unsigned)append, d.err);
+    return kind == kPairs    ? go(kv_append_rope_kernel<2, kPairs>)
+           : kind == kChunks ? go(kv_append_rope_kernel<2, kChunks>)
+                             : go(kv_append_rope_kernel<2, kPieces>);
+  return kind == kPairs    ? go(kv_append_rope_kernel<1, kPairs>)
+         : kind == kChunks ? go(kv_append_rope_kernel<1, kChunks>)
+                           : go(kv_append_rope_kernel<1, kPieces>);
 }
 
 }  // namespace fp4
