@@ -505,6 +505,22 @@ def _need_here(*tensors):
             raise ValueError(f"a tensor of shape {tuple(t.shape)} is on {t.device}, the current device is cuda:{here}")
 
 
+# What a call's tensors are to be, in a few cheap questions (a call costs the host about as much as a launch): where one
+# says no, the checks above find out which it was and say so.
+
+
+def _here() -> int:
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
+
+
+def _fits(t, dtype, shape, here) -> bool:
+    return t.dtype is dtype and t.get_device() == here and t.shape == shape and t.is_contiguous()
+
+
+def _fits_rows(t, dtype, shape, here) -> bool:
+    return t.dtype is dtype and t.get_device() == here and t.shape == shape and t.stride(-1) == 1
+
+
 def _empty(shape, dtype, like, stream):
     """An output, from the memory pool of the stream that writes it."""
     if stream is None:
@@ -527,6 +543,31 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor = None, eps: float = 1e-6, re
     """Root-mean-square norm of the rows of x [rows, cols] (+ residual; their sum is returned too, and written in place
     with sum_out=residual).  Without a mode the result is bf16; with MODE_NVFP4 or MODE_MXFP4 it is codes and scales as
     fp4_quantize makes them, and bf16 as well where out is given."""
+    bf16, shape, here = torch.bfloat16, x.shape, _here()
+    four = mode is not None
+    if not (len(shape) == 2 and _fits_rows(x, bf16, shape, here) and (weight is None or _fits(weight, bf16, shape[1:], here))
+            and (residual is None or _fits_rows(residual, bf16, shape, here))
+            and (sum_out is None or _fits_rows(sum_out, bf16, shape, here)) and (out is None or _fits(out, bf16, shape, here))
+            and xq is None and scales is None and (four or global_scale is None) and (not four or mode == 1 or mode == 2)
+            and (global_scale is None or _fits(global_scale, torch.float32, (), here))):
+        _need_rms_norm(x, weight, residual, mode, global_scale, layout, sum_out, out, xq, scales)
+    rows, cols = shape
+    if residual is not None and sum_out is None:
+        sum_out = _empty(shape, bf16, x, stream)
+    if four:
+        if xq is None:
+            xq = _empty((rows, cols // 8), torch.int32, x, stream)
+        if scales is None:
+            scales = _empty(scales_shape(rows, cols, GROUP[mode], layout), torch.uint8, x, stream)
+    elif out is None:
+        out = _empty(shape, bf16, x, stream)
+    _check(lib().rms_norm(x.data_ptr(), _row_stride(x), _p(residual), _row_stride(residual), _p(weight), eps, rows, cols,
+                          _p(sum_out), _row_stride(sum_out), _p(out), mode or 0, _p(global_scale), _p(xq), _p(scales), layout,
+                          _s(stream)), "rms_norm")
+    return RmsNorm(out, sum_out, xq, scales)
+
+
+def _need_rms_norm(x, weight, residual, mode, global_scale, layout, sum_out, out, xq, scales):
     bf16 = torch.bfloat16
     if x.dim() != 2:
         raise ValueError(f"x: [rows, cols] is needed, got {tuple(x.shape)}")
@@ -539,35 +580,18 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor = None, eps: float = 1e-6, re
         _need("out", out, bf16, (rows, cols))
     if weight is not None:
         _need_vector("weight", weight, bf16, cols)
-    group = shape = None
     if mode is not None:
         if mode not in (MODE_NVFP4, MODE_MXFP4):
             raise ValueError(f"mode: MODE_NVFP4 or MODE_MXFP4 is needed, got {mode}")
-        group = GROUP[mode]
-        shape = scales_shape(rows, cols, group, layout)
         if xq is not None:
             _need("xq", xq, torch.int32, (rows, cols // 8))
         if scales is not None:
-            _need("scales", scales, torch.uint8, shape)
+            _need("scales", scales, torch.uint8, scales_shape(rows, cols, GROUP[mode], layout))
         if global_scale is not None:
             _need_vector("global_scale", global_scale, torch.float32, 1)
     elif global_scale is not None or xq is not None or scales is not None:
         raise ValueError("mode: global_scale, xq and scales belong to a 4-bit output")
     _need_here(x, residual, weight, sum_out, out, global_scale, xq, scales)
-    if residual is not None and sum_out is None:
-        sum_out = _empty((rows, cols), bf16, x, stream)
-    if mode is None:
-        if out is None:
-            out = _empty((rows, cols), bf16, x, stream)
-    else:
-        if xq is None:
-            xq = _empty((rows, cols // 8), torch.int32, x, stream)
-        if scales is None:
-            scales = _empty(shape, torch.uint8, x, stream)
-    _check(lib().rms_norm(_p(x), x.stride(0) if rows > 1 else cols, _p(residual), _row_stride(residual), _p(weight), eps, rows,
-                          cols, _p(sum_out), _row_stride(sum_out), _p(out), mode or 0, _p(global_scale), _p(xq), _p(scales),
-                          layout, _s(stream)), "rms_norm")
-    return RmsNorm(out, sum_out, xq, scales)
 
 
 def _row_stride(t):
@@ -638,16 +662,20 @@ def _need_view(name: str, t: torch.Tensor, shape):
 def rope(rope: Rope, x: torch.Tensor, positions: torch.Tensor, backward: bool = False, out=None, stream=None):
     """x [tokens, heads, head_dim] (views with strides are read in place) rotated by its tokens' positions; backward: the
     transposed rotation.  out=x rotates in place; rows of negative positions are not written."""
-    _need_view("x", x, tuple(x.shape))
-    tokens, heads, dim = x.shape
-    _need_vector("positions", positions, torch.int32, tokens)
-    if out is not None:
-        _need_view("out", out, (tokens, heads, dim))
-    _need_here(x, positions, out, rope.tensor)
+    bf16, shape, here = torch.bfloat16, x.shape, _here()
+    if not (len(shape) == 3 and _fits_rows(x, bf16, shape, here) and _fits(positions, torch.int32, shape[:1], here)
+            and (out is None or _fits_rows(out, bf16, shape, here)) and rope.tensor.get_device() == here):
+        _need_view("x", x, tuple(shape))
+        _need_vector("positions", positions, torch.int32, shape[0])
+        if out is not None:
+            _need_view("out", out, tuple(shape))
+        _need_here(x, positions, out, rope.tensor)
     if out is None:
-        out = _empty((tokens, heads, dim), torch.bfloat16, x, stream)
-    _check(lib().rope(c.byref(rope), _p(x), *_view_strides(x), _p(positions), tokens, heads, dim, 1 if backward else 0,
-                      _p(out), *_view_strides(out), _s(stream)), "rope")
+        out = _empty(shape, bf16, x, stream)
+    xt, xh = _view_strides(x)
+    ot, oh = _view_strides(out)
+    _check(lib().rope(c.byref(rope), x.data_ptr(), xt, xh, positions.data_ptr(), *shape, 1 if backward else 0, out.data_ptr(),
+                      ot, oh, _s(stream)), "rope")
     return out
 
 
@@ -655,25 +683,35 @@ def kv_append_rope(cache: KvCache, rope: Rope, k: torch.Tensor, v: torch.Tensor,
                    positions: torch.Tensor, q: torch.Tensor = None, q_out=None, stream=None):
     """kv_append with K rotated by its tokens' positions; q [tokens, q_heads, head_dim], where given, is rotated by the
     same launch into q_out (q_out=q: in place), which is returned.  Views with strides are read in place."""
-    tokens = slot_map.numel()
+    bf16, here, tokens = torch.bfloat16, _here(), slot_map.numel()
     shape = (tokens, cache.kv_heads, cache.head_dim)
-    _need_vector("slot_map", slot_map, torch.int64, tokens)
-    _need_vector("positions", positions, torch.int32, tokens)
-    _need_view("k", k, shape)
-    _need_view("v", v, shape)
+    qshape = None if q is None else q.shape
+    if not (_fits_rows(k, bf16, shape, here) and _fits_rows(v, bf16, shape, here) and _fits(slot_map, torch.int64, (tokens,), here)
+            and _fits(positions, torch.int32, (tokens,), here)
+            and (q_out is None if q is None else len(qshape) == 3 and qshape[0] == tokens and qshape[2] == shape[2]
+                 and _fits_rows(q, bf16, qshape, here) and (q_out is None or _fits_rows(q_out, bf16, qshape, here)))
+            and cache.tensors[0].get_device() == here and rope.tensor.get_device() == here):
+        _need_vector("slot_map", slot_map, torch.int64, tokens)
+        _need_vector("positions", positions, torch.int32, tokens)
+        _need_view("k", k, shape)
+        _need_view("v", v, shape)
+        if q is not None:
+            _need_view("q", q, (tokens, q.shape[1] if q.dim() == 3 else 0, cache.head_dim))
+            if q_out is not None:
+                _need_view("q_out", q_out, tuple(q.shape))
+        elif q_out is not None:
+            raise ValueError("q_out: there is no q to rotate")
+        _need_here(k, v, slot_map, positions, q, q_out, cache.tensors[0], rope.tensor)
+    qt = qh = heads = ot = oh = 0
     if q is not None:
-        _need_view("q", q, (tokens, q.shape[1] if q.dim() == 3 else 0, cache.head_dim))
-        if q_out is not None:
-            _need_view("q_out", q_out, tuple(q.shape))
-    elif q_out is not None:
-        raise ValueError("q_out: there is no q to rotate")
-    _need_here(k, v, slot_map, positions, q, q_out, cache.tensors[0], rope.tensor)
-    if q is not None and q_out is None:
-        q_out = _empty(tuple(q.shape), torch.bfloat16, q, stream)
-    qs, os_ = (0, 0) if q is None else _view_strides(q), (0, 0) if q is None else _view_strides(q_out)
-    _check(lib().kv_append_rope(c.byref(cache), c.byref(rope), _p(k), *_view_strides(k), _p(v), *_view_strides(v),
-                                _p(slot_map), _p(positions), tokens, _p(q), *qs, 0 if q is None else q.shape[1], _p(q_out),
-                                *os_, _s(stream)), "kv_append_rope")
+        if q_out is None:
+            q_out = _empty(qshape, bf16, q, stream)
+        heads, (qt, qh), (ot, oh) = qshape[1], _view_strides(q), _view_strides(q_out)
+    kt, kh = _view_strides(k)
+    vt, vh = _view_strides(v)
+    _check(lib().kv_append_rope(c.byref(cache), c.byref(rope), k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, slot_map.data_ptr(),
+                                positions.data_ptr(), tokens, _p(q), qt, qh, heads, _p(q_out), ot, oh, _s(stream)),
+           "kv_append_rope")
     return q_out
 
 
@@ -688,28 +726,27 @@ class MoeSort(NamedTuple):
 def moe_sort(ids: torch.Tensor, num_experts: int, plan: MoeSort = None, stream=None) -> MoeSort:
     """The routed rows of ids int32 [tokens, k] in order of their experts: lhs_idx and rhs_idx are what gather_rows and
     gather_qmm take, slot what moe_combine takes.  Negative ids are dropped."""
-    i32 = torch.int32
-    if ids.dim() != 2:
-        raise ValueError(f"ids: [tokens, k] is needed, got {tuple(ids.shape)}")
-    _need("ids", ids, i32, tuple(ids.shape))
-    tokens, k = ids.shape
-    if plan is not None:
-        _need_vector("lhs_idx", plan.lhs_idx, i32, tokens * k)
-        _need_vector("rhs_idx", plan.rhs_idx, i32, tokens * k)
-        _need("slot", plan.slot, i32, (tokens, k))
-        _need_vector("offsets", plan.offsets, i32, num_experts + 1)
-    _need_here(ids, *(plan or ()))
+    i32, shape, here = torch.int32, ids.shape, _here()
+    if not (plan is None and len(shape) == 2 and _fits(ids, i32, shape, here)):
+        if ids.dim() != 2:
+            raise ValueError(f"ids: [tokens, k] is needed, got {tuple(ids.shape)}")
+        _need("ids", ids, i32, tuple(shape))
+        if plan is not None:
+            _need_vector("lhs_idx", plan.lhs_idx, i32, ids.numel())
+            _need_vector("rhs_idx", plan.rhs_idx, i32, ids.numel())
+            _need("slot", plan.slot, i32, tuple(shape))
+            _need_vector("offsets", plan.offsets, i32, num_experts + 1)
+        _need_here(ids, *(plan or ()))
     if plan is None:
-        plan = MoeSort(_empty(tokens * k, i32, ids, stream), _empty(tokens * k, i32, ids, stream),
-                       _empty((tokens, k), i32, ids, stream), _empty(num_experts + 1, i32, ids, stream))
-    _check(lib().moe_sort(_p(ids), tokens, k, num_experts, _p(plan.lhs_idx), _p(plan.rhs_idx), _p(plan.slot),
-                          _p(plan.offsets), _s(stream)), "moe_sort")
+        rows = ids.numel()
+        plan = MoeSort(_empty(rows, i32, ids, stream), _empty(rows, i32, ids, stream), _empty(shape, i32, ids, stream),
+                       _empty(max(num_experts, 0) + 1, i32, ids, stream))
+    _check(lib().moe_sort(ids.data_ptr(), *shape, num_experts, plan.lhs_idx.data_ptr(), plan.rhs_idx.data_ptr(),
+                          plan.slot.data_ptr(), plan.offsets.data_ptr(), _s(stream)), "moe_sort")
     return plan
 
 
 def _need_routing(slot, weights):
-    if slot.dim() != 2:
-        raise ValueError(f"slot: [tokens, k] is needed, got {tuple(slot.shape)}")
     _need("slot", slot, torch.int32, tuple(slot.shape))
     if weights is not None:
         _need("weights", weights, torch.float32, tuple(slot.shape))
@@ -719,20 +756,26 @@ def moe_combine(y: torch.Tensor, slot: torch.Tensor, weights: torch.Tensor = Non
                 stream=None):
     """The experts' rows y [rows, cols] back to their tokens: residual + sum of weights * y[slot] (weights None: 1, which
     with the sorted rows' gradient as y is the gradient of their gather).  out=residual adds in place."""
-    bf16 = torch.bfloat16
-    _need_routing(slot, weights)
-    if y.dim() != 2:
-        raise ValueError(f"y: [rows, cols] is needed, got {tuple(y.shape)}")
-    _need("y", y, bf16, tuple(y.shape))
-    (tokens, k), (rows, cols) = slot.shape, y.shape
-    for name, t in (("residual", residual), ("out", out)):
-        if t is not None:
-            _need(name, t, bf16, (tokens, cols))
-    _need_here(y, slot, weights, residual, out)
+    bf16, here = torch.bfloat16, _here()
+    sshape, yshape = slot.shape, y.shape
+    if len(sshape) != 2:
+        raise ValueError(f"slot: [tokens, k] is needed, got {tuple(sshape)}")
+    if len(yshape) != 2:
+        raise ValueError(f"y: [rows, cols] is needed, got {tuple(yshape)}")
+    oshape = (sshape[0], yshape[1])
+    if not (_fits(slot, torch.int32, sshape, here) and _fits(y, bf16, yshape, here)
+            and (weights is None or _fits(weights, torch.float32, sshape, here))
+            and (residual is None or _fits(residual, bf16, oshape, here)) and (out is None or _fits(out, bf16, oshape, here))):
+        _need_routing(slot, weights)
+        _need("y", y, bf16, tuple(yshape))
+        for name, t in (("residual", residual), ("out", out)):
+            if t is not None:
+                _need(name, t, bf16, oshape)
+        _need_here(y, slot, weights, residual, out)
     if out is None:
-        out = _empty((tokens, cols), bf16, y, stream)
-    _check(lib().moe_combine(_p(y), rows, _p(slot), _p(weights), _p(residual), tokens, k, cols, _p(out), _s(stream)),
-           "moe_combine")
+        out = _empty(oshape, bf16, y, stream)
+    _check(lib().moe_combine(y.data_ptr(), yshape[0], slot.data_ptr(), _p(weights), _p(residual), *sshape, yshape[1],
+                             out.data_ptr(), _s(stream)), "moe_combine")
     return out
 
 
@@ -741,31 +784,38 @@ def moe_combine_backward(dout: torch.Tensor, slot: torch.Tensor, weights: torch.
     """(dy [rows, cols], dweights [tokens, k]) from dout [tokens, cols].  dweights needs y (None without it); rows is y's,
     or dy's, or every routed row's.  offsets (moe_sort's): rows of dy that no slot names are zeros; without it they are
     not written."""
-    bf16 = torch.bfloat16
-    _need_routing(slot, weights)
-    tokens, k = slot.shape
-    if dout.dim() != 2:
-        raise ValueError(f"dout: [tokens, cols] is needed, got {tuple(dout.shape)}")
-    cols = dout.shape[1]
-    _need("dout", dout, bf16, (tokens, cols))
-    rows = y.shape[0] if y is not None else dy.shape[0] if dy is not None else tokens * k
-    for name, t in (("y", y), ("dy", dy)):
-        if t is not None:
-            _need(name, t, bf16, (rows, cols))
-    if dweights is not None:
-        _need("dweights", dweights, torch.float32, (tokens, k))
-        if y is None:
-            raise ValueError("dweights: y is needed for it")
-    if offsets is not None:
-        _need_vector("offsets", offsets, torch.int32, offsets.numel())
-    _need_here(dout, slot, weights, y, offsets, dy, dweights)
+    bf16, f32, here = torch.bfloat16, torch.float32, _here()
+    sshape, gshape = slot.shape, dout.shape
+    if len(sshape) != 2:
+        raise ValueError(f"slot: [tokens, k] is needed, got {tuple(sshape)}")
+    if len(gshape) != 2:
+        raise ValueError(f"dout: [tokens, cols] is needed, got {tuple(gshape)}")
+    rows = y.shape[0] if y is not None else dy.shape[0] if dy is not None else slot.numel()
+    yshape = (rows, gshape[1])
+    if not (gshape[0] == sshape[0] and _fits(slot, torch.int32, sshape, here) and _fits(dout, bf16, gshape, here)
+            and (weights is None or _fits(weights, f32, sshape, here)) and (y is None or _fits(y, bf16, yshape, here))
+            and (dy is None or _fits(dy, bf16, yshape, here)) and dweights is None
+            and (offsets is None or offsets.dtype is torch.int32 and offsets.get_device() == here and offsets.is_contiguous()
+                 and offsets.numel() > 0)):
+        _need_routing(slot, weights)
+        _need("dout", dout, bf16, (sshape[0], gshape[1]))
+        for name, t in (("y", y), ("dy", dy)):
+            if t is not None:
+                _need(name, t, bf16, yshape)
+        if dweights is not None:
+            _need("dweights", dweights, f32, tuple(sshape))
+            if y is None:
+                raise ValueError("dweights: y is needed for it")
+        if offsets is not None:
+            _need_vector("offsets", offsets, torch.int32, max(1, offsets.numel()))
+        _need_here(dout, slot, weights, y, offsets, dy, dweights)
     if dy is None:
-        dy = _empty((rows, cols), bf16, dout, stream)
+        dy = _empty(yshape, bf16, dout, stream)
     if y is not None and dweights is None:
-        dweights = _empty((tokens, k), torch.float32, dout, stream)
+        dweights = _empty(sshape, f32, dout, stream)
     used = None if offsets is None else offsets.data_ptr() + 4 * (offsets.numel() - 1)
-    _check(lib().moe_combine_backward(_p(dout), _p(y), _p(slot), _p(weights), tokens, k, cols, rows, used, _p(dy),
-                                      _p(dweights), _s(stream)), "moe_combine_backward")
+    _check(lib().moe_combine_backward(dout.data_ptr(), _p(y), slot.data_ptr(), _p(weights), *sshape, gshape[1], rows, used,
+                                      dy.data_ptr(), _p(dweights), _s(stream)), "moe_combine_backward")
     return dy, dweights
 
 
