@@ -5,8 +5,8 @@ then every request gets one token a step, from a captured graph.
 
 A step is: projections (qmm over 4-bit weights) -> kv_plan (pages and slots for the new tokens) -> kv_append
 (K and V quantized into them) -> kv_attention -> output projection.  Weights and inputs are random.  --check
-compares every step with attention in 64 bits over the dequantized cache.  (A rotary or other position encoding of q and k
-would go between the projection and kv_append; kv_plan returns the positions.)"""
+compares every step with attention in 64 bits over the dequantized cache.  (Rotary positions: kv_append_rope in place of
+kv_append, with kv_plan's positions; decoder_layer.py beside this file does so.)"""
 import argparse
 import os
 import sys
