@@ -524,9 +524,9 @@ def _fits_rows(t, dtype, shape, here) -> bool:
 def _empty(shape, dtype, like, stream):
     """An output, from the memory pool of the stream that writes it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 class RmsNorm(NamedTuple):

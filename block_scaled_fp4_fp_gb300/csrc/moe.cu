@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(1024) moe_sort_kernel(const int32_t* __restric
 constexpr int kCombineThreads = 128;
 
 template <int K, int P>
-__global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(
+__global__ void __launch_bounds__(kCombineThreads, P == 4 ? 4 : 7) moe_combine_kernel(
     const uint16_t* __restrict__ y, int rows, const int32_t* __restrict__ slot, const float* __restrict__ weights,
     const uint16_t* residual, int64_t T, int k, int pieces, uint16_t* out, unsigned* __restrict__ err) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -309,14 +309,14 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(
 }
 
 // ---------------------------------------------------- moe_combine_backward --
-// A CTA a token: dout's row is read (again from L1 for each further K of the k rows), a row of dy written and a row of y
+// A CTA a token, or a warp a token where rows are short and tokens many: dout's row is read (again from L1 for each further K of the k rows), a row of dy written and a row of y
 // multiplied with it for each j; two pieces of K rows are in flight a thread.  The dot products of the K rows are
 // reduced together: each step of the butterfly halves the number of sums a lane holds, nine shuffles instead of forty for eight.
 // The CTAs from T on clear the rows that no slot names.  Bound by HBM.
 constexpr int kTailCtas = 64, kBackwardThreads = 512;
 
-template <int K>
-__global__ void __launch_bounds__(kBackwardThreads, 1) moe_combine_backward_kernel(
+template <int K, bool WARP>
+__global__ void __launch_bounds__(WARP ? 128 : kBackwardThreads, 1) moe_combine_backward_kernel(
     const uint16_t* __restrict__ dout, const uint16_t* __restrict__ y, const int32_t* __restrict__ slot,
     const float* __restrict__ weights, int64_t T, int k, int pieces, int64_t rows, const int32_t* __restrict__ rows_used,
     uint16_t* __restrict__ dy, float* __restrict__ dweights, unsigned* __restrict__ err) {
@@ -324,15 +324,18 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) moe_combine_backward_kern
   __shared__ float part[kBackwardThreads / 32][K];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int64_t t = blockIdx.x;
-  if (t >= T) {
-    const int64_t tail = (int64_t)gridDim.x - T;
-    for (int64_t r = max(0, __ldg(rows_used)) + (t - T); r < rows; r += tail)
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t token_ctas = WARP ? (T + 3) / 4 : T;
+  if (blockIdx.x >= token_ctas) {
+    const int64_t tail = (int64_t)gridDim.x - token_ctas;
+    for (int64_t r = max(0, __ldg(rows_used)) + (blockIdx.x - token_ctas); r < rows; r += tail)
       for (int p = threadIdx.x; p < pieces; p += (int)blockDim.x)
         *(reinterpret_cast<uint4*>(dy) + r * pieces + p) = make_uint4(0, 0, 0, 0);
     return;
   }
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, step = (int)blockDim.x;
+  const int64_t t = WARP ? (int64_t)blockIdx.x * 4 + warp : blockIdx.x;
+  if (WARP && t >= T) return;
+  const int thread = WARP ? lane : (int)threadIdx.x, step = WARP ? 32 : (int)blockDim.x;  // of the token's
   const uint4* g4 = reinterpret_cast<const uint4*>(dout) + t * pieces;
   for (int j0 = 0; j0 < k; j0 += K) {
     int at[K];
@@ -342,13 +345,13 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) moe_combine_backward_kern
 #pragma unroll
     for (int j = 0; j < K; ++j) {
       if (at[j] >= rows) {
-        if (threadIdx.x == 0) record_error(err, kErrIndex);
+        if (thread == 0) record_error(err, kErrIndex);
         at[j] = -1;
       }
       w[j] = at[j] >= 0 && weights ? __ldg(weights + t * k + j0 + j) : 1.0f;
       dot[j] = 0.f;
     }
-    for (int p0 = threadIdx.x; p0 < pieces; p0 += P * step) {
+    for (int p0 = thread; p0 < pieces; p0 += P * step) {
       uint4 gv[P], v[P][K];
 #pragma unroll
       for (int q = 0; q < P; ++q) {
@@ -396,6 +399,14 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) moe_combine_backward_kern
     float d = dot[0];
 #pragma unroll
     for (int o = 16 / K; o > 0; o >>= 1) d = __fadd_rn(d, __shfl_xor_sync(0xffffffffu, d, o));
+    if (WARP) {
+      const int j = lane / (32 / K);
+      if (lane % (32 / K) == 0 && j0 + j < k) {
+        const int s = __ldg(slot + t * k + j0 + j);
+        dweights[t * k + j0 + j] = s >= 0 && s < rows ? d : 0.0f;
+      }
+      continue;
+    }
     if (lane % (32 / K) == 0) part[warp][lane / (32 / K)] = d;
     __syncthreads();
     if (threadIdx.x < K && j0 + (int)threadIdx.x < k) {
@@ -484,21 +495,21 @@ cudaError_t launch_moe_combine_backward(const DevInfo& d, const uint16_t* dout, 
                                         const float* weights, int64_t T, int k, int cols, int64_t rows,
                                         const int32_t* rows_used, uint16_t* dy, float* dweights, cudaStream_t s) {
   const int pieces = cols / 8;
-  const int64_t grid = T + (rows_used ? std::min<int64_t>(rows, kTailCtas) : 0);
+  // (20,000 x 2 of 512: 20 us a warp a token, 29 a CTA; 5000 x 4 of 1024: 18 and 25; 20,000 x 8 of 256: 39 and 36)
+  const bool warps = pieces > 32 && pieces <= 128 && T >= 32 * (int64_t)d.sm_count;
+  const int64_t grid = (warps ? (T + 3) / 4 : T) + (rows_used ? std::min<int64_t>(rows, kTailCtas) : 0);
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  // many tokens share an SM, few take it whole
+  const int most = warps || T >= 4 * d.sm_count ? 128 : kBackwardThreads;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  // short rows in one go; else many tokens share an SM, and few take it whole
-  const int most = T >= 4 * d.sm_count ? 128 : kBackwardThreads;
-  pdl(cfg, attr, grid, std::min(most, (pieces + 31) / 32 * 32), 0, s);
-  if (k > 4)
-    return cudaLaunchKernelEx(&cfg, moe_combine_backward_kernel<8>, dout, y, slot, weights, T, k, pieces, rows, rows_used,
-                              dy, dweights, d.err);
-  if (k > 2)
-    return cudaLaunchKernelEx(&cfg, moe_combine_backward_kernel<4>, dout, y, slot, weights, T, k, pieces, rows, rows_used,
-                              dy, dweights, d.err);
-  return cudaLaunchKernelEx(&cfg, moe_combine_backward_kernel<2>, dout, y, slot, weights, T, k, pieces, rows, rows_used,
-                            dy, dweights, d.err);
+  pdl(cfg, attr, grid, warps ? 128 : std::min(most, (pieces + 31) / 32 * 32), 0, s);
+  auto go = [&](auto kernel) {
+    return cudaLaunchKernelEx(&cfg, kernel, dout, y, slot, weights, T, k, pieces, rows, rows_used, dy, dweights, d.err);
+  };
+  if (k > 4) return warps ? go(moe_combine_backward_kernel<8, true>) : go(moe_combine_backward_kernel<8, false>);
+  if (k > 2) return warps ? go(moe_combine_backward_kernel<4, true>) : go(moe_combine_backward_kernel<4, false>);
+  return warps ? go(moe_combine_backward_kernel<2, true>) : go(moe_combine_backward_kernel<2, false>);
 }
 
 }  // namespace fp4

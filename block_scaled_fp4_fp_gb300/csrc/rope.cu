@@ -80,14 +80,38 @@ struct VecOf<4> {
   using T = uint2;
 };
 
+// The row of cosines of position `pos`; nullptr where the token is not to be written (padding, or past the table: reported)
+__device__ __forceinline__ const float2* row_of(const RopeDesc& r, int pos, bool reports, unsigned* err) {
+  if (pos < 0) return nullptr;
+  if (pos >= r.positions) {
+    if (reports) record_error(err, kErrIndex);
+    return nullptr;
+  }
+  return r.table + (int64_t)pos * (r.rotary_dim / 2);
+}
+
 template <bool INTERLEAVED, int N>
-__device__ __forceinline__ void rope_vectors(const HeadsView& x, const uint16_t* in, uint16_t* out, const float2* row,
-                                             float sign, int rotary, int u, int first, int step) {
+__device__ __forceinline__ void rope_vectors(const RopeDesc& r, const HeadsView& x, const uint16_t* in, uint16_t* out, int pos,
+                                             float sign, int u, int first, int step, unsigned* err) {
   using T = typename VecOf<N>::T;
   constexpr int NW = N / 2, B = INTERLEAVED ? 8 : 4;  // words of a vector; heads in flight
-  const int turned = rotary / (INTERLEAVED ? N : 2 * N);
+  const int rotary = r.rotary_dim, turned = rotary / (INTERLEAVED ? N : 2 * N);
   const bool stays = u >= turned;
   const int c0 = stays ? rotary + N * (u - turned) : N * u, c1 = c0 + rotary / 2;
+  T a[B], b[B];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      const int h = h0 + i * step;
+      if (h < x.heads) {
+        a[i] = *reinterpret_cast<const T*>(in + h * x.in_head + c0);
+        if (!INTERLEAVED && !stays) b[i] = *reinterpret_cast<const T*>(in + h * x.in_head + c1);
+      }
+    }
+  };
+  load(first);  // (on their way while the position and its row are)
+  const float2* row = row_of(r, pos, u + first == 0, err);
+  if (!row) return;
   uint64_t C[NW], S[NW];
   if (!stays) {
     float2 cs[INTERLEAVED ? NW : N];
@@ -103,16 +127,7 @@ __device__ __forceinline__ void rope_vectors(const HeadsView& x, const uint16_t*
       }
     }
   }
-  for (int h0 = first; h0 < x.heads; h0 += B * step) {
-    T a[B], b[B];
-#pragma unroll
-    for (int i = 0; i < B; ++i) {
-      const int h = h0 + i * step;
-      if (h < x.heads) {
-        a[i] = *reinterpret_cast<const T*>(in + h * x.in_head + c0);
-        if (!INTERLEAVED && !stays) b[i] = *reinterpret_cast<const T*>(in + h * x.in_head + c1);
-      }
-    }
+  for (int h0 = first;;) {
 #pragma unroll
     for (int i = 0; i < B; ++i) {
       const int h = h0 + i * step;
@@ -144,6 +159,9 @@ __device__ __forceinline__ void rope_vectors(const HeadsView& x, const uint16_t*
       *o0 = ya;
       if (!INTERLEAVED) *o1 = yb;
     }
+    h0 += B * step;
+    if (h0 >= x.heads) break;
+    load(h0);
   }
 }
 
@@ -165,8 +183,16 @@ __device__ __forceinline__ void rope_pairs(const RopeDesc& r, const HeadsView& x
   }
 }
 
+// How a view is rotated: which of the above.  (kAny asks: for a kernel whose registers do not go by it.)
+enum RopeKind { kHalves8, kInterleaved8, kHalves4, kInterleaved4, kByPairs, kAny };
+__host__ __device__ inline RopeKind rope_kind(const RopeDesc& r) {
+  const int n = vector_of(r);
+  return n == 1 ? kByPairs : n == 8 ? (r.interleaved ? kInterleaved8 : kHalves8) : (r.interleaved ? kInterleaved4 : kHalves4);
+}
+
 // Thread `i` of the rotation's: unit fastest, so that neighbouring lanes hold neighbouring vectors of a head, then
 // `lanes` threads that take every lanes-th head, then the token.
+template <int KIND>
 __device__ __forceinline__ void rope_item(const RopeDesc& r, const HeadsView& x, const int32_t* positions, int64_t T,
                                           float sign, int units, int lanes, int64_t i, unsigned* err) {
   const unsigned per_token = (unsigned)units * (unsigned)lanes;
@@ -175,31 +201,27 @@ __device__ __forceinline__ void rope_item(const RopeDesc& r, const HeadsView& x,
   const unsigned rem = (unsigned)(i - t * per_token);
   const int hl = (int)(rem / (unsigned)units), u = (int)(rem - (unsigned)hl * (unsigned)units);
   const int pos = __ldg(positions + t);
-  if (pos < 0) return;  // a padding token
-  if (pos >= r.positions) {
-    if (rem == 0) record_error(err, kErrIndex);
-    return;
-  }
-  const float2* row = r.table + (int64_t)pos * (r.rotary_dim / 2);
   const uint16_t* in = x.in + t * x.in_token;
   uint16_t* out = x.out + t * x.out_token;
-  switch (vector_of(r) * 2 + r.interleaved) {
-    case 16: return rope_vectors<false, 8>(x, in, out, row, sign, r.rotary_dim, u, hl, lanes);
-    case 17: return rope_vectors<true, 8>(x, in, out, row, sign, r.rotary_dim, u, hl, lanes);
-    case 8: return rope_vectors<false, 4>(x, in, out, row, sign, r.rotary_dim, u, hl, lanes);
-    case 9: return rope_vectors<true, 4>(x, in, out, row, sign, r.rotary_dim, u, hl, lanes);
-    default: return rope_pairs(r, x, in, out, row, sign, u, hl, lanes);
+  switch (KIND == kAny ? rope_kind(r) : KIND) {
+    case kHalves8: return rope_vectors<false, 8>(r, x, in, out, pos, sign, u, hl, lanes, err);
+    case kInterleaved8: return rope_vectors<true, 8>(r, x, in, out, pos, sign, u, hl, lanes, err);
+    case kHalves4: return rope_vectors<false, 4>(r, x, in, out, pos, sign, u, hl, lanes, err);
+    case kInterleaved4: return rope_vectors<true, 4>(r, x, in, out, pos, sign, u, hl, lanes, err);
+    default:
+      if (const float2* row = row_of(r, pos, rem == 0, err)) rope_pairs(r, x, in, out, row, sign, u, hl, lanes);
   }
 }
 
 constexpr int kRopeThreads = 128;
 
+template <int KIND>
 __global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(const RopeDesc r, const HeadsView x,
                                                             const int32_t* __restrict__ positions, int64_t T, float sign,
                                                             int units, int lanes, unsigned* __restrict__ err) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  rope_item(r, x, positions, T, sign, units, lanes, (int64_t)blockIdx.x * kRopeThreads + threadIdx.x, err);
+  rope_item<KIND>(r, x, positions, T, sign, units, lanes, (int64_t)blockIdx.x * kRopeThreads + threadIdx.x, err);
 }
 
 // ----------------------------------------------------------- kv_append_rope --
@@ -347,7 +369,7 @@ struct PieceTurn {
 };
 
 template <int MODE, int KIND>
-__global__ void __launch_bounds__(kAppendThreads, 5) kv_append_rope_kernel(
+__global__ void __launch_bounds__(kAppendThreads, 6) kv_append_rope_kernel(
     const KvCacheDesc c, const RopeDesc r, const uint16_t* __restrict__ k, int64_t k_token, int64_t k_head,
     const uint16_t* __restrict__ v, int64_t v_token, int64_t v_head, const int64_t* __restrict__ slot_map,
     const int32_t* __restrict__ positions, int64_t T, int append_lanes, const HeadsView q, int units, int lanes,
@@ -355,7 +377,8 @@ __global__ void __launch_bounds__(kAppendThreads, 5) kv_append_rope_kernel(
   asm volatile("griddepcontrol.wait;" ::: "memory");  // k, v and q may come from the previous kernel
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x >= append_blocks) {
-    rope_item(r, q, positions, T, 1.0f, units, lanes, (int64_t)(blockIdx.x - append_blocks) * kAppendThreads + threadIdx.x, err);
+    constexpr int kind = KIND == kPairs ? kHalves8 : KIND == kChunks ? kInterleaved8 : kAny;  // (whole groups are whole vectors)
+    rope_item<kind>(r, q, positions, T, 1.0f, units, lanes, (int64_t)(blockIdx.x - append_blocks) * kAppendThreads + threadIdx.x, err);
     return;
   }
   constexpr int kUnit = KIND == kPieces ? 8 : 16;  // channels
@@ -367,38 +390,55 @@ __global__ void __launch_bounds__(kAppendThreads, 5) kv_append_rope_kernel(
   const int hl = (int)(rem / U), u = (int)(rem - (unsigned)hl * U);
   const int64_t slot = __ldg(slot_map + t);
   const int pos = __ldg(positions + t);
+  const int heads = c.kv_heads, half = r.rotary_dim / 2;
+  const uint16_t* kt = k + t * k_token;
+  const uint16_t* vt = v + t * v_token;
+  // the first heads' loads are on their way while the slot, the position and its row are
+  const bool turned = KIND != kPieces && u < r.rotary_dim / 16;
+  const int p0 = KIND == kPieces || (KIND == kPairs && turned) ? u : 2 * u;  // K's pieces
+  const int p1 = KIND == kPairs && turned ? u + half / 8 : 2 * u + 1;
+  uint4 ka[kAppendBatch][2], va[kAppendBatch][2];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < kAppendBatch; ++i) {
+      const int h = h0 + i * append_lanes;
+      if (h >= heads) continue;
+      const uint4* kh = reinterpret_cast<const uint4*>(kt + h * k_head);
+      const uint4* vh = reinterpret_cast<const uint4*>(vt + h * v_head);
+      ka[i][0] = __ldg(kh + p0);
+      va[i][0] = __ldg(vh + (KIND == kPieces ? u : 2 * u));
+      if (KIND != kPieces) {
+        ka[i][1] = __ldg(kh + p1);
+        va[i][1] = __ldg(vh + 2 * u + 1);
+      }
+    }
+  };
+  load(hl);
   if (slot < 0 || pos < 0) return;  // a padding token
   const unsigned page = (unsigned)slot / (unsigned)c.page_size;
   if (slot > INT32_MAX || page >= c.num_pages || pos >= r.positions) {
     if (rem == 0) record_error(err, kErrIndex);
     return;
   }
-  const int heads = c.kv_heads, half = r.rotary_dim / 2;
   const float2* row = r.table + (int64_t)pos * half;
   const BlockScale rule_k = block_scale<MODE>(c.gs_k), rule_v = block_scale<MODE>(c.gs_v);
   // (num_pages * kv_heads * page_size < 2^31)
   const int at0 = (int)page * heads * c.page_size + (int)((unsigned)slot - page * (unsigned)c.page_size);
   const int words = c.head_dim / 8, groups = c.head_dim / (MODE == 2 ? 16 : 32);
-  const uint16_t* kt = k + t * k_token;
-  const uint16_t* vt = v + t * v_token;
   auto cached = [&](uint32_t* codes, uint8_t* scales, int h) {
     const int64_t at = at0 + h * c.page_size;
     return CacheRow{codes + at * words, scales + at * groups};
   };
-  if (KIND == kPieces) {
-    constexpr int kLanes = MODE == 2 ? 2 : 4;  // of a scale group
-    const unsigned peers = ((1u << kLanes) - 1) << ((threadIdx.x & 31) & ~(kLanes - 1));
+  // (the lanes that share a group are neighbours with the same token and heads: they come to its exchange together)
+  constexpr int kLanes = MODE == 2 ? 2 : 4;
+  const unsigned peers = ((1u << kLanes) - 1) << ((threadIdx.x & 31) & ~(kLanes - 1));
+  if constexpr (KIND == kPieces) {
     const PieceTurn turn(r, row, 8 * u);
-    for (int h0 = hl; h0 < heads; h0 += kAppendBatch * append_lanes) {
-      uint4 own[kAppendBatch][2], other[kAppendBatch];
+    for (int h0 = hl;;) {
+      uint4 other[kAppendBatch];
 #pragma unroll
-      for (int i = 0; i < kAppendBatch; ++i) {
-        const int h = h0 + i * append_lanes;
-        if (h >= heads) continue;
-        own[i][0] = __ldg(reinterpret_cast<const uint4*>(kt + h * k_head) + u);
-        own[i][1] = __ldg(reinterpret_cast<const uint4*>(vt + h * v_head) + u);
-        other[i] = turn.others(r, kt + h * k_head);
-      }
+      for (int i = 0; i < kAppendBatch; ++i)
+        if (const int h = h0 + i * append_lanes; h < heads) other[i] = turn.others(r, kt + h * k_head);
 #pragma unroll
       for (int i = 0; i < kAppendBatch; ++i) {
         const int h = h0 + i * append_lanes;
@@ -406,7 +446,7 @@ __global__ void __launch_bounds__(kAppendThreads, 5) kv_append_rope_kernel(
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
           uint64_t f[4];
-          widen8(own[i][which], f);
+          widen8(which ? va[i][0] : ka[i][0], f);
           if (!which) turn.apply(f, other[i]);
           float m = largest8(f), mul;
 #pragma unroll
@@ -418,68 +458,57 @@ __global__ void __launch_bounds__(kAppendThreads, 5) kv_append_rope_kernel(
           if (u % kLanes == 0) to.scales[u / kLanes] = (uint8_t)sbyte;
         }
       }
+      h0 += kAppendBatch * append_lanes;
+      if (h0 >= heads) break;
+      load(h0);
     }
-    return;
-  }
-  // (the lanes that share a group are neighbours with the same token and heads: they come to its exchange together)
-  constexpr int kLanes = MODE == 2 ? 2 : 4;
-  const unsigned peers = ((1u << kLanes) - 1) << ((threadIdx.x & 31) & ~(kLanes - 1));
-  const unsigned two = 3u << ((threadIdx.x & 31) & ~1);
-  const bool turned = u < r.rotary_dim / 16;
-  const int p0 = KIND == kPairs && turned ? u : 2 * u, p1 = KIND == kPairs && turned ? u + half / 8 : 2 * u + 1;  // K's pieces
-  float2 cs[8];
-  uint64_t C[4], S[4], M[4];
-  if (turned) {
-    load_cs(row + 8 * u, cs);
-    if (KIND == kPairs) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        C[j] = pair_of(cs[2 * j].x, cs[2 * j + 1].x);
-        S[j] = pair_of(cs[2 * j].y, cs[2 * j + 1].y);
-        M[j] = pair_of(-cs[2 * j].y, -cs[2 * j + 1].y);
-      }
-    }
-  }
-  for (int h0 = hl; h0 < heads; h0 += kAppendBatch * append_lanes) {
-    uint4 ka[kAppendBatch][2], va[kAppendBatch][2];
-#pragma unroll
-    for (int i = 0; i < kAppendBatch; ++i) {
-      const int h = h0 + i * append_lanes;
-      if (h >= heads) continue;
-      const uint4* kh = reinterpret_cast<const uint4*>(kt + h * k_head);
-      const uint4* vh = reinterpret_cast<const uint4*>(vt + h * v_head);
-      ka[i][0] = __ldg(kh + p0);
-      ka[i][1] = __ldg(kh + p1);
-      va[i][0] = __ldg(vh + 2 * u);
-      va[i][1] = __ldg(vh + 2 * u + 1);
-    }
-#pragma unroll
-    for (int i = 0; i < kAppendBatch; ++i) {
-      const int h = h0 + i * append_lanes;
-      if (h >= heads) continue;
-      const CacheRow to = cached(c.k_codes, c.k_scales, h);
-      uint64_t f[8];
-      widen8(ka[i][0], f);
-      widen8(ka[i][1], f + 4);
-      if (KIND == kPairs && turned) {
-        uint64_t fa[4], fb[4];
+  } else {
+    const unsigned two = 3u << ((threadIdx.x & 31) & ~1);
+    float2 cs[8];
+    uint64_t C[4], S[4], M[4];
+    if (turned) {
+      load_cs(row + 8 * u, cs);
+      if (KIND == kPairs) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          fa[j] = add2(mul2(f[j], C[j]), mul2(f[4 + j], M[j]));
-          fb[j] = add2(mul2(f[4 + j], C[j]), mul2(f[j], S[j]));
+          C[j] = pair_of(cs[2 * j].x, cs[2 * j + 1].x);
+          S[j] = pair_of(cs[2 * j].y, cs[2 * j + 1].y);
+          M[j] = pair_of(-cs[2 * j].y, -cs[2 * j + 1].y);
         }
-        store_pair<MODE>(to, u, half, fa, fb, rule_k, peers);
-      } else {
-        if (turned) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            f[j] = add2(mul2(f[j], pair_of(cs[j].x)), mul2(swapped(f[j]), pair_of(-cs[j].y, cs[j].y)));
-        }
-        store_chunk<MODE>(to, u, f, rule_k, two);
       }
-      widen8(va[i][0], f);
-      widen8(va[i][1], f + 4);
-      store_chunk<MODE>(cached(c.v_codes, c.v_scales, h), u, f, rule_v, two);
+    }
+    for (int h0 = hl;;) {
+#pragma unroll
+      for (int i = 0; i < kAppendBatch; ++i) {
+        const int h = h0 + i * append_lanes;
+        if (h >= heads) continue;
+        const CacheRow to = cached(c.k_codes, c.k_scales, h);
+        uint64_t f[8];
+        widen8(ka[i][0], f);
+        widen8(ka[i][1], f + 4);
+        if (KIND == kPairs && turned) {
+          uint64_t fa[4], fb[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            fa[j] = add2(mul2(f[j], C[j]), mul2(f[4 + j], M[j]));
+            fb[j] = add2(mul2(f[4 + j], C[j]), mul2(f[j], S[j]));
+          }
+          store_pair<MODE>(to, u, half, fa, fb, rule_k, peers);
+        } else {
+          if (turned) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              f[j] = add2(mul2(f[j], pair_of(cs[j].x)), mul2(swapped(f[j]), pair_of(-cs[j].y, cs[j].y)));
+          }
+          store_chunk<MODE>(to, u, f, rule_k, two);
+        }
+        widen8(va[i][0], f);
+        widen8(va[i][1], f + 4);
+        store_chunk<MODE>(cached(c.v_codes, c.v_scales, h), u, f, rule_v, two);
+      }
+      h0 += kAppendBatch * append_lanes;
+      if (h0 >= heads) break;
+      load(h0);
     }
   }
 }
@@ -547,7 +576,16 @@ cudaError_t launch_rope(const DevInfo& d, const RopeDesc& r, const HeadsView& x,
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   pdl(cfg, attr, grid, kRopeThreads, s);
-  return cudaLaunchKernelEx(&cfg, rope_kernel, r, x, positions, T, backward ? -1.0f : 1.0f, units, lanes, d.err);
+  auto go = [&](auto kernel) {
+    return cudaLaunchKernelEx(&cfg, kernel, r, x, positions, T, backward ? -1.0f : 1.0f, units, lanes, d.err);
+  };
+  switch (rope_kind(r)) {
+    case kHalves8: return go(rope_kernel<kHalves8>);
+    case kInterleaved8: return go(rope_kernel<kInterleaved8>);
+    case kHalves4: return go(rope_kernel<kHalves4>);
+    case kInterleaved4: return go(rope_kernel<kInterleaved4>);
+    default: return go(rope_kernel<kByPairs>);
+  }
 }
 
 cudaError_t launch_kv_append_rope(const DevInfo& d, const KvCacheDesc& c, const RopeDesc& r, const uint16_t* k,

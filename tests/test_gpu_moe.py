@@ -85,7 +85,7 @@ def combine_case(tokens, k, cols, experts=8, seed=0, drop=0.2):
     return slot, y, w, r
 
 
-COMBINES = [(1, 1, 8), (1, 4, 5120), (96, 4, 5120), (7, 8, 2880), (33, 3, 1032), (5, 11, 264), (300, 2, 4104), (2, 40, 4160), (2000, 1, 16)]
+COMBINES = [(1, 1, 8), (1, 4, 5120), (96, 4, 5120), (7, 8, 2880), (33, 3, 1032), (5, 11, 264), (300, 2, 4104), (2, 40, 4160), (2000, 1, 16), (5003, 2, 512), (4870, 3, 1000)]
 
 
 @pytest.mark.parametrize("tokens,k,cols", COMBINES)
