@@ -524,9 +524,9 @@ def _fits_rows(t, dtype, shape, here) -> bool:
 def _empty(shape, dtype, like, stream):
     """An output, from the memory pool of the stream that writes it."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 class RmsNorm(NamedTuple):
@@ -548,7 +548,9 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor = None, eps: float = 1e-6, re
     if not (len(shape) == 2 and _fits_rows(x, bf16, shape, here) and (weight is None or _fits(weight, bf16, shape[1:], here))
             and (residual is None or _fits_rows(residual, bf16, shape, here))
             and (sum_out is None or _fits_rows(sum_out, bf16, shape, here)) and (out is None or _fits(out, bf16, shape, here))
-            and xq is None and scales is None and (four or global_scale is None) and (not four or mode == 1 or mode == 2)
+            and (four or global_scale is None and xq is None and scales is None) and (not four or mode == 1 or mode == 2)
+            and (xq is None or _fits(xq, torch.int32, (shape[0], shape[1] // 8), here))
+            and (scales is None or _fits(scales, torch.uint8, scales_shape(*shape, GROUP[mode], layout), here))
             and (global_scale is None or _fits(global_scale, torch.float32, (), here))):
         _need_rms_norm(x, weight, residual, mode, global_scale, layout, sum_out, out, xq, scales)
     rows, cols = shape
@@ -794,7 +796,8 @@ def moe_combine_backward(dout: torch.Tensor, slot: torch.Tensor, weights: torch.
     yshape = (rows, gshape[1])
     if not (gshape[0] == sshape[0] and _fits(slot, torch.int32, sshape, here) and _fits(dout, bf16, gshape, here)
             and (weights is None or _fits(weights, f32, sshape, here)) and (y is None or _fits(y, bf16, yshape, here))
-            and (dy is None or _fits(dy, bf16, yshape, here)) and dweights is None
+            and (dy is None or _fits(dy, bf16, yshape, here))
+            and (dweights is None or y is not None and _fits(dweights, f32, sshape, here))
             and (offsets is None or offsets.dtype is torch.int32 and offsets.get_device() == here and offsets.is_contiguous()
                  and offsets.numel() > 0)):
         _need_routing(slot, weights)
