@@ -315,12 +315,14 @@ __global__ void __launch_bounds__(kCombineThreads, P == 4 ? 4 : 7) moe_combine_k
 // The CTAs from T on clear the rows that no slot names.  Bound by HBM.
 constexpr int kTailCtas = 64, kBackwardThreads = 512;
 
-template <int K, bool WARP>
-__global__ void __launch_bounds__(WARP ? 128 : kBackwardThreads, 1) moe_combine_backward_kernel(
+enum TokenOf { kCta512, kCta128, kWarp };  // what a token belongs to
+template <int K, int OF>
+__global__ void __launch_bounds__(OF == kCta512 ? kBackwardThreads : 128, OF == kCta512 ? 1 : K == 8 ? 4 : K == 4 ? 5 : 6) moe_combine_backward_kernel(
     const uint16_t* __restrict__ dout, const uint16_t* __restrict__ y, const int32_t* __restrict__ slot,
     const float* __restrict__ weights, int64_t T, int k, int pieces, int64_t rows, const int32_t* __restrict__ rows_used,
     uint16_t* __restrict__ dy, float* __restrict__ dweights, unsigned* __restrict__ err) {
   constexpr int P = 2;
+  constexpr bool WARP = OF == kWarp;
   __shared__ float part[kBackwardThreads / 32][K];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -507,9 +509,17 @@ cudaError_t launch_moe_combine_backward(const DevInfo& d, const uint16_t* dout, 
   auto go = [&](auto kernel) {
     return cudaLaunchKernelEx(&cfg, kernel, dout, y, slot, weights, T, k, pieces, rows, rows_used, dy, dweights, d.err);
   };
-  if (k > 4) return warps ? go(moe_combine_backward_kernel<8, true>) : go(moe_combine_backward_kernel<8, false>);
-  if (k > 2) return warps ? go(moe_combine_backward_kernel<4, true>) : go(moe_combine_backward_kernel<4, false>);
-  return warps ? go(moe_combine_backward_kernel<2, true>) : go(moe_combine_backward_kernel<2, false>);
+  if (warps)
+    return k > 4   ? go(moe_combine_backward_kernel<8, kWarp>)
+           : k > 2 ? go(moe_combine_backward_kernel<4, kWarp>)
+                   : go(moe_combine_backward_kernel<2, kWarp>);
+  if (most == 128)
+    return k > 4   ? go(moe_combine_backward_kernel<8, kCta128>)
+           : k > 2 ? go(moe_combine_backward_kernel<4, kCta128>)
+                   : go(moe_combine_backward_kernel<2, kCta128>);
+  return k > 4   ? go(moe_combine_backward_kernel<8, kCta512>)
+         : k > 2 ? go(moe_combine_backward_kernel<4, kCta512>)
+                 : go(moe_combine_backward_kernel<2, kCta512>);
 }
 
 }  // namespace fp4
