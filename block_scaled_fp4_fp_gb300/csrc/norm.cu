@@ -237,8 +237,11 @@ struct Row {
   }
 };
 
-// Bound by HBM in bf16; with 4-bit results by some 24 instructions an element between the loads and the stores; one row
-// by latency.
+// Bound by HBM in bf16 with a residual (4096 x 5120: 27.6 us, 6.1 TB/s), without one and with 4-bit results by the 10 to 20
+// instructions an element between the loads and the stores (4096 x 5120 with a residual to NVFP4: 25.2 us, 5.5 TB/s;
+// 8001 x 2880 to MXFP4: 16.8 us, 3.5 TB/s), one row by latency (1 x 5120: 2.3 us).
+// Tried: CTAs that stay, the next row on its way into shared memory by bulk copy (31.8 us in bf16 with a residual, 28.3 to NVFP4;
+// without one 17.7 against 18.2 then); four chunks a thread (31 and 34 us); loads past L1 (within 2 %).
 template <int U, int MODE, bool CTA>
 __global__ void __launch_bounds__(CTA ? 1024 : 128) rms_norm_kernel(const RmsNormArgs a, int tpr, int padded_rows, int padded_cols,
                                                         int word_scales, double inv_n) {
