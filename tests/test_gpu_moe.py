@@ -213,3 +213,20 @@ def test_combine_from_a_graph(B):
     got = B.moe_combine(yd, s, wd, residual=rd, stream=side)
     side.synchronize()
     assert torch.equal(got, want)
+
+
+def test_elements_past_32_bits(B):
+    """Rows of y past 2^31 elements, forward and back."""
+    rows, cols, tokens = 300000, 8192, 6
+    y = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    slot = torch.tensor([[0, rows - 1], [262143, 262145], [rows - 2, -1], [5, 6], [131072, 131073], [-1, -1]], dtype=torch.int32, device="cuda")
+    live = slot[slot >= 0].long()
+    y[live] = synth.bf16_normal((live.numel(), cols), 1.0, seed=6).cuda()
+    g = synth.bf16_normal((tokens, cols), 1.0, seed=7).cuda()
+    packed = torch.full_like(slot, -1)
+    packed[slot >= 0] = torch.arange(live.numel(), dtype=torch.int32, device="cuda")
+    assert torch.equal(B.moe_combine(y, slot), B.moe_combine(y[live], packed))
+    dy, dw = B.moe_combine_backward(g, slot, y=y, dy=torch.zeros_like(y))
+    want = B.moe_combine_backward(g, packed, y=y[live])
+    assert torch.equal(dy[live], want[0]) and torch.equal(dw, want[1])
+    assert int((dy != 0).any(-1).sum()) == live.numel()

@@ -202,3 +202,20 @@ def test_many_rows(B):
     part = B.rms_norm(x[pick].cuda(), mode=1)
     assert torch.equal(got.xq.cpu()[pick], part.xq.cpu())
     assert got.scales.shape == B.scales_shape(rows, cols, 32, 1)
+
+
+def test_elements_past_32_bits(B):
+    """Rows whose elements lie past 2^31 (and their bytes past 2^32): the same bits as on their own."""
+    rows, cols = 140000, 16384
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+    pick = torch.tensor([0, 65535, 131071, 131073, rows - 1])
+    part = synth.bf16_normal((len(pick), cols), 1.0, seed=3).cuda()
+    x.zero_()
+    x[pick.cuda()] = part
+    got = B.rms_norm(x, residual=x, mode=2, layout=1, sum_out=x)
+    want = B.rms_norm(part, residual=part, mode=2)
+    assert torch.equal(x[pick.cuda()], want.sum) and torch.equal(got.xq[pick.cuda()], want.xq)
+    r, c = pick[:, None].cuda(), torch.arange(cols // 16, device="cuda")[None]
+    at = ((r // 128) * (cols // 64) + c // 4) * 512 + (r % 32) * 16 + ((r % 128) // 32) * 4 + c % 4
+    assert torch.equal(got.scales.view(-1)[at], want.scales)
+    assert int((got.xq != 0).any(-1).sum()) == len(pick)

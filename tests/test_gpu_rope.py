@@ -265,3 +265,45 @@ def test_append_rope_from_a_graph_after_a_plan(B):
         outs.append(out)
     assert torch.equal(outs[0], outs[1]) and (outs[0][6:] == 0).all() and outs[0][:6].any()
     assert all(torch.equal(a, b) for a, b in zip(caches[0].tensors[:4], caches[1].tensors[:4]))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_heads_before_tokens(B, interleaved):
+    """A [heads, tokens, head_dim] tensor seen as [tokens, heads, head_dim]."""
+    table = B.rope_table(300, 64, interleaved=interleaved)
+    x = synth.bf16_normal((6, 200, 96), 1.0, seed=4).cuda()
+    pos = torch.arange(50, 250, dtype=torch.int32, device="cuda")
+    want = B.rope(table, x.transpose(0, 1).contiguous(), pos)
+    assert torch.equal(B.rope(table, x.transpose(0, 1), pos), want)
+    B.rope(table, x.transpose(0, 1), pos, out=x.transpose(0, 1))
+    assert torch.equal(x.transpose(0, 1), want)
+
+
+def test_elements_past_32_bits(B):
+    """A view of more than 2^31 elements, rotated in place."""
+    tokens, heads, dim = 70000, 128, 256
+    table = B.rope_table(tokens, 64)
+    x = torch.zeros((tokens, heads, dim), dtype=torch.bfloat16, device="cuda")
+    pick = torch.tensor([0, 65535, 65537, tokens - 1], device="cuda")
+    part = synth.bf16_normal((4, heads, dim), 1.0, seed=5).cuda()
+    x[pick] = part
+    pos = torch.arange(tokens, dtype=torch.int32, device="cuda")
+    B.rope(table, x, pos, out=x)
+    assert torch.equal(x[pick], B.rope(table, part, pick.int()))
+
+
+@pytest.mark.parametrize("rotary", [32, 20])
+def test_append_to_a_cache_past_32_bits(B, rotary):
+    """Rows past 2^29, codes past 2^33 bytes, in every kind of append."""
+    for mode, interleaved in ((2, False), (2, True), (1, False)):
+        dim, kv, page, pages = 64 if mode == 1 else 32, 8, 128, 600000
+        cache = B.kv_cache_empty(pages, kv, page, dim, mode)
+        small = B.kv_cache_empty(1, kv, page, dim, mode)
+        table = B.rope_table(100, rotary, interleaved=interleaved)
+        k, v = (synth.bf16_normal((page, kv, dim), 1.0, seed=s).cuda() for s in (1, 2))
+        slots, pos = torch.arange(page, device="cuda"), torch.arange(page, dtype=torch.int32, device="cuda") % 100
+        B.kv_append_rope(cache, table, k, v, slots + (pages - 1) * page, pos)
+        B.kv_append_rope(small, table, k, v, slots, pos)
+        assert all(torch.equal(a[-1], b[0]) for a, b in zip(cache.tensors[:4], small.tensors[:4]))
+        assert not any(bool(t[:-1:5000].any()) for t in cache.tensors[:4])
+        del cache
