@@ -505,20 +505,12 @@ def _need_here(*tensors):
             raise ValueError(f"a tensor of shape {tuple(t.shape)} is on {t.device}, the current device is cuda:{here}")
 
 
-# What a call's tensors are to be, in a few cheap questions (a call costs the host about as much as a launch): where one
-# says no, the checks above find out which it was and say so.
-
-
-def _here() -> int:
-    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
-
-
-def _fits(t, dtype, shape, here) -> bool:
-    return t.dtype is dtype and t.get_device() == here and t.shape == shape and t.is_contiguous()
-
-
-def _fits_rows(t, dtype, shape, here) -> bool:
-    return t.dtype is dtype and t.get_device() == here and t.shape == shape and t.stride(-1) == 1
+# A call of what follows costs the host about as much as a launch does, so its tensors are first asked a few cheap questions
+# in place (a function call each would cost a quarter of the whole); where one says no, the checks above find out which it
+# was and say so.
+_BF16, _I32, _I64, _F32, _U8 = torch.bfloat16, torch.int32, torch.int64, torch.float32, torch.uint8
+_device = getattr(torch._C, "_cuda_getDevice", None)  # (of CUDA tensors only: CUDA is initialised then)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _empty(shape, dtype, like, stream):
@@ -527,6 +519,10 @@ def _empty(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _stream_of(stream, here: int):
+    return _raw_stream(here) if stream is None else stream.cuda_stream
 
 
 class RmsNorm(NamedTuple):
@@ -543,30 +539,39 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor = None, eps: float = 1e-6, re
     """Root-mean-square norm of the rows of x [rows, cols] (+ residual; their sum is returned too, and written in place
     with sum_out=residual).  Without a mode the result is bf16; with MODE_NVFP4 or MODE_MXFP4 it is codes and scales as
     fp4_quantize makes them, and bf16 as well where out is given."""
-    bf16, shape, here = torch.bfloat16, x.shape, _here()
-    four = mode is not None
-    if not (len(shape) == 2 and _fits_rows(x, bf16, shape, here) and (weight is None or _fits(weight, bf16, shape[1:], here))
-            and (residual is None or _fits_rows(residual, bf16, shape, here))
-            and (sum_out is None or _fits_rows(sum_out, bf16, shape, here)) and (out is None or _fits(out, bf16, shape, here))
-            and (four or global_scale is None and xq is None and scales is None) and (not four or mode == 1 or mode == 2)
-            and (xq is None or _fits(xq, torch.int32, (shape[0], shape[1] // 8), here))
-            and (scales is None or _fits(scales, torch.uint8, scales_shape(*shape, GROUP[mode], layout), here))
-            and (global_scale is None or _fits(global_scale, torch.float32, (), here))):
+    shape, here, four, tiled = x.shape, x.get_device(), mode is not None, layout == SCALES_TILED
+    if not (len(shape) == 2 and x.dtype is _BF16 and x.is_cuda and x.stride(1) == 1
+            and (weight is None or weight.dtype is _BF16 and weight.numel() == shape[1] and weight.is_contiguous()
+                 and weight.get_device() == here)
+            and (residual is None or residual.dtype is _BF16 and residual.shape == shape and residual.stride(1) == 1
+                 and residual.get_device() == here)
+            and (sum_out is None or sum_out.dtype is _BF16 and sum_out.shape == shape and sum_out.stride(1) == 1
+                 and sum_out.get_device() == here)
+            and (out is None or out.dtype is _BF16 and out.shape == shape and out.is_contiguous() and out.get_device() == here)
+            and xq is None and scales is None and here == _device()
+            and ((mode == MODE_NVFP4 or mode == MODE_MXFP4) and (global_scale is None or global_scale.dtype is _F32
+                 and global_scale.numel() == 1 and global_scale.get_device() == here) if four else global_scale is None)):
         _need_rms_norm(x, weight, residual, mode, global_scale, layout, sum_out, out, xq, scales)
     rows, cols = shape
     if residual is not None and sum_out is None:
-        sum_out = _empty(shape, bf16, x, stream)
+        sum_out = _empty(shape, _BF16, x, stream)
+    xs = rs = ss = cols  # (the stride of a single row says nothing)
+    if rows > 1:
+        xs, rs, ss = x.stride(0), 0 if residual is None else residual.stride(0), 0 if sum_out is None else sum_out.stride(0)
     if four:
         if xq is None:
-            xq = _empty((rows, cols // 8), torch.int32, x, stream)
+            xq = _empty((rows, cols // 8), _I32, x, stream)
         if scales is None:
-            scales = _empty(scales_shape(rows, cols, GROUP[mode], layout), torch.uint8, x, stream)
+            scales = _empty(_scales_shape(rows, cols // GROUP[mode], tiled), _U8, x, stream)
     elif out is None:
-        out = _empty(shape, bf16, x, stream)
-    _check(lib().rms_norm(x.data_ptr(), _row_stride(x), _p(residual), _row_stride(residual), _p(weight), eps, rows, cols,
-                          _p(sum_out), _row_stride(sum_out), _p(out), mode or 0, _p(global_scale), _p(xq), _p(scales), layout,
-                          _s(stream)), "rms_norm")
+        out = _empty(shape, _BF16, x, stream)
+    _check(lib().rms_norm(x.data_ptr(), xs, _p(residual), rs, _p(weight), eps, rows, cols, _p(sum_out), ss, _p(out), mode or 0,
+                          _p(global_scale), _p(xq), _p(scales), layout, _stream_of(stream, here)), "rms_norm")
     return RmsNorm(out, sum_out, xq, scales)
+
+
+def _scales_shape(rows: int, cols: int, tiled: bool):
+    return ((rows + 127) // 128 * 128, (cols + 3) // 4 * 4) if tiled else (rows, cols)
 
 
 def _need_rms_norm(x, weight, residual, mode, global_scale, layout, sum_out, out, xq, scales):
@@ -596,16 +601,11 @@ def _need_rms_norm(x, weight, residual, mode, global_scale, layout, sum_out, out
     _need_here(x, residual, weight, sum_out, out, global_scale, xq, scales)
 
 
-def _row_stride(t):
-    """Elements between the rows of a matrix (of one row: any; its width)."""
-    return 0 if t is None else t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _view_strides(t):
+def _view_strides(t, tokens: int, heads: int, dim: int):
     """(token, head) strides of a [tokens, heads, dim] view; those of a single token or head say nothing."""
-    tokens, heads, dim = t.shape
-    head = t.stride(1) if heads > 1 else dim
-    return t.stride(0) if tokens > 1 else max(heads * dim, heads * head), head
+    strides = t.stride()
+    head = strides[1] if heads > 1 else dim
+    return strides[0] if tokens > 1 else heads * max(dim, head), head
 
 
 class Rope(c.Structure):
@@ -633,7 +633,7 @@ def rope_from_table(table: torch.Tensor, interleaved: bool = False) -> Rope:
         raise ValueError(f"table: [positions, rotary_dim / 2, 2] is needed, got {tuple(table.shape)}")
     _need("table", table, torch.float32, tuple(table.shape))
     r = Rope(_p(table), table.shape[0], 2 * table.shape[1], 1 if interleaved else 0)
-    r.tensor = table
+    r.tensor, r.device = table, table.get_device()
     return r
 
 
@@ -664,20 +664,23 @@ def _need_view(name: str, t: torch.Tensor, shape):
 def rope(rope: Rope, x: torch.Tensor, positions: torch.Tensor, backward: bool = False, out=None, stream=None):
     """x [tokens, heads, head_dim] (views with strides are read in place) rotated by its tokens' positions; backward: the
     transposed rotation.  out=x rotates in place; rows of negative positions are not written."""
-    bf16, shape, here = torch.bfloat16, x.shape, _here()
-    if not (len(shape) == 3 and _fits_rows(x, bf16, shape, here) and _fits(positions, torch.int32, shape[:1], here)
-            and (out is None or _fits_rows(out, bf16, shape, here)) and rope.tensor.get_device() == here):
+    shape, here = x.shape, x.get_device()
+    if not (len(shape) == 3 and x.dtype is _BF16 and x.is_cuda and x.stride(2) == 1 and positions.dtype is _I32
+            and positions.numel() == shape[0] and positions.is_contiguous() and positions.get_device() == here
+            and (out is None or out.dtype is _BF16 and out.shape == shape and out.stride(2) == 1 and out.get_device() == here)
+            and rope.device == here == _device()):
         _need_view("x", x, tuple(shape))
-        _need_vector("positions", positions, torch.int32, shape[0])
+        _need_vector("positions", positions, _I32, shape[0])
         if out is not None:
             _need_view("out", out, tuple(shape))
         _need_here(x, positions, out, rope.tensor)
+    tokens, heads, dim = shape
     if out is None:
-        out = _empty(shape, bf16, x, stream)
-    xt, xh = _view_strides(x)
-    ot, oh = _view_strides(out)
-    _check(lib().rope(c.byref(rope), x.data_ptr(), xt, xh, positions.data_ptr(), *shape, 1 if backward else 0, out.data_ptr(),
-                      ot, oh, _s(stream)), "rope")
+        out = _empty(shape, _BF16, x, stream)
+    xt, xh = _view_strides(x, tokens, heads, dim)
+    ot, oh = _view_strides(out, tokens, heads, dim)
+    _check(lib().rope(c.byref(rope), x.data_ptr(), xt, xh, positions.data_ptr(), tokens, heads, dim, 1 if backward else 0,
+                      out.data_ptr(), ot, oh, _stream_of(stream, here)), "rope")
     return out
 
 
@@ -685,34 +688,38 @@ def kv_append_rope(cache: KvCache, rope: Rope, k: torch.Tensor, v: torch.Tensor,
                    positions: torch.Tensor, q: torch.Tensor = None, q_out=None, stream=None):
     """kv_append with K rotated by its tokens' positions; q [tokens, q_heads, head_dim], where given, is rotated by the
     same launch into q_out (q_out=q: in place), which is returned.  Views with strides are read in place."""
-    bf16, here, tokens = torch.bfloat16, _here(), slot_map.numel()
-    shape = (tokens, cache.kv_heads, cache.head_dim)
-    qshape = None if q is None else q.shape
-    if not (_fits_rows(k, bf16, shape, here) and _fits_rows(v, bf16, shape, here) and _fits(slot_map, torch.int64, (tokens,), here)
-            and _fits(positions, torch.int32, (tokens,), here)
-            and (q_out is None if q is None else len(qshape) == 3 and qshape[0] == tokens and qshape[2] == shape[2]
-                 and _fits_rows(q, bf16, qshape, here) and (q_out is None or _fits_rows(q_out, bf16, qshape, here)))
-            and cache.tensors[0].get_device() == here and rope.tensor.get_device() == here):
-        _need_vector("slot_map", slot_map, torch.int64, tokens)
-        _need_vector("positions", positions, torch.int32, tokens)
+    here, tokens, heads, dim = k.get_device(), slot_map.numel(), cache.kv_heads, cache.head_dim
+    shape, qshape = (tokens, heads, dim), None if q is None else q.shape
+    if not (k.dtype is _BF16 and k.is_cuda and k.shape == shape and k.stride(2) == 1
+            and v.dtype is _BF16 and v.shape == shape and v.stride(2) == 1 and v.get_device() == here
+            and slot_map.dtype is _I64 and slot_map.is_contiguous() and slot_map.get_device() == here
+            and positions.dtype is _I32 and positions.numel() == tokens and positions.is_contiguous() and positions.get_device() == here
+            and (q_out is None if q is None else q.dtype is _BF16 and len(qshape) == 3 and qshape[0] == tokens and qshape[2] == dim
+                 and q.stride(2) == 1 and q.get_device() == here
+                 and (q_out is None or q_out.dtype is _BF16 and q_out.shape == qshape and q_out.stride(2) == 1 and q_out.get_device() == here))
+            and cache.tensors[0].get_device() == rope.device == here == _device()):
+        _need_vector("slot_map", slot_map, _I64, tokens)
+        _need_vector("positions", positions, _I32, tokens)
         _need_view("k", k, shape)
         _need_view("v", v, shape)
         if q is not None:
-            _need_view("q", q, (tokens, q.shape[1] if q.dim() == 3 else 0, cache.head_dim))
+            _need_view("q", q, (tokens, q.shape[1] if q.dim() == 3 else 0, dim))
             if q_out is not None:
                 _need_view("q_out", q_out, tuple(q.shape))
         elif q_out is not None:
             raise ValueError("q_out: there is no q to rotate")
         _need_here(k, v, slot_map, positions, q, q_out, cache.tensors[0], rope.tensor)
-    qt = qh = heads = ot = oh = 0
+    qt = qh = qheads = ot = oh = 0
     if q is not None:
         if q_out is None:
-            q_out = _empty(qshape, bf16, q, stream)
-        heads, (qt, qh), (ot, oh) = qshape[1], _view_strides(q), _view_strides(q_out)
-    kt, kh = _view_strides(k)
-    vt, vh = _view_strides(v)
+            q_out = _empty(qshape, _BF16, q, stream)
+        qheads = qshape[1]
+        qt, qh = _view_strides(q, tokens, qheads, dim)
+        ot, oh = _view_strides(q_out, tokens, qheads, dim)
+    kt, kh = _view_strides(k, tokens, heads, dim)
+    vt, vh = _view_strides(v, tokens, heads, dim)
     _check(lib().kv_append_rope(c.byref(cache), c.byref(rope), k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, slot_map.data_ptr(),
-                                positions.data_ptr(), tokens, _p(q), qt, qh, heads, _p(q_out), ot, oh, _s(stream)),
+                                positions.data_ptr(), tokens, _p(q), qt, qh, qheads, _p(q_out), ot, oh, _stream_of(stream, here)),
            "kv_append_rope")
     return q_out
 
@@ -728,23 +735,24 @@ class MoeSort(NamedTuple):
 def moe_sort(ids: torch.Tensor, num_experts: int, plan: MoeSort = None, stream=None) -> MoeSort:
     """The routed rows of ids int32 [tokens, k] in order of their experts: lhs_idx and rhs_idx are what gather_rows and
     gather_qmm take, slot what moe_combine takes.  Negative ids are dropped."""
-    i32, shape, here = torch.int32, ids.shape, _here()
-    if not (plan is None and len(shape) == 2 and _fits(ids, i32, shape, here)):
-        if ids.dim() != 2:
-            raise ValueError(f"ids: [tokens, k] is needed, got {tuple(ids.shape)}")
-        _need("ids", ids, i32, tuple(shape))
+    shape, here = ids.shape, ids.get_device()
+    if not (plan is None and len(shape) == 2 and ids.dtype is _I32 and ids.is_cuda and ids.is_contiguous() and here == _device()):
+        if len(shape) != 2:
+            raise ValueError(f"ids: [tokens, k] is needed, got {tuple(shape)}")
+        _need("ids", ids, _I32, tuple(shape))
         if plan is not None:
-            _need_vector("lhs_idx", plan.lhs_idx, i32, ids.numel())
-            _need_vector("rhs_idx", plan.rhs_idx, i32, ids.numel())
-            _need("slot", plan.slot, i32, tuple(shape))
-            _need_vector("offsets", plan.offsets, i32, num_experts + 1)
+            _need_vector("lhs_idx", plan.lhs_idx, _I32, ids.numel())
+            _need_vector("rhs_idx", plan.rhs_idx, _I32, ids.numel())
+            _need("slot", plan.slot, _I32, tuple(shape))
+            _need_vector("offsets", plan.offsets, _I32, num_experts + 1)
         _need_here(ids, *(plan or ()))
+    tokens, k = shape
     if plan is None:
-        rows = ids.numel()
-        plan = MoeSort(_empty(rows, i32, ids, stream), _empty(rows, i32, ids, stream), _empty(shape, i32, ids, stream),
-                       _empty(max(num_experts, 0) + 1, i32, ids, stream))
-    _check(lib().moe_sort(ids.data_ptr(), *shape, num_experts, plan.lhs_idx.data_ptr(), plan.rhs_idx.data_ptr(),
-                          plan.slot.data_ptr(), plan.offsets.data_ptr(), _s(stream)), "moe_sort")
+        rows = tokens * k
+        plan = MoeSort(_empty(rows, _I32, ids, stream), _empty(rows, _I32, ids, stream), _empty(shape, _I32, ids, stream),
+                       _empty(max(num_experts, 0) + 1, _I32, ids, stream))
+    _check(lib().moe_sort(ids.data_ptr(), tokens, k, num_experts, plan.lhs_idx.data_ptr(), plan.rhs_idx.data_ptr(),
+                          plan.slot.data_ptr(), plan.offsets.data_ptr(), _stream_of(stream, here)), "moe_sort")
     return plan
 
 
@@ -758,26 +766,29 @@ def moe_combine(y: torch.Tensor, slot: torch.Tensor, weights: torch.Tensor = Non
                 stream=None):
     """The experts' rows y [rows, cols] back to their tokens: residual + sum of weights * y[slot] (weights None: 1, which
     with the sorted rows' gradient as y is the gradient of their gather).  out=residual adds in place."""
-    bf16, here = torch.bfloat16, _here()
-    sshape, yshape = slot.shape, y.shape
+    sshape, yshape, here = slot.shape, y.shape, y.get_device()
     if len(sshape) != 2:
         raise ValueError(f"slot: [tokens, k] is needed, got {tuple(sshape)}")
     if len(yshape) != 2:
         raise ValueError(f"y: [rows, cols] is needed, got {tuple(yshape)}")
-    oshape = (sshape[0], yshape[1])
-    if not (_fits(slot, torch.int32, sshape, here) and _fits(y, bf16, yshape, here)
-            and (weights is None or _fits(weights, torch.float32, sshape, here))
-            and (residual is None or _fits(residual, bf16, oshape, here)) and (out is None or _fits(out, bf16, oshape, here))):
+    (tokens, k), (rows, cols) = sshape, yshape
+    oshape = (tokens, cols)
+    if not (slot.dtype is _I32 and slot.is_contiguous() and slot.get_device() == here and y.dtype is _BF16 and y.is_cuda and y.is_contiguous()
+            and (weights is None or weights.dtype is _F32 and weights.shape == sshape and weights.is_contiguous() and weights.get_device() == here)
+            and (residual is None or residual.dtype is _BF16 and residual.shape == oshape and residual.is_contiguous()
+                 and residual.get_device() == here)
+            and (out is None or out.dtype is _BF16 and out.shape == oshape and out.is_contiguous() and out.get_device() == here)
+            and here == _device()):
         _need_routing(slot, weights)
-        _need("y", y, bf16, tuple(yshape))
+        _need("y", y, _BF16, tuple(yshape))
         for name, t in (("residual", residual), ("out", out)):
             if t is not None:
-                _need(name, t, bf16, oshape)
+                _need(name, t, _BF16, oshape)
         _need_here(y, slot, weights, residual, out)
     if out is None:
-        out = _empty(oshape, bf16, y, stream)
-    _check(lib().moe_combine(y.data_ptr(), yshape[0], slot.data_ptr(), _p(weights), _p(residual), *sshape, yshape[1],
-                             out.data_ptr(), _s(stream)), "moe_combine")
+        out = _empty(oshape, _BF16, y, stream)
+    _check(lib().moe_combine(y.data_ptr(), rows, slot.data_ptr(), _p(weights), _p(residual), tokens, k, cols, out.data_ptr(),
+                             _stream_of(stream, here)), "moe_combine")
     return out
 
 
@@ -786,39 +797,39 @@ def moe_combine_backward(dout: torch.Tensor, slot: torch.Tensor, weights: torch.
     """(dy [rows, cols], dweights [tokens, k]) from dout [tokens, cols].  dweights needs y (None without it); rows is y's,
     or dy's, or every routed row's.  offsets (moe_sort's): rows of dy that no slot names are zeros; without it they are
     not written."""
-    bf16, f32, here = torch.bfloat16, torch.float32, _here()
-    sshape, gshape = slot.shape, dout.shape
+    sshape, gshape, here = slot.shape, dout.shape, dout.get_device()
     if len(sshape) != 2:
         raise ValueError(f"slot: [tokens, k] is needed, got {tuple(sshape)}")
     if len(gshape) != 2:
         raise ValueError(f"dout: [tokens, cols] is needed, got {tuple(gshape)}")
-    rows = y.shape[0] if y is not None else dy.shape[0] if dy is not None else slot.numel()
-    yshape = (rows, gshape[1])
-    if not (gshape[0] == sshape[0] and _fits(slot, torch.int32, sshape, here) and _fits(dout, bf16, gshape, here)
-            and (weights is None or _fits(weights, f32, sshape, here)) and (y is None or _fits(y, bf16, yshape, here))
-            and (dy is None or _fits(dy, bf16, yshape, here))
-            and (dweights is None or y is not None and _fits(dweights, f32, sshape, here))
-            and (offsets is None or offsets.dtype is torch.int32 and offsets.get_device() == here and offsets.is_contiguous()
-                 and offsets.numel() > 0)):
+    (tokens, k), cols = sshape, gshape[1]
+    rows = y.shape[0] if y is not None else dy.shape[0] if dy is not None else tokens * k
+    yshape = (rows, cols)
+    if not (gshape[0] == tokens and slot.dtype is _I32 and slot.is_contiguous() and slot.get_device() == here
+            and dout.dtype is _BF16 and dout.is_cuda and dout.is_contiguous()
+            and (weights is None or weights.dtype is _F32 and weights.shape == sshape and weights.is_contiguous() and weights.get_device() == here)
+            and (y is None or y.dtype is _BF16 and y.shape == yshape and y.is_contiguous() and y.get_device() == here)
+            and (offsets is None or offsets.dtype is _I32 and offsets.numel() > 0 and offsets.is_contiguous() and offsets.get_device() == here)
+            and dy is None and dweights is None and here == _device()):
         _need_routing(slot, weights)
-        _need("dout", dout, bf16, (sshape[0], gshape[1]))
+        _need("dout", dout, _BF16, (tokens, cols))
         for name, t in (("y", y), ("dy", dy)):
             if t is not None:
-                _need(name, t, bf16, yshape)
+                _need(name, t, _BF16, yshape)
         if dweights is not None:
-            _need("dweights", dweights, f32, tuple(sshape))
+            _need("dweights", dweights, _F32, tuple(sshape))
             if y is None:
                 raise ValueError("dweights: y is needed for it")
         if offsets is not None:
-            _need_vector("offsets", offsets, torch.int32, max(1, offsets.numel()))
+            _need_vector("offsets", offsets, _I32, max(1, offsets.numel()))
         _need_here(dout, slot, weights, y, offsets, dy, dweights)
     if dy is None:
-        dy = _empty(yshape, bf16, dout, stream)
+        dy = _empty(yshape, _BF16, dout, stream)
     if y is not None and dweights is None:
-        dweights = _empty(sshape, f32, dout, stream)
+        dweights = _empty(sshape, _F32, dout, stream)
     used = None if offsets is None else offsets.data_ptr() + 4 * (offsets.numel() - 1)
-    _check(lib().moe_combine_backward(dout.data_ptr(), _p(y), slot.data_ptr(), _p(weights), *sshape, gshape[1], rows, used,
-                                      dy.data_ptr(), _p(dweights), _s(stream)), "moe_combine_backward")
+    _check(lib().moe_combine_backward(dout.data_ptr(), _p(y), slot.data_ptr(), _p(weights), tokens, k, cols, rows, used,
+                                      dy.data_ptr(), _p(dweights), _stream_of(stream, here)), "moe_combine_backward")
     return dy, dweights
 
 
