@@ -102,6 +102,7 @@ struct Shared {
   float2 part[32];
   double part64[32];
   double sum64;
+  float rstd;
 };
 
 template <int U>
@@ -296,16 +297,29 @@ __global__ void __launch_bounds__(CTA ? 1024 : 128) rms_norm_kernel(const RmsNor
     warp_sum(hi, hi, lo);
   else
     group_sum(hi, lo, tpr);
-  if (CTA) {  // every warp adds the warps' sums up for itself, each aligned group of lanes all of them: one barrier
+  // The warps' sums: added up by every warp for itself (each aligned group of lanes all of them), which saves a barrier, or
+  // with 4-bit results, where instructions count, by the first warp (4096 x 5120 to NVFP4: 15.7 us against 17.2 without a
+  // residual, 24.9 against 25.2 with one; to bf16 16.6 against 16.4, and 28.0 against 27.6).
+  constexpr bool kEvery = MODE == 0;
+  if (CTA) {
     const int nw = (int)blockDim.x >> 5, width = nw <= 4 ? 4 : nw <= 8 ? 8 : nw <= 16 ? 16 : 32, w = lane & (width - 1);
     if (lane == 0) sh.part[warp] = make_float2(hi, lo);
     __syncthreads();
-    const float2 t = w < nw ? sh.part[w] : make_float2(0.f, 0.f);
-    hi = t.x;
-    lo = t.y;
-    group_sum(hi, lo, width);
+    if (kEvery || warp == 0) {
+      const float2 t = w < nw ? sh.part[w] : make_float2(0.f, 0.f);
+      hi = t.x;
+      lo = t.y;
+      group_sum(hi, lo, width);
+    }
   }
-  float rstd = out_of_range(hi, a.eps) ? -1.0f : inv_rms(hi, lo, (float)a.cols, (float)inv_n, a.eps);
+  float rstd = 0.0f;
+  if (!CTA || kEvery || warp == 0)
+    rstd = out_of_range(hi, a.eps) ? -1.0f : inv_rms(hi, lo, (float)a.cols, (float)inv_n, a.eps);
+  if (CTA && !kEvery) {
+    if (threadIdx.x == 0) sh.rstd = rstd;
+    __syncthreads();
+    rstd = sh.rstd;
+  }
   rstd = r.template scale<CTA>(rstd, a, tpr, inv_n, sh);
   r.template write<MODE>(a, rstd, block_scale<MODE>(a.gs), row, live, l, tpr, pieces, padded_rows, padded_cols, word_scales);
 }
