@@ -239,13 +239,14 @@ struct Row {
 };
 
 // Bound by HBM in bf16 with a residual (4096 x 5120: 27.6 us, 6.1 TB/s), without one and with 4-bit results by the 10 to 20
-// instructions an element between the loads and the stores (4096 x 5120 with a residual to NVFP4: 25.2 us, 5.5 TB/s;
-// 8001 x 2880 to MXFP4: 16.8 us, 3.5 TB/s), one row by latency (1 x 5120: 2.3 us).
+// instructions an element between the loads and the stores (4096 x 5120 with a residual to NVFP4: 24.9 us, 5.5 TB/s;
+// 8001 x 2880 to MXFP4: 16.5 us, 3.5 TB/s), one row by latency (1 x 5120: 2.2 us).
 // Tried: CTAs that stay, the next row on its way into shared memory by bulk copy (31.8 us in bf16 with a residual, 28.3 to NVFP4;
-// without one 17.7 against 18.2 then); four chunks a thread (31 and 34 us); loads past L1 (within 2 %).
+// without one 17.7 against 18.2 then); four chunks a thread (31 and 34 us; without a residual, x kept as bf16 and widened twice,
+// 24 against 16.4 in bf16: spills); loads past L1 (within 2 %).
 template <int U, int MODE, bool CTA>
-__global__ void __launch_bounds__(CTA ? 1024 : 128) rms_norm_kernel(const RmsNormArgs a, int tpr, int padded_rows, int padded_cols,
-                                                        int word_scales, double inv_n) {
+__global__ void __launch_bounds__(CTA ? 1024 : 128) rms_norm_kernel(const RmsNormArgs a, int tpr, int padded_rows,
+                                                                     int padded_cols, int word_scales, double inv_n) {
   __shared__ Shared sh;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -345,7 +346,8 @@ cudaError_t launch_rms_norm(const DevInfo& d, const RmsNormArgs& a, cudaStream_t
     chunks = (chunks + least - 1) / least * least;  // (whole words of scales, and the padding's)
   }
   // Two chunks a thread where the rows fill the GPU anyway (4096 x 5120: 27.6 us against 28.9 in bf16, 26.5 against 31.8 to
-  // NVFP4), one where latency counts (1 x 5120: 2.4 us against 2.7, 2.8 against 3.3); more than 1024 chunks need two.
+  // NVFP4, when both were measured), one where latency counts (1 x 5120: 2.4 us against 2.7, 2.8 against 3.3); more than 1024
+  // chunks need two.
   const int U = chunks > 1024 || (int64_t)chunks * prows >= (int64_t)d.sm_count * 1024 ? 2 : 1;
   const int need = (chunks + U - 1) / U;
   int tpr = (need + 31) / 32 * 32;
