@@ -311,9 +311,10 @@ __global__ void __launch_bounds__(kCombineThreads, P == 4 ? 4 : 7) moe_combine_k
 }
 
 // ---------------------------------------------------- moe_combine_backward --
-// A CTA a token, or a warp a token where rows are short and tokens many: dout's row is read (again from L1 for each further K of the k rows), a row of dy written and a row of y
-// multiplied with it for each j; two pieces of K rows are in flight a thread.  The dot products of the K rows are
-// reduced together: each step of the butterfly halves the number of sums a lane holds, nine shuffles instead of forty for eight.
+// A CTA a token, or a warp a token where rows are short and tokens many: dout's row is read (again from L1 for each
+// further K of the k rows), a row of dy written and a row of y multiplied with it for each j; two pieces of K rows are in
+// flight a thread.  The dot products of the K rows are reduced together: each step of the butterfly halves the number of
+// sums a lane holds, nine shuffles instead of forty for eight.
 // The CTAs behind the tokens' clear the rows that no slot names.  Bound by HBM: 4096 x 8 of 5120 110 us, 6.5 TB/s; 2048 x 4
 // of 2880 21 us, 5.0 TB/s.
 constexpr int kTailCtas = 64, kBackwardThreads = 512;
