@@ -9,6 +9,7 @@ gather_qmm (gate and up) -> silu(gate) up -> gather_qmm (down) -> moe_combine wi
 random; the router's softmax and the activation are torch's.  --check compares every step's stages with 64 bits, and the
 gradients of moe_combine after the prompts."""
 import argparse
+import math
 import os
 import sys
 
@@ -18,6 +19,29 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 from block_scaled_fp4_fp_gb300 import binding as B, build
 
 MODES = {"nvfp4": B.MODE_NVFP4, "mxfp4": B.MODE_MXFP4}
+
+
+def rel(got, want):
+    """Relative error; a NaN among them is infinitely far off (max and comparisons would drop it)."""
+    e = float((got.double() - want).norm() / want.norm().clamp(min=1e-300))
+    return e if math.isfinite(e) else math.inf
+
+
+def further(got, base, want):
+    """How much further from `want` got is than base."""
+    e = rel(got, want)
+    return e if e == math.inf else max(0.0, e - rel(base, want))
+
+
+def gather(worst, found):
+    for name, v in found.items():
+        worst[name] = max(worst.get(name, 0.0), v)
+
+
+def off_limits(worst):
+    """Stages further off than bf16 results are (2^-8 at most), attention's 8-bit probabilities twice that; the 4-bit norm is
+    no further from the exact rows than the quantizer's own codes of them are, but for a few blocks."""
+    return [name for name, v in worst.items() if not v <= (2.0 ** -7 if name == "attention" else 2.0 ** -8)]
 
 
 class Layer:
@@ -94,13 +118,12 @@ class Layer:
     def check(self, k):
         """How far a step's stages are from 64 bits: the largest relative errors by name."""
         a, T, off = self.a, k["x"].shape[0], {}
-        rel = lambda got, want: float((got.double() - want).norm() / want.norm().clamp(min=1e-300))  # noqa: E731
         norm = lambda h, w: h * (h.square().mean(-1, keepdim=True) + 1e-6).rsqrt() * w.double()  # noqa: E731
         # the first norm's codes are the quantizer's of the exact rows, but for blocks next to a border
         y = norm(k["x"].double(), self.norms[0])
         codes, scales = B.fp4_quantize(y.bfloat16(), self.mode, global_scale=self.gs, layout=B.SCALES_TILED)
         read = lambda c, s: B.fp4_dequantize(c, s, mode=self.mode, global_scale=self.gs, layout=B.SCALES_TILED).double()  # noqa: E731
-        off["norm to 4 bits"] = max(0.0, rel(read(k["n1"].xq, k["n1"].scales), y) - rel(read(codes, scales), y))
+        off["norm to 4 bits"] = further(read(k["n1"].xq, k["n1"].scales), read(codes, scales), y)
         h = k["o"].double() + k["x"].double()
         off["residual"], off["norm"] = rel(k["n2"].sum, h), rel(k["n2"].out, norm(h, self.norms[1]))
         # rotary positions of q
@@ -149,8 +172,7 @@ class Layer:
         live = route.slot >= 0
         picked = torch.where(live[..., None], y[route.slot.clamp(min=0).long()], 0.0)
         ((w[..., None] * picked).sum(1) * dout.double()).sum().backward()
-        return {"rows' gradient": float((dy.double() - y.grad).norm() / y.grad.norm()),
-                "weights' gradient": float((dw.double() - w.grad).norm() / w.grad.norm())}
+        return {"rows' gradient": rel(dy, y.grad), "weights' gradient": rel(dw, w.grad)}
 
 
 def main():
@@ -175,17 +197,13 @@ def main():
     B.fp4_init(0)
     layer, n, worst = Layer(a), len(a.prompts), {}
 
-    def check(found):
-        for name, v in found.items():
-            worst[name] = max(worst.get(name, 0.0), v)
-
     # prompts
     x = torch.randn((sum(a.prompts), a.hidden), device="cuda").bfloat16()
     keep = {}
     layer.step(x, torch.tensor(a.prompts, dtype=torch.int32, device="cuda"), max(a.prompts), keep)
     if a.check:
-        check(layer.check(keep))
-        check(layer.gradients(keep))
+        gather(worst, layer.check(keep))
+        gather(worst, layer.gradients(keep))
     # tokens: one step runs eagerly, the others from a graph
     x = torch.randn((n + a.pad, a.hidden), device="cuda").bfloat16()
     one = torch.ones(n, dtype=torch.int32, device="cuda")
@@ -195,7 +213,7 @@ def main():
         layer.step(x, one, 1, keep)
     torch.cuda.current_stream().wait_stream(side)
     if a.check:
-        check(layer.check(keep))
+        gather(worst, layer.check(keep))
     keep, graph = {} if a.check else None, torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         y = layer.step(x, one, 1, keep)
@@ -206,7 +224,7 @@ def main():
             x.copy_(y)
         graph.replay()
         if a.check:
-            check(layer.check(keep))
+            gather(worst, layer.check(keep))
     ev[1].record()
     torch.cuda.synchronize()
     status = B.fp4_check_device_error()
@@ -218,11 +236,8 @@ def main():
     if a.check:
         for name, v in worst.items():
             print(f"largest relative error, {name}: {v:.2e}")
-        # bf16 results (2^-8 at most), attention's 8-bit probabilities twice that; the 4-bit norm is no further from the exact rows
-        # than the quantizer's own codes of them are, but for a few blocks
-        over = [name for name, v in worst.items() if not v <= (2.0 ** -7 if name == "attention" else 2.0 ** -8)]
-        if over:
-            raise SystemExit("off: " + ", ".join(over))
+        if off_limits(worst):
+            raise SystemExit("off: " + ", ".join(off_limits(worst)))
     else:
         print(f"{n} requests, {sum(want)} tokens cached: {ev[0].elapsed_time(ev[1]) / max(a.steps - 1, 1) * 1e3:.1f} us a step")
     print("ok")
