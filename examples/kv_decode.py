@@ -8,6 +8,7 @@ A step is: projections (qmm over 4-bit weights) -> kv_plan (pages and slots for 
 compares every step with attention in 64 bits over the dequantized cache.  (Rotary positions: kv_append_rope in place of
 kv_append, with kv_plan's positions; decoder_layer.py beside this file does so.)"""
 import argparse
+import math
 import os
 import sys
 
@@ -17,6 +18,12 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 from block_scaled_fp4_fp_gb300 import binding as B, build
 
 MODES = {"nvfp4": B.MODE_NVFP4, "mxfp4": B.MODE_MXFP4}
+
+
+def rel(got, want):
+    """Relative error; a NaN among them is infinitely far off (max and comparisons would drop it)."""
+    e = float((got.double() - want).norm() / want.norm().clamp(min=1e-300))
+    return e if math.isfinite(e) else math.inf
 
 
 class Block:
@@ -111,7 +118,7 @@ def main():
     def check(keep):
         nonlocal worst
         want = block.exact(keep["q"], keep["plan"])
-        worst = max(worst, float((keep["out"].double() - want).norm() / want.norm()))
+        worst = max(worst, rel(keep["out"], want))
 
     # one workspace for prompts and tokens
     ws = block.workspace(max(a.prompts))

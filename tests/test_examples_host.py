@@ -52,3 +52,11 @@ def test_decoder_layer_check_passes_what_is_right_and_names_what_is_off():
     E.gather(worst, {"rope": E.rel(want * 1.01, want), "sort": float("inf")})
     E.gather(worst, {"rope": 0.0, "sort": 0.0})
     assert sorted(E.off_limits(worst)) == ["rope", "sort"]
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_kv_decode_check_fails_on_a_step_that_is_not_finite(value):
+    E = load("kv_decode")
+    want = torch.randn((4, 16), dtype=torch.float64)
+    assert E.rel(spoilt(want.bfloat16(), value), want) == E.rel(want.bfloat16(), spoilt(want, float("nan"))) == math.inf
+    assert max(0.0, E.rel(spoilt(want.bfloat16(), value), want)) == math.inf and E.rel(want.bfloat16(), want) <= 2.0 ** -8
