@@ -602,10 +602,10 @@ def _need_rms_norm(x, weight, residual, mode, global_scale, layout, sum_out, out
 
 
 def _view_strides(t, tokens: int, heads: int, dim: int):
-    """(token, head) strides of a [tokens, heads, dim] view; those of a single token or head say nothing."""
+    """(token, head) strides of a [tokens, heads, dim] view; those of a single token or head say nothing (dim is as good as
+    any that the library takes)."""
     strides = t.stride()
-    head = strides[1] if heads > 1 else dim
-    return strides[0] if tokens > 1 else heads * max(dim, head), head
+    return strides[0] if tokens > 1 else dim, strides[1] if heads > 1 else dim
 
 
 class Rope(c.Structure):

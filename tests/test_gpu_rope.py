@@ -307,3 +307,26 @@ def test_append_to_a_cache_past_32_bits(B, rotary):
         assert all(torch.equal(a[-1], b[0]) for a, b in zip(cache.tensors[:4], small.tensors[:4]))
         assert not any(bool(t[:-1:5000].any()) for t in cache.tensors[:4])
         del cache
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_one_token_of_heads_before_tokens(B, interleaved):
+    """A single token of a [heads, tokens, head_dim] buffer whose heads lie more than 2^31 / 64 elements apart: rotated from there, in
+    place, and appended."""
+    heads, tokens, dim, at = 64, 300000, 128, 299998
+    buffer = torch.zeros((heads, tokens, dim), dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    x = synth.bf16_normal((2, heads, dim), 1.0, seed=7).cuda()
+    buffer[at:at + 2] = x
+    table, pos = B.rope_table(300, dim, interleaved=interleaved), ints([250, 251])
+    want = B.rope(table, x, pos)
+    assert torch.equal(B.rope(table, buffer[at + 1:], pos[1:]), want[1:])
+    a, b = (B.kv_cache_empty(1, heads, 16, dim) for _ in range(2))
+    slots = torch.arange(2, device="cuda")
+    B.kv_append_rope(a, table, x, x, slots, pos)
+    for i in range(2):
+        one = buffer[at + i:at + i + 1]
+        assert torch.equal(B.kv_append_rope(b, table, one, one, slots[i:i + 1], pos[i:i + 1], q=one), want[i:i + 1])
+    assert all(torch.equal(s, t) for s, t in zip(a.tensors[:4], b.tensors[:4]))
+    one = buffer[at + 1:]
+    assert B.rope(table, one, pos[1:], out=one) is one and torch.equal(one, want[1:]) and torch.equal(buffer[at:at + 1], x[:1])
+    assert not buffer[:at].any()

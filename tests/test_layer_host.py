@@ -243,3 +243,16 @@ def test_binding_refuses_another_devices_tensors(B, monkeypatch):
         B._need_here(None, Elsewhere())
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
     B._need_here(None, Elsewhere())
+
+
+def test_a_single_token_of_heads_before_tokens(B):
+    """One token of a long [heads, tokens, head_dim] buffer: a head stride in range is all that its view has, and the library
+    takes the strides that the binding gives it (the addresses here are refused behind them)."""
+    buffer = torch.empty((64, 300000, 128), dtype=torch.bfloat16, device="meta").transpose(0, 1)
+    strides = B._view_strides(buffer[7:8], 1, 64, 128)
+    assert strides[1] == 300000 * 128 and B._view_strides(buffer[7:9], 2, 64, 128) == (128, 300000 * 128)
+    L, r = B.lib(), rope(B)
+    assert L.rope(ctypes.byref(r), P + 2, *strides, P, 1, 64, 128, 0, P + 2, *strides, None) == B.FP4_ERR_ALIGNMENT
+    cache = B.KvCache(P, P, P, P, None, None, 4, 64, 64, 128, B.MODE_NVFP4)
+    assert L.kv_append_rope(ctypes.byref(cache), ctypes.byref(r), P, *strides, P, *strides, P, P, 1, P + 2, *strides, 64, P + 2, *strides,
+                            None) == B.FP4_ERR_ALIGNMENT
