@@ -47,6 +47,29 @@ __device__ __forceinline__ void warp_sum(float s, float& hi, float& lo) {
   lo *= unit;
 }
 
+// The lanes' sums in two parts (the second at most 2^-16 of the first), exactly enough: the first as whole numbers of 2^-26
+// of the largest's power of two, what is left and the second parts as whole numbers of 2^-14 of those.  Off by no more than
+// 2^-36 of the largest.
+__device__ __forceinline__ void warp_sum_exactly(float& hi, float& lo) {
+  const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(hi));
+  if (most >= 0x7f800000u) {  // overflown, or NaN
+    hi = __uint_as_float(most);
+    lo = 0.0f;
+    return;
+  }
+  const int e = max((int)(most >> 23) - 127, -90);
+  const float up = exp2i_f32(26 - e), v = __fmul_rn(hi, up);
+  const uint32_t n = __float2uint_rz(v);
+  const float rest = __fmaf_rn(lo, up, __fsub_rn(v, __uint2float_rz(n)));  // (n: 24 bits, so the difference is exact)
+  const uint32_t t = __reduce_add_sync(0xffffffffu, n);
+  const int r = __reduce_add_sync(0xffffffffu, __float2int_rn(__fmul_rn(rest, 0x1p14f)));
+  hi = __uint2float_rz(t);
+  lo = __fmaf_rn((float)r, 0x1p-14f, (float)(int)(t - __float2uint_rz(hi)));
+  const float unit = exp2i_f32(e - 26);
+  hi *= unit;
+  lo *= unit;
+}
+
 // 1 / sqrt(m + e), e small beside m: the hardware's approximation and one Newton step whose residual 1 - (m + e) r^2 is
 // formed in two parts, which leaves little but the rounding of the result
 __device__ __forceinline__ float inv_sqrt(float m, float e) {
@@ -93,9 +116,14 @@ __device__ __forceinline__ bool out_of_range(float sum, float eps) {
 // chunk is a scale group of NVFP4, two lanes' chunks are one of MXFP4.  The row stays in registers from its one reading
 // to its last writing; between them the sum of squares goes through the CTA.
 //
-// Precision: a thread's up to 32 squares are added in fp32, the threads' sums as integers or in pairs hi + lo, so that rstd
-// is the rounding of its exact value but for a few rows in a hundred.  Elements next to a border of the 4-bit formats move
-// by a whole step with rstd's last bit.
+// Precision: a thread's up to 32 squares are added in two chains in fp32, the threads' sums as integers or in pairs hi + lo.
+// What the chains round away averages out over a row's threads, but not where one thread holds most of the sum (a massive
+// channel: what is added behind its square loses its low bits; 4e-7 of the sum, three units of 1/rms): a warp with a
+// thread of more than a quarter of the warp's sum, or half of a row that is part of a warp, adds up again with nothing lost.
+// The sum is then off by less than 2^-23 of itself (2^-22 in rows of up to 1024 columns several of which are massive), and 1/rms
+// is the rounding of its exact value in nine rows of ten, else the number beside it.  (bf16 results do not feel that; elements
+// next to a border of the 4-bit formats move by a whole step.)  Adding up exactly always, which makes it the
+// rounding in every row, takes 18.1 us in place of 15.7 for 4096 x 5120 to NVFP4 without a residual.
 // Squares outside fp32's range (|h| near 2^60 and above, or sums below 2^-80 beside an eps that does not hide them):
 // the row is summed again in fp64.
 struct Shared {
@@ -129,6 +157,30 @@ struct Row {
 #pragma unroll
       for (int j = 0; j < 8; ++j) s = fma2(h[u][j], h[u][j], s);
     return __fadd_rn(lo_of(s), hi_of(s));
+  }
+  // The same in two parts, with nothing lost: sums that start from a power of two no smaller than any of the squares never
+  // meet a larger one, so what a step rounds away, h^2 + (s - t), comes out exactly, and so does the power's subtraction.
+  // (Squares near fp32's end make it NaN: out_of_range then, as they are.)
+  __device__ __forceinline__ void squares_exactly(float& hi, float& lo) const {
+    float m = 0.0f;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max_abs3(m, lo_of(h[u][j]), hi_of(h[u][j]));
+    const int e = 2 * (int)(__float_as_uint(m) >> 23) - 125;
+    const uint64_t base = pair_of(__uint_as_float((uint32_t)min(max(e, 1), 255) << 23)), minus = pair_of(-1.0f);
+    uint64_t s = base, err = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint64_t t = fma2(h[u][j], h[u][j], s);
+        err = add2(err, fma2(h[u][j], h[u][j], fma2(t, minus, s)));
+        s = t;
+      }
+    s = fma2(base, minus, s);
+    two_sum(lo_of(s), hi_of(s), hi, lo);
+    lo = __fadd_rn(lo, __fadd_rn(lo_of(err), hi_of(err)));
   }
   // rstd (or, in fp64, a row that fp32's squares do not hold: then scaled by its power of two) for this thread's row
   template <bool CTA>
@@ -292,12 +344,20 @@ __global__ void __launch_bounds__(CTA ? 1024 : 128) rms_norm_kernel(const RmsNor
         if (a.residual) r.add(u, i, rv[u][i]);
       }
   }
-  float hi = r.squares(), lo = 0.0f;
+  const float own = r.squares();
+  float hi = own, lo = 0.0f;
   if (a.sum_out) r.write_sum(a, row, live, l, tpr, pieces);
   if (CTA || tpr == 32)
-    warp_sum(hi, hi, lo);
+    warp_sum(own, hi, lo);
   else
     group_sum(hi, lo, tpr);
+  if (__any_sync(0xffffffffu, own * (CTA || tpr == 32 ? 4.0f : 2.0f) > hi)) {
+    r.squares_exactly(hi, lo);
+    if (CTA || tpr == 32)
+      warp_sum_exactly(hi, lo);
+    else
+      group_sum(hi, lo, tpr);
+  }
   // The warps' sums: added up by every warp for itself (each aligned group of lanes all of them), which saves a barrier, or
   // with 4-bit results, where instructions count, by the first warp (4096 x 5120 to NVFP4: 15.7 us against 17.2 without a
   // residual, 24.9 against 25.2 with one; to bf16 16.6 against 16.4, and 28.0 against 27.6).

@@ -501,8 +501,10 @@ fp4_status kv_attention(const fp4_kv_cache* cache, const fp4_bf16* q, int64_t q_
  *   out      bf16[rows, cols] or NULL, contiguous, 16-byte aligned; may be x itself
  *   xq       uint32[rows, cols/8] or NULL (at least one of out and xq), 8-byte aligned;
  *            mode, global_scale, scales, layout: as for fp4_quantize, read only with xq
- * rstd is held in fp32 from a sum of squares of at least fp32's precision; it holds
- * over bf16's whole range (squares that fp32 cannot hold are summed in fp64).  A row
+ * rstd is held in fp32 from a sum of squares that is off by less than 2^-23 of itself
+ * (2^-22 in rows of up to 1024 columns several of which hold most of it), so within one
+ * unit of fp32's last place (two); it holds over bf16's whole range (squares that fp32
+ * cannot hold are summed in fp64).  A row
  * of zeros gives zeros also where eps is 0.  An infinity or a NaN in a row gives what the
  * formula gives in out (NaN), and unspecified codes.
  * Requires cols a multiple of 8 (with xq, of 16 or 32, the group), at most 32768;

@@ -219,3 +219,42 @@ def test_elements_past_32_bits(B):
     at = ((r // 128) * (cols // 64) + c // 4) * 512 + (r % 32) * 16 + ((r % 128) // 32) * 4 + c % 4
     assert torch.equal(got.scales.view(-1)[at], want.scales)
     assert int((got.xq != 0).any(-1).sum()) == len(pick)
+
+
+def massive(rows, cols, channels, seed):
+    """Normal rows with channels that hold nearly all of a row's squares, as a residual stream has them."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn((rows, cols), generator=g, device="cuda")
+    for c in channels:
+        x[:, c] = 3000 * (1 + 0.01 * x[:, c])
+    return x.bfloat16()
+
+
+# 1/rms of such rows before what is made of it: its rounding (2^-24), the square root's own arithmetic and the sum of squares.  The
+# other channels hold at most 2^-8 of the sum and their chains lose at most 17 times 2^-24 of that, 2^-28; the rest is exact.
+RSTD = 2.0 ** -24 + 2.0 ** -27
+
+
+@pytest.mark.parametrize("rows,cols,channels", [(4096, 5120, [5]), (4096, 5120, [5, 4000]), (200, 5120, [3777]), (1200, 17408, [17000]), (8000, 2880, [0]),
+                                                (30000, 512, [100]), (60000, 128, [5, 9]), (3000, 1024, [1023]), (3000, 64, [33]), (1, 5120, [9]), (50000, 24, [17])])
+def test_massive_channels(B, rows, cols, channels):
+    """Each result is the rounding of a value within 1/rms's and one product's error of the exact one."""
+    x = massive(rows, cols, channels, cols)
+    out = B.rms_norm(x, eps=float(np.float32(1e-6))).out.double()
+    h = x.double()
+    y = h / (h.square().mean(-1, keepdim=True) + float(np.float32(1e-6))).sqrt()
+    b = RSTD + 2.0 ** -24
+    half = torch.ldexp(torch.ones_like(out), torch.frexp(out.abs().clamp(min=2.0 ** -120)).exponent - 9)  # half a step of bf16
+    off = (out - y).abs() - half - b * y.abs()
+    assert off.max() <= 0, f"{int((off > 0).sum())} elements, by up to {float((off / y.abs()).max()) * 2 ** 24:.2f} of 2^-24"
+
+
+@pytest.mark.parametrize("mode", [2, 1])
+@pytest.mark.parametrize("rows,cols,channels", [(300, 5120, [5, 4000]), (1000, 128, [9]), (2, 17408, [3000]), (700, 2880, [2879])])
+def test_massive_channels_in_four_bits(B, rows, cols, channels, mode):
+    x, r = massive(rows, cols, channels, 1).cpu(), synth.bf16_normal((rows, cols), 1.0, seed=2)
+    w = (1 + 0.3 * synth.bf16_normal((1, cols), 1.0, seed=3).float()).bfloat16().view(-1)
+    gs = float(np.float32(0.0003)) if mode == 2 else None  # (the other channels' results are near 0.02)
+    got = B.rms_norm(x.cuda(), w.cuda(), residual=r.cuda(), mode=mode, global_scale=None if gs is None else torch.tensor(gs, device="cuda"))
+    y = R.rms_norm(x, w, float(np.float32(1e-6)), r)[1]
+    R.check_codes(u32(got.xq), u8(got.scales), y, (RSTD + 3 * 2.0 ** -24) * np.abs(y), mode, 1.0 if gs is None else gs)
