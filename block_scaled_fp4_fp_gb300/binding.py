@@ -55,6 +55,7 @@ SIGNATURES = {
     "qqmm_quantize_x": (_INT, [_VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _INT, _VP, c.c_size_t, _VP, _VP, _VP]),
     "qmm": (_INT, [_VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _INT, _INT, _INT, _VP, _VP]),
     "fp4_debug_inject_wait_timeout": (_INT, [_INT]),
+    "fp4_debug_limit_sort_ctas": (_INT, [_INT]),
     "fp4_debug_stream_weights": (_INT, [_VP, _VP, _I64, _I64, _VP]),
     "kv_plan": (_INT, [_VP, _VP, _I64, _INT, _VP, _I64, _VP, _I64, _I64, _VP, _VP, _VP, _VP, _I64, _VP, _VP]),
     "kv_append": (_INT, [_VP, _VP, _I64, _I64, _VP, _I64, _I64, _VP, _I64, _VP]),
@@ -842,3 +843,8 @@ def fp4_debug_stream_weights(wq: torch.Tensor, scales: torch.Tensor, stream=None
 
 def fp4_debug_inject_wait_timeout(enable: bool):
     _check(lib().fp4_debug_inject_wait_timeout(1 if enable else 0), "fp4_debug_inject_wait_timeout")
+
+
+def fp4_debug_limit_sort_ctas(most: int):
+    """moe_sort with clusters of at most `most` CTAs, as on a part of a GPU (0: as the device allows)."""
+    _check(lib().fp4_debug_limit_sort_ctas(most), "fp4_debug_limit_sort_ctas")

@@ -21,6 +21,7 @@ constexpr int kMaxDevices = 64;
 DevInfo g_dev[kMaxDevices];
 std::mutex g_mu;
 std::atomic<int> g_inject_timeout{0};
+std::atomic<int> g_sort_ctas{0};
 
 fp4_status init_device(int device, const DevInfo** out) {
   if (device < 0 || device >= kMaxDevices) return FP4_ERR_INVALID_ARG;
@@ -823,7 +824,8 @@ fp4_status moe_sort(const int32_t* ids, int64_t tokens, int64_t k, int64_t num_e
   const DevInfo* d = nullptr;
   const fp4_status st = current(&d);
   if (st != FP4_OK) return st;
-  return from_cuda(launch_moe_sort(*d, ids, tokens, (int)k, (int)num_experts, lhs_idx, rhs_idx, slot, offsets, stream));
+  return from_cuda(launch_moe_sort(*d, ids, tokens, (int)k, (int)num_experts, lhs_idx, rhs_idx, slot, offsets,
+                                   g_sort_ctas.load(), stream));
 }
 
 namespace {
@@ -878,6 +880,12 @@ fp4_status fp4_debug_stream_weights(const uint32_t* w, const uint8_t* scales, in
 
 fp4_status fp4_debug_inject_wait_timeout(int enable) {
   g_inject_timeout.store(enable ? 1 : 0);
+  return FP4_OK;
+}
+
+fp4_status fp4_debug_limit_sort_ctas(int most) {
+  if (most < 0) return FP4_ERR_INVALID_ARG;
+  g_sort_ctas.store(most);
   return FP4_OK;
 }
 

@@ -202,8 +202,9 @@ cudaError_t launch_kv_append_rope(const DevInfo& d, const KvCacheDesc& c, const 
                                   cudaStream_t s);
 
 // moe.cu: routed rows by expert and back
+// (most_ctas: 0, or a limit on the cluster's CTAs)
 cudaError_t launch_moe_sort(const DevInfo& d, const int32_t* ids, int64_t T, int k, int E, int32_t* lhs, int32_t* rhs,
-                            int32_t* slot, int32_t* offsets, cudaStream_t s);
+                            int32_t* slot, int32_t* offsets, int most_ctas, cudaStream_t s);
 cudaError_t launch_moe_combine(const DevInfo& d, const uint16_t* y, int64_t rows, const int32_t* slot,
                                const float* weights, const uint16_t* residual, int64_t T, int k, int cols,
                                uint16_t* out, cudaStream_t s);

@@ -439,36 +439,62 @@ void pdl(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int64_t grid, int b
 }  // namespace
 
 // Rows that one CTA sorts (2048 of 32 experts: 4.5 us, with a cluster 4.4; 4096: 5.7 against 4.4), and the CTAs of a
-// cluster above: 16, the most there is (131,072 rows of 256 experts: 12.5 us, with eight 22).
-constexpr int kSortOne = 2048, kSortCtas = 16;
+// cluster above: 16, the most there is (131,072 rows of 256 experts: 12.5 us, with eight 22).  A CTA takes an SM whole, and a
+// part of a GPU may hold no 16 of them side by side: then eight, or one.
+constexpr int kSortOne = 2048, kSortCtas[] = {16, 8, 1};
 
-cudaError_t launch_moe_sort(const DevInfo& d, const int32_t* ids, int64_t T, int k, int E, int32_t* lhs, int32_t* rhs,
-                            int32_t* slot, int32_t* offsets, cudaStream_t s) {
-  const int64_t R = T * k;
-  const int ctas = R > kSortOne ? kSortCtas : 1;
-  const int64_t whole = std::max<int64_t>((E + 31) / 32 * 32, std::min<int64_t>((R + 31) / 32 * 32, 1024));
-  const int threads = ctas > 1 ? 1024 : (int)whole, warps = threads / 32;
-  const int64_t rows_cta = (R + ctas - 1) / ctas;
-  const int run = (int)std::min<int64_t>((rows_cta + threads - 1) / threads, kRunRows) * 32;
-  int bits = 0;
-  while ((1 << bits) < E) ++bits;
-  const int smem = ((warps + 3) * E + run * warps) * 4;
-  static std::atomic<uint64_t> done{0}, wide{0};
-  cudaError_t e = allow_smem(d, moe_sort_kernel, (35 * 1024 + kTileRows) * 4, done);
-  if (e != cudaSuccess) return e;
-  if (const uint64_t bit = 1ull << (d.device & 63); !(wide.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(moe_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    wide.fetch_or(bit, std::memory_order_release);
-  }
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
+namespace {
+constexpr int kSortSmem = (35 * 1024 + kTileRows) * 4;  // the most that a CTA wants
+
+void sort_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], int ctas, int threads, int smem, cudaStream_t s) {
   pdl(cfg, attr, ctas, threads, (size_t)smem, s);
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = (unsigned)ctas;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.numAttrs = 2;
+}
+
+// The largest of kSortCtas that the device has room for, asked once a device (where the kernel's attributes are set too).
+cudaError_t sort_ctas(const DevInfo& d, int& most) {
+  static std::atomic<int> known[64];
+  std::atomic<int>& mine = known[d.device & 63];
+  if ((most = mine.load(std::memory_order_acquire)) != 0) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(moe_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(moe_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  for (int ctas : kSortCtas) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    sort_config(cfg, attr, ctas, 1024, kSortSmem, nullptr);
+    int clusters = 0;
+    most = ctas;
+    if (ctas == 1 || (cudaOccupancyMaxActiveClusters(&clusters, moe_sort_kernel, &cfg) == cudaSuccess && clusters > 0)) break;
+    (void)cudaGetLastError();
+  }
+  mine.store(most, std::memory_order_release);
+  return cudaSuccess;
+}
+}  // namespace
+
+cudaError_t launch_moe_sort(const DevInfo& d, const int32_t* ids, int64_t T, int k, int E, int32_t* lhs, int32_t* rhs,
+                            int32_t* slot, int32_t* offsets, int most_ctas, cudaStream_t s) {
+  const int64_t R = T * k;
+  int most = 1, ctas = 1;
+  const cudaError_t e = sort_ctas(d, most);
+  if (e != cudaSuccess) return e;
+  if (most_ctas > 0) most = std::min(most, most_ctas);
+  if (R > kSortOne)
+    for (int n : kSortCtas) ctas = std::max(ctas, n <= most ? n : 1);
+  const int64_t whole = std::max<int64_t>((E + 31) / 32 * 32, std::min<int64_t>((R + 31) / 32 * 32, 1024));
+  const int threads = ctas > 1 ? 1024 : (int)whole, warps = threads / 32;
+  const int64_t rows_cta = (R + ctas - 1) / ctas;
+  const int run = (int)std::min<int64_t>((rows_cta + threads - 1) / threads, kRunRows) * 32;
+  int bits = 0;
+  while ((1 << bits) < E) ++bits;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  sort_config(cfg, attr, ctas, threads, ((warps + 3) * E + run * warps) * 4, s);
   return cudaLaunchKernelEx(&cfg, moe_sort_kernel, ids, (int)R, k, E, bits, (int)rows_cta, run, lhs, rhs, slot, offsets,
                             d.err);
 }

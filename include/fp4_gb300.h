@@ -598,7 +598,8 @@ fp4_status kv_append_rope(const fp4_kv_cache* cache, const fp4_rope* rope, const
  *   offsets  int32[num_experts + 1] out: first sorted row of each expert, then the number of rows kept
  * Sorted rows from offsets[num_experts] on (as many as were dropped) get token 0 and the last expert, so that the
  * lists stay what gather_qmm wants; no slot names them.
- * num_experts and k in [1, 1024], R <= 2^30. */
+ * num_experts and k in [1, 1024], R <= 2^30.  Above 2048 routed rows a cluster of 16 CTAs sorts, of eight or one where the
+ * device has no room for them. */
 fp4_status moe_sort(const int32_t* ids, int64_t tokens, int64_t k, int64_t num_experts, int32_t* lhs_idx,
                     int32_t* rhs_idx, int32_t* slot, int32_t* offsets, cudaStream_t stream);
 
@@ -634,6 +635,10 @@ fp4_status moe_combine_backward(const fp4_bf16* dout, const fp4_bf16* y, const i
  * FP4_ERR_TIMEOUT and still completes with a correct result; nothing faults or
  * hangs. */
 fp4_status fp4_debug_inject_wait_timeout(int enable);
+
+/* Test hook, off by default (0): the next launches of moe_sort use clusters of at most `most` CTAs, as they do where
+ * the device has no room for more side by side (16, 8 or 1).  The results are the same. */
+fp4_status fp4_debug_limit_sort_ctas(int most);
 
 /* Measurement aid (no counterpart on the pages): moves NVFP4 weights from HBM
  * into shared memory exactly as qmv's tensor-core path streams them -- the same

@@ -230,3 +230,30 @@ def test_elements_past_32_bits(B):
     want = B.moe_combine_backward(g, packed, y=y[live])
     assert torch.equal(dy[live], want[0]) and torch.equal(dw, want[1])
     assert int((dy != 0).any(-1).sum()) == live.numel()
+
+
+@pytest.mark.parametrize("most", [1, 8, 9])
+def test_sort_by_smaller_clusters(B, most):
+    """The launches that a part of a GPU without room for 16 CTAs side by side gets: one tile and many a CTA, every id dropped,
+    replayed from a graph, the same lists."""
+    B.fp4_debug_limit_sort_ctas(most)
+    try:
+        for tokens, k, experts, drop in ((700, 3, 32, 0.0), (2049, 1, 1, 0.0), (4096, 4, 60, 0.3), (70000, 8, 256, 0.1), (9000, 8, 1024, 0.0), (3000, 2, 16, 1.0),
+                                         (1, 1, 1, 0.0)):
+            check_sort(B, routing(tokens, k, experts, tokens, drop), experts)
+        ids = torch.zeros((9000, 4), dtype=torch.int32, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            plan = B.moe_sort(ids, 64)
+        host = routing(9000, 4, 64, 1, 0.2)
+        ids.copy_(torch.from_numpy(host))
+        graph.replay()
+        for g, w in zip(plan, R.moe_sort(host, 64)):
+            assert np.array_equal(g.cpu().numpy(), w)
+    finally:
+        B.fp4_debug_limit_sort_ctas(0)
+
+
+def test_the_limit_of_a_sorts_cluster_is_checked(B):
+    with pytest.raises(B.Fp4Error):
+        B.fp4_debug_limit_sort_ctas(-1)
