@@ -64,12 +64,15 @@ __host__ __device__ inline int vector_of(const RopeDesc& r) {
 }
 
 // -------------------------------------------------------------------- rope --
-// What one thread does of a token's heads first, first + step, ..: unit `u` of each.  A unit is two vectors of a head's
-// halves, or an interleaved vector, then the vectors that stay as they are; its cosines are loaded once for all its
-// heads, and several heads' loads are in flight.  Rotations that are no whole vectors (rotary/2 or, interleaved, rotary
-// no multiple of 4) are done a pair at a time.  Whatever is written was read by the same thread before: in place is fine.
-// Bound by HBM: 4096 tokens x 40 heads of 128 14.7 us in halves, 14.0 interleaved (5.8 and 6.1 TB/s); a quarter of heads of
-// 96 in halves (vectors of four) 17 us, a pair at a time 108.
+// What one thread does of a token's heads first, first + step, ..: unit `u` of each (no more of them than its batch:
+// head_lanes).  A unit is two vectors of a head's halves, or an interleaved vector, then the vectors that stay as they
+// are; its cosines are loaded once for all its heads, whose loads are all in flight.  Rotations that are no whole vectors
+// (rotary/2 or, interleaved, rotary no multiple of 4) are done a pair at a time.  Whatever is written was read by the same
+// thread before: in place is fine.
+// Bound by HBM: 4096 tokens x 40 heads of 128 14.7 us in halves, 14.3 interleaved (5.9 and 6.0 TB/s); a quarter of heads of
+// 96 in halves (vectors of four) 15.4 us, a pair at a time 108.
+constexpr int kRopeBatchHalves = 4, kRopeBatchInterleaved = 8;
+
 template <int N>
 struct VecOf;
 template <>
@@ -95,22 +98,19 @@ template <bool INTERLEAVED, int N>
 __device__ __forceinline__ void rope_vectors(const RopeDesc& r, const HeadsView& x, const uint16_t* in, uint16_t* out, int pos,
                                              float sign, int u, int first, int step, unsigned* err) {
   using T = typename VecOf<N>::T;
-  constexpr int NW = N / 2, B = INTERLEAVED ? 8 : 4;  // words of a vector; heads in flight
+  constexpr int NW = N / 2, B = INTERLEAVED ? kRopeBatchInterleaved : kRopeBatchHalves;  // words of a vector; heads, all in flight
   const int rotary = r.rotary_dim, turned = rotary / (INTERLEAVED ? N : 2 * N);
   const bool stays = u >= turned;
   const int c0 = stays ? rotary + N * (u - turned) : N * u, c1 = c0 + rotary / 2;
+  // on their way while the position and its row are; past the last head its own first again (no branch a load: 4096 x 40 of 128
+  // in halves 14.7 us, with one 15.4)
   T a[B], b[B];
-  auto load = [&](int h0) {
 #pragma unroll
-    for (int i = 0; i < B; ++i) {
-      const int h = h0 + i * step;
-      if (h < x.heads) {
-        a[i] = *reinterpret_cast<const T*>(in + h * x.in_head + c0);
-        if (!INTERLEAVED && !stays) b[i] = *reinterpret_cast<const T*>(in + h * x.in_head + c1);
-      }
-    }
-  };
-  load(first);  // (on their way while the position and its row are)
+  for (int i = 0; i < B; ++i) {
+    const int h = first + i * step < x.heads ? first + i * step : first;
+    a[i] = *reinterpret_cast<const T*>(in + h * x.in_head + c0);
+    if (!INTERLEAVED && !stays) b[i] = *reinterpret_cast<const T*>(in + h * x.in_head + c1);
+  }
   const float2* row = row_of(r, pos, u + first == 0, err);
   if (!row) return;
   uint64_t C[NW], S[NW];
@@ -128,41 +128,36 @@ __device__ __forceinline__ void rope_vectors(const RopeDesc& r, const HeadsView&
       }
     }
   }
-  for (int h0 = first;;) {
 #pragma unroll
-    for (int i = 0; i < B; ++i) {
-      const int h = h0 + i * step;
-      if (h >= x.heads) continue;
-      T* o0 = reinterpret_cast<T*>(out + h * x.out_head + c0);
-      T* o1 = reinterpret_cast<T*>(out + h * x.out_head + c1);
-      if (stays) {
-        *o0 = a[i];
-        continue;
-      }
-      const uint32_t* aw = reinterpret_cast<const uint32_t*>(&a[i]);
-      const uint32_t* bw = reinterpret_cast<const uint32_t*>(&b[i]);
-      T ya, yb;
-      uint32_t* yaw = reinterpret_cast<uint32_t*>(&ya);
-      uint32_t* ybw = reinterpret_cast<uint32_t*>(&yb);
-#pragma unroll
-      for (int j = 0; j < NW; ++j) {
-        const uint64_t p = widen(aw[j]);
-        if (INTERLEAVED) {
-          const uint64_t y = add2(mul2(p, C[j]), mul2(swapped(p), S[j]));
-          yaw[j] = pack_bf16x2_rn(lo_of(y), hi_of(y));
-        } else {
-          const uint64_t q = widen(bw[j]), minus = pair_of(-lo_of(S[j]), -hi_of(S[j]));
-          const uint64_t y0 = add2(mul2(p, C[j]), mul2(q, minus)), y1 = add2(mul2(q, C[j]), mul2(p, S[j]));
-          yaw[j] = pack_bf16x2_rn(lo_of(y0), hi_of(y0));
-          ybw[j] = pack_bf16x2_rn(lo_of(y1), hi_of(y1));
-        }
-      }
-      *o0 = ya;
-      if (!INTERLEAVED) *o1 = yb;
+  for (int i = 0; i < B; ++i) {
+    const int h = first + i * step;
+    if (h >= x.heads) break;
+    T* o0 = reinterpret_cast<T*>(out + h * x.out_head + c0);
+    T* o1 = reinterpret_cast<T*>(out + h * x.out_head + c1);
+    if (stays) {
+      *o0 = a[i];
+      continue;
     }
-    h0 += B * step;
-    if (h0 >= x.heads) break;
-    load(h0);
+    const uint32_t* aw = reinterpret_cast<const uint32_t*>(&a[i]);
+    const uint32_t* bw = reinterpret_cast<const uint32_t*>(&b[i]);
+    T ya, yb;
+    uint32_t* yaw = reinterpret_cast<uint32_t*>(&ya);
+    uint32_t* ybw = reinterpret_cast<uint32_t*>(&yb);
+#pragma unroll
+    for (int j = 0; j < NW; ++j) {
+      const uint64_t p = widen(aw[j]);
+      if (INTERLEAVED) {
+        const uint64_t y = add2(mul2(p, C[j]), mul2(swapped(p), S[j]));
+        yaw[j] = pack_bf16x2_rn(lo_of(y), hi_of(y));
+      } else {
+        const uint64_t q = widen(bw[j]), minus = pair_of(-lo_of(S[j]), -hi_of(S[j]));
+        const uint64_t y0 = add2(mul2(p, C[j]), mul2(q, minus)), y1 = add2(mul2(q, C[j]), mul2(p, S[j]));
+        yaw[j] = pack_bf16x2_rn(lo_of(y0), hi_of(y0));
+        ybw[j] = pack_bf16x2_rn(lo_of(y1), hi_of(y1));
+      }
+    }
+    *o0 = ya;
+    if (!INTERLEAVED) *o1 = yb;
   }
 }
 
@@ -227,7 +222,7 @@ __global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(const RopeDesc r,
 
 // ----------------------------------------------------------- kv_append_rope --
 // The first blocks append, the blocks behind them rotate q.  An appending thread has a unit of every lanes-th kv head
-// of a token, of K and of V, its cosines loaded once for all its heads.  A unit is
+// of a token (kAppendBatch of them at most: head_lanes), of K and of V, its cosines loaded once for all its heads.  A unit is
 //   kPairs   (halves of whole scale groups): two pieces of 8 channels of K's halves, which turn each other.  The lanes that
 //            share two groups (2 of NVFP4, 4 of MXFP4) do the rule of one of them each and exchange multipliers;
 //   kChunks  (interleaved): 16 channels of K;  both: 16 channels of V, and of K where it stays;
@@ -396,27 +391,24 @@ __global__ void __launch_bounds__(kAppendThreads, 6) kv_append_rope_kernel(
   const int heads = c.kv_heads, half = r.rotary_dim / 2;
   const uint16_t* kt = k + t * k_token;
   const uint16_t* vt = v + t * v_token;
-  // the first heads' loads are on their way while the slot, the position and its row are
+  // the heads' loads are on their way while the slot, the position and its row are
   const bool turned = KIND != kPieces && u < r.rotary_dim / 16;
   const int p0 = KIND == kPieces || (KIND == kPairs && turned) ? u : 2 * u;  // K's pieces
   const int p1 = KIND == kPairs && turned ? u + half / 8 : 2 * u + 1;
   uint4 ka[kAppendBatch][2], va[kAppendBatch][2];
-  auto load = [&](int h0) {
 #pragma unroll
-    for (int i = 0; i < kAppendBatch; ++i) {
-      const int h = h0 + i * append_lanes;
-      if (h >= heads) continue;
-      const uint4* kh = reinterpret_cast<const uint4*>(kt + h * k_head);
-      const uint4* vh = reinterpret_cast<const uint4*>(vt + h * v_head);
-      ka[i][0] = __ldg(kh + p0);
-      va[i][0] = __ldg(vh + (KIND == kPieces ? u : 2 * u));
-      if (KIND != kPieces) {
-        ka[i][1] = __ldg(kh + p1);
-        va[i][1] = __ldg(vh + 2 * u + 1);
-      }
+  for (int i = 0; i < kAppendBatch; ++i) {
+    const int h = hl + i * append_lanes;
+    if (h >= heads) continue;
+    const uint4* kh = reinterpret_cast<const uint4*>(kt + h * k_head);
+    const uint4* vh = reinterpret_cast<const uint4*>(vt + h * v_head);
+    ka[i][0] = __ldg(kh + p0);
+    va[i][0] = __ldg(vh + (KIND == kPieces ? u : 2 * u));
+    if (KIND != kPieces) {
+      ka[i][1] = __ldg(kh + p1);
+      va[i][1] = __ldg(vh + 2 * u + 1);
     }
-  };
-  load(hl);
+  }
   if (slot < 0 || pos < 0) return;  // a padding token
   const unsigned page = (unsigned)slot / (unsigned)c.page_size;
   if (slot > INT32_MAX || page >= c.num_pages || pos >= r.positions) {
@@ -437,33 +429,28 @@ __global__ void __launch_bounds__(kAppendThreads, 6) kv_append_rope_kernel(
   const unsigned peers = ((1u << kLanes) - 1) << ((threadIdx.x & 31) & ~(kLanes - 1));
   if constexpr (KIND == kPieces) {
     const PieceTurn turn(r, row, 8 * u);
-    for (int h0 = hl;;) {
-      uint4 other[kAppendBatch];
+    uint4 other[kAppendBatch];
 #pragma unroll
-      for (int i = 0; i < kAppendBatch; ++i)
-        if (const int h = h0 + i * append_lanes; h < heads) other[i] = turn.others(r, kt + h * k_head);
+    for (int i = 0; i < kAppendBatch; ++i)
+      if (const int h = hl + i * append_lanes; h < heads) other[i] = turn.others(r, kt + h * k_head);
 #pragma unroll
-      for (int i = 0; i < kAppendBatch; ++i) {
-        const int h = h0 + i * append_lanes;
-        if (h >= heads) continue;
+    for (int i = 0; i < kAppendBatch; ++i) {
+      const int h = hl + i * append_lanes;
+      if (h >= heads) continue;
 #pragma unroll
-        for (int which = 0; which < 2; ++which) {
-          uint64_t f[4];
-          widen8(which ? va[i][0] : ka[i][0], f);
-          if (!which) turn.apply(f, other[i]);
-          float m = largest8(f), mul;
+      for (int which = 0; which < 2; ++which) {
+        uint64_t f[4];
+        widen8(which ? va[i][0] : ka[i][0], f);
+        if (!which) turn.apply(f, other[i]);
+        float m = largest8(f), mul;
 #pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(peers, m, o));
-          uint32_t sbyte;
-          block_scale_rule_f32<MODE>(m, which ? rule_v : rule_k, mul, sbyte);
-          const CacheRow to = which ? cached(c.v_codes, c.v_scales, h) : cached(c.k_codes, c.k_scales, h);
-          to.codes[u] = codes8(f, mul);
-          if (u % kLanes == 0) to.scales[u / kLanes] = (uint8_t)sbyte;
-        }
+        for (int o = 1; o < kLanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(peers, m, o));
+        uint32_t sbyte;
+        block_scale_rule_f32<MODE>(m, which ? rule_v : rule_k, mul, sbyte);
+        const CacheRow to = which ? cached(c.v_codes, c.v_scales, h) : cached(c.k_codes, c.k_scales, h);
+        to.codes[u] = codes8(f, mul);
+        if (u % kLanes == 0) to.scales[u / kLanes] = (uint8_t)sbyte;
       }
-      h0 += kAppendBatch * append_lanes;
-      if (h0 >= heads) break;
-      load(h0);
     }
   } else {
     const unsigned two = 3u << ((threadIdx.x & 31) & ~1);
@@ -480,38 +467,33 @@ __global__ void __launch_bounds__(kAppendThreads, 6) kv_append_rope_kernel(
         }
       }
     }
-    for (int h0 = hl;;) {
 #pragma unroll
-      for (int i = 0; i < kAppendBatch; ++i) {
-        const int h = h0 + i * append_lanes;
-        if (h >= heads) continue;
-        const CacheRow to = cached(c.k_codes, c.k_scales, h);
-        uint64_t f[8];
-        widen8(ka[i][0], f);
-        widen8(ka[i][1], f + 4);
-        if (KIND == kPairs && turned) {
-          uint64_t fa[4], fb[4];
+    for (int i = 0; i < kAppendBatch; ++i) {
+      const int h = hl + i * append_lanes;
+      if (h >= heads) continue;
+      const CacheRow to = cached(c.k_codes, c.k_scales, h);
+      uint64_t f[8];
+      widen8(ka[i][0], f);
+      widen8(ka[i][1], f + 4);
+      if (KIND == kPairs && turned) {
+        uint64_t fa[4], fb[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            fa[j] = add2(mul2(f[j], C[j]), mul2(f[4 + j], M[j]));
-            fb[j] = add2(mul2(f[4 + j], C[j]), mul2(f[j], S[j]));
-          }
-          store_pair<MODE>(to, u, half, fa, fb, rule_k, peers);
-        } else {
-          if (turned) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              f[j] = add2(mul2(f[j], pair_of(cs[j].x)), mul2(swapped(f[j]), pair_of(-cs[j].y, cs[j].y)));
-          }
-          store_chunk<MODE>(to, u, f, rule_k, two);
+        for (int j = 0; j < 4; ++j) {
+          fa[j] = add2(mul2(f[j], C[j]), mul2(f[4 + j], M[j]));
+          fb[j] = add2(mul2(f[4 + j], C[j]), mul2(f[j], S[j]));
         }
-        widen8(va[i][0], f);
-        widen8(va[i][1], f + 4);
-        store_chunk<MODE>(cached(c.v_codes, c.v_scales, h), u, f, rule_v, two);
+        store_pair<MODE>(to, u, half, fa, fb, rule_k, peers);
+      } else {
+        if (turned) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            f[j] = add2(mul2(f[j], pair_of(cs[j].x)), mul2(swapped(f[j]), pair_of(-cs[j].y, cs[j].y)));
+        }
+        store_chunk<MODE>(to, u, f, rule_k, two);
       }
-      h0 += kAppendBatch * append_lanes;
-      if (h0 >= heads) break;
-      load(h0);
+      widen8(va[i][0], f);
+      widen8(va[i][1], f + 4);
+      store_chunk<MODE>(cached(c.v_codes, c.v_scales, h), u, f, rule_v, two);
     }
   }
 }
@@ -523,8 +505,9 @@ AppendKind append_kind(const KvCacheDesc& c, const RopeDesc& r) {
   return r.rotary_dim / 2 % group == 0 && c.head_dim % (2 * group) == 0 ? kPairs : kPieces;
 }
 
-// How many threads share a token's heads: one for every `batch` heads where there are then threads enough for the GPU, up to
-// one a head where there are not (1001 tokens x 64 heads of 64: 5 us, with one a head 11).
+// How many threads share a token's heads: one for every `batch` heads, which is what a thread takes at most (in vectors), where
+// there are then threads enough for the GPU, up to one a head where there are not (1001 tokens x 64 heads of 64: 5 us, with
+// one a head 11).
 int head_lanes(const DevInfo& d, int64_t T, int units, int heads, int batch) {
   const int64_t some = (heads + batch - 1) / batch, wanted = (int64_t)d.sm_count * 512 / (T * units);
   return (int)std::max<int64_t>(some, std::min<int64_t>(heads, wanted));
@@ -544,7 +527,7 @@ void pdl(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int64_t grid, int b
 void rope_shape(const DevInfo& d, const RopeDesc& r, const HeadsView& x, int64_t T, int& units, int& lanes) {
   const int rest = x.in != x.out ? x.dim - r.rotary_dim : 0, n = vector_of(r);
   units = n == 1 ? r.rotary_dim / 2 + rest : r.rotary_dim / (r.interleaved ? n : 2 * n) + rest / n;
-  lanes = head_lanes(d, T, units, x.heads, r.interleaved ? 8 : 4);
+  lanes = head_lanes(d, T, units, x.heads, r.interleaved ? kRopeBatchInterleaved : kRopeBatchHalves);
 }
 
 }  // namespace
