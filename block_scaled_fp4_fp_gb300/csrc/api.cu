@@ -818,7 +818,8 @@ fp4_status moe_sort(const int32_t* ids, int64_t tokens, int64_t k, int64_t num_e
   if (!ids || !lhs_idx || !rhs_idx || !slot || !offsets || tokens < 1 || k < 1 || k > 1024 || num_experts < 1 ||
       num_experts > 1024 || tokens > ((int64_t)1 << 30) / k)
     return FP4_ERR_INVALID_ARG;
-  if (slot == ids || lhs_idx == ids || rhs_idx == ids) return FP4_ERR_INVALID_ARG;  // (ids are read twice)
+  // (ids are read twice, by a cluster's CTAs at their own pace)
+  if (slot == ids || lhs_idx == ids || rhs_idx == ids || offsets == ids) return FP4_ERR_INVALID_ARG;
   if (!aligned(ids, 4) || !aligned(lhs_idx, 4) || !aligned(rhs_idx, 4) || !aligned(slot, 4) || !aligned(offsets, 4))
     return FP4_ERR_ALIGNMENT;
   const DevInfo* d = nullptr;

@@ -596,6 +596,7 @@ fp4_status kv_append_rope(const fp4_kv_cache* cache, const fp4_rope* rope, const
  *   rhs_idx  int32[R] out: its expert
  *   slot     int32[tokens, k] out: where each routed row went, -1 if it was dropped
  *   offsets  int32[num_experts + 1] out: first sorted row of each expert, then the number of rows kept
+ * The outputs are four buffers of their own, none of them ids (which are read twice).
  * Sorted rows from offsets[num_experts] on (as many as were dropped) get token 0 and the last expert, so that the
  * lists stay what gather_qmm wants; no slot names them.
  * num_experts and k in [1, 1024], R <= 2^30.  Above 2048 routed rows a cluster of 16 CTAs sorts, of eight or one where the

@@ -256,3 +256,12 @@ def test_a_single_token_of_heads_before_tokens(B):
     cache = B.KvCache(P, P, P, P, None, None, 4, 64, 64, 128, B.MODE_NVFP4)
     assert L.kv_append_rope(ctypes.byref(cache), ctypes.byref(r), P, *strides, P, *strides, P, P, 1, P + 2, *strides, 64, P + 2, *strides,
                             None) == B.FP4_ERR_ALIGNMENT
+
+
+def test_no_output_of_a_sort_is_its_ids(B):
+    """They are read twice: offsets written over them would change what the second reading finds."""
+    L = B.lib()
+    good = dict(lhs=P + 1024, rhs=P + 2048, slot=P + 3200, off=P + 4096)
+    for name in good:
+        b = dict(good, **{name: P})
+        assert L.moe_sort(P, 4000, 2, 8, b["lhs"], b["rhs"], b["slot"], b["off"], None) == B.FP4_ERR_INVALID_ARG, name
