@@ -804,6 +804,7 @@ fp4_status kv_append_rope(const fp4_kv_cache* cache, const fp4_rope* r, const fp
   if (q || q_out || q_heads != 0) {
     st = check_heads(q, q_token_stride, q_head_stride, q_out, q_out_token_stride, q_out_head_stride, q_heads, cache->head_dim);
     if (st != FP4_OK) return st;
+    if (q_out == k || q_out == v) return FP4_ERR_INVALID_ARG;  // (other blocks read them meanwhile)
     view = heads_view(q, q_token_stride, q_head_stride, q_out, q_out_token_stride, q_out_head_stride, q_heads, cache->head_dim);
   }
   const DevInfo* d = nullptr;

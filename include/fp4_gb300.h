@@ -569,7 +569,8 @@ fp4_status rope_table(const double* frequencies, int rotary_dim, double scale, i
  *              itself (same strides), else they do not overlap
  *   positions  int32[tokens]; a token with a negative position (padding) is not written; one past the table is not
  *              written and makes the next fp4_check_device_error return FP4_ERR_INVALID_ARG
- * Requires head_dim a multiple of 8, at most 256, rotary_dim <= head_dim. */
+ * Requires head_dim a multiple of 8, at most 256, rotary_dim <= head_dim, at most 65535 heads, strides below 2^31 (that of
+ * a single token or head: any from head_dim on). */
 fp4_status rope(const fp4_rope* rope, const fp4_bf16* x, int64_t x_token_stride, int64_t x_head_stride,
                 const int32_t* positions, int64_t tokens, int64_t heads, int64_t head_dim, int backward, fp4_bf16* out,
                 int64_t out_token_stride, int64_t out_head_stride, cudaStream_t stream);
@@ -577,7 +578,8 @@ fp4_status rope(const fp4_rope* rope, const fp4_bf16* x, int64_t x_token_stride,
 /* kv_append_rope: kv_append with K rotated on the way (fp32; not rounded to bf16 between rotation and
  * quantization), and the step's queries rotated by the same launch.
  *   cache, k, v, slot_map, tokens: as for kv_append;  rope, positions: as for rope
- *   q, q_out   bf16[tokens, q_heads, head_dim], as rope's x and out (q_out may be q), or both NULL (q_heads 0)
+ *   q, q_out   bf16[tokens, q_heads, head_dim], as rope's x and out (q_out may be q), or both NULL (q_heads 0); q_out
+ *              overlaps neither k nor v, which are read at the same time
  * A token with a negative position is skipped altogether; one with a negative slot has its q rotated only.  A
  * position past the table skips the token, a slot past the cache its K and V, and either makes the next
  * fp4_check_device_error return FP4_ERR_INVALID_ARG. */

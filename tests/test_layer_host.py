@@ -265,3 +265,16 @@ def test_no_output_of_a_sort_is_its_ids(B):
     for name in good:
         b = dict(good, **{name: P})
         assert L.moe_sort(P, 4000, 2, 8, b["lhs"], b["rhs"], b["slot"], b["off"], None) == B.FP4_ERR_INVALID_ARG, name
+
+
+def test_rotated_queries_do_not_go_over_k_or_v(B):
+    """One launch appends K and V and writes the queries: over them, what is appended would depend on which block is first."""
+    L, r = B.lib(), rope(B)
+    cache = B.KvCache(P, P, P, P, None, None, 4, 64, 2, 128, B.MODE_NVFP4)
+    k, v, q = P + 8192, P + 16384, P + 32768
+
+    def go(q_out):
+        return L.kv_append_rope(ctypes.byref(cache), ctypes.byref(r), k, 256, 128, v, 256, 128, P, P, 4, q, 256, 128, 2, q_out, 256, 128, None)
+
+    assert go(k) == go(v) == B.FP4_ERR_INVALID_ARG
+    assert go(q + 2) == B.FP4_ERR_ALIGNMENT  # (elsewhere the call gets as far as its other checks)
