@@ -244,7 +244,8 @@ __global__ void __launch_bounds__(1024) moe_sort_kernel(const int32_t* __restric
 // A thread has P 16-byte pieces of tokens' rows, K rows of each in flight: eight loads whatever k is (bytes in flight are
 // what the rate goes by: 2048 x 4 of 2880 took 17.9 us with four).  Added in fp32 in order of j, rounded once.
 // Bound by HBM: 8192 x 8 of 2880 66 us, 6.4 TB/s; 2048 x 4 of 2880 12.5 us, 4.7 TB/s (seven CTAs of 128 an SM, 2.7 waves:
-// the loads behind a slot wait for it).
+// the loads behind a slot wait for it).  Tried: CTAs that stay and fetch the next slots while rows are on their way (13.1 and
+// 69.0 us).
 constexpr int kCombineThreads = 128;
 
 template <int K, int P>
@@ -316,7 +317,8 @@ __global__ void __launch_bounds__(kCombineThreads, P == 4 ? 4 : 7) moe_combine_k
 // flight a thread.  The dot products of the K rows are reduced together: each step of the butterfly halves the number of
 // sums a lane holds, nine shuffles instead of forty for eight.
 // The CTAs behind the tokens' clear the rows that no slot names.  Bound by HBM: 4096 x 8 of 5120 110 us, 6.5 TB/s; 2048 x 4
-// of 2880 21 us, 5.0 TB/s.
+// of 2880 21 us, 5.0 TB/s.  Tried: packed fp32 for the products (no change, here as in moe_combine: loads are what is waited
+// for).
 constexpr int kTailCtas = 64, kBackwardThreads = 512;
 
 enum TokenOf { kCta512, kCta128, kWarp };  // what a token belongs to

@@ -290,9 +290,11 @@ struct Row {
   }
 };
 
-// Bound by HBM in bf16 with a residual (4096 x 5120: 27.6 us, 6.1 TB/s), without one and with 4-bit results by the 10 to 20
-// instructions an element between the loads and the stores (4096 x 5120 with a residual to NVFP4: 24.9 us, 5.5 TB/s;
-// 8001 x 2880 to MXFP4: 16.5 us, 3.5 TB/s), one row by latency (1 x 5120: 2.2 us).
+// Bound by HBM in bf16 with a residual (4096 x 5120: 27.5 us, 6.1 TB/s).  Without one, and with 4-bit results, by latency:
+// registers hold the warps to half of what an SM takes, each CTA loads, sums, computes and stores one after the other, and
+// while it computes it has nothing in flight; loads are the first stall by a factor of three, half of the issue slots are used
+// (4096 x 5120 with a residual to NVFP4: 24.8 us, 5.5 TB/s, without one 15.75; 8001 x 2880 to MXFP4: 16.7 us, 3.5 TB/s).
+// One row by latency alone (1 x 5120: 2.2 us).
 // Tried: CTAs that stay, the next row on its way into shared memory by bulk copy (31.8 us in bf16 with a residual, 28.3 to NVFP4;
 // without one 17.7 against 18.2 then); four chunks a thread (31 and 34 us; without a residual, x kept as bf16 and widened twice,
 // 24 against 16.4 in bf16: spills); loads past L1 (within 2 %).
@@ -359,7 +361,7 @@ __global__ void __launch_bounds__(CTA ? 1024 : 128) rms_norm_kernel(const RmsNor
       group_sum(hi, lo, tpr);
   }
   // The warps' sums: added up by every warp for itself (each aligned group of lanes all of them), which saves a barrier, or
-  // with 4-bit results, where instructions count, by the first warp (4096 x 5120 to NVFP4: 15.7 us against 17.2 without a
+  // with 4-bit results, where each warp has more to do, by the first warp (4096 x 5120 to NVFP4: 15.7 us against 17.2 without a
   // residual, 24.9 against 25.2 with one; to bf16 16.6 against 16.4, and 28.0 against 27.6).
   constexpr bool kEvery = MODE == 0;
   if (CTA) {

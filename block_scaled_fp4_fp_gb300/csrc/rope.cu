@@ -227,8 +227,8 @@ __global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(const RopeDesc r,
 //            share two groups (2 of NVFP4, 4 of MXFP4) do the rule of one of them each and exchange multipliers;
 //   kChunks  (interleaved): 16 channels of K;  both: 16 channels of V, and of K where it stays;
 //   kPieces  (any other rotation): 8 channels; what they are paired with is read beside them.
-// 17,500 tokens, 8 heads of 128: MXFP4 25 us, NVFP4 27 us, where the bytes take 15; with 32 query heads 66 and 68 us,
-// 5.8 TB/s.  A third of the SM's warps (80 registers) wait for loads; a scale group a thread, its partner read beside it,
+// 17,500 tokens, 8 heads of 128: MXFP4 23 us, NVFP4 27 us, where the bytes take 15; with 32 query heads 62 and 67 us, 6.2
+// and 5.8 TB/s.  A third of the SM's warps (80 registers) wait for loads; a scale group a thread, its partner read beside it,
 // took 39 and 54 us, a piece a thread with the maximum shared by shuffles 47 and 64 (instructions).
 constexpr int kAppendThreads = 128, kAppendBatch = 2;
 enum AppendKind { kPairs, kChunks, kPieces };
