@@ -353,12 +353,18 @@ __global__ void __launch_bounds__(CTA ? 1024 : 128) rms_norm_kernel(const RmsNor
     warp_sum(own, hi, lo);
   else
     group_sum(hi, lo, tpr);
-  if (__any_sync(0xffffffffu, own * (CTA || tpr == 32 ? 4.0f : 2.0f) > hi)) {
-    r.squares_exactly(hi, lo);
+  if (const unsigned votes = __ballot_sync(0xffffffffu, own * (CTA || tpr == 32 ? 4.0f : 2.0f) > hi)) {
+    float whole, rest;
+    r.squares_exactly(whole, rest);
     if (CTA || tpr == 32)
-      warp_sum_exactly(hi, lo);
+      warp_sum_exactly(whole, rest);
     else
-      group_sum(hi, lo, tpr);
+      group_sum(whole, rest, tpr);
+    // (a row that shares its warp goes by its own vote: its bits do not depend on its neighbours)
+    if (CTA || tpr == 32 || votes >> (lane & -tpr) & ((1u << tpr) - 1)) {
+      hi = whole;
+      lo = rest;
+    }
   }
   // The warps' sums: added up by every warp for itself (each aligned group of lanes all of them), which saves a barrier, or
   // with 4-bit results, where each warp has more to do, by the first warp (4096 x 5120 to NVFP4: 15.7 us against 17.2 without a

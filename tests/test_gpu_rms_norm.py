@@ -258,3 +258,16 @@ def test_massive_channels_in_four_bits(B, rows, cols, channels, mode):
     got = B.rms_norm(x.cuda(), w.cuda(), residual=r.cuda(), mode=mode, global_scale=None if gs is None else torch.tensor(gs, device="cuda"))
     y = R.rms_norm(x, w, float(np.float32(1e-6)), r)[1]
     R.check_codes(u32(got.xq), u8(got.scales), y, (RSTD + 3 * 2.0 ** -24) * np.abs(y), mode, 1.0 if gs is None else gs)
+
+
+@pytest.mark.parametrize("cols", [128, 512])
+def test_a_rows_bits_do_not_depend_on_its_neighbours(B, cols):
+    """Rows that share a warp with massive ones: the same bits as among others."""
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    x = torch.randn((400000, cols), generator=g, device="cuda").bfloat16()
+    beside = x.clone()
+    beside[::8, 5] = 3000
+    a, b = B.rms_norm(x).out, B.rms_norm(beside).out
+    rest = torch.ones(x.shape[0], dtype=torch.bool, device="cuda")
+    rest[::8] = False
+    assert int((a[rest] != b[rest]).sum()) == 0
