@@ -165,10 +165,11 @@ fp4_status fp4_dequantize(const uint32_t* wq, const void* scales, const fp4_bf16
  * Requires K % 32 == 0 and K % group_size == 0.
  * Launch order: qmv uses programmatic dependent launch and may read w and its
  * scales before the kernel launched just before it on the stream has finished;
- * x, global_scale_w and y are touched only after that kernel completes.  No
- * kernel of this library writes weights and releases its dependents early, so
- * any sequence of calls through this header is ordered; a caller's own kernel
- * that writes w and triggers its dependents early must not directly precede qmv.
+ * x, global_scale_w and y are touched only after that kernel completes.  What
+ * fp4_quantize and fp4_quantize_sr write is complete before a kernel behind them
+ * starts, so any sequence of those calls and qmv is ordered.  A kernel that writes
+ * w or scales and triggers its dependents early must not directly precede qmv: a
+ * caller's own, or rms_norm, whose codes are activations.
  * A NaN or infinity in x gives non-finite rows (tensor-core path, NVFP4 and MXFP4: NaN). */
 fp4_status qmv(const fp4_bf16* x, const uint32_t* w, const void* scales, const fp4_bf16* biases,
                const float* global_scale_w, int64_t N, int64_t K, fp4_mode mode, int bits,
